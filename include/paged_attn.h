@@ -70,7 +70,21 @@ typedef enum {
   PA_ERR_SCRATCH_LIMIT = 7   /* the static-scratch decode needs more than its fixed array      */
 } pa_status;
 
-typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1 } pa_kv_dtype;
+typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_FP4_E2M1 = 2 } pa_kv_dtype;
+
+/*
+ * 4-bit caches (PA_KV_FP4_E2M1).  Each 16 consecutive dims of one token's head row are stored as 16
+ * OCP E2M1 codes (two a byte, the lower dim in the low nibble) and one OCP E4M3 scale; the value of a
+ * code is e2m1(code) * e4m3(scale) * k_scale[g] (or v_scale[g]), with one fp32 scale per kv head:
+ *   k_cache, v_cache  [num_blocks, num_kv_heads, 16, 9 * head_dim / 16] bytes, 16-byte aligned.  A
+ *                     (block, head) page of 9 * head_dim bytes holds the codes of its 16 tokens
+ *                     (head_dim / 2 bytes each), then their scales (head_dim / 16 bytes each).
+ *   k_scale, v_scale  [num_kv_heads] fp32, device, positive and finite; NULL means 1.  Static: a
+ *                     value near amax / (6 * 448) over the head's expected keys (values) centres the
+ *                     E4M3 scales.
+ * Accepted by paged_attn_append_kv, paged_attn_read_kv, paged_attn_decode, paged_attn_verify,
+ * paged_attn_tree_verify, paged_attn_prefill and the window forms.
+ */
 
 /*
  * Single-token decode for a continuous batch with ragged context lengths (studybook section
@@ -180,6 +194,10 @@ int paged_attn_prefill(const void* q, const void* k_cache, const void* v_cache,
  *   context_lens [num_seqs] int32, device: lengths AFTER the append; sequence b's new tokens
  *     take positions [context_lens[b] - n_new, context_lens[b]).
  *   kv_dtype PA_KV_BF16: the rows are stored unchanged.
+ *   kv_dtype PA_KV_FP4_E2M1: each 16 dims get scale = e4m3(min(amax / (6 s), 448)), s = k_scale[g]
+ *     (v_scale[g]), read only, and codes e2m1(x / (scale * s)); both roundings to nearest even, fp32
+ *     arithmetic (6 s and scale * s rounded first).  A zero scale stores zeros; infinities store the
+ *     largest magnitude, NaNs +6 * scale * s.  Stored tokens do not change.
  *   kv_dtype PA_KV_FP8_E4M3: k_scale / v_scale [num_blocks, num_kv_heads] fp32, device, read
  *     and written.  Each touched (block, head) gets the scale amax / 448 over its valid tokens
  *     (1 if all are zero) -- symmetric per-block scale quantisation (studybook section 10.8.2);
@@ -199,6 +217,53 @@ int paged_attn_append_kv(const void* k_new, const void* v_new, void* k_cache, vo
                          int n_new, int max_blocks_per_seq, int num_blocks, int num_kv_heads,
                          int head_dim, int block_size, int kv_dtype, float* k_scale,
                          float* v_scale, void* stream);
+
+/*
+ * Read stored tokens back as bf16: the inverse of paged_attn_append_kv.  For every sequence the rows
+ * of its last n tokens, positions [context_lens[b] - n, context_lens[b]), are gathered through the
+ * block table, turned into the values that they stand for and rounded to bf16 once.
+ *   caches, block_table, context_lens, kv_dtype, k_scale, v_scale as in paged_attn_decode (E4M3:
+ *   scales [num_blocks, num_kv_heads]; E2M1: [num_kv_heads] or NULL).
+ *   k_out, v_out [num_seqs, n, num_kv_heads, head_dim] bf16, device, 16-byte aligned, written.
+ * Tokens before a sequence's first, and tokens in out-of-range blocks, come out as zeros and are
+ * flagged (PA_ERR_DEVICE_BOUNDS from paged_attn_check_device_errors).  Asynchronous on `stream`;
+ * never allocates.  Returns as paged_attn_append_kv.
+ */
+int paged_attn_read_kv(const void* k_cache, const void* v_cache, const int32_t* block_table,
+                       const int32_t* context_lens, int num_seqs, int n, int max_blocks_per_seq,
+                       int num_blocks, int num_kv_heads, int head_dim, int block_size, int kv_dtype,
+                       const float* k_scale, const float* v_scale, void* k_out, void* v_out,
+                       void* stream);
+
+/*
+ * Norm and rotation of queries and keys, the step before paged_attn_append_kv, in one pass.  Each
+ * head row x of q and k becomes y = x / sqrt(mean(x^2) + eps) * weight; then the first rotary_dim
+ * dims are rotated in pairs by the angles of the token's position:
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin),
+ * pair i being dims (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved != 0.  fp32 arithmetic,
+ * one rounding to bf16.
+ *   q, k         [num_tokens, num_q_heads (num_kv_heads), head_dim] bf16, device, 16-byte aligned;
+ *                q_stride and k_stride are the elements from one token to the next (multiples of 8, at
+ *                least heads * head_dim), so both may be slices of one packed projection.
+ *   q_weight,
+ *   k_weight     [head_dim] bf16, device, 16-byte aligned.
+ *   cos_sin      [max_position, rotary_dim] fp32, device, 16-byte aligned: row p holds the rotary_dim
+ *                / 2 cosines, then the sines, of position p.
+ *   positions    [num_tokens] int32, device.  A position outside [0, max_position) makes its token's
+ *                rows zeros and is flagged (PA_ERR_DEVICE_BOUNDS).
+ *   q_out, k_out as q and k with strides of their own; each may be its input with the same stride
+ *                (in place) and otherwise must not overlap q or k.
+ * Limits: head_dim 64 or 128, rotary_dim a multiple of 16 in [16, head_dim].  Asynchronous on
+ * `stream`; never allocates.  Returns PA_OK (also for num_tokens == 0), PA_ERR_INVALID_ARG (NULL
+ * pointer, negative size, misalignment, a stride too short, eps negative or not finite),
+ * PA_ERR_UNSUPPORTED or PA_ERR_CUDA.
+ */
+int paged_attn_qk_norm_rope(const void* q, const void* k, const void* q_weight,
+                            const void* k_weight, const float* cos_sin, const int32_t* positions,
+                            int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                            int rotary_dim, int interleaved, int max_position, float eps,
+                            int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                            int64_t k_out_stride, void* q_out, void* k_out, void* stream);
 
 /*
  * Speculative acceptance, the step after paged_attn_verify: decide which of the K drafted tokens

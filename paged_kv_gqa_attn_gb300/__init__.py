@@ -24,6 +24,8 @@ __all__ = [
     "tree_verify",
     "prefill",
     "append_kv",
+    "read_kv",
+    "qk_norm_rope",
     "spec_accept",
     "check_device_errors",
     "set_max_partitions",
@@ -44,6 +46,7 @@ PA_ERR_DEVICE_TIMEOUT = 6
 PA_ERR_SCRATCH_LIMIT = 7
 PA_KV_BF16 = 0
 PA_KV_FP8_E4M3 = 1
+PA_KV_FP4_E2M1 = 2
 PA_WAIT_LIMIT = 1 << 18   # suspending mbarrier polls before a kernel wait gives up
 PA_SPIN_LIMIT = 1 << 22   # non-suspending probe iterations before an issuer loop gives up
 
@@ -92,6 +95,11 @@ def load_library(build_if_missing: bool = True, timeline: Optional[bool] = None)
             lib.paged_attn_prefill.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, I, P, P, P, P]
             lib.paged_attn_append_kv.restype = I
             lib.paged_attn_append_kv.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P]
+            lib.paged_attn_read_kv.restype = I
+            lib.paged_attn_read_kv.argtypes = [P, P, P, P, I, I, I, I, I, I, I, I, P, P, P, P, P]
+            L = ctypes.c_int64
+            lib.paged_attn_qk_norm_rope.restype = I
+            lib.paged_attn_qk_norm_rope.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, F, L, L, L, L, P, P, P]
             lib.paged_attn_spec_accept.restype = I
             lib.paged_attn_spec_accept.argtypes = [P, P, P, P, P, I, I, I, P, P, P]
             lib.paged_attn_check_device_errors.restype = I
@@ -183,6 +191,35 @@ def _check_cuda(name, t, dtypes):
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _kv_dtype(k_cache, v_cache, head_dim, k_scale, v_scale):
+    """The cache type by the caches' dtype and last dim (bf16 [.., d], E4M3 bytes [.., d], 4-bit bytes
+    [.., 9 d / 16]), with the checks of the scales that it takes."""
+    if k_cache.dtype == torch.bfloat16:
+        kv = PA_KV_BF16
+    elif k_cache.dtype == torch.uint8 and k_cache.dim() == 4 and 16 * k_cache.shape[3] == 9 * head_dim:
+        kv = PA_KV_FP4_E2M1
+    else:
+        kv = PA_KV_FP8_E4M3
+    types = {PA_KV_BF16: (torch.bfloat16,), PA_KV_FP4_E2M1: (torch.uint8,),
+             PA_KV_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn)}[kv]
+    _check_cuda("k_cache", k_cache, types)
+    _check_cuda("v_cache", v_cache, types)
+    if kv == PA_KV_FP8_E4M3:
+        _check_cuda("k_scale", k_scale, (torch.float32,))
+        _check_cuda("v_scale", v_scale, (torch.float32,))
+    if kv == PA_KV_FP4_E2M1:
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None:
+                _check_cuda(name, t, (torch.float32,))
+                if t.shape != (k_cache.shape[1],):
+                    raise ValueError(f"{name} must be [num_kv_heads] for a 4-bit cache")
+    return kv
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_scale=None,
@@ -305,40 +342,132 @@ def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, sca
 def append_kv(k_new, v_new, k_cache, v_cache, block_table, context_lens, *, k_scale=None,
               v_scale=None, stream=None):
     """Store the new tokens' K/V [B, n_new, Hkv, d] bf16 in the paged cache, in place (and, for an
-    fp8 cache, update the per-(block, head) scales).  context_lens holds the lengths after the
-    append.  See paged_attn_append_kv."""
+    fp8 cache, update the per-(block, head) scales; a 4-bit cache takes optional per-head scales
+    [Hkv] that it only reads).  context_lens holds the lengths after the append.  See
+    paged_attn_append_kv."""
     lib = load_library()
     _check_cuda("k_new", k_new, (torch.bfloat16,))
     _check_cuda("v_new", v_new, (torch.bfloat16,))
-    fp8 = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
-    kv_dtypes = (torch.uint8, torch.float8_e4m3fn) if fp8 else (torch.bfloat16,)
-    _check_cuda("k_cache", k_cache, kv_dtypes)
-    _check_cuda("v_cache", v_cache, kv_dtypes)
-    _check_cuda("block_table", block_table, (torch.int32,))
-    _check_cuda("context_lens", context_lens, (torch.int32,))
-    if fp8:
-        _check_cuda("k_scale", k_scale, (torch.float32,))
-        _check_cuda("v_scale", v_scale, (torch.float32,))
     if k_new.dim() != 4 or k_new.shape != v_new.shape or k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
         raise ValueError("expected k_new/v_new [B, n_new, Hkv, d] and caches [NB, Hkv, bs, d]")
     B, n_new, Hkv, d = k_new.shape
+    kv = _kv_dtype(k_cache, v_cache, d, k_scale, v_scale)
+    _check_cuda("block_table", block_table, (torch.int32,))
+    _check_cuda("context_lens", context_lens, (torch.int32,))
     NB, Hkv2, bs, d2 = k_cache.shape
-    if (Hkv2, d2) != (Hkv, d) or block_table.dim() != 2 or block_table.shape[0] != B \
-            or context_lens.shape != (B,):
+    if Hkv2 != Hkv or (d2 != d and kv != PA_KV_FP4_E2M1) or block_table.dim() != 2 \
+            or block_table.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("shape mismatch between new rows, caches, block_table and context_lens")
-    if fp8 and (k_scale.shape != (NB, Hkv) or v_scale.shape != (NB, Hkv)):
+    if kv == PA_KV_BF16:
+        k_scale = v_scale = None
+    if kv == PA_KV_FP8_E4M3 and (k_scale.shape != (NB, Hkv) or v_scale.shape != (NB, Hkv)):
         raise ValueError("k_scale / v_scale must be [num_blocks, num_kv_heads]")
     with _one_device(stream, k_new=k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache,
-                     block_table=block_table, context_lens=context_lens,
-                     k_scale=k_scale if fp8 else None, v_scale=v_scale if fp8 else None):
+                     block_table=block_table, context_lens=context_lens, k_scale=k_scale, v_scale=v_scale):
         st = lib.paged_attn_append_kv(
             k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_table.data_ptr(), context_lens.data_ptr(), B, n_new, int(block_table.shape[1]), NB,
-            Hkv, d, bs, PA_KV_FP8_E4M3 if fp8 else PA_KV_BF16,
-            k_scale.data_ptr() if fp8 else None, v_scale.data_ptr() if fp8 else None,
-            _stream_handle(stream))
+            Hkv, d, bs, kv, _ptr(k_scale), _ptr(v_scale), _stream_handle(stream))
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attn_append_kv")
+
+
+def read_kv(k_cache, v_cache, block_table, context_lens, n, *, k_scale=None, v_scale=None, k_out=None,
+            v_out=None, head_dim=None, stream=None):
+    """The last n stored tokens of every sequence as bf16 (k, v), each [B, n, Hkv, d]: the inverse of
+    append_kv.  Caches and scales of any type; head_dim is needed only where a byte cache's last dim
+    could be read two ways (E4M3 bytes of d against 4-bit bytes of 9 d / 16: 36 and 72 are 4-bit
+    caches of 64 and 128).  See paged_attn_read_kv."""
+    lib = load_library()
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or k_cache.shape != v_cache.shape \
+            or block_table.dim() != 2:
+        raise ValueError("expected caches [NB, Hkv, bs, d] and block_table [B, M]")
+    NB, Hkv, bs, last = k_cache.shape
+    if head_dim is None:
+        head_dim = {36: 64, 72: 128}.get(last, last) if k_cache.dtype == torch.uint8 else last
+    d = int(head_dim)
+    kv = _kv_dtype(k_cache, v_cache, d, k_scale, v_scale)
+    _check_cuda("block_table", block_table, (torch.int32,))
+    _check_cuda("context_lens", context_lens, (torch.int32,))
+    B, n = int(block_table.shape[0]), int(n)
+    if context_lens.shape != (B,) or (last != d and kv != PA_KV_FP4_E2M1) or n < 0:
+        raise ValueError("shape mismatch between caches, block_table, context_lens, n and head_dim")
+    if kv == PA_KV_BF16:
+        k_scale = v_scale = None
+    if kv == PA_KV_FP8_E4M3 and (k_scale.shape != (NB, Hkv) or v_scale.shape != (NB, Hkv)):
+        raise ValueError("k_scale / v_scale must be [num_blocks, num_kv_heads]")
+    outs = []
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            t = torch.empty(B, n, Hkv, d, dtype=torch.bfloat16, device=k_cache.device)
+        _check_cuda(name, t, (torch.bfloat16,))
+        if t.shape != (B, n, Hkv, d):
+            raise ValueError(f"{name} must be [B, n, Hkv, d]")
+        outs.append(t)
+    if n == 0 or B == 0:
+        return tuple(outs)
+    with _one_device(stream, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                     context_lens=context_lens, k_scale=k_scale, v_scale=v_scale, k_out=outs[0], v_out=outs[1]):
+        st = lib.paged_attn_read_kv(
+            k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), B, n,
+            int(block_table.shape[1]), NB, Hkv, d, bs, kv, _ptr(k_scale), _ptr(v_scale), outs[0].data_ptr(),
+            outs[1].data_ptr(), _stream_handle(stream))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attn_read_kv")
+    return tuple(outs)
+
+
+def _check_rows(name, t):
+    """bf16 [T, heads, d] on the GPU whose tokens may be strided (a slice of a packed projection)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, d]")
+    if t.shape[0] and (t.stride(2) != 1 or t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    # a single token's stride says nothing
+    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1] * t.shape[2])
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, *, eps=1e-6, interleaved=False, q_out=None,
+                 k_out=None, stream=None):
+    """RMS norm of every head row of q [T, Hq, d] and k [T, Hkv, d] bf16 and the rotation of its first
+    cos_sin.shape[1] dims by the token's position, in one pass; returns (q_out, k_out).  q and k may be
+    slices of one packed projection (tokens strided); q_out / k_out may be q / k themselves.  Weights
+    [d] bf16, cos_sin [max_position, rotary_dim] fp32 (cosines, then sines), positions [T] int32.  See
+    paged_attn_qk_norm_rope."""
+    lib = load_library()
+    strides = [_check_rows("q", q), _check_rows("k", k)]
+    _check_cuda("q_weight", q_weight, (torch.bfloat16,))
+    _check_cuda("k_weight", k_weight, (torch.bfloat16,))
+    _check_cuda("cos_sin", cos_sin, (torch.float32,))
+    _check_cuda("positions", positions, (torch.int32,))
+    T, Hq, d = q.shape
+    Hkv = int(k.shape[1])
+    if k.shape != (T, Hkv, d) or q_weight.shape != (d,) or k_weight.shape != (d,) or cos_sin.dim() != 2 \
+            or positions.shape != (T,):
+        raise ValueError("expected q [T, Hq, d], k [T, Hkv, d], weights [d], cos_sin [P, rotary], positions [T]")
+    if q_out is None:
+        q_out = torch.empty(T, Hq, d, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(T, Hkv, d, dtype=k.dtype, device=k.device)
+    strides += [_check_rows("q_out", q_out), _check_rows("k_out", k_out)]
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must have q's and k's shapes")
+    if T == 0:
+        return q_out, k_out
+    with _one_device(stream, q=q, k=k, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
+                     positions=positions, q_out=q_out, k_out=k_out):
+        st = lib.paged_attn_qk_norm_rope(
+            q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), cos_sin.data_ptr(),
+            positions.data_ptr(), T, Hq, Hkv, d, int(cos_sin.shape[1]), int(bool(interleaved)),
+            int(cos_sin.shape[0]), float(eps), *strides, q_out.data_ptr(), k_out.data_ptr(),
+            _stream_handle(stream))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attn_qk_norm_rope")
+    return q_out, k_out
 
 
 def spec_accept(p, q, draft_tokens, u_accept, u_sample, *, out_tokens=None, num_accepted=None,

@@ -69,6 +69,10 @@ int device_state(DeviceState** out) {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+bool known_kv_dtype(int kv_dtype) {
+  return kv_dtype == PA_KV_BF16 || kv_dtype == PA_KV_FP8_E4M3 || kv_dtype == PA_KV_FP4_E2M1;
+}
+
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link needed).
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
@@ -472,9 +476,8 @@ int paged_attn_append_kv(const void* k_new, const void* v_new, void* k_cache, vo
   if (num_seqs < 0 || n_new < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || num_kv_heads < 1 ||
       head_dim < 1 || block_size < 1)
     return PA_ERR_INVALID_ARG;
-  if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3) return PA_ERR_INVALID_ARG;
-  const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
-  if (fp8 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  if (!known_kv_dtype(kv_dtype)) return PA_ERR_INVALID_ARG;
+  if (kv_dtype == PA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
   if ((int64_t)n_new > (int64_t)max_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
   if (block_size != 16 || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
   if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
@@ -487,9 +490,96 @@ int paged_attn_append_kv(const void* k_new, const void* v_new, void* k_cache, vo
   int st = device_state(&dev);
   if (st != PA_OK) return st;
   cudaError_t e = pa::launch_append(k_new, v_new, k_cache, v_cache, block_table, context_lens, num_seqs, n_new,
-                                    max_blocks_per_seq, num_blocks, num_kv_heads, head_dim, fp8, k_scale, v_scale,
+                                    max_blocks_per_seq, num_blocks, num_kv_heads, head_dim, kv_dtype, k_scale, v_scale,
                                     dev->err, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int paged_attn_read_kv(const void* k_cache, const void* v_cache, const int32_t* block_table,
+                       const int32_t* context_lens, int num_seqs, int n, int max_blocks_per_seq, int num_blocks,
+                       int num_kv_heads, int head_dim, int block_size, int kv_dtype, const float* k_scale,
+                       const float* v_scale, void* k_out, void* v_out, void* stream) {
+  if (!k_cache || !v_cache || !block_table || !context_lens || !k_out || !v_out) return PA_ERR_INVALID_ARG;
+  if (num_seqs < 0 || n < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || num_kv_heads < 1 || head_dim < 1 ||
+      block_size < 1)
+    return PA_ERR_INVALID_ARG;
+  if (!known_kv_dtype(kv_dtype)) return PA_ERR_INVALID_ARG;
+  if (kv_dtype == PA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  if ((int64_t)n > (int64_t)max_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
+  if (block_size != 16 || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)num_seqs * n > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;  // one CTA per token
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || n == 0) return PA_OK;
+  DeviceState* dev = nullptr;
+  int st = device_state(&dev);
+  if (st != PA_OK) return st;
+  pa::ReadParams p = {};
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.block_table = block_table;
+  p.context_lens = context_lens;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.err = dev->err;
+  p.num_seqs = num_seqs;
+  p.n = n;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.num_kv_heads = num_kv_heads;
+  return pa::launch_read_kv(p, head_dim, kv_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                                     : PA_ERR_CUDA;
+}
+
+int paged_attn_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                            const float* cos_sin, const int32_t* positions, int num_tokens, int num_q_heads,
+                            int num_kv_heads, int head_dim, int rotary_dim, int interleaved, int max_position,
+                            float eps, int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                            int64_t k_out_stride, void* q_out, void* k_out, void* stream) {
+  if (!q || !k || !q_weight || !k_weight || !cos_sin || !positions || !q_out || !k_out) return PA_ERR_INVALID_ARG;
+  if (num_tokens < 0 || num_q_heads < 1 || num_kv_heads < 1 || head_dim < 1 || max_position < 1)
+    return PA_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || eps > 3.4e38f) return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (rotary_dim < 16 || rotary_dim > head_dim || rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+  if (num_q_heads > 65536 || num_kv_heads > 65536) return PA_ERR_UNSUPPORTED;  // grid.y of the kernel
+  const int64_t q_row = (int64_t)num_q_heads * head_dim, k_row = (int64_t)num_kv_heads * head_dim;
+  if (q_stride < q_row || q_out_stride < q_row || k_stride < k_row || k_out_stride < k_row) return PA_ERR_INVALID_ARG;
+  // rows are moved in 16-byte pieces
+  if ((q_stride | k_stride | q_out_stride | k_out_stride) % 8 != 0) return PA_ERR_INVALID_ARG;
+  const uintptr_t align = (uintptr_t)q | (uintptr_t)k | (uintptr_t)q_weight | (uintptr_t)k_weight |
+                          (uintptr_t)cos_sin | (uintptr_t)q_out | (uintptr_t)k_out;
+  if (align % 16 != 0) return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  DeviceState* dev = nullptr;
+  int st = device_state(&dev);
+  if (st != PA_OK) return st;
+  pa::RopeParams p = {};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
+  p.k_weight = static_cast<const __nv_bfloat16*>(k_weight);
+  p.cos_sin = cos_sin;
+  p.positions = positions;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.err = dev->err;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_out_stride = k_out_stride;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.rotary = rotary_dim;
+  p.max_position = max_position;
+  p.eps = eps;
+  return pa::launch_qk_norm_rope(p, head_dim, interleaved != 0, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
 }
 
 int paged_attn_spec_accept(const float* p, const float* q, const int32_t* draft_tokens, const float* u_accept,

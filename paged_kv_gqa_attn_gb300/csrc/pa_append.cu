@@ -12,8 +12,13 @@
 // re-encodes the older tokens when the scale changes, and encodes the new ones; all arithmetic
 // fp32, rounding to E4M3 nearest-even with saturation (cvt.rn.satfinite).
 //
+// 4-bit caches (E2M1 codes, one E4M3 scale for each 16 dims of a token, one fp32 scale s per kv head):
+// scale = e4m3(min(amax / (6 s), 448)), code = e2m1(x / (scale * s)), both to nearest even, fp32
+// arithmetic; a zero scale stores zeros.  The scales belong to the token, so nothing older is read.
+//
 // The blocks written are assumed to belong to their sequence alone (a block shared with another
 // sequence is copied before it is written: the scheduler's job).
+#include "pa_fp4.cuh"
 #include "pa_kernels.h"
 
 namespace pa {
@@ -177,9 +182,60 @@ __global__ void __launch_bounds__(128) append_fp8_kernel(const AppendParams p) {
   }
 }
 
+// 4-bit: one CTA per new token, a thread per 16-dim block of K or V (32 bytes read, 8 + 1 written).
+// The source loads are issued before the dependent context-length and block-table loads.
 template <int D>
-cudaError_t launch_d(const AppendParams& p, bool fp8, cudaStream_t st) {
-  if (fp8) {
+__global__ void __launch_bounds__(128) append_fp4_kernel(const AppendParams p) {
+  using P = Fp4Page<D>;
+  constexpr int kC = D / 16;  // 16-dim blocks per head row
+  const int row = blockIdx.x;  // b * n_new + t
+  const int b = row / p.n_new, t = row - b * p.n_new;
+  const int per_side = p.num_kv_heads * kC;
+  for (int i = threadIdx.x; i < 2 * per_side; i += blockDim.x) {
+    const bool is_v = i >= per_side;
+    const int r = is_v ? i - per_side : i;
+    const uint4* src = reinterpret_cast<const uint4*>(is_v ? p.v_new : p.k_new) + ((size_t)row * per_side + r) * 2;
+    const uint4 a = src[0], c4 = src[1];
+    const int g = r / kC, c = r - g * kC;
+    const float* scales = is_v ? p.v_scale : p.k_scale;
+    const float s = scales ? scales[g] : 1.f;
+    const int L = p.context_lens[b];
+    if (L < p.n_new || L > p.max_blocks_per_seq * 16) {
+      if (threadIdx.x == 0) record_error(p.err, kErrShortContext);
+      return;
+    }
+    const int j = L - p.n_new + t;
+    const int pb = p.block_table[(size_t)b * p.max_blocks_per_seq + j / 16];
+    if (pb < 0 || pb >= p.num_blocks) {
+      if (threadIdx.x == 0) record_error(p.err, kErrBlockId);
+      return;
+    }
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, c4.x, c4.y, c4.z, c4.w};
+    float f[16];
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 x = bf16x2_to_f2(w[k]);
+      f[2 * k] = x.x;
+      f[2 * k + 1] = x.y;
+      amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
+    const uint16_t sc = f32x2_to_e4m3x2(fminf(amax / (6.f * s), 448.f), 0.f);
+    const float step = e4m3x2_to_f2(sc).x * s;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) f[k] = step > 0.f ? f[k] / step : 0.f;
+    uint8_t* page = (is_v ? p.v_cache : p.k_cache) + ((size_t)pb * p.num_kv_heads + g) * P::kBytes;
+    const int slot = j & 15;
+    *reinterpret_cast<uint2*>(page + slot * P::kCodeRow + c * 8) = make_uint2(f32x8_to_e2m1(f), f32x8_to_e2m1(f + 8));
+    page[P::kCodeBytes + slot * P::kScaleRow + c] = (uint8_t)sc;
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const AppendParams& p, int kv, cudaStream_t st) {
+  if (kv == kKvFp4) {
+    append_fp4_kernel<D><<<(unsigned)(p.num_seqs * p.n_new), 128, 0, st>>>(p);
+  } else if (kv == kKvE4m3) {
     append_fp8_kernel<D><<<dim3(p.num_kv_heads, p.num_seqs, 2), 128, 0, st>>>(p);
   } else {
     append_bf16_kernel<D><<<(unsigned)(p.num_seqs * p.n_new), 128, 0, st>>>(p);
@@ -191,7 +247,7 @@ cudaError_t launch_d(const AppendParams& p, bool fp8, cudaStream_t st) {
 
 cudaError_t launch_append(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
                           const int32_t* block_table, const int32_t* context_lens, int num_seqs, int n_new,
-                          int max_blocks_per_seq, int num_blocks, int num_kv_heads, int head_dim, bool fp8,
+                          int max_blocks_per_seq, int num_blocks, int num_kv_heads, int head_dim, int kv_dtype,
                           float* k_scale, float* v_scale, unsigned* err, cudaStream_t stream) {
   AppendParams p;
   p.k_new = static_cast<const __nv_bfloat16*>(k_new);
@@ -208,8 +264,8 @@ cudaError_t launch_append(const void* k_new, const void* v_new, void* k_cache, v
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.num_kv_heads = num_kv_heads;
-  if (head_dim == 128) return launch_d<128>(p, fp8, stream);
-  if (head_dim == 64) return launch_d<64>(p, fp8, stream);
+  if (head_dim == 128) return launch_d<128>(p, kv_dtype, stream);
+  if (head_dim == 64) return launch_d<64>(p, kv_dtype, stream);
   return cudaErrorInvalidConfiguration;
 }
 

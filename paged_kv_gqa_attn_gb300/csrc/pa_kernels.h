@@ -8,6 +8,9 @@
 
 namespace pa {
 
+// Cache types, numbered as pa_kv_dtype.
+constexpr int kKvBf16 = 0, kKvE4m3 = 1, kKvFp4 = 2;
+
 // Split-KV launch geometry: grid = (max_partitions, num_kv_heads, num_seqs).
 struct Launch {
   int head_dim;
@@ -44,11 +47,44 @@ size_t prefill_scratch_bytes(int num_seqs, int max_q_len, int group);
 cudaError_t launch_verify_split(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
 cudaError_t launch_prefill_tc(const AttnParams& p, const Launch& l, int max_q_len, void* scratch, const CUtensorMap& tk,
                               const CUtensorMap& tv);
-// KV append (bf16 scatter, or fp8 with per-(block, head) rescaling); arguments already checked.
+// KV append (bf16 scatter, fp8 with per-(block, head) rescaling, or E2M1 codes with a scale for each
+// 16 dims of a token); arguments already checked.
 cudaError_t launch_append(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
                           const int32_t* block_table, const int32_t* context_lens, int num_seqs, int n_new,
-                          int max_blocks_per_seq, int num_blocks, int num_kv_heads, int head_dim, bool fp8,
+                          int max_blocks_per_seq, int num_blocks, int num_kv_heads, int head_dim, int kv_dtype,
                           float* k_scale, float* v_scale, unsigned* err, cudaStream_t stream);
+
+// Read the last n tokens of every sequence back as bf16 rows; arguments already checked.
+struct ReadParams {
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const int32_t* block_table;
+  const int32_t* context_lens;
+  const float* k_scale;   // as the cache type's (E2M1: [Hkv] or null)
+  const float* v_scale;
+  __nv_bfloat16* k_out;   // [B, n, Hkv, d]
+  __nv_bfloat16* v_out;
+  unsigned* err;
+  int num_seqs, n, max_blocks_per_seq, num_blocks, num_kv_heads;
+};
+cudaError_t launch_read_kv(const ReadParams& p, int head_dim, int kv_dtype, cudaStream_t st);
+
+// RMS norm and rotation of the query and key head rows; strides in elements between tokens.
+struct RopeParams {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* q_weight;  // [d]
+  const __nv_bfloat16* k_weight;
+  const float* cos_sin;           // [max_position, rotary]
+  const int32_t* positions;       // [T]
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;
+  unsigned* err;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  int num_tokens, num_q_heads, num_kv_heads, rotary, max_position;
+  float eps;
+};
+cudaError_t launch_qk_norm_rope(const RopeParams& p, int head_dim, bool interleaved, cudaStream_t st);
 
 // Speculative acceptance: scan kernel over vocabulary chunks, then the pick kernel (programmatic
 // dependent).  chunk_sums holds accept_scratch_bytes(num_seqs, vocab) bytes.

@@ -1,0 +1,74 @@
+"""Host-side argument checks of qk_norm_rope, read_kv and the 4-bit cache type through the C ABI: no
+call here reaches a GPU."""
+
+import ctypes
+
+import pytest
+
+import paged_kv_gqa_attn_gb300 as pa
+
+FAKE = 1 << 20  # a 16-byte aligned non-null address that is never dereferenced
+
+
+def _rope(**over):
+    a = dict(q=FAKE, k=FAKE, qw=FAKE, kw=FAKE, cs=FAKE, pos=FAKE, T=0, Hq=8, Hkv=2, d=128, rot=128, inter=0,
+             P=100, eps=1e-6, qs=1024, ks=256, qos=1024, kos=256, qo=FAKE, ko=FAKE)
+    a.update(over)
+    return pa.load_library().paged_attn_qk_norm_rope(*a.values(), None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(), pa.PA_OK),
+    (dict(q=None), pa.PA_ERR_INVALID_ARG),
+    (dict(pos=None), pa.PA_ERR_INVALID_ARG),
+    (dict(ko=None), pa.PA_ERR_INVALID_ARG),
+    (dict(T=-1), pa.PA_ERR_INVALID_ARG),
+    (dict(Hkv=0), pa.PA_ERR_INVALID_ARG),
+    (dict(P=0), pa.PA_ERR_INVALID_ARG),
+    (dict(eps=-1e-6), pa.PA_ERR_INVALID_ARG),
+    (dict(eps=float("nan")), pa.PA_ERR_INVALID_ARG),
+    (dict(eps=float("inf")), pa.PA_ERR_INVALID_ARG),
+    (dict(qs=1016), pa.PA_ERR_INVALID_ARG),
+    (dict(kos=257), pa.PA_ERR_INVALID_ARG),
+    (dict(q=FAKE + 8), pa.PA_ERR_INVALID_ARG),
+    (dict(cs=FAKE + 4), pa.PA_ERR_INVALID_ARG),
+    (dict(d=96), pa.PA_ERR_UNSUPPORTED),
+    (dict(rot=0), pa.PA_ERR_UNSUPPORTED),
+    (dict(rot=24), pa.PA_ERR_UNSUPPORTED),
+    (dict(rot=144), pa.PA_ERR_UNSUPPORTED),
+])
+def test_qk_norm_rope_checks(over, status):
+    assert _rope(**over) == status
+
+
+def _read(**over):
+    a = dict(k=FAKE, v=FAKE, bt=FAKE, cl=FAKE, B=0, n=1, M=4, NB=8, Hkv=2, d=128, bs=16, dt=2, ks=None, vs=None,
+             ko=FAKE, vo=FAKE)
+    a.update(over)
+    return pa.load_library().paged_attn_read_kv(*a.values(), None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(), pa.PA_OK),
+    (dict(B=2, n=0), pa.PA_OK),
+    (dict(k=None), pa.PA_ERR_INVALID_ARG),
+    (dict(vo=None), pa.PA_ERR_INVALID_ARG),
+    (dict(n=65), pa.PA_ERR_INVALID_ARG),
+    (dict(n=-1), pa.PA_ERR_INVALID_ARG),
+    (dict(dt=3), pa.PA_ERR_INVALID_ARG),
+    (dict(dt=1), pa.PA_ERR_INVALID_ARG),
+    (dict(ko=FAKE + 8), pa.PA_ERR_INVALID_ARG),
+    (dict(d=32), pa.PA_ERR_UNSUPPORTED),
+    (dict(bs=8), pa.PA_ERR_UNSUPPORTED),
+    (dict(B=65536), pa.PA_ERR_UNSUPPORTED),
+])
+def test_read_kv_checks(over, status):
+    assert _read(**over) == status
+
+
+def test_append_takes_the_4_bit_type_without_scales():
+    fn = pa.load_library().paged_attn_append_kv
+    lead = [FAKE] * 6
+    assert fn(*lead, 0, 1, 4, 8, 2, 128, 16, 2, None, None, None) == pa.PA_OK
+    assert fn(*lead, 0, 1, 4, 8, 2, 128, 16, 3, None, None, None) == pa.PA_ERR_INVALID_ARG
+    assert fn(*lead, 0, 1, 4, 8, 2, 128, 16, 1, None, None, None) == pa.PA_ERR_INVALID_ARG
