@@ -185,6 +185,40 @@ int paged_attn_prefill(const void* q, const void* k_cache, const void* v_cache,
                        void* out, void* stream);
 
 /*
+ * Sliding window with sinks: paged_attn_decode, paged_attn_verify and paged_attn_prefill in which a
+ * row that would see the n first tokens sees token j < n only when j >= n - window (the window counts
+ * the row's own token) or j < sinks (the first tokens, which take the softmax's surplus mass when the
+ * middle of a long context is dropped).
+ *   window >= 1; sinks >= 0; either may exceed the context, which then hides nothing.
+ * Block-table entries of blocks that no row of the sequence sees are not read: a caller may give such
+ * blocks back to its pool and leave any value there.  A token that no row of a (sequence, 128-row
+ * tile) sees does not reach the output even as NaN; one that some row of the tile sees must be finite.
+ * Work and scratch are those of the visible tokens.  Same arguments, errors and limits otherwise, but
+ * max_context_len at most 2^30.  Kernels: the decode kernel (groups of 1, 2, 4 and 8) and the prefill
+ * kernel, for verify rows and other groups of decode split like decode; the pages that are left are
+ * numbered without the gap.
+ */
+int paged_attn_window_decode(const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_table, const int32_t* context_lens, int num_seqs,
+                             int max_blocks_per_seq, int num_blocks, int max_context_len, int q_len,
+                             int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                             int window, int sinks, float scale, int kv_dtype, const float* k_scale,
+                             const float* v_scale, void* out, void* stream);
+int paged_attn_window_verify(const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_table, const int32_t* context_lens, int num_seqs,
+                             int max_blocks_per_seq, int num_blocks, int max_context_len, int q_len,
+                             int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                             int window, int sinks, float scale, int kv_dtype, const float* k_scale,
+                             const float* v_scale, void* out, void* stream);
+int paged_attn_window_prefill(const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_table, const int32_t* context_lens,
+                              const int32_t* query_start_loc, int num_seqs, int total_q,
+                              int max_q_len, int max_blocks_per_seq, int num_blocks,
+                              int max_context_len, int num_q_heads, int num_kv_heads, int head_dim,
+                              int block_size, int window, int sinks, float scale, int kv_dtype,
+                              const float* k_scale, const float* v_scale, void* out, void* stream);
+
+/*
  * KV append: store the new tokens' K and V in the paged cache, the step that precedes the
  * attention call of each decode or verify step (studybook fde-roadmap ch.10, sections 10.2.2
  * and 10.3.2: the step's K/V join the cache; section 10.12.2 and aegloslab servingai 5.3.7:

@@ -105,14 +105,17 @@ def sees(n, j, window=None, sinks=0):
     return (j < n) & (True if window is None else ((j >= n - window) | (j < sinks)))
 
 
-def attend(q, keys, values, table, lens, rows, scale, window=None, sinks=0, masks=None):
+def attend(q, keys, values, table, lens, rows, scale, window=None, sinks=0, masks=None, sizes=False):
     """Attention of packed rows.  q [total, Hq, d]; keys, values [NB, Hkv, 16, d] fp64; rows[b] new rows
     of sequence b, the last of its lens[b] tokens; masks: optional ancestor bitmasks [total] over the new
-    tokens.  A row that sees nothing is zeros; blocks outside the pool are left out.  fp64 [total, Hq, d]."""
+    tokens.  A row that sees nothing is zeros; blocks outside the pool are left out.  fp64 [total, Hq, d].
+    With sizes=True also sum_j p_j |v_j| [total, Hq, d] and max_j sum |q k_j| scale [total, Hq, 1] over the
+    tokens each row sees: what the rounding errors of an evaluation are proportional to."""
     q = to_f64(q)
     hkv, d = keys.shape[1], keys.shape[3]
     group = q.shape[1] // hkv
     out = np.zeros(q.shape)
+    spread, dots = np.zeros(q.shape), np.zeros((*q.shape[:2], 1))
     first = 0
     for b, r in enumerate(rows):
         n_all = int(lens[b])
@@ -135,11 +138,19 @@ def attend(q, keys, values, table, lens, rows, scale, window=None, sinks=0, mask
         top = np.where(any_seen, x.max(-1, keepdims=True, initial=-np.inf), 0)
         p = np.where(np.isneginf(x), 0, np.exp(x - top))
         # a token that a row does not see gives it nothing, whatever is stored there
+        # (callers store non-finite values only where no row sees them)
         v = np.where(np.isnan(v) | np.isinf(v), 0, v) if not np.isfinite(v).all() else v
         o = np.einsum("rhgp,phd->rhgd", p, v) / np.maximum(p.sum(-1, keepdims=True), 1e-300)
         out[first: first + r] = np.where(any_seen, o, 0).reshape(r, -1, d)
+        if sizes:
+            a = np.einsum("rhgp,phd->rhgd", p, np.abs(v)) / np.maximum(p.sum(-1, keepdims=True), 1e-300)
+            spread[first: first + r] = np.where(any_seen, a, 0).reshape(r, -1, d)
+            k0 = np.where(np.isfinite(k), np.abs(k), 0)
+            y = np.einsum("rhgd,phd->rhgp", np.abs(q[first: first + r]).reshape(r, hkv, group, d), k0) * abs(scale)
+            y = np.where(see[:, used][:, None, None], y, 0)
+            dots[first: first + r] = y.max(-1, keepdims=True, initial=0).reshape(r, -1, 1)
         first += r
-    return out
+    return (out, spread, dots) if sizes else out
 
 
 def norm_rope(x, weight, cos_sin, positions, eps, interleaved=False):

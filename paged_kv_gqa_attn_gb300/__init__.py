@@ -93,6 +93,13 @@ def load_library(build_if_missing: bool = True, timeline: Optional[bool] = None)
             lib.paged_attn_tree_verify.argtypes = attn_args[:5] + [P] + attn_args[5:]
             lib.paged_attn_prefill.restype = I
             lib.paged_attn_prefill.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, I, P, P, P, P]
+            for name in ("paged_attn_window_decode", "paged_attn_window_verify"):
+                fn = getattr(lib, name)
+                fn.restype = I
+                fn.argtypes = attn_args[:14] + [I, I] + attn_args[14:]
+            lib.paged_attn_window_prefill.restype = I
+            lib.paged_attn_window_prefill.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, I, F, I, P,
+                                                      P, P, P]
             lib.paged_attn_append_kv.restype = I
             lib.paged_attn_append_kv.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P]
             lib.paged_attn_read_kv.restype = I
@@ -222,24 +229,29 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _window(fn_name, window, sinks):
+    """The C entry of a call with or without a window, and the window's arguments."""
+    if window is None:
+        if sinks:
+            raise ValueError("sinks need a window: without one every token is visible")
+        return fn_name, ()
+    return fn_name.replace("paged_attn_", "paged_attn_window_"), (int(window), int(sinks))
+
+
 def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_scale=None,
-          v_scale=None, max_context_len=None, out=None, stream=None, tree_mask=None):
+          v_scale=None, max_context_len=None, out=None, stream=None, tree_mask=None, window=None, sinks=0):
     lib = load_library()
     _check_cuda("q", q, (torch.bfloat16,))
-    fp8 = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
-    kv_dtypes = (torch.uint8, torch.float8_e4m3fn) if fp8 else (torch.bfloat16,)
-    _check_cuda("k_cache", k_cache, kv_dtypes)
-    _check_cuda("v_cache", v_cache, kv_dtypes)
-    _check_cuda("block_table", block_table, (torch.int32,))
-    _check_cuda("context_lens", context_lens, (torch.int32,))
-    if fp8:
-        _check_cuda("k_scale", k_scale, (torch.float32,))
-        _check_cuda("v_scale", v_scale, (torch.float32,))
     if q.dim() != 4 or k_cache.dim() != 4 or k_cache.shape != v_cache.shape or block_table.dim() != 2:
         raise ValueError("expected q [B, q_len, Hq, d], caches [NB, Hkv, bs, d], block_table [B, M]")
     B, q_len, Hq, d = q.shape
+    kv = _kv_dtype(k_cache, v_cache, d, k_scale, v_scale)
+    _check_cuda("block_table", block_table, (torch.int32,))
+    _check_cuda("context_lens", context_lens, (torch.int32,))
+    if kv == PA_KV_BF16:
+        k_scale = v_scale = None
     NB, Hkv, bs, d2 = k_cache.shape
-    if d2 != d or block_table.shape[0] != B or context_lens.shape != (B,):
+    if (d2 != d and kv != PA_KV_FP4_E2M1) or block_table.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("shape mismatch between q, caches, block_table and context_lens")
     if out is None:
         out = torch.empty_like(q)
@@ -250,6 +262,7 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
     max_blocks = int(block_table.shape[1])
     if max_context_len is None:
         max_context_len = max_blocks * bs  # an upper bound known without reading the device
+    fn_name, span = _window(fn_name, window, sinks)
     lead = [q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
             context_lens.data_ptr()]
     if fn_name == "paged_attn_tree_verify":
@@ -258,60 +271,62 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
             raise ValueError("tree_mask must be [B, q_len]")
         lead.append(tree_mask.data_ptr())
     with _one_device(stream, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                     context_lens=context_lens, tree_mask=tree_mask, out=out,
-                     k_scale=k_scale if fp8 else None, v_scale=v_scale if fp8 else None):
+                     context_lens=context_lens, tree_mask=tree_mask, out=out, k_scale=k_scale, v_scale=v_scale):
         st = getattr(lib, fn_name)(
-            *lead, B, max_blocks, NB, int(max_context_len), q_len, Hq, Hkv, d, bs,
-            float(scale), PA_KV_FP8_E4M3 if fp8 else PA_KV_BF16,
-            k_scale.data_ptr() if fp8 else None, v_scale.data_ptr() if fp8 else None, out.data_ptr(),
-            _stream_handle(stream))
+            *lead, B, max_blocks, NB, int(max_context_len), q_len, Hq, Hkv, d, bs, *span,
+            float(scale), kv, _ptr(k_scale), _ptr(v_scale), out.data_ptr(), _stream_handle(stream))
     if st != PA_OK:
         raise PagedAttnError(st, fn_name)
     return out
 
 
 def decode(q, k_cache, v_cache, block_table, context_lens, scale, **kw):
-    """Single-token paged GQA decode; q [B, 1, Hq, d] bf16.  See paged_attn_decode."""
+    """Single-token paged GQA decode; q [B, 1, Hq, d] bf16.  With window=W (and sinks=S) the token sees
+    the last W tokens, itself included, and the first S.  See paged_attn_decode,
+    paged_attn_window_decode."""
     return _call("paged_attn_decode", q, k_cache, v_cache, block_table, context_lens, scale, **kw)
 
 
 def verify(q, k_cache, v_cache, block_table, context_lens, scale, **kw):
-    """(K+1)-row causal speculative-verify attention; q [B, K+1, Hq, d] bf16.  See paged_attn_verify."""
+    """(K+1)-row causal speculative-verify attention; q [B, K+1, Hq, d] bf16.  window and sinks as in
+    decode, each row's window ending at its own token.  See paged_attn_verify,
+    paged_attn_window_verify."""
     return _call("paged_attn_verify", q, k_cache, v_cache, block_table, context_lens, scale, **kw)
 
 
 def tree_verify(q, k_cache, v_cache, block_table, context_lens, tree_mask, scale, **kw):
     """Verify over a tree of drafts: tree_mask int32 [B, q_len] ancestor bitmasks over the new
-    tokens (bit t of row i: row i sees new token t).  See paged_attn_tree_verify."""
+    tokens (bit t of row i: row i sees new token t).  It takes no window.  See
+    paged_attn_tree_verify."""
+    if kw.get("window") is not None:
+        raise ValueError("tree_verify takes no window")
     return _call("paged_attn_tree_verify", q, k_cache, v_cache, block_table, context_lens, scale,
                  tree_mask=tree_mask, **kw)
 
 
 def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, scale, *,
-            max_q_len=None, max_context_len=None, out=None, stream=None, k_scale=None, v_scale=None):
+            max_q_len=None, max_context_len=None, out=None, stream=None, k_scale=None, v_scale=None,
+            window=None, sinks=0):
     """Paged attention over packed variable-length query rows (chunked prefill, with decode or
     verify rows alongside): q [total_q, Hq, d] bf16, query_start_loc [B+1] int32 (device); caches
-    bf16, or E4M3 bytes (uint8 / float8_e4m3fn) with k_scale / v_scale [NB, Hkv] fp32.
+    bf16, E4M3 bytes (uint8 / float8_e4m3fn) with k_scale / v_scale [NB, Hkv] fp32, or 4-bit.
     max_q_len must bound every sequence's rows; by default it is read from query_start_loc
-    (one device-to-host copy).  See paged_attn_prefill."""
+    (one device-to-host copy).  window and sinks as in verify.  See paged_attn_prefill,
+    paged_attn_window_prefill."""
     lib = load_library()
     _check_cuda("q", q, (torch.bfloat16,))
-    fp8 = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
-    kv_dtypes = (torch.uint8, torch.float8_e4m3fn) if fp8 else (torch.bfloat16,)
-    _check_cuda("k_cache", k_cache, kv_dtypes)
-    _check_cuda("v_cache", v_cache, kv_dtypes)
-    if fp8:
-        _check_cuda("k_scale", k_scale, (torch.float32,))
-        _check_cuda("v_scale", v_scale, (torch.float32,))
-    _check_cuda("block_table", block_table, (torch.int32,))
-    _check_cuda("context_lens", context_lens, (torch.int32,))
-    _check_cuda("query_start_loc", query_start_loc, (torch.int32,))
     if q.dim() != 3 or k_cache.dim() != 4 or k_cache.shape != v_cache.shape or block_table.dim() != 2:
         raise ValueError("expected q [total_q, Hq, d], caches [NB, Hkv, bs, d], block_table [B, M]")
     total_q, Hq, d = q.shape
+    kv = _kv_dtype(k_cache, v_cache, d, k_scale, v_scale)
+    _check_cuda("block_table", block_table, (torch.int32,))
+    _check_cuda("context_lens", context_lens, (torch.int32,))
+    _check_cuda("query_start_loc", query_start_loc, (torch.int32,))
+    if kv == PA_KV_BF16:
+        k_scale = v_scale = None
     NB, Hkv, bs, d2 = k_cache.shape
     B = int(block_table.shape[0])
-    if d2 != d or context_lens.shape != (B,) or query_start_loc.shape != (B + 1,):
+    if (d2 != d and kv != PA_KV_FP4_E2M1) or context_lens.shape != (B,) or query_start_loc.shape != (B + 1,):
         raise ValueError("shape mismatch between q, caches, block_table, context_lens, query_start_loc")
     if out is None:
         out = torch.empty_like(q)
@@ -325,17 +340,17 @@ def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, sca
     max_blocks = int(block_table.shape[1])
     if max_context_len is None:
         max_context_len = max_blocks * bs
+    fn_name, span = _window("paged_attn_prefill", window, sinks)
     with _one_device(stream, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                     context_lens=context_lens, query_start_loc=query_start_loc, out=out,
-                     k_scale=k_scale if fp8 else None, v_scale=v_scale if fp8 else None):
-        st = lib.paged_attn_prefill(
+                     context_lens=context_lens, query_start_loc=query_start_loc, out=out, k_scale=k_scale,
+                     v_scale=v_scale):
+        st = getattr(lib, fn_name)(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
             context_lens.data_ptr(), query_start_loc.data_ptr(), B, total_q, max(1, int(max_q_len)),
-            max_blocks, NB, int(max_context_len), Hq, Hkv, d, bs, float(scale),
-            PA_KV_FP8_E4M3 if fp8 else PA_KV_BF16, k_scale.data_ptr() if fp8 else None,
-            v_scale.data_ptr() if fp8 else None, out.data_ptr(), _stream_handle(stream))
+            max_blocks, NB, int(max_context_len), Hq, Hkv, d, bs, *span, float(scale), kv, _ptr(k_scale),
+            _ptr(v_scale), out.data_ptr(), _stream_handle(stream))
     if st != PA_OK:
-        raise PagedAttnError(st, "paged_attn_prefill")
+        raise PagedAttnError(st, fn_name)
     return out
 
 

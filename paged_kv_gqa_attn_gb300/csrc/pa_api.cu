@@ -135,7 +135,7 @@ int validate(Form form, const void* q, const void* k_cache, const void* v_cache,
   if (num_seqs < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || max_context_len < 0) return PA_ERR_INVALID_ARG;
   if (num_q_heads < 1 || num_kv_heads < 1 || head_dim < 1 || block_size < 1 || q_len < 1) return PA_ERR_INVALID_ARG;
   if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
-  if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3) return PA_ERR_INVALID_ARG;
+  if (!known_kv_dtype(kv_dtype)) return PA_ERR_INVALID_ARG;
   if (kv_dtype == PA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
   if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, 16) || !aligned(out, 16))
@@ -156,7 +156,38 @@ int validate(Form form, const void* q, const void* k_cache, const void* v_cache,
   return PA_OK;
 }
 
-int run(Form form, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+// What a window with sinks leaves of an attention call (window 0: no window, every token).
+struct Window {
+  int window;
+  int sinks;
+};
+constexpr Window kNoWindow = {0, 0};
+
+// The arguments of a window form: window at least 1, sinks not negative.  The kernels' position
+// arithmetic is 32-bit, so contexts stay below 2^30.
+int check_window(const Window& w, int max_context_len) {
+  if (w.window < 1 || w.sinks < 0) return PA_ERR_INVALID_ARG;
+  return max_context_len > (1 << 30) ? PA_ERR_UNSUPPORTED : PA_OK;
+}
+
+void set_window(pa::AttnParams* p, const Window& w, int max_context_len, int align) {
+  if (w.window == 0) return;
+  const int most = max_context_len > 0 ? max_context_len : 1;
+  p->window = w.window < most ? w.window : most;  // a window past the bound hides nothing
+  p->sinks = w.sinks < most ? w.sinks : most;
+  p->page_align = align;
+}
+
+// Upper bound of the tokens (in whole pages) that the split of one sequence covers: the sinks' pages and
+// the window's, both edges rounded to `align` pages, or the whole context.
+int visible_context(const Window& w, int max_context_len, int q_len, int align) {
+  if (w.window == 0) return max_context_len;
+  const int64_t head = (((int64_t)w.sinks + 15) / 16 + align - 1) / align * align;
+  const int64_t pages = head + ((int64_t)w.window + q_len - 1) / 16 + 2 + (align - 1);
+  return pages * 16 < max_context_len ? (int)(pages * 16) : max_context_len;
+}
+
+int run(Form form, const Window& win, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
         const int32_t* context_lens, const uint32_t* tree_mask, int num_seqs, int max_blocks_per_seq,
         int num_blocks, int max_context_len, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
         int block_size, float scale, int kv_dtype, const float* k_scale, const float* v_scale, void* out,
@@ -195,6 +226,7 @@ int run(Form form, const void* q, const void* k_cache, const void* v_cache, cons
   l.head_dim = head_dim;
   l.group = num_q_heads / num_kv_heads;
   l.fp8 = kv_dtype == PA_KV_FP8_E4M3;
+  l.kv = kv_dtype;
   l.stream = s;
 
   cudaError_t e;
@@ -204,9 +236,14 @@ int run(Form form, const void* q, const void* k_cache, const void* v_cache, cons
   // tcgen05 kernel (balanced persistent split + merge), decode as its q_len = 1 rows.
   // Verify with more than the verify kernel's 64 rows per kv head (bf16, up to 128) runs the
   // chunked-prefill kernel split into partitions like decode, with the same merge.
+  // So does what the verify kernel has no form for: a window, or a 4-bit cache.
   const bool mma_group = l.group == 1 || l.group == 2 || l.group == 4 || l.group == 8;
-  const bool wide_verify = form == Form::kVerify && l.group * q_len > 64;
-  const bool on_tensor_cores = (form == Form::kVerify && !wide_verify) || (form == Form::kDecode && !mma_group);
+  const bool fp4 = kv_dtype == PA_KV_FP4_E2M1;
+  const bool mma_decode = form == Form::kDecode && mma_group && !fp4;
+  const bool split_tiles = !mma_decode && (l.group * q_len > 64 || win.window > 0 || fp4);
+  const bool on_tensor_cores = !mma_decode && !split_tiles;
+  const int align = mma_decode ? 1 : 4;  // the split prefill kernel walks whole 64-token steps
+  set_window(&p, win, max_context_len, align);
   if (on_tensor_cores) {
     // balanced persistent split: planner, tcgen05 kernel, segment merge
     const int ncta = pa::verify_resident_ctas(dev->num_sms);
@@ -228,11 +265,11 @@ int run(Form form, const void* q, const void* k_cache, const void* v_cache, cons
     e = (r1 == PA_OK && r2 == PA_OK) ? pa::launch_verify_tc(p, l, scratch, ncta, tk, tv) : cudaErrorInvalidValue;
   } else {
     int ppp = 0, nparts = 0;
-    st = paged_attn_plan(dev->num_sms, num_seqs, num_kv_heads, max_context_len, block_size, q_len, kv_dtype, &ppp,
-                         &nparts);
+    const int covered = visible_context(win, max_context_len, q_len, align);
+    st = paged_attn_plan(dev->num_sms, num_seqs, num_kv_heads, covered, block_size, q_len, kv_dtype, &ppp, &nparts);
     if (st != PA_OK) return st;
-    if (wide_verify && ppp % 4 != 0) {  // the prefill kernel walks whole 64-token steps
-      const int pages = (max_context_len + block_size - 1) / block_size;
+    if (split_tiles && ppp % 4 != 0) {  // the prefill kernel walks whole 64-token steps
+      const int pages = (covered + block_size - 1) / block_size;
       ppp = (ppp + 3) / 4 * 4;
       nparts = pages > 0 ? (pages + ppp - 1) / ppp : 1;
     }
@@ -250,17 +287,98 @@ int run(Form form, const void* q, const void* k_cache, const void* v_cache, cons
     }
     // 2-D TMA maps of the pools (bf16: 16 x 64-dim boxes; E4M3: one 16 x d box per page)
     CUtensorMap tk = {}, tv = {};
-    const int r1 = l.fp8 ? encode_e4m3_pool_map(&tk, k_cache, num_blocks, num_kv_heads, block_size, head_dim)
-                         : encode_pool_map(&tk, k_cache, num_blocks, num_kv_heads, block_size, head_dim);
-    const int r2 = l.fp8 ? encode_e4m3_pool_map(&tv, v_cache, num_blocks, num_kv_heads, block_size, head_dim)
-                         : encode_pool_map(&tv, v_cache, num_blocks, num_kv_heads, block_size, head_dim);
+    int r1 = PA_OK, r2 = PA_OK;  // (4-bit pages move as plain bulk copies)
+    if (!fp4) {
+      r1 = l.fp8 ? encode_e4m3_pool_map(&tk, k_cache, num_blocks, num_kv_heads, block_size, head_dim)
+                 : encode_pool_map(&tk, k_cache, num_blocks, num_kv_heads, block_size, head_dim);
+      r2 = l.fp8 ? encode_e4m3_pool_map(&tv, v_cache, num_blocks, num_kv_heads, block_size, head_dim)
+                 : encode_pool_map(&tv, v_cache, num_blocks, num_kv_heads, block_size, head_dim);
+    }
     if (r1 != PA_OK || r2 != PA_OK)
       e = cudaErrorInvalidValue;
     else
-      e = wide_verify ? pa::launch_verify_split(p, l, tk, tv) : pa::launch_decode_mma(p, l, tk, tv);
+      e = split_tiles ? pa::launch_verify_split(p, l, tk, tv) : pa::launch_decode_mma(p, l, tk, tv);
     if (e == cudaSuccess && nparts > 1) e = pa::launch_merge(p, l);
   }
   if (scratch) cudaFreeAsync(scratch, s);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int run_prefill(const Window& win, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                       const int32_t* context_lens, const int32_t* query_start_loc, int num_seqs, int total_q,
+                       int max_q_len, int max_blocks_per_seq, int num_blocks, int max_context_len, int num_q_heads,
+                       int num_kv_heads, int head_dim, int block_size, float scale, int kv_dtype,
+                       const float* k_scale, const float* v_scale, void* out, void* stream) {
+  if (!q || !k_cache || !v_cache || !block_table || !context_lens || !query_start_loc || !out)
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs < 0 || total_q < 0 || max_q_len < 1 || max_blocks_per_seq < 1 || num_blocks < 1 ||
+      max_context_len < 0)
+    return PA_ERR_INVALID_ARG;
+  if (num_q_heads < 1 || num_kv_heads < 1 || head_dim < 1 || block_size < 1) return PA_ERR_INVALID_ARG;
+  if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+  if (!known_kv_dtype(kv_dtype)) return PA_ERR_INVALID_ARG;
+  if (kv_dtype == PA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) % 16 != 0) return PA_ERR_INVALID_ARG;
+  // bf16 pages move as 2-D tensor boxes, E4M3 pages as 16-byte-aligned bulk copies
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return PA_ERR_INVALID_ARG;
+  const int group = num_q_heads / num_kv_heads;
+  if (block_size != 16 || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
+  if (group != 1 && group != 2 && group != 4 && group != 8) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)num_seqs * num_kv_heads > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+  if (((int64_t)max_q_len + 128 / group - 1) / (128 / group) > 65535) return PA_ERR_UNSUPPORTED;  // tile < 2^16
+  if ((int64_t)num_seqs * ((max_q_len + 128 / group - 1) / (128 / group)) * num_kv_heads > 0x7fffffffLL)
+    return PA_ERR_UNSUPPORTED;  // one CTA per (tile, kv head)
+  // TMA row coordinates are signed 32-bit
+  if ((int64_t)num_blocks * num_kv_heads * block_size > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || total_q == 0) return PA_OK;
+  DeviceState* dev = nullptr;
+  int st = device_state(&dev);
+  if (st != PA_OK) return st;
+  pa::AttnParams p = {};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.block_table = block_table;
+  p.context_lens = context_lens;
+  p.query_start_loc = query_start_loc;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.err = dev->err;
+  p.num_seqs = num_seqs;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.q_len = max_q_len;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.max_context_len = max_context_len;
+  p.total_q = total_q;
+  p.scale_log2 = scale * pa::kLog2e;
+  set_window(&p, win, max_context_len, 4);
+  pa::Launch l;
+  l.head_dim = head_dim;
+  l.group = group;
+  l.fp8 = kv_dtype == PA_KV_FP8_E4M3;
+  l.kv = kv_dtype;
+  l.stream = static_cast<cudaStream_t>(stream);
+  // bf16: 2-D TMA maps of the pools; 4-bit: none, bulk copies; E4M3: K pages as 2-D boxes in the swizzled layout the E4M3
+  // products read (head_dim 128), V pages (and head_dim 64 K pages) as bulk copies
+  CUtensorMap tk = {}, tv = {};
+  if (kv_dtype == PA_KV_BF16 && (encode_pool_map(&tk, k_cache, num_blocks, num_kv_heads, block_size, head_dim) != PA_OK ||
+                                 encode_pool_map(&tv, v_cache, num_blocks, num_kv_heads, block_size, head_dim) != PA_OK))
+    return PA_ERR_CUDA;
+  if (l.fp8 && head_dim == 128 &&
+      encode_e4m3_pool_map(&tk, k_cache, num_blocks, num_kv_heads, block_size, head_dim) != PA_OK)
+    return PA_ERR_CUDA;
+  void* scratch = nullptr;
+  if (cudaMallocFromPoolAsync(&scratch, pa::prefill_scratch_bytes(num_seqs, max_q_len, group), dev->pool, l.stream) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return PA_ERR_NO_MEMORY;
+  }
+  const cudaError_t e = pa::launch_prefill_tc(p, l, max_q_len, scratch, tk, tv);
+  cudaFreeAsync(scratch, l.stream);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -342,13 +460,14 @@ int paged_attn_plan(int num_sms, int num_seqs, int num_kv_heads, int max_context
     return PA_OK;
   }
   const int64_t units = (int64_t)(num_seqs > 0 ? num_seqs : 1) * num_kv_heads;
-  const int64_t target = (int64_t)(kv_dtype == PA_KV_FP8_E4M3 ? kCtasPerSmTargetE4M3 : kCtasPerSmTarget) * num_sms;
+  const bool narrow = kv_dtype == PA_KV_FP8_E4M3 || kv_dtype == PA_KV_FP4_E2M1;
+  const int64_t target = (int64_t)(narrow ? kCtasPerSmTargetE4M3 : kCtasPerSmTarget) * num_sms;
   P = (target + units - 1) / units;
   // E4M3: when one partition per (sequence, kv head) already fills 80 % of the target, splitting
   // costs more (a merge, twice the fixed start and end per CTA) than the idle slots it fills
   // (llama8b-shaped decode 48.2 -> 46.8 us, groups of 8 52.9 -> 48.9 us)
-  if (kv_dtype == PA_KV_FP8_E4M3 && units * 5 >= target * 4) P = 1;
-  const int64_t cap = kv_dtype == PA_KV_FP8_E4M3 ? kAutoPagesCapE4M3 : kAutoPagesCap;
+  if (narrow && units * 5 >= target * 4) P = 1;
+  const int64_t cap = narrow ? kAutoPagesCapE4M3 : kAutoPagesCap;
   const int64_t by_cap = (pages + cap - 1) / cap;
   if (by_cap > P) P = by_cap;
   if (P > kAutoMaxPartitions) P = kAutoMaxPartitions;
@@ -366,7 +485,7 @@ int paged_attn_decode(const void* q, const void* k_cache, const void* v_cache, c
                       int max_context_len, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
                       int block_size, float scale, int kv_dtype, const float* k_scale, const float* v_scale,
                       void* out, void* stream) {
-  return run(Form::kDecode, q, k_cache, v_cache, block_table, context_lens, nullptr, num_seqs, max_blocks_per_seq,
+  return run(Form::kDecode, kNoWindow, q, k_cache, v_cache, block_table, context_lens, nullptr, num_seqs, max_blocks_per_seq,
              num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim, block_size, scale, kv_dtype,
              k_scale, v_scale, out, stream);
 }
@@ -376,7 +495,33 @@ int paged_attn_verify(const void* q, const void* k_cache, const void* v_cache, c
                       int max_context_len, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
                       int block_size, float scale, int kv_dtype, const float* k_scale, const float* v_scale,
                       void* out, void* stream) {
-  return run(Form::kVerify, q, k_cache, v_cache, block_table, context_lens, nullptr, num_seqs, max_blocks_per_seq,
+  return run(Form::kVerify, kNoWindow, q, k_cache, v_cache, block_table, context_lens, nullptr, num_seqs, max_blocks_per_seq,
+             num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim, block_size, scale, kv_dtype,
+             k_scale, v_scale, out, stream);
+}
+
+int paged_attn_window_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                             const int32_t* context_lens, int num_seqs, int max_blocks_per_seq, int num_blocks,
+                             int max_context_len, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                             int block_size, int window, int sinks, float scale, int kv_dtype, const float* k_scale,
+                             const float* v_scale, void* out, void* stream) {
+  const Window win = {window, sinks};
+  const int st = check_window(win, max_context_len);
+  if (st != PA_OK) return st;
+  return run(Form::kDecode, win, q, k_cache, v_cache, block_table, context_lens, nullptr, num_seqs, max_blocks_per_seq,
+             num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim, block_size, scale, kv_dtype,
+             k_scale, v_scale, out, stream);
+}
+
+int paged_attn_window_verify(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                             const int32_t* context_lens, int num_seqs, int max_blocks_per_seq, int num_blocks,
+                             int max_context_len, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                             int block_size, int window, int sinks, float scale, int kv_dtype, const float* k_scale,
+                             const float* v_scale, void* out, void* stream) {
+  const Window win = {window, sinks};
+  const int st = check_window(win, max_context_len);
+  if (st != PA_OK) return st;
+  return run(Form::kVerify, win, q, k_cache, v_cache, block_table, context_lens, nullptr, num_seqs, max_blocks_per_seq,
              num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim, block_size, scale, kv_dtype,
              k_scale, v_scale, out, stream);
 }
@@ -387,7 +532,7 @@ int paged_attn_tree_verify(const void* q, const void* k_cache, const void* v_cac
                            int num_kv_heads, int head_dim, int block_size, float scale, int kv_dtype,
                            const float* k_scale, const float* v_scale, void* out, void* stream) {
   if (!tree_mask) return PA_ERR_INVALID_ARG;
-  return run(Form::kVerify, q, k_cache, v_cache, block_table, context_lens, tree_mask, num_seqs,
+  return run(Form::kVerify, kNoWindow, q, k_cache, v_cache, block_table, context_lens, tree_mask, num_seqs,
              max_blocks_per_seq, num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim, block_size,
              scale, kv_dtype, k_scale, v_scale, out, stream);
 }
@@ -397,75 +542,22 @@ int paged_attn_prefill(const void* q, const void* k_cache, const void* v_cache, 
                        int max_q_len, int max_blocks_per_seq, int num_blocks, int max_context_len, int num_q_heads,
                        int num_kv_heads, int head_dim, int block_size, float scale, int kv_dtype,
                        const float* k_scale, const float* v_scale, void* out, void* stream) {
-  if (!q || !k_cache || !v_cache || !block_table || !context_lens || !query_start_loc || !out)
-    return PA_ERR_INVALID_ARG;
-  if (num_seqs < 0 || total_q < 0 || max_q_len < 1 || max_blocks_per_seq < 1 || num_blocks < 1 ||
-      max_context_len < 0)
-    return PA_ERR_INVALID_ARG;
-  if (num_q_heads < 1 || num_kv_heads < 1 || head_dim < 1 || block_size < 1) return PA_ERR_INVALID_ARG;
-  if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
-  if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3) return PA_ERR_INVALID_ARG;
-  if (kv_dtype == PA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
-  if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) % 16 != 0) return PA_ERR_INVALID_ARG;
-  // bf16 pages move as 2-D tensor boxes, E4M3 pages as 16-byte-aligned bulk copies
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return PA_ERR_INVALID_ARG;
-  const int group = num_q_heads / num_kv_heads;
-  if (block_size != 16 || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
-  if (group != 1 && group != 2 && group != 4 && group != 8) return PA_ERR_UNSUPPORTED;
-  if ((int64_t)num_seqs * num_kv_heads > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
-  if (((int64_t)max_q_len + 128 / group - 1) / (128 / group) > 65535) return PA_ERR_UNSUPPORTED;  // tile < 2^16
-  if ((int64_t)num_seqs * ((max_q_len + 128 / group - 1) / (128 / group)) * num_kv_heads > 0x7fffffffLL)
-    return PA_ERR_UNSUPPORTED;  // one CTA per (tile, kv head)
-  // TMA row coordinates are signed 32-bit
-  if ((int64_t)num_blocks * num_kv_heads * block_size > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
-  if (num_seqs == 0 || total_q == 0) return PA_OK;
-  DeviceState* dev = nullptr;
-  int st = device_state(&dev);
+  return run_prefill(kNoWindow, q, k_cache, v_cache, block_table, context_lens, query_start_loc, num_seqs, total_q, max_q_len,
+                     max_blocks_per_seq, num_blocks, max_context_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                     scale, kv_dtype, k_scale, v_scale, out, stream);
+}
+
+int paged_attn_window_prefill(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                       const int32_t* context_lens, const int32_t* query_start_loc, int num_seqs, int total_q,
+                       int max_q_len, int max_blocks_per_seq, int num_blocks, int max_context_len, int num_q_heads,
+                       int num_kv_heads, int head_dim, int block_size, int window, int sinks, float scale, int kv_dtype,
+                       const float* k_scale, const float* v_scale, void* out, void* stream) {
+  const Window win = {window, sinks};
+  const int st = check_window(win, max_context_len);
   if (st != PA_OK) return st;
-  pa::AttnParams p = {};
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_cache = static_cast<const uint8_t*>(k_cache);
-  p.v_cache = static_cast<const uint8_t*>(v_cache);
-  p.block_table = block_table;
-  p.context_lens = context_lens;
-  p.query_start_loc = query_start_loc;
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
-  p.out = static_cast<__nv_bfloat16*>(out);
-  p.err = dev->err;
-  p.num_seqs = num_seqs;
-  p.max_blocks_per_seq = max_blocks_per_seq;
-  p.num_blocks = num_blocks;
-  p.q_len = max_q_len;
-  p.num_q_heads = num_q_heads;
-  p.num_kv_heads = num_kv_heads;
-  p.max_context_len = max_context_len;
-  p.total_q = total_q;
-  p.scale_log2 = scale * pa::kLog2e;
-  pa::Launch l;
-  l.head_dim = head_dim;
-  l.group = group;
-  l.fp8 = kv_dtype == PA_KV_FP8_E4M3;
-  l.stream = static_cast<cudaStream_t>(stream);
-  // bf16: 2-D TMA maps of the pools; E4M3: K pages as 2-D boxes in the swizzled layout the E4M3
-  // products read (head_dim 128), V pages (and head_dim 64 K pages) as bulk copies
-  CUtensorMap tk = {}, tv = {};
-  if (!l.fp8 && (encode_pool_map(&tk, k_cache, num_blocks, num_kv_heads, block_size, head_dim) != PA_OK ||
-                 encode_pool_map(&tv, v_cache, num_blocks, num_kv_heads, block_size, head_dim) != PA_OK))
-    return PA_ERR_CUDA;
-  if (l.fp8 && head_dim == 128 &&
-      encode_e4m3_pool_map(&tk, k_cache, num_blocks, num_kv_heads, block_size, head_dim) != PA_OK)
-    return PA_ERR_CUDA;
-  void* scratch = nullptr;
-  if (cudaMallocFromPoolAsync(&scratch, pa::prefill_scratch_bytes(num_seqs, max_q_len, group), dev->pool, l.stream) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return PA_ERR_NO_MEMORY;
-  }
-  const cudaError_t e = pa::launch_prefill_tc(p, l, max_q_len, scratch, tk, tv);
-  cudaFreeAsync(scratch, l.stream);
-  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return run_prefill(win, q, k_cache, v_cache, block_table, context_lens, query_start_loc, num_seqs, total_q, max_q_len,
+                     max_blocks_per_seq, num_blocks, max_context_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                     scale, kv_dtype, k_scale, v_scale, out, stream);
 }
 
 int paged_attn_append_kv(const void* k_new, const void* v_new, void* k_cache, void* v_cache,

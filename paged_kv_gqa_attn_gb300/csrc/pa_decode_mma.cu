@@ -31,6 +31,11 @@
 // shuffles per column, the outputs rescaled) only when some score passes it by more than kTau.
 // The CTA's warps (two for bf16, four for E4M3) take the partition's pages round-robin, each with
 // its own ring of stages; the CTA then combines the warps and stores the rows or the partials.
+//
+// Sliding window with sinks (WIN): the pages are the sinks' and those of the window, numbered without
+// the gap between (page_span), so the split covers only what is read; the two or three pages that an
+// edge cuts mask their tokens like the sequence's last page.  Block ids wait for the context length,
+// which says where the window begins: one dependent load more than without a window.
 #include "pa_kernels.h"
 #include "pa_tc.cuh"
 
@@ -131,7 +136,7 @@ __device__ __forceinline__ float bf16_part(float p, int c) {
   return c < G ? p : bf16_rem(p);
 }
 
-template <int D, int G, bool FP8>
+template <int D, int G, bool FP8, bool WIN>
 __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDecodeTraits<D, G, FP8>::kMinBlocks))
     decode_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv) {
@@ -154,8 +159,8 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
   const int first = pbeg + warp;
   const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
   const int row0 = first + T::kWarps * lane, row1 = first + T::kWarps * (32 + lane);
-  const int raw0 = row0 < p.max_blocks_per_seq ? bt[row0] : -1;
-  const int raw1 = row1 < p.max_blocks_per_seq ? bt[row1] : -1;
+  const int raw0 = !WIN && row0 < p.max_blocks_per_seq ? bt[row0] : -1;
+  const int raw1 = !WIN && row1 < p.max_blocks_per_seq ? bt[row1] : -1;
   const int L = context_len(p, b, part == 0 && g == 0 && threadIdx.x == 0);
 
   if (L <= 0) {  // no token to attend to: zero the group's rows once, flag it
@@ -166,7 +171,10 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
     }
     return;
   }
-  const int npages = (L + T::kBS - 1) / T::kBS;
+  const int win_lo = WIN ? max(0, L - p.window) : 0;
+  PageSpan span = {0, 0, (L + T::kBS - 1) / T::kBS};
+  if constexpr (WIN) span = page_span(span.count, win_lo, p.sinks, 1);
+  const int npages = span.count;  // pages that the row sees
   if (pbeg >= npages) return;
   const int pend = min(npages, pbeg + ppp);
   const int nparts = (npages + ppp - 1) / ppp;
@@ -192,14 +200,15 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
   // shuffles.
   auto load_window = [&](int kb) {
     const int kk = kb + lane;
-    return kk < nk ? bt[first + T::kWarps * kk] : -1;
+    const int v = first + T::kWarps * kk;
+    return kk < nk ? bt[WIN ? span.real(v) : v] : -1;
   };
   auto load_scale = [&](const float* sc, int id) {
     return (FP8 && id >= 0 && id < p.num_blocks) ? sc[(size_t)id * p.num_kv_heads + g] : 1.f;
   };
   int wb = 0;
-  int idw0 = lane < nk ? raw0 : -1;
-  int idw1 = 32 + lane < nk ? raw1 : -1;
+  int idw0 = WIN ? load_window(0) : lane < nk ? raw0 : -1;
+  int idw1 = WIN ? load_window(32) : 32 + lane < nk ? raw1 : -1;
   float ksw0 = load_scale(p.k_scale, idw0), vsw0 = load_scale(p.v_scale, idw0);
   float ksw1 = load_scale(p.k_scale, idw1), vsw1 = load_scale(p.v_scale, idw1);
   auto id_of = [&](int k) {  // k in [wb, wb + 64), warp-uniform
@@ -312,10 +321,18 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
         vsw1 = load_scale(p.v_scale, idw1);
       }
     }
-    const int page = first + T::kWarps * k;
+    const int page = WIN ? span.real(first + T::kWarps * k) : first + T::kWarps * k;
     const int pb = id_of(k);
     if (pb >= 0 && pb < p.num_blocks) {
       const int valid = min(T::kBS, L - page * T::kBS);
+      // tokens of the page that the row sees (bit per token) and whether it sees them all
+      uint32_t vis = 0xffffu;
+      if constexpr (WIN) {
+        const int t0 = page * T::kBS;
+        vis = (uint32_t)(low_bits64(valid) & (low_bits64(p.sinks - t0) | ~low_bits64(win_lo - t0)));
+      }
+      const bool whole = WIN ? vis == 0xffffu : valid >= T::kBS;
+      auto sees = [&](int t) { return WIN ? ((vis >> t) & 1u) != 0 : t < valid; };
       const uint8_t* kp = stages + s * T::kStageBytes;
       const uint8_t* vp = kp + T::kPageBytes;
 
@@ -356,9 +373,9 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
       const float ksc0 = FP8 ? ksc * qdiv0 : ksc, ksc1 = FP8 ? ksc * qdiv1 : ksc;
       float x0 = fmaf(sc[0], ksc0, lv), x1 = fmaf(sc[1], ksc1, lv);
       float x2 = fmaf(sc[2], ksc0, lv), x3 = fmaf(sc[3], ksc1, lv);
-      if (valid < T::kBS) {
-        if (gi >= valid) x0 = x1 = -INFINITY;
-        if (gi + 8 >= valid) x2 = x3 = -INFINITY;
+      if (!whole) {
+        if (!sees(gi)) x0 = x1 = -INFINITY;
+        if (!sees(gi + 8)) x2 = x3 = -INFINITY;
       }
       float lm0 = fmaxf(x0, x2), lm1 = fmaxf(x1, x3);
       if (__any_sync(0xffffffffu, lm0 > m0 + kTau || lm1 > m1 + kTau)) {
@@ -416,11 +433,11 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
           }
         }
       }
-      if (valid < T::kBS) {  // values past the context may be anything (even NaN): zero them
+      if (!whole) {  // values the row does not see may be anything (even NaN): zero them
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int t = 2 * qi + (r & 1) + 8 * (r >> 1);
-          if (t >= valid)
+          if (!sees(t))
 #pragma unroll
             for (int w = 0; w < T::kPVWords; ++w) v[r][w] = 0u;
         }
@@ -509,14 +526,20 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
   store_partition<G, D, T::kWarps>(p, wacc, wm, wl, b, g, part, nparts);
 }
 
-template <int D, int G, bool FP8>
-cudaError_t launch_one(const AttnParams& p, cudaStream_t stream, const CUtensorMap& tk, const CUtensorMap& tv) {
+template <int D, int G, bool FP8, bool WIN>
+cudaError_t launch_form(const AttnParams& p, cudaStream_t stream, const CUtensorMap& tk, const CUtensorMap& tv) {
   using T = MmaDecodeTraits<D, G, FP8>;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(decode_mma_kernel<D, G, FP8>), T::kSmem);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(decode_mma_kernel<D, G, FP8, WIN>), T::kSmem);
   if (e != cudaSuccess) return e;
   dim3 grid(p.max_partitions, p.num_kv_heads, p.num_seqs);
-  decode_mma_kernel<D, G, FP8><<<grid, T::kThreads, T::kSmem, stream>>>(p, tk, tv);
+  decode_mma_kernel<D, G, FP8, WIN><<<grid, T::kThreads, T::kSmem, stream>>>(p, tk, tv);
   return cudaGetLastError();
+}
+
+template <int D, int G, bool FP8>
+cudaError_t launch_one(const AttnParams& p, cudaStream_t stream, const CUtensorMap& tk, const CUtensorMap& tv) {
+  return p.window > 0 ? launch_form<D, G, FP8, true>(p, stream, tk, tv)
+                      : launch_form<D, G, FP8, false>(p, stream, tk, tv);
 }
 
 template <int D, bool FP8>

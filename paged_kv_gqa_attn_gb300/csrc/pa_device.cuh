@@ -49,7 +49,24 @@ struct AttnParams {
   int max_context_len;          // host-side bound; longer contexts are clamped and flagged
   int total_q;                  // rows of the packed q / out (prefill)
   float scale_log2;             // scale * log2(e): scores are kept in base-2 units
+  int window;                   // tokens a row sees up to its own, past the sinks; 0: all
+  int sinks;                    // first tokens that stay visible (with a window)
+  int page_align;               // window: pages that page_span rounds its edges to (see there)
 };
+
+// The pages of a sequence (or tile) that a window with sinks leaves, numbered without the gap: page v
+// of [0, count) is column v of the block table before `head` and column v + gap from there on.  With
+// align > 1 both edges of the gap are whole multiples of it (a few unseen pages count too).
+struct PageSpan {
+  int head, gap, count;
+  __device__ __forceinline__ int real(int v) const { return v < head ? v : v + gap; }
+};
+__device__ __forceinline__ PageSpan page_span(int npages, int win_lo, int sinks, int align) {
+  const int head = ((sinks + 15) / 16 + align - 1) / align * align;
+  const int first = win_lo / 16 / align * align;
+  const int gap = max(0, first - head);
+  return {head, gap, npages - gap};
+}
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

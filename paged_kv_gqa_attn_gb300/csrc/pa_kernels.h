@@ -17,6 +17,7 @@ struct Launch {
   int group;  // num_q_heads / num_kv_heads
   bool fp8;
   cudaStream_t stream;
+  int kv = kKvBf16;  // cache type (fp8: kv == kKvE4m3)
 };
 
 // Each returns cudaSuccess or the launch error.  Unsupported combinations return
@@ -47,6 +48,12 @@ size_t prefill_scratch_bytes(int num_seqs, int max_q_len, int group);
 cudaError_t launch_verify_split(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
 cudaError_t launch_prefill_tc(const AttnParams& p, const Launch& l, int max_q_len, void* scratch, const CUtensorMap& tk,
                               const CUtensorMap& tv);
+// Its parts: the planner's work list, and the tile kernel's forms with a window and over 4-bit caches
+// (tiles null: the split form).
+cudaError_t launch_prefill_plan(const AttnParams& p, int tiles_per_row, int32_t* tiles, cudaStream_t st);
+cudaError_t prefill_window_form(const AttnParams& p, const Launch& l, int max_q_len, int32_t* tiles,
+                                const CUtensorMap& tk, const CUtensorMap& tv);
+cudaError_t prefill_fp4_form(const AttnParams& p, const Launch& l, int max_q_len, int32_t* tiles);
 // KV append (bf16 scatter, fp8 with per-(block, head) rescaling, or E2M1 codes with a scale for each
 // 16 dims of a token); arguments already checked.
 cudaError_t launch_append(const void* k_new, const void* v_new, void* k_cache, void* v_cache,

@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttnParams p) {
   const int b = (int)(row / ((long)p.q_len * Hq));
   const int L = context_len(p, b, false);
   if (L <= 0) return;
-  const int npages = (L + 15) / 16;
+  int npages = (L + 15) / 16;
+  if (p.window > 0) npages = page_span(npages, max(0, L - p.q_len + 1 - p.window), p.sinks, p.page_align).count;
   const int nparts = (npages + p.pages_per_partition - 1) / p.pages_per_partition;
   if (nparts <= 1) return;  // the attention kernel wrote this row directly
   // launched as a programmatic dependent of the attention kernel: wait for its partials

@@ -84,6 +84,7 @@ extern "C" int paged_attn_decode_static_scratch(const void* q, const void* k_cac
                                     num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim,
                                     block_size, kv_dtype, k_scale, v_scale, out);
   if (st != PA_OK) return st;
+  if (kv_dtype == PA_KV_FP4_E2M1) return PA_ERR_UNSUPPORTED;  // the CUDA-core kernel's cache types
   const int group = num_q_heads / num_kv_heads;  // the CUDA-core kernel's groups
   if (group != 1 && group != 2 && group != 4 && group != 8) return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;

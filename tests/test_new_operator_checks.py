@@ -72,3 +72,56 @@ def test_append_takes_the_4_bit_type_without_scales():
     assert fn(*lead, 0, 1, 4, 8, 2, 128, 16, 2, None, None, None) == pa.PA_OK
     assert fn(*lead, 0, 1, 4, 8, 2, 128, 16, 3, None, None, None) == pa.PA_ERR_INVALID_ARG
     assert fn(*lead, 0, 1, 4, 8, 2, 128, 16, 1, None, None, None) == pa.PA_ERR_INVALID_ARG
+
+
+def _attn(name, **over):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, bt=FAKE, cl=FAKE, B=0, M=4, NB=8, maxL=64, q_len=1, Hq=8, Hkv=2, d=128, bs=16,
+             window=5, sinks=2, scale=0.1, dt=0, ks=None, vs=None, out=FAKE)
+    a.update(over)
+    if name in ("decode", "verify"):
+        del a["window"], a["sinks"]
+    return getattr(pa.load_library(), "paged_attn_" + name)(*a.values(), None)
+
+
+@pytest.mark.parametrize("name", ["window_decode", "window_verify"])
+@pytest.mark.parametrize("over,status", [
+    (dict(), pa.PA_OK),
+    (dict(window=0), pa.PA_ERR_INVALID_ARG),
+    (dict(window=-4), pa.PA_ERR_INVALID_ARG),
+    (dict(sinks=-1), pa.PA_ERR_INVALID_ARG),
+    (dict(window=2 ** 31 - 1, sinks=2 ** 31 - 1), pa.PA_OK),
+    (dict(maxL=2 ** 30 + 1, M=2 ** 27), pa.PA_ERR_UNSUPPORTED),
+    (dict(out=None), pa.PA_ERR_INVALID_ARG),
+    (dict(dt=1), pa.PA_ERR_INVALID_ARG),
+    (dict(dt=2), pa.PA_OK),
+    (dict(d=32), pa.PA_ERR_UNSUPPORTED),
+])
+def test_window_checks(name, over, status):
+    assert _attn(name, **over) == status
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dt=2), pa.PA_OK),
+    (dict(dt=3), pa.PA_ERR_INVALID_ARG),
+    (dict(dt=2, Hq=256), pa.PA_ERR_UNSUPPORTED),
+    (dict(dt=2, k=FAKE + 8), pa.PA_ERR_INVALID_ARG),
+])
+def test_4_bit_decode_checks(over, status):
+    assert _attn("decode", **over) == status
+
+
+def test_static_scratch_decode_refuses_the_4_bit_type():
+    fn = pa.load_library().paged_attn_decode_static_scratch
+    P, I = ctypes.c_void_p, ctypes.c_int
+    fn.restype, fn.argtypes = I, [P] * 5 + [I] * 9 + [ctypes.c_float, I] + [P] * 4
+    a = [FAKE] * 5 + [2, 4, 8, 64, 1, 8, 2, 128, 16, 0.1]
+    assert fn(*a, 2, None, None, FAKE, None) == pa.PA_ERR_UNSUPPORTED
+
+
+def test_window_prefill_checks():
+    fn = pa.load_library().paged_attn_window_prefill
+    lead = [FAKE] * 6 + [0, 0, 1, 4, 8, 64, 8, 2, 128, 16]
+    assert fn(*lead, 5, 2, 0.1, 2, None, None, FAKE, None) == pa.PA_OK
+    assert fn(*lead, 0, 2, 0.1, 0, None, None, FAKE, None) == pa.PA_ERR_INVALID_ARG
+    assert fn(*lead, 5, -2, 0.1, 0, None, None, FAKE, None) == pa.PA_ERR_INVALID_ARG
+    assert fn(*lead, 5, 2, 0.1, 4, None, None, FAKE, None) == pa.PA_ERR_INVALID_ARG
