@@ -236,13 +236,15 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
   // tcgen05 kernel (balanced persistent split + merge), decode as its q_len = 1 rows.
   // Verify with more than the verify kernel's 64 rows per kv head (bf16, up to 128) runs the
   // chunked-prefill kernel split into partitions like decode, with the same merge.
-  // So does what the verify kernel has no form for: a window, or a 4-bit cache.
+  // 4-bit caches, and the window forms but decode's, take the rows kernel up to its kRowsMax rows per kv
+  // head and the split prefill kernel beyond.
   const bool mma_group = l.group == 1 || l.group == 2 || l.group == 4 || l.group == 8;
   const bool fp4 = kv_dtype == PA_KV_FP4_E2M1;
   const bool mma_decode = form == Form::kDecode && mma_group && !fp4;
-  const bool split_tiles = !mma_decode && (l.group * q_len > 64 || win.window > 0 || fp4);
-  const bool on_tensor_cores = !mma_decode && !split_tiles;
-  const int align = mma_decode ? 1 : 4;  // the split prefill kernel walks whole 64-token steps
+  const bool few_rows = !mma_decode && (win.window > 0 || fp4) && l.group * q_len <= pa::kRowsMax;
+  const bool split_tiles = !mma_decode && !few_rows && (l.group * q_len > 64 || win.window > 0 || fp4);
+  const bool on_tensor_cores = !mma_decode && !few_rows && !split_tiles;
+  const int align = split_tiles ? 4 : 1;  // the split prefill kernel walks whole 64-token steps
   set_window(&p, win, max_context_len, align);
   if (on_tensor_cores) {
     // balanced persistent split: planner, tcgen05 kernel, segment merge
@@ -297,7 +299,10 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
     if (r1 != PA_OK || r2 != PA_OK)
       e = cudaErrorInvalidValue;
     else
-      e = split_tiles ? pa::launch_verify_split(p, l, tk, tv) : pa::launch_decode_mma(p, l, tk, tv);
+      e = split_tiles        ? pa::launch_verify_split(p, l, tk, tv)
+          : few_rows && fp4 ? pa::rows_fp4_form(p, l)
+          : few_rows        ? pa::rows_window_form(p, l, tk, tv)
+                            : pa::launch_decode_mma(p, l, tk, tv);
     if (e == cudaSuccess && nparts > 1) e = pa::launch_merge(p, l);
   }
   if (scratch) cudaFreeAsync(scratch, s);

@@ -37,6 +37,7 @@
 // edge cuts mask their tokens like the sequence's last page.  Block ids wait for the context length,
 // which says where the window begins: one dependent load more than without a window.
 #include "pa_kernels.h"
+#include "pa_mma.cuh"
 #include "pa_tc.cuh"
 
 namespace pa {
@@ -75,59 +76,6 @@ struct MmaDecodeTraits {
   static_assert(kWarps * G * D * 4 + 2 * kWarps * G * 4 <= kStageRegion, "merge scratch fits");
   static_assert(kCols <= 8, "the columns of the products are the 8 of one n-tile");
 };
-
-constexpr float kTau = 8.f;  // largest softmax weight, log2, before the running max is refreshed
-
-// Byte offset of 16-byte chunk `c` of row `r` of a page as the TMA unit writes it.  Rows of 128 B
-// or more arrive as boxes of 128-byte rows with the 128-byte swizzle (chunk ^ row % 8), box j
-// holding chunks 8j .. 8j+7 of every row; 64-byte rows use the 64-byte swizzle
-// (chunk ^ (row / 2) % 4).  Pages are 1 KiB aligned.
-template <int RB>
-__device__ __forceinline__ uint32_t chunk_off(int r, int c) {
-  if constexpr (RB == 64)
-    return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-  else
-    return (c >> 3) * (16 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-}
-
-// The c-th K chunk of thread q: a quarter of the row, taken as chunk pairs 2q, 2q+1 of each
-// 128-byte box (so that the 8 threads of a load phase hit 8 different bank groups), or chunk q
-// of a 64-byte row.
-template <int RB>
-__device__ __forceinline__ int qk_chunk(int q, int c) {
-  if constexpr (RB == 64)
-    return q;
-  else
-    return 8 * (c >> 1) + 2 * q + (c & 1);
-}
-
-// D[16x8] += A[16x16] . B[16x8], f16 (or bf16) operands, fp32 accumulators (warp-collective).
-template <bool BF16>
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-  if constexpr (BF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Transpose of an 8x8 matrix of 16-bit elements held as mma fragments (warp-collective).
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
-// What bf16 rounding leaves of p (rounded to bf16 again, it carries p's next 8 significant bits).
-__device__ __forceinline__ float bf16_rem(float p) { return p - __bfloat162float(__float2bfloat16_rn(p)); }
 
 // bf16 weight of column c when the low parts share the n-tile: the head's weight (rounded to bf16
 // by the packing) in the first G columns, its remainder in the next G.

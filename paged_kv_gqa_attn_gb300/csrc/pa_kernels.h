@@ -54,6 +54,11 @@ cudaError_t launch_prefill_plan(const AttnParams& p, int tiles_per_row, int32_t*
 cudaError_t prefill_window_form(const AttnParams& p, const Launch& l, int max_q_len, int32_t* tiles,
                                 const CUtensorMap& tk, const CUtensorMap& tv);
 cudaError_t prefill_fp4_form(const AttnParams& p, const Launch& l, int max_q_len, int32_t* tiles);
+// A few rows per kv head (group * q_len at most kRowsMax) on mma.sync: 4-bit caches, and window forms of
+// bf16 and E4M3 caches; same grid, partitions (any page count) and partials as launch_decode_mma.
+constexpr int kRowsMax = 32;
+cudaError_t rows_fp4_form(const AttnParams& p, const Launch& l);
+cudaError_t rows_window_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
 // KV append (bf16 scatter, fp8 with per-(block, head) rescaling, or E2M1 codes with a scale for each
 // 16 dims of a token); arguments already checked.
 cudaError_t launch_append(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
