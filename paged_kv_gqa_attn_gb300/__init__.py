@@ -71,6 +71,8 @@ def load_library(build_if_missing: bool = True, timeline: Optional[bool] = None)
     timeline=True loads the instrumented variant instead (per-CTA time stamps in the verify
     kernel, for ``paged_kv_gqa_attn_gb300.timeline``); it must be the first load of the process."""
     global _lib
+    if _lib is not None and (timeline is None or timeline == _lib._pa_timeline):
+        return _lib
     with _lock:
         if _lib is not None and timeline is not None and timeline != _lib._pa_timeline:
             raise RuntimeError("the other variant of the library is already loaded in this process")
@@ -151,9 +153,16 @@ def plan(num_sms: int, num_seqs: int, num_kv_heads: int, max_context_len: int, b
     return a.value, b.value
 
 
+# The current stream's handle of a device, without building a Stream object (0.1 us against 3 us); and
+# the index of the current device.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+    if stream is None:
+        return _raw_stream(torch.cuda.current_device())
+    return int(stream.cuda_stream)
 
 
 def check_device_errors(stream: Optional[torch.cuda.Stream] = None) -> int:
@@ -177,18 +186,39 @@ def selftest_wait(helper: int, polls: int, stream: Optional[torch.cuda.Stream] =
     return elapsed
 
 
-def _one_device(stream, **tensors):
+class _Here:
+    """The context of a call on the current device: nothing to change."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _one_device(stream, *tensors, **named):
     """Check that every tensor (and the stream, if one is given) is on one CUDA device and return
     a context that makes it the current device for the call: the library launches on the
     current device."""
-    devs = {t.device for t in tensors.values() if t is not None}
-    if len(devs) != 1:
-        where = {k: str(t.device) for k, t in tensors.items() if t is not None}
-        raise ValueError(f"tensors must be on one CUDA device, got {where}")
-    dev = devs.pop()
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, tensors on {dev}")
-    return torch.cuda.device(dev)
+    if named:
+        tensors += tuple(named.values())
+    index = -1
+    for t in tensors:
+        if t is not None:
+            at = t.get_device()
+            if at != index:
+                if index >= 0 or at < 0:
+                    where = [str(x.device) for x in tensors if x is not None]
+                    raise ValueError(f"tensors must be on one CUDA device, got {where}")
+                index = at
+    if index < 0:
+        raise ValueError("tensors must be on one CUDA device, got none")
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, tensors on cuda:{index}")
+    return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
 def _check_cuda(name, t, dtypes):
@@ -200,6 +230,11 @@ def _check_cuda(name, t, dtypes):
         raise ValueError(f"{name} must be contiguous")
 
 
+# (names of the accepted types, made once: every call passes them)
+_BF16, _I32, _F32, _BYTES = (torch.bfloat16,), (torch.int32,), (torch.float32,), (torch.uint8,)
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+
+
 def _kv_dtype(k_cache, v_cache, head_dim, k_scale, v_scale):
     """The cache type by the caches' dtype and last dim (bf16 [.., d], E4M3 bytes [.., d], 4-bit bytes
     [.., 9 d / 16]), with the checks of the scales that it takes."""
@@ -209,17 +244,16 @@ def _kv_dtype(k_cache, v_cache, head_dim, k_scale, v_scale):
         kv = PA_KV_FP4_E2M1
     else:
         kv = PA_KV_FP8_E4M3
-    types = {PA_KV_BF16: (torch.bfloat16,), PA_KV_FP4_E2M1: (torch.uint8,),
-             PA_KV_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn)}[kv]
+    types = _BF16 if kv == PA_KV_BF16 else _E4M3 if kv == PA_KV_FP8_E4M3 else _BYTES
     _check_cuda("k_cache", k_cache, types)
     _check_cuda("v_cache", v_cache, types)
     if kv == PA_KV_FP8_E4M3:
-        _check_cuda("k_scale", k_scale, (torch.float32,))
-        _check_cuda("v_scale", v_scale, (torch.float32,))
+        _check_cuda("k_scale", k_scale, _F32)
+        _check_cuda("v_scale", v_scale, _F32)
     if kv == PA_KV_FP4_E2M1:
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None:
-                _check_cuda(name, t, (torch.float32,))
+                _check_cuda(name, t, _F32)
                 if t.shape != (k_cache.shape[1],):
                     raise ValueError(f"{name} must be [num_kv_heads] for a 4-bit cache")
     return kv
@@ -241,13 +275,13 @@ def _window(fn_name, window, sinks):
 def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_scale=None,
           v_scale=None, max_context_len=None, out=None, stream=None, tree_mask=None, window=None, sinks=0):
     lib = load_library()
-    _check_cuda("q", q, (torch.bfloat16,))
+    _check_cuda("q", q, _BF16)
     if q.dim() != 4 or k_cache.dim() != 4 or k_cache.shape != v_cache.shape or block_table.dim() != 2:
         raise ValueError("expected q [B, q_len, Hq, d], caches [NB, Hkv, bs, d], block_table [B, M]")
     B, q_len, Hq, d = q.shape
     kv = _kv_dtype(k_cache, v_cache, d, k_scale, v_scale)
-    _check_cuda("block_table", block_table, (torch.int32,))
-    _check_cuda("context_lens", context_lens, (torch.int32,))
+    _check_cuda("block_table", block_table, _I32)
+    _check_cuda("context_lens", context_lens, _I32)
     if kv == PA_KV_BF16:
         k_scale = v_scale = None
     NB, Hkv, bs, d2 = k_cache.shape
@@ -256,7 +290,7 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
     if out is None:
         out = torch.empty_like(q)
     else:
-        _check_cuda("out", out, (torch.bfloat16,))
+        _check_cuda("out", out, _BF16)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
     max_blocks = int(block_table.shape[1])
@@ -266,12 +300,11 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
     lead = [q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
             context_lens.data_ptr()]
     if fn_name == "paged_attn_tree_verify":
-        _check_cuda("tree_mask", tree_mask, (torch.int32,))
+        _check_cuda("tree_mask", tree_mask, _I32)
         if tree_mask.shape != (B, q_len):
             raise ValueError("tree_mask must be [B, q_len]")
         lead.append(tree_mask.data_ptr())
-    with _one_device(stream, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                     context_lens=context_lens, tree_mask=tree_mask, out=out, k_scale=k_scale, v_scale=v_scale):
+    with _one_device(stream, q, k_cache, v_cache, block_table, context_lens, tree_mask, out, k_scale, v_scale):
         st = getattr(lib, fn_name)(
             *lead, B, max_blocks, NB, int(max_context_len), q_len, Hq, Hkv, d, bs, *span,
             float(scale), kv, _ptr(k_scale), _ptr(v_scale), out.data_ptr(), _stream_handle(stream))
@@ -314,14 +347,14 @@ def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, sca
     (one device-to-host copy).  window and sinks as in verify.  See paged_attn_prefill,
     paged_attn_window_prefill."""
     lib = load_library()
-    _check_cuda("q", q, (torch.bfloat16,))
+    _check_cuda("q", q, _BF16)
     if q.dim() != 3 or k_cache.dim() != 4 or k_cache.shape != v_cache.shape or block_table.dim() != 2:
         raise ValueError("expected q [total_q, Hq, d], caches [NB, Hkv, bs, d], block_table [B, M]")
     total_q, Hq, d = q.shape
     kv = _kv_dtype(k_cache, v_cache, d, k_scale, v_scale)
-    _check_cuda("block_table", block_table, (torch.int32,))
-    _check_cuda("context_lens", context_lens, (torch.int32,))
-    _check_cuda("query_start_loc", query_start_loc, (torch.int32,))
+    _check_cuda("block_table", block_table, _I32)
+    _check_cuda("context_lens", context_lens, _I32)
+    _check_cuda("query_start_loc", query_start_loc, _I32)
     if kv == PA_KV_BF16:
         k_scale = v_scale = None
     NB, Hkv, bs, d2 = k_cache.shape
@@ -331,7 +364,7 @@ def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, sca
     if out is None:
         out = torch.empty_like(q)
     else:
-        _check_cuda("out", out, (torch.bfloat16,))
+        _check_cuda("out", out, _BF16)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
     if max_q_len is None:
@@ -341,9 +374,8 @@ def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, sca
     if max_context_len is None:
         max_context_len = max_blocks * bs
     fn_name, span = _window("paged_attn_prefill", window, sinks)
-    with _one_device(stream, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                     context_lens=context_lens, query_start_loc=query_start_loc, out=out, k_scale=k_scale,
-                     v_scale=v_scale):
+    with _one_device(stream, q, k_cache, v_cache, block_table, context_lens, query_start_loc, out, k_scale,
+                     v_scale):
         st = getattr(lib, fn_name)(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
             context_lens.data_ptr(), query_start_loc.data_ptr(), B, total_q, max(1, int(max_q_len)),
@@ -361,14 +393,14 @@ def append_kv(k_new, v_new, k_cache, v_cache, block_table, context_lens, *, k_sc
     [Hkv] that it only reads).  context_lens holds the lengths after the append.  See
     paged_attn_append_kv."""
     lib = load_library()
-    _check_cuda("k_new", k_new, (torch.bfloat16,))
-    _check_cuda("v_new", v_new, (torch.bfloat16,))
+    _check_cuda("k_new", k_new, _BF16)
+    _check_cuda("v_new", v_new, _BF16)
     if k_new.dim() != 4 or k_new.shape != v_new.shape or k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
         raise ValueError("expected k_new/v_new [B, n_new, Hkv, d] and caches [NB, Hkv, bs, d]")
     B, n_new, Hkv, d = k_new.shape
     kv = _kv_dtype(k_cache, v_cache, d, k_scale, v_scale)
-    _check_cuda("block_table", block_table, (torch.int32,))
-    _check_cuda("context_lens", context_lens, (torch.int32,))
+    _check_cuda("block_table", block_table, _I32)
+    _check_cuda("context_lens", context_lens, _I32)
     NB, Hkv2, bs, d2 = k_cache.shape
     if Hkv2 != Hkv or (d2 != d and kv != PA_KV_FP4_E2M1) or block_table.dim() != 2 \
             or block_table.shape[0] != B or context_lens.shape != (B,):
@@ -377,8 +409,7 @@ def append_kv(k_new, v_new, k_cache, v_cache, block_table, context_lens, *, k_sc
         k_scale = v_scale = None
     if kv == PA_KV_FP8_E4M3 and (k_scale.shape != (NB, Hkv) or v_scale.shape != (NB, Hkv)):
         raise ValueError("k_scale / v_scale must be [num_blocks, num_kv_heads]")
-    with _one_device(stream, k_new=k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache,
-                     block_table=block_table, context_lens=context_lens, k_scale=k_scale, v_scale=v_scale):
+    with _one_device(stream, k_new, v_new, k_cache, v_cache, block_table, context_lens, k_scale, v_scale):
         st = lib.paged_attn_append_kv(
             k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_table.data_ptr(), context_lens.data_ptr(), B, n_new, int(block_table.shape[1]), NB,
@@ -402,8 +433,8 @@ def read_kv(k_cache, v_cache, block_table, context_lens, n, *, k_scale=None, v_s
         head_dim = {36: 64, 72: 128}.get(last, last) if k_cache.dtype == torch.uint8 else last
     d = int(head_dim)
     kv = _kv_dtype(k_cache, v_cache, d, k_scale, v_scale)
-    _check_cuda("block_table", block_table, (torch.int32,))
-    _check_cuda("context_lens", context_lens, (torch.int32,))
+    _check_cuda("block_table", block_table, _I32)
+    _check_cuda("context_lens", context_lens, _I32)
     B, n = int(block_table.shape[0]), int(n)
     if context_lens.shape != (B,) or (last != d and kv != PA_KV_FP4_E2M1) or n < 0:
         raise ValueError("shape mismatch between caches, block_table, context_lens, n and head_dim")
@@ -414,15 +445,15 @@ def read_kv(k_cache, v_cache, block_table, context_lens, n, *, k_scale=None, v_s
     outs = []
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is None:
-            t = torch.empty(B, n, Hkv, d, dtype=torch.bfloat16, device=k_cache.device)
-        _check_cuda(name, t, (torch.bfloat16,))
-        if t.shape != (B, n, Hkv, d):
-            raise ValueError(f"{name} must be [B, n, Hkv, d]")
+            t = torch.empty((B, n, Hkv, d), dtype=torch.bfloat16, device=k_cache.device)
+        else:
+            _check_cuda(name, t, _BF16)
+            if t.shape != (B, n, Hkv, d):
+                raise ValueError(f"{name} must be [B, n, Hkv, d]")
         outs.append(t)
     if n == 0 or B == 0:
         return tuple(outs)
-    with _one_device(stream, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                     context_lens=context_lens, k_scale=k_scale, v_scale=v_scale, k_out=outs[0], v_out=outs[1]):
+    with _one_device(stream, k_cache, v_cache, block_table, context_lens, k_scale, v_scale, *outs):
         st = lib.paged_attn_read_kv(
             k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), B, n,
             int(block_table.shape[1]), NB, Hkv, d, bs, kv, _ptr(k_scale), _ptr(v_scale), outs[0].data_ptr(),
@@ -432,18 +463,22 @@ def read_kv(k_cache, v_cache, block_table, context_lens, n, *, k_scale=None, v_s
     return tuple(outs)
 
 
-def _check_rows(name, t):
-    """bf16 [T, heads, d] on the GPU whose tokens may be strided (a slice of a packed projection)."""
+def _token_stride(name, t, heads_dims):
+    """Elements from one token of a bf16 [T, heads, d] tensor to the next (a slice of a packed
+    projection is strided), after its checks."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [T, heads, d]")
-    if t.shape[0] and (t.stride(2) != 1 or t.stride(1) != t.shape[2]):
+    shape = tuple(t.shape)
+    if shape != heads_dims:
+        raise ValueError(f"{name} must be {list(heads_dims)}, got {list(shape)}")
+    step, head, one = t.stride()
+    if shape[0] < 2:  # a single token's stride says nothing
+        step = shape[1] * shape[2]
+    if shape[0] and (one != 1 or (head != shape[2] and shape[1] > 1)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    # a single token's stride says nothing
-    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1] * t.shape[2])
+    return step
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, *, eps=1e-6, interleaved=False, q_out=None,
@@ -454,32 +489,36 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, *, eps=1e-6, inte
     [d] bf16, cos_sin [max_position, rotary_dim] fp32 (cosines, then sines), positions [T] int32.  See
     paged_attn_qk_norm_rope."""
     lib = load_library()
-    strides = [_check_rows("q", q), _check_rows("k", k)]
-    _check_cuda("q_weight", q_weight, (torch.bfloat16,))
-    _check_cuda("k_weight", k_weight, (torch.bfloat16,))
-    _check_cuda("cos_sin", cos_sin, (torch.float32,))
-    _check_cuda("positions", positions, (torch.int32,))
-    T, Hq, d = q.shape
-    Hkv = int(k.shape[1])
-    if k.shape != (T, Hkv, d) or q_weight.shape != (d,) or k_weight.shape != (d,) or cos_sin.dim() != 2 \
-            or positions.shape != (T,):
-        raise ValueError("expected q [T, Hq, d], k [T, Hkv, d], weights [d], cos_sin [P, rotary], positions [T]")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("expected q [T, Hq, d] and k [T, Hkv, d]")
+    T, Hq, d = q_shape = tuple(q.shape)
+    Hkv = k.shape[1]
+    k_shape = (T, Hkv, d)
+    strides = [_token_stride("q", q, q_shape), _token_stride("k", k, k_shape)]
+    _check_cuda("q_weight", q_weight, _BF16)
+    _check_cuda("k_weight", k_weight, _BF16)
+    _check_cuda("cos_sin", cos_sin, _F32)
+    _check_cuda("positions", positions, _I32)
+    if q_weight.shape != (d,) or k_weight.shape != (d,) or cos_sin.dim() != 2 or positions.shape != (T,):
+        raise ValueError("expected weights [d], cos_sin [max_position, rotary_dim], positions [T]")
     if q_out is None:
-        q_out = torch.empty(T, Hq, d, dtype=q.dtype, device=q.device)
+        q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+        strides.append(Hq * d)
+    else:
+        strides.append(_token_stride("q_out", q_out, q_shape))
     if k_out is None:
-        k_out = torch.empty(T, Hkv, d, dtype=k.dtype, device=k.device)
-    strides += [_check_rows("q_out", q_out), _check_rows("k_out", k_out)]
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError("q_out and k_out must have q's and k's shapes")
+        k_out = torch.empty(k_shape, dtype=torch.bfloat16, device=k.device)
+        strides.append(Hkv * d)
+    else:
+        strides.append(_token_stride("k_out", k_out, k_shape))
     if T == 0:
         return q_out, k_out
-    with _one_device(stream, q=q, k=k, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
-                     positions=positions, q_out=q_out, k_out=k_out):
+    max_position, rotary = cos_sin.shape
+    with _one_device(stream, q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out):
         st = lib.paged_attn_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), cos_sin.data_ptr(),
-            positions.data_ptr(), T, Hq, Hkv, d, int(cos_sin.shape[1]), int(bool(interleaved)),
-            int(cos_sin.shape[0]), float(eps), *strides, q_out.data_ptr(), k_out.data_ptr(),
-            _stream_handle(stream))
+            positions.data_ptr(), T, Hq, Hkv, d, rotary, 1 if interleaved else 0, max_position, eps, *strides,
+            q_out.data_ptr(), k_out.data_ptr(), _stream_handle(stream))
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attn_qk_norm_rope")
     return q_out, k_out
@@ -492,16 +531,16 @@ def spec_accept(p, q, draft_tokens, u_accept, u_sample, *, out_tokens=None, num_
     (uint32 bit patterns).  Returns (num_accepted [B] int32, out_tokens [B, K+1] int32).  See
     paged_attn_spec_accept."""
     lib = load_library()
-    _check_cuda("p", p, (torch.float32,))
-    _check_cuda("u_sample", u_sample, (torch.int32,))
+    _check_cuda("p", p, _F32)
+    _check_cuda("u_sample", u_sample, _I32)
     if p.dim() != 3:
         raise ValueError("p must be [B, K+1, V]")
     B, K1, V = p.shape
     K = K1 - 1
     if K > 0:
-        _check_cuda("q", q, (torch.float32,))
-        _check_cuda("draft_tokens", draft_tokens, (torch.int32,))
-        _check_cuda("u_accept", u_accept, (torch.float32,))
+        _check_cuda("q", q, _F32)
+        _check_cuda("draft_tokens", draft_tokens, _I32)
+        _check_cuda("u_accept", u_accept, _F32)
         if q.shape != (B, K, V) or draft_tokens.shape != (B, K) or u_accept.shape != (B, K):
             raise ValueError("q [B, K, V], draft_tokens [B, K] and u_accept [B, K] must match p")
     if u_sample.shape != (B,):
@@ -510,8 +549,8 @@ def spec_accept(p, q, draft_tokens, u_accept, u_sample, *, out_tokens=None, num_
         out_tokens = torch.empty(B, K + 1, dtype=torch.int32, device=p.device)
     if num_accepted is None:
         num_accepted = torch.empty(B, dtype=torch.int32, device=p.device)
-    _check_cuda("out_tokens", out_tokens, (torch.int32,))
-    _check_cuda("num_accepted", num_accepted, (torch.int32,))
+    _check_cuda("out_tokens", out_tokens, _I32)
+    _check_cuda("num_accepted", num_accepted, _I32)
     if out_tokens.shape != (B, K + 1) or num_accepted.shape != (B,):
         raise ValueError("out_tokens must be [B, K+1] and num_accepted [B]")
     ptr = (lambda t: t.data_ptr() if K > 0 else None)

@@ -187,6 +187,39 @@ int visible_context(const Window& w, int max_context_len, int q_len, int align) 
   return pages * 16 < max_context_len ? (int)(pages * 16) : max_context_len;
 }
 
+// The split of the rows kernel and of the window forms, N pages a (sequence, kv head) at most, `units` of
+// those, `slots` resident CTAs.  A CTA's start and end cost what `fixed` pages cost.
+//   Ragged contexts (no window; half of N on average): work shrinks to N units / 2 slots + P fixed units / 2
+//   slots + the last CTA's N / P of which half overlaps: least at P = sqrt(N slots / (units fixed)).
+//   Windows (every sequence near N): P that makes ceil(units P / slots) (N / P + fixed) + P merge least.
+// Measured at 4 to 512 units (4-bit, fixed = 38): the formula's P is within 3 % of the best of a sweep.
+void plan_rows(bool windowed, int64_t units, int64_t slots, int64_t pages, double fixed, double merge, int align, int* ppp,
+               int* nparts) {
+  if (pages < 1) pages = 1;
+  int64_t P = 1;
+  const int forced = g_forced_partitions.load();
+  if (forced > 0) {
+    P = forced;
+  } else if (windowed) {
+    double best = 0.;
+    for (int64_t c = 1; c <= kAutoMaxPartitions; ++c) {
+      const double t = (double)((units * c + slots - 1) / slots) * ((double)pages / c + fixed) + merge * c;
+      if (c == 1 || t < best) {
+        best = t;
+        P = c;
+      }
+    }
+  } else {
+    const double x = (double)pages * slots / ((double)units * fixed);
+    while ((P + 1) * (P + 1) <= x && P < kAutoMaxPartitions) ++P;
+  }
+  if (P > pages) P = pages;
+  int64_t per = (pages + P - 1) / P;
+  per = (per + align - 1) / align * align;
+  *ppp = (int)per;
+  *nparts = (int)((pages + per - 1) / per);
+}
+
 int run(Form form, const Window& win, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
         const int32_t* context_lens, const uint32_t* tree_mask, int num_seqs, int max_blocks_per_seq,
         int num_blocks, int max_context_len, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
@@ -268,12 +301,21 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
   } else {
     int ppp = 0, nparts = 0;
     const int covered = visible_context(win, max_context_len, q_len, align);
-    st = paged_attn_plan(dev->num_sms, num_seqs, num_kv_heads, covered, block_size, q_len, kv_dtype, &ppp, &nparts);
-    if (st != PA_OK) return st;
-    if (split_tiles && ppp % 4 != 0) {  // the prefill kernel walks whole 64-token steps
-      const int pages = (covered + block_size - 1) / block_size;
-      ppp = (ppp + 3) / 4 * 4;
-      nparts = pages > 0 ? (pages + ppp - 1) / ppp : 1;
+    if (few_rows || win.window > 0 || fp4) {
+      // resident CTAs per SM and the cost of one in pages, by kernel
+      const int rows = l.group * q_len;
+      const int per_sm = few_rows ? pa::rows_resident_ctas(rows) : mma_decode && !l.fp8 ? 6 : mma_decode ? 4 : 2;
+      const bool bf16 = kv_dtype == PA_KV_BF16;
+      plan_rows(win.window > 0, (int64_t)num_seqs * num_kv_heads, (int64_t)dev->num_sms * per_sm,
+                ((int64_t)covered + block_size - 1) / block_size, bf16 ? 20. : 38., bf16 ? 1.2 : 0.5, align, &ppp, &nparts);
+    } else {
+      st = paged_attn_plan(dev->num_sms, num_seqs, num_kv_heads, covered, block_size, q_len, kv_dtype, &ppp, &nparts);
+      if (st != PA_OK) return st;
+      if (split_tiles && ppp % 4 != 0) {  // the prefill kernel walks whole 64-token steps
+        const int pages = (covered + block_size - 1) / block_size;
+        ppp = (ppp + 3) / 4 * 4;
+        nparts = pages > 0 ? (pages + ppp - 1) / ppp : 1;
+      }
     }
     p.pages_per_partition = ppp;
     p.max_partitions = nparts;
@@ -465,14 +507,18 @@ int paged_attn_plan(int num_sms, int num_seqs, int num_kv_heads, int max_context
     return PA_OK;
   }
   const int64_t units = (int64_t)(num_seqs > 0 ? num_seqs : 1) * num_kv_heads;
-  const bool narrow = kv_dtype == PA_KV_FP8_E4M3 || kv_dtype == PA_KV_FP4_E2M1;
-  const int64_t target = (int64_t)(narrow ? kCtasPerSmTargetE4M3 : kCtasPerSmTarget) * num_sms;
+  if (kv_dtype == PA_KV_FP4_E2M1 && block_size > 0) {  // the rows kernel's rule, one n-tile
+    plan_rows(false, (int64_t)(num_seqs > 0 ? num_seqs : 1) * num_kv_heads, (int64_t)num_sms * pa::rows_resident_ctas(1),
+              ((int64_t)max_context_len + block_size - 1) / block_size, 38., 0.5, 1, pages_per_partition, max_partitions);
+    return PA_OK;
+  }
+  const int64_t target = (int64_t)(kv_dtype == PA_KV_FP8_E4M3 ? kCtasPerSmTargetE4M3 : kCtasPerSmTarget) * num_sms;
   P = (target + units - 1) / units;
   // E4M3: when one partition per (sequence, kv head) already fills 80 % of the target, splitting
   // costs more (a merge, twice the fixed start and end per CTA) than the idle slots it fills
   // (llama8b-shaped decode 48.2 -> 46.8 us, groups of 8 52.9 -> 48.9 us)
-  if (narrow && units * 5 >= target * 4) P = 1;
-  const int64_t cap = narrow ? kAutoPagesCapE4M3 : kAutoPagesCap;
+  if (kv_dtype == PA_KV_FP8_E4M3 && units * 5 >= target * 4) P = 1;
+  const int64_t cap = kv_dtype == PA_KV_FP8_E4M3 ? kAutoPagesCapE4M3 : kAutoPagesCap;
   const int64_t by_cap = (pages + cap - 1) / cap;
   if (by_cap > P) P = by_cap;
   if (P > kAutoMaxPartitions) P = kAutoMaxPartitions;

@@ -57,6 +57,8 @@ cudaError_t prefill_fp4_form(const AttnParams& p, const Launch& l, int max_q_len
 // A few rows per kv head (group * q_len at most kRowsMax) on mma.sync: 4-bit caches, and window forms of
 // bf16 and E4M3 caches; same grid, partitions (any page count) and partials as launch_decode_mma.
 constexpr int kRowsMax = 32;
+// CTAs of it that share an SM, by the rows per kv head (its accumulators' registers).
+constexpr int rows_resident_ctas(int rows) { return rows <= 8 ? 4 : rows <= 16 ? 3 : 2; }
 cudaError_t rows_fp4_form(const AttnParams& p, const Launch& l);
 cudaError_t rows_window_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
 // KV append (bf16 scatter, fp8 with per-(block, head) rescaling, or E2M1 codes with a scale for each

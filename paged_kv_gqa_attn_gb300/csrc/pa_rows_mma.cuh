@@ -16,7 +16,9 @@
 // (exact: at most six significant bits).  Per 16-token page of d = 128 about 64 conversions, 64
 // multiplications and 16 products an n-tile: near 260 warp instructions for 2304 bytes, about two
 // thirds of what an SM issues while it receives them, so bytes stay the bound if enough loads are in
-// flight: rings of six pages a warp, four warps a CTA, two to four CTAs an SM.
+// flight: rings of two steps of two pages a warp, four warps a CTA, two to four CTAs an SM.  A page is 72 (d = 128) 16-byte pieces: the lanes copy
+// them with cp.async, nine instructions for a step of four pages with no barrier to poll (the bulk-copy
+// unit's uniform operands cost one lane near 60 instructions a page here: 285 -> 268 us for 64 ragged contexts).
 // f16 weights, q re-encoded as f16 after a power of two a row, and E4M3's folded page scales are as in
 // the decode kernel; the head's K scale joins the row's score factor, its V scale the epilogue.
 //
@@ -42,18 +44,20 @@ struct RowsTraits {
   static constexpr int kCols = 8 * NT;
   static constexpr int kRowBytes = kBf16 ? 2 * D : kFp8 ? D : D / 2;  // of codes
   static constexpr int kPageBytes = kFp4 ? Fp4Page<D>::kBytes : kBS * kRowBytes;
-  static constexpr int kStageBytes = 2 * kPageBytes;  // K page then V page
-  static constexpr int kStages = kBf16 ? 2 : kFp8 ? 3 : 6;
-  static constexpr int kMinBlocks = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr int kPP = kFp4 ? 2 : 1;       // pages per step of a warp
+  static constexpr int kStageBytes = 2 * kPP * kPageBytes;  // K page then V page, for each page
+  static constexpr int kStages = kBf16 ? 2 : kFp8 ? 3 : 4 / kPP;
+  static constexpr int kMinBlocks = rows_resident_ctas(8 * NT);
   static constexpr int kBoxes = kRowBytes >= 128 ? kRowBytes / 128 : 1;  // TMA boxes per page (not 4-bit)
   static constexpr int kKSteps = D / 16;
   static constexpr int kMTiles = D / 16;
   static constexpr int kMerge = kWarps * kCols * (D + 2) * 4;  // per-warp outputs, maxima, sums
   static constexpr int kStageRegion = kWarps * kStages * kStageBytes;
   static constexpr int kDataRegion = kStageRegion > kMerge ? kStageRegion : kMerge;
-  static constexpr int kBarRegion = kWarps * kStages * 8;
-  static constexpr int kSmem = 1024 + kDataRegion + kBarRegion;  // 1 KiB: alignment of the swizzle
-  static_assert(kDataRegion % 8 == 0, "barriers are 8-byte aligned");
+  static constexpr int kBarRegion = kWarps * kStages * 8;  // (a multiple of 16: kWarps is even)
+  static constexpr int kQRegion = NT * (kKSteps / 2) * 32 * 16;
+  static constexpr int kSmem = 1024 + kDataRegion + kBarRegion + kQRegion;  // 1 KiB: alignment of the swizzle
+  static_assert(kDataRegion % 16 == 0 && kBarRegion % 16 == 0, "barriers and Q fragments are aligned");
 };
 
 // First dim of a lane's four contraction dims in k-step st (the order of each row's words).
@@ -205,10 +209,11 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
   const int R = p.q_len * G;  // columns in use
   const int ppp = p.pages_per_partition;
   const int pbeg = part * ppp;
-  const int first = pbeg + warp;
+  // the warp's j-th page: steps of kPP consecutive pages, dealt to the warps in turn
+  auto page_no = [&](int j) { return pbeg + (warp + T::kWarps * (j / T::kPP)) * T::kPP + j % T::kPP; };
   const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
   // without a window the first block ids depend on the partition only: load them with the length
-  const int row0 = first + T::kWarps * lane, row1 = first + T::kWarps * (32 + lane);
+  const int row0 = page_no(lane), row1 = page_no(32 + lane);
   const int raw0 = !WIN && row0 < p.max_blocks_per_seq ? bt[row0] : -1;
   const int raw1 = !WIN && row1 < p.max_blocks_per_seq ? bt[row1] : -1;
   const int L = context_len(p, b, part == 0 && g == 0 && threadIdx.x == 0);
@@ -238,9 +243,10 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmv)) : "memory");
   }
   uint8_t* stages = smem + warp * T::kStages * T::kStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::kDataRegion) + warp * T::kStages;
-  const int nk = first < pend ? (pend - first + T::kWarps - 1) / T::kWarps : 0;
-  if (lane == 0) {
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::kDataRegion) + warp * T::kStages;  // (not 4-bit)
+  const int nsteps = (pend - pbeg + T::kPP - 1) / T::kPP;
+  const int nk = warp < nsteps ? (nsteps - warp + T::kWarps - 1) / T::kWarps : 0;  // the warp's steps
+  if (!T::kFp4 && lane == 0) {
 #pragma unroll
     for (int s = 0; s < T::kStages; ++s) mbar_init(smem_addr(&bars[s]), 1);
     fence_mbar_init();
@@ -248,58 +254,91 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
   __syncwarp();
 
   // block ids (E4M3: and scales) of the warp's pages, two windows of 32 in lane registers
-  auto load_window = [&](int kb) {
-    const int kk = kb + lane;
-    const int v = first + T::kWarps * kk;
-    return kk < nk ? bt[WIN ? span.real(v) : v] : -1;
+  auto load_window = [&](int jb) {
+    const int v = page_no(jb + lane);
+    return v < pend ? bt[WIN ? span.real(v) : v] : -1;
   };
   auto load_scale = [&](const float* sc, int id) {
     return (T::kFp8 && id >= 0 && id < p.num_blocks) ? sc[(size_t)id * Hkv + g] : 1.f;
   };
   int wb = 0;
-  int idw0 = WIN ? load_window(0) : lane < nk ? raw0 : -1;
-  int idw1 = WIN ? load_window(32) : 32 + lane < nk ? raw1 : -1;
+  int idw0 = WIN ? load_window(0) : row0 < pend ? raw0 : -1;
+  int idw1 = WIN ? load_window(32) : row1 < pend ? raw1 : -1;
   float ksw0 = load_scale(p.k_scale, idw0), vsw0 = load_scale(p.v_scale, idw0);
   float ksw1 = load_scale(p.k_scale, idw1), vsw1 = load_scale(p.v_scale, idw1);
-  auto id_of = [&](int k) {  // k in [wb, wb + 64), warp-uniform
-    const int o = k - wb;
+  auto id_of = [&](int j) {  // j in [wb, wb + 64), warp-uniform
+    const int o = j - wb;
     return o < 32 ? __shfl_sync(0xffffffffu, idw0, o) : __shfl_sync(0xffffffffu, idw1, o - 32);
   };
   const uint64_t kv_policy = l2_evict_first_policy();
-  auto issue = [&](int k) {  // whole warp: lane 0 starts the copies of the warp's k-th page
-    const int pb = id_of(k);
-    if (lane != 0) return;
+  // 4-bit pages: lanes take 16-byte pieces, the codes of each page in whole-warp copies, then the scales of
+  // all the step's pages in one (lane / kScalePieces of them: K, V of the first page, K, V of the second).
+  constexpr int kScalePieces = D / 16;  // 16-byte pieces of a page's scales
+  const bool scale_v = (lane / kScalePieces) & 1;
+  const int scale_page = lane / (2 * kScalePieces);
+  const unsigned block_bytes = (unsigned)Hkv * T::kPageBytes;  // at most 65535 * 1152
+  const unsigned head = (unsigned)g * T::kPageBytes + lane * 16;
+  auto issue = [&](int k) {  // whole warp: start the copies of the warp's k-th step
+    int ids[T::kPP];
+    bool ok[T::kPP];
+#pragma unroll
+    for (int pp = 0; pp < T::kPP; ++pp) {
+      ids[pp] = id_of(k * T::kPP + pp);
+      ok[pp] = (unsigned)ids[pp] < (unsigned)p.num_blocks;
+      if (!ok[pp] && lane == 0 && page_no(k * T::kPP + pp) < pend) record_error(p.err, kErrBlockId);
+    }
     const int s = k % T::kStages;
+    const uint32_t stage = smem_addr(stages + s * T::kStageBytes);
+    if constexpr (T::kFp4) {
+      using P = Fp4Page<D>;
+#pragma unroll
+      for (int pp = 0; pp < T::kPP; ++pp) {
+        if (!ok[pp]) continue;
+        const uint64_t at = (uint64_t)(unsigned)ids[pp] * block_bytes + head;
+        const uint32_t dst = stage + pp * 2 * T::kPageBytes + lane * 16;
+#pragma unroll
+        for (int i = 0; i < P::kCodeBytes; i += 512) {
+          cp_async_16(dst + i, p.k_cache + at + i, kv_policy);
+          cp_async_16(dst + T::kPageBytes + i, p.v_cache + at + i, kv_policy);
+        }
+      }
+      static_assert(T::kPP <= 2 && 2 * 2 * kScalePieces <= 32, "a step's scales are one copy a lane");
+      const int sid = scale_page == 0 ? ids[0] : ids[T::kPP - 1];
+      if (scale_page < T::kPP && (unsigned)sid < (unsigned)p.num_blocks) {
+        // piece lane % kScalePieces of that page's scales (head holds lane * 16 already)
+        const int piece = P::kCodeBytes - (lane - lane % kScalePieces) * 16;
+        cp_async_16(stage + (2 * scale_page + scale_v) * T::kPageBytes + piece + lane * 16,
+                    (scale_v ? p.v_cache : p.k_cache) + ((uint64_t)(unsigned)sid * block_bytes + head) + piece, kv_policy);
+      }
+      return;
+    }
+    if (lane != 0) return;
     const uint32_t bar = smem_addr(&bars[s]);
-    if (pb < 0 || pb >= p.num_blocks) {
-      record_error(p.err, kErrBlockId);
+    static_assert(T::kFp4 || T::kPP == 1, "one page a step");
+    if (!ok[0]) {
       mbar_arrive(bar);
       return;
     }
-    const uint32_t dst = smem_addr(stages + s * T::kStageBytes);
     mbar_arrive_expect_tx(bar, 2 * T::kPageBytes);
-    if constexpr (T::kFp4) {
-      const size_t at = ((size_t)pb * Hkv + g) * T::kPageBytes;
-      bulk_copy_g2s_hint(dst, p.k_cache + at, T::kPageBytes, bar, kv_policy);
-      bulk_copy_g2s_hint(dst + T::kPageBytes, p.v_cache + at, T::kPageBytes, bar, kv_policy);
-    } else {
-      const int row = (int)(((int64_t)pb * Hkv + g) * T::kBS);
+    const int row = (int)(((int64_t)ids[0] * Hkv + g) * T::kBS);
 #pragma unroll
-      for (int j = 0; j < T::kBoxes; ++j) {
-        const int x = j * (T::kBf16 ? 64 : 128);
-        tma_load_2d_hint(dst + j * (16 * 128), &tmk, x, row, bar, kv_policy);
-        tma_load_2d_hint(dst + T::kPageBytes + j * (16 * 128), &tmv, x, row, bar, kv_policy);
-      }
+    for (int j = 0; j < T::kBoxes; ++j) {
+      const int x = j * (T::kBf16 ? 64 : 128);
+      tma_load_2d_hint(stage + j * (16 * 128), &tmk, x, row, bar, kv_policy);
+      tma_load_2d_hint(stage + T::kPageBytes + j * (16 * 128), &tmv, x, row, bar, kv_policy);
     }
   };
-  {
-    const int n0 = nk < T::kStages ? nk : T::kStages;
-    for (int k = 0; k < n0; ++k) issue(k);
+#pragma unroll
+  for (int k = 0; k < T::kStages; ++k) {
+    if (k < nk) issue(k);
+    if constexpr (T::kFp4) cp_async_commit();  // one group a step, empty or not
   }
 
-  // B fragments of Q^T: column gi of each n-tile.  Byte caches: each row scaled by a power of two before
-  // its f16 re-encoding; mul[nt][e] = what turns a raw score of column 2qi + e into base-2 units.
-  uint32_t qf[NT][T::kKSteps][2];
+  // B fragments of Q^T (column gi of each n-tile), two k-steps a 16-byte piece, in shared memory: they are
+  // the same for every warp, and registers hold the accumulators of more CTAs instead.  Byte caches: each
+  // row scaled by a power of two before its f16 re-encoding; mul[nt][e] = what turns a raw score of column
+  // 2qi + e into base-2 units.
+  uint4* q_frag = reinterpret_cast<uint4*>(smem + T::kDataRegion + T::kBarRegion);
   float mul[NT][2];
   const float head_mul = p.scale_log2 * (T::kFp4 && p.k_scale ? p.k_scale[g] : 1.f);
 #pragma unroll
@@ -314,14 +353,8 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
       xs[st] = real ? *reinterpret_cast<const uint2*>(qrow + q_dim<D, KV>(qi, st)) : make_uint2(0u, 0u);
       if constexpr (!T::kBf16) emax = max(emax, max(bf16x2_max_exp(xs[st].x), bf16x2_max_exp(xs[st].y)));
     }
-    if constexpr (T::kBf16) {
-#pragma unroll
-      for (int st = 0; st < T::kKSteps; ++st) {
-        qf[nt][st][0] = xs[st].x;
-        qf[nt][st][1] = xs[st].y;
-      }
-      mul[nt][0] = mul[nt][1] = head_mul;
-    } else {
+    mul[nt][0] = mul[nt][1] = head_mul;
+    if constexpr (!T::kBf16) {
       emax = max(emax, __shfl_xor_sync(0xffffffffu, emax, 1));
       emax = max(emax, __shfl_xor_sync(0xffffffffu, emax, 2));
       const int kq = f16_prescale_exp(emax);
@@ -329,14 +362,18 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
 #pragma unroll
       for (int st = 0; st < T::kKSteps; ++st) {
         const float2 lo = bf16x2_to_f2(xs[st].x), hi = bf16x2_to_f2(xs[st].y);
-        qf[nt][st][0] = pack_f16(lo.x * up, lo.y * up);
-        qf[nt][st][1] = pack_f16(hi.x * up, hi.y * up);
+        xs[st] = make_uint2(pack_f16(lo.x * up, lo.y * up), pack_f16(hi.x * up, hi.y * up));
       }
       // score column 2qi + e of the tile is the row whose exponent sits in the lanes of row 2qi + e
-      mul[nt][0] = head_mul * exp2_int(-__shfl_sync(0xffffffffu, kq, (2 * qi) * 4));
-      mul[nt][1] = head_mul * exp2_int(-__shfl_sync(0xffffffffu, kq, (2 * qi + 1) * 4));
+      mul[nt][0] *= exp2_int(-__shfl_sync(0xffffffffu, kq, (2 * qi) * 4));
+      mul[nt][1] *= exp2_int(-__shfl_sync(0xffffffffu, kq, (2 * qi + 1) * 4));
     }
+#pragma unroll
+    for (int st = 0; st < T::kKSteps; st += 2)
+      if (st / 2 % T::kWarps == warp)
+        q_frag[(nt * (T::kKSteps / 2) + st / 2) * 32 + lane] = make_uint4(xs[st].x, xs[st].y, xs[st + 1].x, xs[st + 1].y);
   }
+  __syncthreads();
 
   float o[NT][T::kMTiles][4];
   float m[NT][2], l[NT][2];  // running maximum and sum of columns 2qi, 2qi+1 (l: this thread's tokens)
@@ -352,13 +389,18 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
   bool timed_out = false;
   for (int k = 0; k < nk; ++k) {
     const int s = k % T::kStages;
-    const bool landed = mbar_wait(smem_addr(&bars[s]), (k / T::kStages) & 1);
-    if (__any_sync(0xffffffffu, !landed)) {
-      timed_out = true;
-      break;
+    if constexpr (T::kFp4) {
+      cp_async_wait<T::kStages - 1>();  // this lane's pieces of the step; the others' by the warp barrier
+      __syncwarp();
+    } else {
+      const bool landed = mbar_wait(smem_addr(&bars[s]), (k / T::kStages) & 1);
+      if (__any_sync(0xffffffffu, !landed)) {
+        timed_out = true;
+        break;
+      }
+      k_done = k + 1;
     }
-    k_done = k + 1;
-    if (k == wb + 32) {  // slide the windows (the issue below looks at most kStages ahead)
+    if (k * T::kPP == wb + 32) {  // slide the windows (the issue below looks at most kStages ahead)
       wb += 32;
       idw0 = idw1;
       idw1 = load_window(wb + 32);
@@ -369,37 +411,50 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
         vsw1 = load_scale(p.v_scale, idw1);
       }
     }
-    const int pb = id_of(k);
-    if (pb >= 0 && pb < p.num_blocks) {
-      const int v_at = first + T::kWarps * k;
-      const int tok0 = (WIN ? span.real(v_at) : v_at) * T::kBS;
-      // every row sees the whole page; tokens that some row sees
-      const bool whole = tok0 + T::kBS <= first_new + (mask.tree ? 0 : 1) &&
-                         (!WIN || tok0 >= lo_last || tok0 + T::kBS <= p.sinks);
-      uint32_t live = 0xffffu;
-      if (!whole) {
-        live = (uint32_t)low_bits64(L - tok0);
-        if constexpr (WIN) live &= (uint32_t)(low_bits64(p.sinks - tok0) | ~low_bits64(lo_first - tok0));
-        live &= 0xffffu;
+    // the step's pages: the tokens that some row sees (none where there is no page), and whether every row
+    // sees every token
+    int tok0[T::kPP];
+    uint32_t live[T::kPP];
+    bool whole = true, any_page = false;
+#pragma unroll
+    for (int pp = 0; pp < T::kPP; ++pp) {
+      const int pb = id_of(k * T::kPP + pp);
+      const bool ok = pb >= 0 && pb < p.num_blocks;
+      const int v_at = page_no(k * T::kPP + pp);
+      tok0[pp] = (WIN ? span.real(v_at) : v_at) * T::kBS;
+      const bool all = ok && tok0[pp] + T::kBS <= first_new + (mask.tree ? 0 : 1) &&
+                       (!WIN || tok0[pp] >= lo_last || tok0[pp] + T::kBS <= p.sinks);
+      live[pp] = 0xffffu;
+      if (!all) {
+        uint64_t some = low_bits64(L - tok0[pp]);
+        if constexpr (WIN) some &= low_bits64(p.sinks - tok0[pp]) | ~low_bits64(lo_first - tok0[pp]);
+        live[pp] = ok ? (uint32_t)some & 0xffffu : 0u;
       }
+      whole = whole && all;
+      any_page = any_page || ok;
+    }
+    if (any_page) {
       const uint8_t* kp = stages + s * T::kStageBytes;
-      const uint8_t* vp = kp + T::kPageBytes;
 
       // ---- S^T = K . Q^T ----
-      float x[NT][4];
-      {
+      float x[T::kPP][NT][4];
+#pragma unroll
+      for (int pp = 0; pp < T::kPP; ++pp) {
         uint32_t a[T::kKSteps][4];
-        k_fragments<D, KV>(kp, gi, qi, a);
+        k_fragments<D, KV>(kp + pp * 2 * T::kPageBytes, gi, qi, a);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+          x[pp][nt][0] = x[pp][nt][1] = x[pp][nt][2] = x[pp][nt][3] = 0.f;
 #pragma unroll
-          for (int st = 0; st < T::kKSteps; ++st)
-            mma_16816<T::kBf16>(x[nt], a[st][0], a[st][1], a[st][2], a[st][3], qf[nt][st][0], qf[nt][st][1]);
+          for (int st = 0; st < T::kKSteps; st += 2) {
+            const uint4 qf = q_frag[(nt * (T::kKSteps / 2) + st / 2) * 32 + lane];
+            mma_16816<T::kBf16>(x[pp][nt], a[st][0], a[st][1], a[st][2], a[st][3], qf.x, qf.y);
+            mma_16816<T::kBf16>(x[pp][nt], a[st + 1][0], a[st + 1][1], a[st + 1][2], a[st + 1][3], qf.z, qf.w);
+          }
         }
       }
 
-      // ---- online softmax: x[nt][0..1] = token gi, columns 2qi, 2qi+1; x[nt][2..3] = token gi + 8 ----
+      // ---- online softmax: x[..][0..1] = token gi, columns 2qi, 2qi+1; x[..][2..3] = token gi + 8 ----
       float ks = 1.f, lv = 0.f, rvs = 1.f;
       uint32_t neg = 0u;
       if constexpr (T::kFp8) {
@@ -411,26 +466,37 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
         neg = vs < 0.f ? 0x80008000u : 0u;
       }
       bool need = false;
+      float top[NT][2];  // the step's largest score of the thread's columns
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(x[nt][e], mul[nt][e & 1] * ks, lv);
-        if (!whole) {
+        for (int pp = 0; pp < T::kPP; ++pp) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int c = 8 * nt + 2 * qi + (e & 1), t = gi + 8 * (e >> 1);
-            const bool see = ((live >> t) & 1u) && (c >= R || mask.template sees<WIN>(c / G, tok0 + t));
-            if (!see) x[nt][e] = -INFINITY;
+          for (int e = 0; e < 4; ++e)
+            x[pp][nt][e] = T::kFp8 ? fmaf(x[pp][nt][e], mul[nt][e & 1] * ks, lv) : x[pp][nt][e] * mul[nt][e & 1];
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int c = 8 * nt + 2 * qi + (e & 1), t = gi + 8 * (e >> 1);
+              const bool see = ((live[pp] >> t) & 1u) && (c >= R || mask.template sees<WIN>(c / G, tok0[pp] + t));
+              if (!see) x[pp][nt][e] = -INFINITY;
+            }
           }
         }
-        need |= fmaxf(x[nt][0], x[nt][2]) > m[nt][0] + kTau || fmaxf(x[nt][1], x[nt][3]) > m[nt][1] + kTau;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[nt][e] = fmaxf(x[0][nt][e], x[0][nt][e + 2]);
+#pragma unroll
+          for (int pp = 1; pp < T::kPP; ++pp) top[nt][e] = fmaxf(top[nt][e], fmaxf(x[pp][nt][e], x[pp][nt][e + 2]));
+          need |= top[nt][e] > m[nt][e] + kTau;
+        }
       }
       if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float lm = fmaxf(x[nt][e], x[nt][e + 2]);
+            float lm = top[nt][e];
 #pragma unroll
             for (int sh = 4; sh < 32; sh <<= 1) lm = fmaxf(lm, __shfl_xor_sync(0xffffffffu, lm, sh));
             const float n = fmaxf(m[nt][e], lm);
@@ -445,68 +511,73 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
           }
         }
       }
-      // B fragments of P^T: b[nt][0] = tokens 2qi, 2qi+1 of column gi, b[nt][1] = tokens 2qi+8, 2qi+9
-      uint32_t bf[NT][2], bl[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = fast_exp2(x[nt][e] - m[nt][e & 1]);
-        if (!whole)  // a column that has seen nothing yet has no maximum
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = x[nt][e] == -INFINITY ? 0.f : w[e];
-        l[nt][0] += (w[0] + w[2]) * rvs;
-        l[nt][1] += (w[1] + w[3]) * rvs;
-        if constexpr (T::kBf16) {
-          bf[nt][0] = movmatrix_trans(pack_bf16(w[0], w[1]));
-          bf[nt][1] = movmatrix_trans(pack_bf16(w[2], w[3]));
-          bl[nt][0] = movmatrix_trans(pack_bf16(bf16_rem(w[0]), bf16_rem(w[1])));
-          bl[nt][1] = movmatrix_trans(pack_bf16(bf16_rem(w[2]), bf16_rem(w[3])));
-        } else {
-          bf[nt][0] = movmatrix_trans(pack_f16(w[0], w[1]) ^ neg);
-          bf[nt][1] = movmatrix_trans(pack_f16(w[2], w[3]) ^ neg);
-        }
-      }
-
-      // ---- O^T += V^T . P^T ----
-      constexpr int kWords = T::kRowBytes / 32;
-      uint32_t v[4][kWords], sc[2];
-      v_words<D, KV>(vp, gi, qi, live, v, sc);
-      auto pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+      for (int pp = 0; pp < T::kPP; ++pp) {
+        // B fragments of P^T: b[nt][0] = tokens 2qi, 2qi+1 of column gi, b[nt][1] = tokens 2qi+8, 2qi+9
+        uint32_t bf[NT][2], bl[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_16816<T::kBf16>(o[nt][i], a0, a1, a2, a3, bf[nt][0], bf[nt][1]);
-          if constexpr (T::kBf16) mma_16816<true>(o[nt][i], a0, a1, a2, a3, bl[nt][0], bl[nt][1]);
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = fast_exp2(x[pp][nt][e] - m[nt][e & 1]);
+          if (!whole)  // a column that has seen nothing yet has no maximum
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = x[pp][nt][e] == -INFINITY ? 0.f : w[e];
+          l[nt][0] += (w[0] + w[2]) * rvs;
+          l[nt][1] += (w[1] + w[3]) * rvs;
+          if constexpr (T::kBf16) {
+            bf[nt][0] = movmatrix_trans(pack_bf16(w[0], w[1]));
+            bf[nt][1] = movmatrix_trans(pack_bf16(w[2], w[3]));
+            bl[nt][0] = movmatrix_trans(pack_bf16(bf16_rem(w[0]), bf16_rem(w[1])));
+            bl[nt][1] = movmatrix_trans(pack_bf16(bf16_rem(w[2]), bf16_rem(w[3])));
+          } else {
+            bf[nt][0] = movmatrix_trans(pack_f16(w[0], w[1]) ^ neg);
+            bf[nt][1] = movmatrix_trans(pack_f16(w[2], w[3]) ^ neg);
+          }
         }
-      };
+
+        // ---- O^T += V^T . P^T ----
+        constexpr int kWords = T::kRowBytes / 32;
+        uint32_t v[4][kWords], sc[2];
+        v_words<D, KV>(kp + pp * 2 * T::kPageBytes + T::kPageBytes, gi, qi, live[pp], v, sc);
+        auto pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        if constexpr (T::kBf16) {
-          pv(w, __byte_perm(v[0][w], v[1][w], 0x5410), __byte_perm(v[0][w], v[1][w], 0x7632),
-             __byte_perm(v[2][w], v[3][w], 0x5410), __byte_perm(v[2][w], v[3][w], 0x7632));
-        } else if constexpr (T::kFp8) {
-          const uint32_t xa = __byte_perm(v[0][w], v[1][w], 0x5140), ya = __byte_perm(v[0][w], v[1][w], 0x7362);
-          const uint32_t xb = __byte_perm(v[2][w], v[3][w], 0x5140), yb = __byte_perm(v[2][w], v[3][w], 0x7362);
-          pv(2 * w, e4m3x2_to_f16x2(xa), e4m3x2_to_f16x2(xa >> 16), e4m3x2_to_f16x2(xb), e4m3x2_to_f16x2(xb >> 16));
-          pv(2 * w + 1, e4m3x2_to_f16x2(ya), e4m3x2_to_f16x2(ya >> 16), e4m3x2_to_f16x2(yb),
-             e4m3x2_to_f16x2(yb >> 16));
-        } else {
-          // byte i of lo / hi: the low / high nibbles (dims 2i / 2i+1) of two tokens
-          uint32_t lo[4], hi[4], lo8[4], hi8[4];
-          e2m1x8_to_f16x2((v[0][w] & 0x0f0f0f0fu) | ((v[1][w] << 4) & 0xf0f0f0f0u), lo);
-          e2m1x8_to_f16x2(((v[0][w] >> 4) & 0x0f0f0f0fu) | (v[1][w] & 0xf0f0f0f0u), hi);
-          e2m1x8_to_f16x2((v[2][w] & 0x0f0f0f0fu) | ((v[3][w] << 4) & 0xf0f0f0f0u), lo8);
-          e2m1x8_to_f16x2(((v[2][w] >> 4) & 0x0f0f0f0fu) | (v[3][w] & 0xf0f0f0f0u), hi8);
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816<T::kBf16>(o[nt][i], a0, a1, a2, a3, bf[nt][0], bf[nt][1]);
+            if constexpr (T::kBf16) mma_16816<true>(o[nt][i], a0, a1, a2, a3, bl[nt][0], bl[nt][1]);
+          }
+        };
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            pv(4 * w + i, mul_f16x2(lo[i], sc[0]), mul_f16x2(hi[i], sc[0]), mul_f16x2(lo8[i], sc[1]),
-               mul_f16x2(hi8[i], sc[1]));
+        for (int w = 0; w < kWords; ++w) {
+          if constexpr (T::kBf16) {
+            pv(w, __byte_perm(v[0][w], v[1][w], 0x5410), __byte_perm(v[0][w], v[1][w], 0x7632),
+               __byte_perm(v[2][w], v[3][w], 0x5410), __byte_perm(v[2][w], v[3][w], 0x7632));
+          } else if constexpr (T::kFp8) {
+            const uint32_t xa = __byte_perm(v[0][w], v[1][w], 0x5140), ya = __byte_perm(v[0][w], v[1][w], 0x7362);
+            const uint32_t xb = __byte_perm(v[2][w], v[3][w], 0x5140), yb = __byte_perm(v[2][w], v[3][w], 0x7362);
+            pv(2 * w, e4m3x2_to_f16x2(xa), e4m3x2_to_f16x2(xa >> 16), e4m3x2_to_f16x2(xb), e4m3x2_to_f16x2(xb >> 16));
+            pv(2 * w + 1, e4m3x2_to_f16x2(ya), e4m3x2_to_f16x2(ya >> 16), e4m3x2_to_f16x2(yb),
+               e4m3x2_to_f16x2(yb >> 16));
+          } else {
+            // byte i of lo / hi: the low / high nibbles (dims 2i / 2i+1) of two tokens
+            uint32_t lo[4], hi[4], lo8[4], hi8[4];
+            e2m1x8_to_f16x2((v[0][w] & 0x0f0f0f0fu) | ((v[1][w] << 4) & 0xf0f0f0f0u), lo);
+            e2m1x8_to_f16x2(((v[0][w] >> 4) & 0x0f0f0f0fu) | (v[1][w] & 0xf0f0f0f0u), hi);
+            e2m1x8_to_f16x2((v[2][w] & 0x0f0f0f0fu) | ((v[3][w] << 4) & 0xf0f0f0f0u), lo8);
+            e2m1x8_to_f16x2(((v[2][w] >> 4) & 0x0f0f0f0fu) | (v[3][w] & 0xf0f0f0f0u), hi8);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              pv(4 * w + i, mul_f16x2(lo[i], sc[0]), mul_f16x2(hi[i], sc[0]), mul_f16x2(lo8[i], sc[1]),
+                 mul_f16x2(hi8[i], sc[1]));
+          }
         }
       }
     }
     __syncwarp();
     if (k + T::kStages < nk) issue(k + T::kStages);
+    if constexpr (T::kFp4) cp_async_commit();
   }
+  if constexpr (T::kFp4) cp_async_wait<0>();
   if (timed_out) {
     // let every copy this warp started land (bounded) before its stages are reused
     if (lane == 0) {
