@@ -238,29 +238,34 @@ _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 def _kv_dtype(k_cache, v_cache, head_dim, k_scale, v_scale):
     """The cache type by the caches' dtype and last dim (bf16 [.., d], E4M3 bytes [.., d], 4-bit bytes
     [.., 9 d / 16]), with the checks of the scales that it takes."""
-    if k_cache.dtype == torch.bfloat16:
-        kv = PA_KV_BF16
-    elif k_cache.dtype == torch.uint8 and k_cache.dim() == 4 and 16 * k_cache.shape[3] == 9 * head_dim:
-        kv = PA_KV_FP4_E2M1
-    else:
-        kv = PA_KV_FP8_E4M3
-    types = _BF16 if kv == PA_KV_BF16 else _E4M3 if kv == PA_KV_FP8_E4M3 else _BYTES
-    _check_cuda("k_cache", k_cache, types)
-    _check_cuda("v_cache", v_cache, types)
-    if kv == PA_KV_FP8_E4M3:
-        _check_cuda("k_scale", k_scale, _F32)
-        _check_cuda("v_scale", v_scale, _F32)
-    if kv == PA_KV_FP4_E2M1:
+    dtype = k_cache.dtype
+    if dtype is torch.bfloat16:
+        _check_cuda("k_cache", k_cache, _BF16)
+        _check_cuda("v_cache", v_cache, _BF16)
+        return PA_KV_BF16
+    if dtype is torch.uint8 and k_cache.dim() == 4 and 16 * k_cache.shape[3] == 9 * head_dim:
+        _check_cuda("k_cache", k_cache, _BYTES)
+        _check_cuda("v_cache", v_cache, _BYTES)
+        heads = k_cache.shape[1:2]
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None:
                 _check_cuda(name, t, _F32)
-                if t.shape != (k_cache.shape[1],):
+                if t.shape != heads:
                     raise ValueError(f"{name} must be [num_kv_heads] for a 4-bit cache")
-    return kv
+        return PA_KV_FP4_E2M1
+    _check_cuda("k_cache", k_cache, _E4M3)
+    _check_cuda("v_cache", v_cache, _E4M3)
+    _check_cuda("k_scale", k_scale, _F32)
+    _check_cuda("v_scale", v_scale, _F32)
+    return PA_KV_FP8_E4M3
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+_WINDOW_FORMS = {"paged_attn_decode": "paged_attn_window_decode", "paged_attn_verify": "paged_attn_window_verify",
+                 "paged_attn_prefill": "paged_attn_window_prefill"}
 
 
 def _window(fn_name, window, sinks):
@@ -269,14 +274,15 @@ def _window(fn_name, window, sinks):
         if sinks:
             raise ValueError("sinks need a window: without one every token is visible")
         return fn_name, ()
-    return fn_name.replace("paged_attn_", "paged_attn_window_"), (int(window), int(sinks))
+    return _WINDOW_FORMS[fn_name], (int(window), int(sinks))
 
 
 def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_scale=None,
           v_scale=None, max_context_len=None, out=None, stream=None, tree_mask=None, window=None, sinks=0):
     lib = load_library()
     _check_cuda("q", q, _BF16)
-    if q.dim() != 4 or k_cache.dim() != 4 or k_cache.shape != v_cache.shape or block_table.dim() != 2:
+    cache_shape = k_cache.shape
+    if q.dim() != 4 or len(cache_shape) != 4 or cache_shape != v_cache.shape or block_table.dim() != 2:
         raise ValueError("expected q [B, q_len, Hq, d], caches [NB, Hkv, bs, d], block_table [B, M]")
     B, q_len, Hq, d = q.shape
     kv = _kv_dtype(k_cache, v_cache, d, k_scale, v_scale)
@@ -284,8 +290,9 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
     _check_cuda("context_lens", context_lens, _I32)
     if kv == PA_KV_BF16:
         k_scale = v_scale = None
-    NB, Hkv, bs, d2 = k_cache.shape
-    if (d2 != d and kv != PA_KV_FP4_E2M1) or block_table.shape[0] != B or context_lens.shape != (B,):
+    NB, Hkv, bs, d2 = cache_shape
+    rows, max_blocks = block_table.shape
+    if (d2 != d and kv != PA_KV_FP4_E2M1) or rows != B or context_lens.shape != (B,):
         raise ValueError("shape mismatch between q, caches, block_table and context_lens")
     if out is None:
         out = torch.empty_like(q)
@@ -293,20 +300,21 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
         _check_cuda("out", out, _BF16)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
-    max_blocks = int(block_table.shape[1])
     if max_context_len is None:
         max_context_len = max_blocks * bs  # an upper bound known without reading the device
-    fn_name, span = _window(fn_name, window, sinks)
-    lead = [q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-            context_lens.data_ptr()]
+    span = ()
+    if window is not None or sinks:
+        fn_name, span = _window(fn_name, window, sinks)
+    mask = ()
     if fn_name == "paged_attn_tree_verify":
         _check_cuda("tree_mask", tree_mask, _I32)
         if tree_mask.shape != (B, q_len):
             raise ValueError("tree_mask must be [B, q_len]")
-        lead.append(tree_mask.data_ptr())
+        mask = (tree_mask.data_ptr(),)
     with _one_device(stream, q, k_cache, v_cache, block_table, context_lens, tree_mask, out, k_scale, v_scale):
         st = getattr(lib, fn_name)(
-            *lead, B, max_blocks, NB, int(max_context_len), q_len, Hq, Hkv, d, bs, *span,
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), *mask,
+            B, max_blocks, NB, int(max_context_len), q_len, Hq, Hkv, d, bs, *span,
             float(scale), kv, _ptr(k_scale), _ptr(v_scale), out.data_ptr(), _stream_handle(stream))
     if st != PA_OK:
         raise PagedAttnError(st, fn_name)

@@ -29,9 +29,9 @@
 // f16 (exact), zeroing pages without a block and tokens past the tile's last row; P.V runs on f16
 // with P carrying each page's V scale.  With head_dim 64 K is converted the same way and Q.K^T
 // runs on f16 (Q re-encoded after the row scale).
-// 4-bit caches: a bulk copy lands each page (codes, then scales) in the upper part of the step's f16
-// tile; once a step has landed its warp takes all of it into registers and writes the f16 rows over it
-// (code * scale is exact in f16).  No scale belongs to a page: the head's K scale is part of the row's
+// 4-bit caches: a producer warp loads the next step's codes and scales into registers while it writes
+// this step's f16 rows (code * scale is exact in f16); staged in shared memory behind the tile they
+// replaced, the copies waited for the tile (chunks of 1024 behind 16384 tokens 734 -> XXX us).  No scale belongs to a page: the head's K scale is part of the row's
 // score factor and its V scale of the epilogue's, so the softmax runs the bf16 form's raw-score path.
 // Sliding window with sinks (WIN): the tile's pages are the sinks' and those from its first row's
 // window on, numbered without the gap between (page_span; both edges on whole steps, so that a step
@@ -63,14 +63,18 @@ struct PfTraits {
   static constexpr int kOffQ = kOffV + 2 * kTile;
   static constexpr int kOffBar = kOffQ + kQBytes;
   // kfull[2], vfull[2], kempty[2], o_done[2], s_ready[2], p_ready[2], q_ready, final, and for
-  // E4M3 caches kready[2], vready[2] (tile converted to f16)
-  static constexpr int kNumBars = 18;
+  // E4M3 and 4-bit caches kready[2], vready[2] (tile converted to f16), raw_full[3], raw_empty[3] (4-bit:
+  // staged pages landed, and read)
+  static constexpr int kNumBars = 24;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem base, abort flag
-  static constexpr int kSmem = kOffMisc + 16 + 1024;       // + slack for 1024-byte alignment
+  static constexpr int kOffRaw = kOffMisc + 16;            // 4-bit: three slots for a step's K or V pages as they came
+  static constexpr int smem(int kv) {                      // + slack for 1024-byte alignment
+    return kOffRaw + (kv == kKvFp4 ? 3 * kTP * Fp4Page<D>::kBytes : 0) + 1024;
+  }
   static constexpr int kSCol = 0;                          // S/P buffer j: columns 64 j ..
   static constexpr int kOCol = 128;
   static constexpr int kTmemCols = 256;
-  static constexpr int kThreads = 224;
+  static constexpr int threads(int kv) { return kv == kKvFp4 ? 256 : 224; }
   // kind::f16: D fp32 (bit 4), A bf16 (7-9), B bf16 (10-12), B MN-major (16), N >> 3 (17), M >> 4 (24)
   static constexpr uint32_t kIdescQK =
       (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kStepTokens >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -115,7 +119,7 @@ __device__ __forceinline__ void pf_tl_put(int slot, unsigned long long v) {
 // when the sequence has several partitions, writes the normalised partial rows and their
 // log2-sum-exp for the log-sum-exp merge kernel; p.tree_mask, when set, replaces the causal mask.
 template <int D, bool SPLIT, int KV, bool WIN>
-__global__ void __launch_bounds__(224, 2) prefill_tc_kernel(const AttnParams p, const int32_t* __restrict__ tiles,
+__global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel(const AttnParams p, const int32_t* __restrict__ tiles,
                                                             const __grid_constant__ CUtensorMap tmk,
                                                             const __grid_constant__ CUtensorMap tmv) {
   using T = PfTraits<D>;
@@ -160,6 +164,8 @@ __global__ void __launch_bounds__(224, 2) prefill_tc_kernel(const AttnParams p, 
   const uint32_t bar_final = bar_q_ready + 8;    // every MMA issued has completed
   const uint32_t bar_kready = bar_final + 8;     // E4M3: + 8 * stage: K tile converted to f16
   const uint32_t bar_vready = bar_kready + 16;   // E4M3: + 8 * stage: V tile converted to f16
+  const uint32_t bar_raw_full = bar_vready + 16;     // 4-bit: + 8 * slot: a step's K or V pages staged
+  const uint32_t bar_raw_empty = bar_raw_full + 24;  // 4-bit: + 8 * slot: and taken into registers
   uint32_t* misc = reinterpret_cast<uint32_t*>(gbase + T::kOffMisc);
   volatile uint32_t* abort_flag = misc + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -238,6 +244,11 @@ __global__ void __launch_bounds__(224, 2) prefill_tc_kernel(const AttnParams p, 
       mbar_init(bar_kready + 8 * s, 1);
       mbar_init(bar_vready + 8 * s, kKDirect ? 2 : 1);  // head_dim 128: both producer warps convert V
     }
+    if constexpr (FP4)
+      for (int s = 0; s < 3; ++s) {
+        mbar_init(bar_raw_full + 8 * s, 1);
+        mbar_init(bar_raw_empty + 8 * s, 1);
+      }
     mbar_init(bar_q_ready, 4);
     mbar_init(bar_final, 1);
     *abort_flag = 0u;
@@ -415,131 +426,148 @@ __global__ void __launch_bounds__(224, 2) prefill_tc_kernel(const AttnParams p, 
     if (lane == 0)
       for (int k = max(0, gi - 2); k < gi; ++k) mbar_wait(bar_full + 8 * (k & 1), (k >> 1) & 1);
     __syncwarp();
-  } else if ((warp == 4 || warp == 5) && FP4) {
-    // ======== 4-bit producers: warp 4 copies and converts the K ring, warp 5 the V ring (2 stages each)
+  } else if (FP4 && warp != 6 && warp >= 4) {
+    // ======== 4-bit producers.  Warp 7 stages a step's K pages, then its V pages, by bulk copies into a ring
+    // of three such slots, so copies run a step and a half ahead of warp 4, which converts K, and warp 5,
+    // which converts V: each takes its pages into registers, gives the slot back and writes the f16 tile
+    // once QK (PV) of the step two before is done.  (Staged in the tile's own space, or one step ahead only,
+    // the copies' latency was in every step: 651-840 us where this takes XXX.)
     using P = Fp4Page<D>;
-    const bool is_k = warp == 4;
-    const uint32_t ring = is_k ? sK : sV;
-    const uint32_t bar_full = is_k ? bar_kfull : bar_vfull;    // codes landed
-    const uint32_t bar_ready = is_k ? bar_kready : bar_vready;  // tile converted
-    const uint32_t bar_free = is_k ? bar_kempty : bar_o_done;  // QK / PV of the step two before done
-    const uint8_t* cache = is_k ? p.k_cache : p.v_cache;
-    constexpr int kRaw = T::kTile - T::kTP * P::kBytes;  // the step's pages, at the end of its tile
-    static_assert(kRaw >= 0 && kRaw % 16 == 0, "a step's 4-bit pages fit its f16 tile");
-    constexpr int kUnitsRow = D / 32;                           // 32 dims: 16 code bytes, 2 scales
-    constexpr int kPerLane = T::kStepTokens * kUnitsRow / 32;
-    auto step_id = [&](int s, bool flag) {
-      const int page = column(pfirst + s * T::kTP + (lane & 3));
+    constexpr uint32_t kSlot = T::kTP * P::kBytes;
+    const uint32_t staging = base + T::kOffRaw;
+    // block ids of 32 pages (8 steps) in the lanes; -1: no page, or outside the pool
+    auto load_ids = [&](int v0) {
+      const int page = column(v0 + lane);
       int v = -1;
-      if (lane < T::kTP && page >= 0) {
+      if (page >= 0) {
         v = bt[page];
         if (v < 0 || v >= p.num_blocks) {
-          if (flag) record_error(p.err, kErrBlockId);
+          if (warp == 7) record_error(p.err, kErrBlockId);
           v = -1;
         }
       }
       return v;
     };
-    int gi = 0, gc = 0;  // steps copied, steps converted
-    uint32_t idle = 0;
-    while (gc < nsteps) {
-      bool progressed = false;
-      if (gi < nsteps && gi < gc + 2) {  // (a) copy the next step's pages once its stage is free
-        bool free_ok = gi < 2;
-        if (!free_ok && lane == 0) free_ok = mbar_test_wait(bar_free + 8 * (gi & 1), ((gi - 2) >> 1) & 1);
-        if (__shfl_sync(0xffffffffu, free_ok, 0)) {
-          const int v = step_id(gi, is_k);
-          int pbs[T::kTP];
+    int ids = -1;
+    if (warp == 7) {
+      int u = 0;  // slots filled: K of step 0, V of step 0, K of step 1, ...
+      bool go = true;
+      for (int s = 0; s < nsteps && go; ++s) {
+        if (s % 8 == 0) ids = load_ids(pfirst + s * T::kTP);
+        int pbs[T::kTP];
+        int npg = 0;
 #pragma unroll
-          for (int pg = 0; pg < T::kTP; ++pg) pbs[pg] = __shfl_sync(0xffffffffu, v, pg);
-          if (lane == 0) {
-            const uint32_t bar = bar_full + 8 * (gi & 1);
-            int npg = 0;
+        for (int pg = 0; pg < T::kTP; ++pg) {
+          pbs[pg] = __shfl_sync(0xffffffffu, ids, (s % 8) * T::kTP + pg);
+          npg += pbs[pg] >= 0;
+        }
 #pragma unroll
-            for (int pg = 0; pg < T::kTP; ++pg) npg += pbs[pg] >= 0;
-            if (npg == 0) {
-              mbar_arrive(bar);
-            } else {
-              const uint32_t dst = ring + (gi & 1) * T::kTile + kRaw;
-              mbar_arrive_expect_tx(bar, npg * P::kBytes);
+        for (int kv = 0; kv < 2; ++kv) {
+          if (lane == 0 && go) {
+            const int slot = u % 3;
+            const uint32_t bar = bar_raw_full + 8 * slot;
+            if (u >= 3) go = wait_or_abort(bar_raw_empty + 8 * slot, (u / 3 - 1) & 1, abort_flag, p.err);
+            if (go) {
+              if (npg == 0) {
+                mbar_arrive(bar);
+              } else {
+                mbar_arrive_expect_tx(bar, npg * P::kBytes);
+                const uint8_t* cache = kv == 0 ? p.k_cache : p.v_cache;
 #pragma unroll
-              for (int pg = 0; pg < T::kTP; ++pg)
-                if (pbs[pg] >= 0)
-                  bulk_copy_g2s(dst + pg * P::kBytes, cache + ((size_t)pbs[pg] * Hkv + g) * P::kBytes, P::kBytes, bar);
+                for (int pg = 0; pg < T::kTP; ++pg)
+                  if (pbs[pg] >= 0)
+                    bulk_copy_g2s(staging + slot * kSlot + pg * P::kBytes,
+                                  cache + ((size_t)pbs[pg] * Hkv + g) * P::kBytes, P::kBytes, bar);
+              }
+              ++u;
             }
           }
-          ++gi;
-          progressed = true;
         }
+        go = __shfl_sync(0xffffffffu, go, 0);
       }
-      if (gc < gi) {  // (b) convert the oldest unconverted step once its codes have landed
-        bool landed = false;
-        if (lane == 0) landed = mbar_test_wait(bar_full + 8 * (gc & 1), (gc >> 1) & 1);
-        if (__shfl_sync(0xffffffffu, landed, 0)) {
-          const uint32_t tile = ring + (gc & 1) * T::kTile;
-          const uint32_t src = tile + kRaw;
-          const unsigned okm = __ballot_sync(0xffffffffu, step_id(gc, false) >= 0) & ((1u << T::kTP) - 1u);
-          const int tok = step_token(gc);
-          const int rows_ok = min(n_max - tok, min(T::kTP, plast - pfirst - gc * T::kTP) * T::kBS);
-          // the whole step into registers: the f16 rows below overwrite its codes
-          uint4 code[kPerLane];
-          uint16_t scl[kPerLane];
+      // every copy started has landed before the CTA's shared memory can go away
+      if (lane == 0)
+        for (int k = max(0, u - 3); k < u; ++k) mbar_wait(bar_raw_full + 8 * (k % 3), (k / 3) & 1);
+    } else {
+      const bool is_k = warp == 4;
+      const uint32_t ring = is_k ? sK : sV;
+      const uint32_t bar_ready = is_k ? bar_kready : bar_vready;
+      const uint32_t bar_free = is_k ? bar_kempty : bar_o_done;
+      constexpr int kUnitsRow = D / 32;                  // 32 dims: 16 code bytes, 2 scales
+      constexpr int kPerPage = T::kBS * kUnitsRow / 32;  // of them per lane and page
+      constexpr int kPerLane = T::kTP * kPerPage;
+      // The lane's 32-dim columns and rows: the eight lanes of a 16-byte access meet eight different bank
+      // groups both reading the codes (rows of d / 2 bytes) and writing the swizzled f16 rows.  d = 128: lanes
+      // of columns 0, 1 and of columns 2, 3 take different row pairs of the same four rows.
+      const int dq = lane % kUnitsRow;
+      const int row_in = D == 128 ? ((lane >> 2) & 1) + 2 * (((lane >> 3) & 1) ^ (dq >> 1)) + 4 * (lane >> 4) : lane >> 1;
+      constexpr int kRowsPer = 32 / kUnitsRow;  // token rows of one unit of all lanes
+      for (int s = 0; s < nsteps; ++s) {
+        if (s % 8 == 0) ids = load_ids(pfirst + s * T::kTP);
+        const int u = 2 * s + (is_k ? 0 : 1), slot = u % 3;
+        bool go = true;
+        if (lane == 0) go = wait_or_abort(bar_raw_full + 8 * slot, (u / 3) & 1, abort_flag, p.err);
+        if (!__shfl_sync(0xffffffffu, go, 0)) break;
+        uint4 code[kPerLane];
+        uint16_t scl[kPerLane];
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+          const uint32_t page = staging + slot * kSlot + (i / kPerPage) * P::kBytes;
+          const int tr = row_in + kRowsPer * (i % kPerPage);
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(code[i].x), "=r"(code[i].y), "=r"(code[i].z), "=r"(code[i].w)
+                       : "r"(page + tr * P::kCodeRow + dq * 16)
+                       : "memory");
+          asm volatile("ld.shared.u16 %0, [%1];"
+                       : "=h"(scl[i])
+                       : "r"(page + P::kCodeBytes + tr * P::kScaleRow + dq * 2)
+                       : "memory");
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_raw_empty + 8 * slot);
+        if (lane == 0 && s >= 2) go = wait_or_abort(bar_free + 8 * (s & 1), ((s - 2) >> 1) & 1, abort_flag, p.err);
+        if (!__shfl_sync(0xffffffffu, go, 0)) break;
+        const uint32_t tile = ring + (s & 1) * T::kTile;
+        const int tok = step_token(s);
+        // pages that hold data; token rows [0, rows_ok), but for those between the sinks and the window
+        const unsigned okm = (__ballot_sync(0xffffffffu, ids >= 0) >> ((s % 8) * T::kTP)) & ((1u << T::kTP) - 1u);
+        const int rows_ok = min(n_max - tok, min(T::kTP, plast - pfirst - s * T::kTP) * T::kBS);
+        const bool all = okm == (1u << T::kTP) - 1u && rows_ok >= T::kStepTokens &&
+                         (!WIN || tok >= win_lo || tok + T::kStepTokens <= p.sinks);
+        if (!all) {  // a token without data becomes zeros (its scale too: a stray one may be a NaN)
 #pragma unroll
           for (int i = 0; i < kPerLane; ++i) {
-            const int u = lane + 32 * i, tr = u / kUnitsRow, dq = u % kUnitsRow;
-            const uint32_t at = src + (tr / T::kBS) * P::kBytes;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(code[i].x), "=r"(code[i].y), "=r"(code[i].z), "=r"(code[i].w)
-                         : "r"(at + (tr % T::kBS) * P::kCodeRow + dq * 16)
-                         : "memory");
-            asm volatile("ld.shared.u16 %0, [%1];"
-                         : "=h"(scl[i])
-                         : "r"(at + P::kCodeBytes + (tr % T::kBS) * P::kScaleRow + dq * 2)
-                         : "memory");
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < kPerLane; ++i) {
-            const int u = lane + 32 * i, tr = u / kUnitsRow, dq = u % kUnitsRow;
-            // a token without data becomes zeros (its scale too: a stray one may be a NaN)
-            const bool keep = ((okm >> (tr / T::kBS)) & 1u) && tr < rows_ok &&
-                              (!WIN || tok + tr >= win_lo || tok + tr < p.sinks);
-            const uint32_t c4[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-            const uint32_t s2 = e4m3x2_to_f16x2(keep ? scl[i] : 0u);
-            const uint32_t row = tile + (dq >> 1) * T::kRegion + tr * 128;
-            const int c8 = (dq & 1) * 4;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {  // eight dims: one 16-byte chunk of the swizzled f16 row
-              const uint32_t sp = __byte_perm(s2, s2, j < 2 ? 0x1010 : 0x3232);
-              uint32_t h[4];
-              e2m1x8_to_f16x2(keep ? c4[j] : 0u, h);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) h[e] = mul_f16x2(h[e], sp);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((c8 + j) ^ (tr & 7)) << 4)), "r"(h[0]),
-                           "r"(h[1]), "r"(h[2]), "r"(h[3])
-                           : "memory");
+            const int tr = row_in + kRowsPer * i;
+            if (!((okm >> (i / kPerPage)) & 1u) || tr >= rows_ok || (WIN && tok + tr < win_lo && tok + tr >= p.sinks)) {
+              code[i] = make_uint4(0u, 0u, 0u, 0u);
+              scl[i] = 0;
             }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_ready + 8 * (gc & 1));
-          ++gc;
-          progressed = true;
         }
-      }
-      if (progressed) {
-        idle = 0;
-      } else if (++idle >= kSpinLimit || ((idle & 1023u) == 0 && *abort_flag)) {
-        if (lane == 0) {
-          if (!*abort_flag) record_error(p.err, kErrTimeout);
-          *abort_flag = 1u;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+          const int tr = row_in + kRowsPer * i;
+          const uint32_t c4[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+          const uint32_t s2 = e4m3x2_to_f16x2(scl[i]);
+          const uint32_t row = tile + (dq >> 1) * T::kRegion + tr * 128;
+          const int c8 = (dq & 1) * 4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // eight dims: one 16-byte chunk of the swizzled f16 row
+            const uint32_t sp = __byte_perm(s2, s2, j < 2 ? 0x1010 : 0x3232);
+            uint32_t h[4];
+            e2m1x8_to_f16x2(c4[j], h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = mul_f16x2(h[e], sp);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((c8 + j) ^ (tr & 7)) << 4)), "r"(h[0]),
+                         "r"(h[1]), "r"(h[2]), "r"(h[3])
+                         : "memory");
+          }
         }
-        break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_ready + 8 * (s & 1));
       }
     }
-    // every copy started has landed before the CTA's shared memory can go away
-    if (lane == 0)
-      for (int k = max(0, gi - 2); k < gi; ++k) mbar_wait(bar_full + 8 * (k & 1), (k >> 1) & 1);
     __syncwarp();
   } else if (warp == 4 || warp == 5) {
     // ======== TMA producers: warp 4 fills the K ring, warp 5 the V ring (2 stages each) ========
@@ -1150,7 +1178,7 @@ cudaError_t prefill_tiles(const AttnParams& p, int max_q_len, int group, int32_t
                           const CUtensorMap& tv, cudaStream_t st) {
   using T = PfTraits<D>;
   const void* fn = reinterpret_cast<const void*>(prefill_tc_kernel<D, false, KV, WIN>);
-  cudaError_t e = set_smem_once(fn, T::kSmem);
+  cudaError_t e = set_smem_once(fn, T::smem(KV));
   if (e != cudaSuccess) return e;
   const int tt = T::kRows / group;
   e = launch_prefill_plan(p, tt, tiles, st);
@@ -1161,16 +1189,16 @@ cudaError_t prefill_tiles(const AttnParams& p, int max_q_len, int group, int32_t
   CUtensorMap k = tk, v = tv;
   void* args[] = {&pp, &ct, &k, &v};
   // x = rank * Hkv + kv head: the heaviest pairs, all heads of each, are dispatched first
-  return launch_pdl(fn, dim3((unsigned)(bound * p.num_kv_heads)), dim3(T::kThreads), T::kSmem, st, args);
+  return launch_pdl(fn, dim3((unsigned)(bound * p.num_kv_heads)), dim3(T::threads(KV)), T::smem(KV), st, args);
 }
 
 template <int D, int KV, bool WIN>
 cudaError_t prefill_split(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   using T = PfTraits<D>;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(prefill_tc_kernel<D, true, KV, WIN>), T::kSmem);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(prefill_tc_kernel<D, true, KV, WIN>), T::smem(KV));
   if (e != cudaSuccess) return e;
   dim3 grid(p.max_partitions, p.num_kv_heads, p.num_seqs);
-  prefill_tc_kernel<D, true, KV, WIN><<<grid, T::kThreads, T::kSmem, st>>>(p, nullptr, tk, tv);
+  prefill_tc_kernel<D, true, KV, WIN><<<grid, T::threads(KV), T::smem(KV), st>>>(p, nullptr, tk, tv);
   return cudaGetLastError();
 }
 
