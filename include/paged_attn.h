@@ -83,7 +83,10 @@ typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_FP4_E2M1 = 2 } pa_kv_dt
  *                     value near amax / (6 * 448) over the head's expected keys (values) centres the
  *                     E4M3 scales.
  * Accepted by paged_attn_append_kv, paged_attn_read_kv, paged_attn_decode, paged_attn_verify,
- * paged_attn_tree_verify, paged_attn_prefill and the window forms.
+ * paged_attn_tree_verify, paged_attn_prefill and the window forms.  Attention turns a page into f16
+ * operands exactly (code * scale has at most six significant bits); q is re-encoded as f16 as for E4M3
+ * caches, weights are f16, sums and softmax statistics fp32.  Decode and verify of up to 32 rows per kv
+ * head run the rows kernel (mma.sync), anything else the prefill kernel.
  */
 
 /*
@@ -194,8 +197,9 @@ int paged_attn_prefill(const void* q, const void* k_cache, const void* v_cache,
  * blocks back to its pool and leave any value there.  A token that no row of a (sequence, 128-row
  * tile) sees does not reach the output even as NaN; one that some row of the tile sees must be finite.
  * Work and scratch are those of the visible tokens.  Same arguments, errors and limits otherwise, but
- * max_context_len at most 2^30.  Kernels: the decode kernel (groups of 1, 2, 4 and 8) and the prefill
- * kernel, for verify rows and other groups of decode split like decode; the pages that are left are
+ * max_context_len at most 2^30.  Kernels: the decode kernel (groups of 1, 2, 4 and 8), the rows kernel
+ * (verify rows and other groups of decode, up to 32 rows per kv head: mma.sync, a row for each column
+ * of its n-tiles) and the prefill kernel (beyond, split like decode); the pages that are left are
  * numbered without the gap.
  */
 int paged_attn_window_decode(const void* q, const void* k_cache, const void* v_cache,

@@ -264,6 +264,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _made_for(stream, *outs):
+    """Outputs that a call made itself belong to the current stream's memory: where another stream writes
+    them, the allocator keeps them until that stream is done."""
+    if stream is not None:
+        for t in outs:
+            t.record_stream(stream)
+
+
 _WINDOW_FORMS = {"paged_attn_decode": "paged_attn_window_decode", "paged_attn_verify": "paged_attn_window_verify",
                  "paged_attn_prefill": "paged_attn_window_prefill"}
 
@@ -296,6 +304,7 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
         raise ValueError("shape mismatch between q, caches, block_table and context_lens")
     if out is None:
         out = torch.empty_like(q)
+        _made_for(stream, out)
     else:
         _check_cuda("out", out, _BF16)
         if out.shape != q.shape:
@@ -371,6 +380,7 @@ def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, sca
         raise ValueError("shape mismatch between q, caches, block_table, context_lens, query_start_loc")
     if out is None:
         out = torch.empty_like(q)
+        _made_for(stream, out)
     else:
         _check_cuda("out", out, _BF16)
         if out.shape != q.shape:
@@ -454,6 +464,7 @@ def read_kv(k_cache, v_cache, block_table, context_lens, n, *, k_scale=None, v_s
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is None:
             t = torch.empty((B, n, Hkv, d), dtype=torch.bfloat16, device=k_cache.device)
+            _made_for(stream, t)
         else:
             _check_cuda(name, t, _BF16)
             if t.shape != (B, n, Hkv, d):
@@ -511,11 +522,13 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, *, eps=1e-6, inte
         raise ValueError("expected weights [d], cos_sin [max_position, rotary_dim], positions [T]")
     if q_out is None:
         q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+        _made_for(stream, q_out)
         strides.append(Hq * d)
     else:
         strides.append(_token_stride("q_out", q_out, q_shape))
     if k_out is None:
         k_out = torch.empty(k_shape, dtype=torch.bfloat16, device=k.device)
+        _made_for(stream, k_out)
         strides.append(Hkv * d)
     else:
         strides.append(_token_stride("k_out", k_out, k_shape))

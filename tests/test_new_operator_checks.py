@@ -125,3 +125,13 @@ def test_window_prefill_checks():
     assert fn(*lead, 0, 2, 0.1, 0, None, None, FAKE, None) == pa.PA_ERR_INVALID_ARG
     assert fn(*lead, 5, -2, 0.1, 0, None, None, FAKE, None) == pa.PA_ERR_INVALID_ARG
     assert fn(*lead, 5, 2, 0.1, 4, None, None, FAKE, None) == pa.PA_ERR_INVALID_ARG
+
+
+def test_plan_of_4_bit_pages():
+    pa.set_max_partitions(0)
+    for units_b, pages in ((1, 513), (16, 257), (64, 2048), (256, 100), (1, 1)):
+        ppp, parts = pa.plan(152, units_b, 8, pages * 16, kv_dtype=pa.PA_KV_FP4_E2M1)
+        assert ppp * parts >= pages and ppp * (parts - 1) < pages and parts <= 64
+    # few contexts are cut finely, many coarsely
+    assert pa.plan(152, 1, 8, 8208, kv_dtype=pa.PA_KV_FP4_E2M1)[1] > 16
+    assert pa.plan(152, 512, 8, 2048, kv_dtype=pa.PA_KV_FP4_E2M1)[1] == 1
