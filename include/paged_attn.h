@@ -198,8 +198,8 @@ int paged_attn_prefill(const void* q, const void* k_cache, const void* v_cache,
  * tile) sees does not reach the output even as NaN; one that some row of the tile sees must be finite.
  * Work and scratch are those of the visible tokens.  Same arguments, errors and limits otherwise, but
  * max_context_len at most 2^30.  Kernels: the decode kernel (groups of 1, 2, 4 and 8), the rows kernel
- * (verify rows and other groups of decode, up to 32 rows per kv head: mma.sync, a row for each column
- * of its n-tiles) and the prefill kernel (beyond, split like decode); the pages that are left are
+ * (verify rows and other groups of decode, up to 32 rows per kv head, 16 over bf16 caches: mma.sync, a
+ * row for each column of its n-tiles) and the prefill kernel (beyond, split like decode); the pages that are left are
  * numbered without the gap.
  */
 int paged_attn_window_decode(const void* q, const void* k_cache, const void* v_cache,

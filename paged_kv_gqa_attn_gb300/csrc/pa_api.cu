@@ -269,12 +269,15 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
   // tcgen05 kernel (balanced persistent split + merge), decode as its q_len = 1 rows.
   // Verify with more than the verify kernel's 64 rows per kv head (bf16, up to 128) runs the
   // chunked-prefill kernel split into partitions like decode, with the same merge.
-  // 4-bit caches, and the window forms but decode's, take the rows kernel up to its kRowsMax rows per kv
-  // head and the split prefill kernel beyond.
+  // 4-bit caches, and the window forms but decode's, take the rows kernel up to its 32 rows per kv head and
+  // the split prefill kernel beyond; bf16 pages, which cost neither a conversion, only up to 16 (32
+  // sequences of up to 2048 + 16 visible tokens, 8 kv heads: 12 rows 49 / 55 us, 20 rows 59 / 55, 32 rows
+  // 77 / 54; E4M3 44 / 87, 51 / 86, 60 / 80; 4-bit, 8192 tokens: 79 / 152, 95 / 154, 125 / 150).
   const bool mma_group = l.group == 1 || l.group == 2 || l.group == 4 || l.group == 8;
   const bool fp4 = kv_dtype == PA_KV_FP4_E2M1;
   const bool mma_decode = form == Form::kDecode && mma_group && !fp4;
-  const bool few_rows = !mma_decode && (win.window > 0 || fp4) && l.group * q_len <= pa::kRowsMax;
+  const bool few_rows = !mma_decode && (win.window > 0 || fp4) &&
+                        l.group * q_len <= (kv_dtype == PA_KV_BF16 ? pa::kRowsMaxBf16 : pa::kRowsMax);
   const bool split_tiles = !mma_decode && !few_rows && (l.group * q_len > 64 || win.window > 0 || fp4);
   const bool on_tensor_cores = !mma_decode && !few_rows && !split_tiles;
   const int align = split_tiles ? 4 : 1;  // the split prefill kernel walks whole 64-token steps
@@ -306,8 +309,9 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
       const int rows = l.group * q_len;
       const int per_sm = few_rows ? pa::rows_resident_ctas(rows) : mma_decode && !l.fp8 ? 6 : mma_decode ? 4 : 2;
       const bool bf16 = kv_dtype == PA_KV_BF16;
+      const double fixed = few_rows && win.window > 0 && rows > 8 ? 60. : bf16 && mma_decode ? 20. : 38.;
       plan_rows(win.window > 0, (int64_t)num_seqs * num_kv_heads, (int64_t)dev->num_sms * per_sm,
-                ((int64_t)covered + block_size - 1) / block_size, bf16 ? 20. : 38., bf16 ? 1.2 : 0.5, align, &ppp, &nparts);
+                ((int64_t)covered + block_size - 1) / block_size, fixed, bf16 ? 1.2 : 0.5, align, &ppp, &nparts);
     } else {
       st = paged_attn_plan(dev->num_sms, num_seqs, num_kv_heads, covered, block_size, q_len, kv_dtype, &ppp, &nparts);
       if (st != PA_OK) return st;

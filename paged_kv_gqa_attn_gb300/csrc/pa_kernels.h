@@ -54,9 +54,9 @@ cudaError_t launch_prefill_plan(const AttnParams& p, int tiles_per_row, int32_t*
 cudaError_t prefill_window_form(const AttnParams& p, const Launch& l, int max_q_len, int32_t* tiles,
                                 const CUtensorMap& tk, const CUtensorMap& tv);
 cudaError_t prefill_fp4_form(const AttnParams& p, const Launch& l, int max_q_len, int32_t* tiles);
-// A few rows per kv head (group * q_len at most kRowsMax) on mma.sync: 4-bit caches, and window forms of
+// A few rows per kv head (group * q_len at most kRowsMax, bf16 kRowsMaxBf16) on mma.sync: 4-bit caches, and window forms of
 // bf16 and E4M3 caches; same grid, partitions (any page count) and partials as launch_decode_mma.
-constexpr int kRowsMax = 32;
+constexpr int kRowsMax = 32, kRowsMaxBf16 = 16;
 // CTAs of it that share an SM, by the rows per kv head (its accumulators' registers).
 constexpr int rows_resident_ctas(int rows) { return rows <= 8 ? 4 : rows <= 16 ? 3 : 2; }
 cudaError_t rows_fp4_form(const AttnParams& p, const Launch& l);

@@ -29,10 +29,12 @@
 // f16 (exact), zeroing pages without a block and tokens past the tile's last row; P.V runs on f16
 // with P carrying each page's V scale.  With head_dim 64 K is converted the same way and Q.K^T
 // runs on f16 (Q re-encoded after the row scale).
-// 4-bit caches: a producer warp loads the next step's codes and scales into registers while it writes
-// this step's f16 rows (code * scale is exact in f16); staged in shared memory behind the tile they
-// replaced, the copies waited for the tile (chunks of 1024 behind 16384 tokens 734 -> XXX us).  No scale belongs to a page: the head's K scale is part of the row's
-// score factor and its V scale of the epilogue's, so the softmax runs the bf16 form's raw-score path.
+// 4-bit caches: an eighth warp stages a step's pages (codes and scales) ahead, warp 4 turns K and warp 5 V into
+// the f16 tiles (code * scale is exact in f16).  No scale belongs to a page: the head's K scale is part of
+// the row's score factor and its V scale of the epilogue's, so the softmax runs the bf16 form's raw-score
+// path.  2 x 1024 new tokens behind up to 16384: 637 us (bf16 pages 512): the conversions' stores and the
+// products' operand reads fill most of the shared memory's cycles, and the converting warps slow the softmax
+// warps of their sub-partitions.
 // Sliding window with sinks (WIN): the tile's pages are the sinks' and those from its first row's
 // window on, numbered without the gap between (page_span; both edges on whole steps, so that a step
 // never straddles the gap); pages of a step that no row of the tile sees are neither looked up nor
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     // of three such slots, so copies run a step and a half ahead of warp 4, which converts K, and warp 5,
     // which converts V: each takes its pages into registers, gives the slot back and writes the f16 tile
     // once QK (PV) of the step two before is done.  (Staged in the tile's own space, or one step ahead only,
-    // the copies' latency was in every step: 651-840 us where this takes XXX.)
+    // the copies' latency was in every step: 651-840 us where this takes 637.)
     using P = Fp4Page<D>;
     constexpr uint32_t kSlot = T::kTP * P::kBytes;
     const uint32_t staging = base + T::kOffRaw;

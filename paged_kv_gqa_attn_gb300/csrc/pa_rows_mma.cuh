@@ -15,10 +15,14 @@
 // across two tokens by two logic operations a word; each pair is multiplied by its 16-dim scale in f16
 // (exact: at most six significant bits).  Per 16-token page of d = 128 about 64 conversions, 64
 // multiplications and 16 products an n-tile: near 260 warp instructions for 2304 bytes, about two
-// thirds of what an SM issues while it receives them, so bytes stay the bound if enough loads are in
-// flight: rings of two steps of two pages a warp, four warps a CTA, two to four CTAs an SM.  A page is 72 (d = 128) 16-byte pieces: the lanes copy
-// them with cp.async, nine instructions for a step of four pages with no barrier to poll (the bulk-copy
-// unit's uniform operands cost one lane near 60 instructions a page here: 285 -> 268 us for 64 ragged contexts).
+// thirds of what an SM issues while it receives them.  Measured (64 contexts of 1000 to 32768 tokens, 32 / 8
+// heads of 128): 268 us, 70 % of the copy rate; with the arithmetic left out the same copies take 193 us, the
+// copy rate.  The logic unit, which the conversions share at half rate, and the issue slots are each busy
+// little more than half the time: 16 warps an SM do not cover their chains, and a fifth CTA would need
+// fewer than 96 registers.  Pages go two to a step (301 -> 285 us), and move as 16-byte cp.async pieces of
+// all lanes with no barrier to poll, nine instructions a step: the bulk-copy unit's uniform operands cost one
+// lane near 60 instructions a page (285 -> 268 us).  At 20 rows (four drafts, groups of 4) the accumulators
+// leave two CTAs an SM: 95 us for 32 contexts up to 8192 tokens, 25 %.
 // f16 weights, q re-encoded as f16 after a power of two a row, and E4M3's folded page scales are as in
 // the decode kernel; the head's K scale joins the row's score factor, its V scale the epilogue.
 //
@@ -658,13 +662,14 @@ cudaError_t rows_launch(const AttnParams& p, const CUtensorMap& tk, const CUtens
 
 template <int D, int KV, bool WIN>
 cudaError_t rows_tiles(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv) {
-  switch ((l.group * p.q_len + 7) / 8) {
-    case 1: return rows_launch<D, 1, KV, WIN>(p, tk, tv, l.stream);
-    case 2: return rows_launch<D, 2, KV, WIN>(p, tk, tv, l.stream);
-    case 3: return rows_launch<D, 3, KV, WIN>(p, tk, tv, l.stream);
-    case 4: return rows_launch<D, 4, KV, WIN>(p, tk, tv, l.stream);
-    default: return cudaErrorInvalidConfiguration;
+  const int nt = (l.group * p.q_len + 7) / 8;
+  if (nt == 1) return rows_launch<D, 1, KV, WIN>(p, tk, tv, l.stream);
+  if (nt == 2) return rows_launch<D, 2, KV, WIN>(p, tk, tv, l.stream);
+  if constexpr (KV != kKvBf16) {  // (more bf16 rows run the tile kernel)
+    if (nt == 3) return rows_launch<D, 3, KV, WIN>(p, tk, tv, l.stream);
+    if (nt == 4) return rows_launch<D, 4, KV, WIN>(p, tk, tv, l.stream);
   }
+  return cudaErrorInvalidConfiguration;
 }
 
 }  // namespace
