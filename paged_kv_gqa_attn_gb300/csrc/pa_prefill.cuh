@@ -430,9 +430,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     __syncwarp();
   } else if (FP4 && warp != 6 && warp >= 4) {
     // ======== 4-bit producers.  Warp 7 stages a step's K pages, then its V pages, by bulk copies into a ring
-    // of three such slots, so copies run a step and a half ahead of warp 4, which converts K, and warp 5,
-    // which converts V: each takes its pages into registers, gives the slot back and writes the f16 tile
-    // once QK (PV) of the step two before is done.  (Staged in the tile's own space, or one step ahead only,
+    // of three such slots, so copies run ahead of warp 4, which converts K, and warp 5, which converts V: each
+    // writes the f16 tile once QK (PV) of the step two before is done, and gives the slot back.  (Staged in the tile's own space, or one step ahead only,
     // the copies' latency was in every step: 651-840 us where this takes 637.)
     using P = Fp4Page<D>;
     constexpr uint32_t kSlot = T::kTP * P::kBytes;
@@ -497,7 +496,6 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
       const uint32_t bar_free = is_k ? bar_kempty : bar_o_done;
       constexpr int kUnitsRow = D / 32;                  // 32 dims: 16 code bytes, 2 scales
       constexpr int kPerPage = T::kBS * kUnitsRow / 32;  // of them per lane and page
-      constexpr int kPerLane = T::kTP * kPerPage;
       // The lane's 32-dim columns and rows: the eight lanes of a 16-byte access meet eight different bank
       // groups both reading the codes (rows of d / 2 bytes) and writing the swizzled f16 rows.  d = 128: lanes
       // of columns 0, 1 and of columns 2, 3 take different row pairs of the same four rows.
@@ -510,23 +508,6 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
         bool go = true;
         if (lane == 0) go = wait_or_abort(bar_raw_full + 8 * slot, (u / 3) & 1, abort_flag, p.err);
         if (!__shfl_sync(0xffffffffu, go, 0)) break;
-        uint4 code[kPerLane];
-        uint16_t scl[kPerLane];
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-          const uint32_t page = staging + slot * kSlot + (i / kPerPage) * P::kBytes;
-          const int tr = row_in + kRowsPer * (i % kPerPage);
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(code[i].x), "=r"(code[i].y), "=r"(code[i].z), "=r"(code[i].w)
-                       : "r"(page + tr * P::kCodeRow + dq * 16)
-                       : "memory");
-          asm volatile("ld.shared.u16 %0, [%1];"
-                       : "=h"(scl[i])
-                       : "r"(page + P::kCodeBytes + tr * P::kScaleRow + dq * 2)
-                       : "memory");
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_raw_empty + 8 * slot);
         if (lane == 0 && s >= 2) go = wait_or_abort(bar_free + 8 * (s & 1), ((s - 2) >> 1) & 1, abort_flag, p.err);
         if (!__shfl_sync(0xffffffffu, go, 0)) break;
         const uint32_t tile = ring + (s & 1) * T::kTile;
@@ -536,38 +517,62 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
         const int rows_ok = min(n_max - tok, min(T::kTP, plast - pfirst - s * T::kTP) * T::kBS);
         const bool all = okm == (1u << T::kTP) - 1u && rows_ok >= T::kStepTokens &&
                          (!WIN || tok >= win_lo || tok + T::kStepTokens <= p.sinks);
-        if (!all) {  // a token without data becomes zeros (its scale too: a stray one may be a NaN)
+        // a page at a time, the next one's codes loaded before this one's are written: a small loop (unrolled
+        // over the step, its instructions were fetched again and again between the softmax's)
+        uint4 code[2][kPerPage];
+        uint16_t scl[2][kPerPage];
+        auto load_page = [&](int pg, uint4 (&c)[kPerPage], uint16_t (&sc)[kPerPage]) {
+          const uint32_t page = staging + slot * kSlot + pg * P::kBytes;
 #pragma unroll
-          for (int i = 0; i < kPerLane; ++i) {
+          for (int i = 0; i < kPerPage; ++i) {
             const int tr = row_in + kRowsPer * i;
-            if (!((okm >> (i / kPerPage)) & 1u) || tr >= rows_ok || (WIN && tok + tr < win_lo && tok + tr >= p.sinks)) {
-              code[i] = make_uint4(0u, 0u, 0u, 0u);
-              scl[i] = 0;
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-          const int tr = row_in + kRowsPer * i;
-          const uint32_t c4[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-          const uint32_t s2 = e4m3x2_to_f16x2(scl[i]);
-          const uint32_t row = tile + (dq >> 1) * T::kRegion + tr * 128;
-          const int c8 = (dq & 1) * 4;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {  // eight dims: one 16-byte chunk of the swizzled f16 row
-            const uint32_t sp = __byte_perm(s2, s2, j < 2 ? 0x1010 : 0x3232);
-            uint32_t h[4];
-            e2m1x8_to_f16x2(c4[j], h);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = mul_f16x2(h[e], sp);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((c8 + j) ^ (tr & 7)) << 4)), "r"(h[0]),
-                         "r"(h[1]), "r"(h[2]), "r"(h[3])
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(c[i].x), "=r"(c[i].y), "=r"(c[i].z), "=r"(c[i].w)
+                         : "r"(page + tr * P::kCodeRow + dq * 16)
                          : "memory");
+            asm volatile("ld.shared.u16 %0, [%1];"
+                         : "=h"(sc[i])
+                         : "r"(page + P::kCodeBytes + tr * P::kScaleRow + dq * 2)
+                         : "memory");
+          }
+        };
+        load_page(0, code[0], scl[0]);
+#pragma unroll 1
+        for (int pg = 0; pg < T::kTP; ++pg) {
+          if (pg + 1 < T::kTP) load_page(pg + 1, code[1], scl[1]);
+#pragma unroll
+          for (int i = 0; i < kPerPage; ++i) {
+            const int tr = pg * T::kBS + row_in + kRowsPer * i;
+            // a token without data becomes zeros (its scale too: a stray one may be a NaN)
+            if (!all && (!((okm >> pg) & 1u) || tr >= rows_ok || (WIN && tok + tr < win_lo && tok + tr >= p.sinks))) {
+              code[0][i] = make_uint4(0u, 0u, 0u, 0u);
+              scl[0][i] = 0;
+            }
+            const uint32_t c4[4] = {code[0][i].x, code[0][i].y, code[0][i].z, code[0][i].w};
+            const uint32_t s2 = e4m3x2_to_f16x2(scl[0][i]);
+            const uint32_t row = tile + (dq >> 1) * T::kRegion + tr * 128;
+            const int c8 = (dq & 1) * 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // eight dims: one 16-byte chunk of the swizzled f16 row
+              const uint32_t sp = __byte_perm(s2, s2, j < 2 ? 0x1010 : 0x3232);
+              uint32_t h[4];
+              e2m1x8_to_f16x2(c4[j], h);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) h[e] = mul_f16x2(h[e], sp);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((c8 + j) ^ (tr & 7)) << 4)), "r"(h[0]),
+                           "r"(h[1]), "r"(h[2]), "r"(h[3])
+                           : "memory");
+            }
+            code[0][i] = code[1][i];
+            scl[0][i] = scl[1][i];
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_ready + 8 * (s & 1));
+        if (lane == 0) {
+          mbar_arrive(bar_ready + 8 * (s & 1));
+          mbar_arrive(bar_raw_empty + 8 * slot);
+        }
       }
     }
     __syncwarp();
