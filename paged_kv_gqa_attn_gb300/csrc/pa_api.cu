@@ -187,13 +187,20 @@ int visible_context(const Window& w, int max_context_len, int q_len, int align) 
   return pages * 16 < max_context_len ? (int)(pages * 16) : max_context_len;
 }
 
-// The split of the rows kernel and of the window forms, N pages a (sequence, kv head) at most, `units` of
-// those, `slots` resident CTAs.  A CTA's start and end cost what `fixed` pages cost.
+// The split of the rows kernel and of the window forms: `units` (sequence, kv head) pairs of N pages at most,
+// `slots` resident CTAs.  Costs in pages of one CTA's work: `fixed` a CTA's start and end, `join` a merge at
+// all, `merge` each partition it joins.
+struct SplitCost {
+  double fixed, join, merge;
+};
 //   Ragged contexts (no window; half of N on average): work shrinks to N units / 2 slots + P fixed units / 2
 //   slots + the last CTA's N / P of which half overlaps: least at P = sqrt(N slots / (units fixed)).
-//   Windows (every sequence near N): P that makes ceil(units P / slots) (N / P + fixed) + P merge least.
-// Measured at 4 to 512 units (4-bit, fixed = 38): the formula's P is within 3 % of the best of a sweep.
-void plan_rows(bool windowed, int64_t units, int64_t slots, int64_t pages, double fixed, double merge, int align, int* ppp,
+//   Windows (every sequence near N): the P that makes
+//     ceil(units P / slots) (N / P + fixed) + (P > 1: join + P merge)
+//   least.
+// Measured over 8 to 2048 units and 17 to 2048 pages of each cache type: within 10 % of the best of a sweep
+// over P, mostly within 3 %.
+void plan_rows(bool windowed, int64_t units, int64_t slots, int64_t pages, const SplitCost& cost, int align, int* ppp,
                int* nparts) {
   if (pages < 1) pages = 1;
   int64_t P = 1;
@@ -201,16 +208,18 @@ void plan_rows(bool windowed, int64_t units, int64_t slots, int64_t pages, doubl
   if (forced > 0) {
     P = forced;
   } else if (windowed) {
-    double best = 0.;
-    for (int64_t c = 1; c <= kAutoMaxPartitions; ++c) {
-      const double t = (double)((units * c + slots - 1) / slots) * ((double)pages / c + fixed) + merge * c;
-      if (c == 1 || t < best) {
+    double best = (double)((units + slots - 1) / slots) * (pages + cost.fixed);
+    for (int64_t c = 2; c <= kAutoMaxPartitions; ++c) {
+      const double merge = cost.join + cost.merge * c;
+      if ((double)(units * c) / slots * cost.fixed + merge > best) break;  // this much only grows with c
+      const double t = (double)((units * c + slots - 1) / slots) * ((double)pages / c + cost.fixed) + merge;
+      if (t < best) {
         best = t;
         P = c;
       }
     }
   } else {
-    const double x = (double)pages * slots / ((double)units * fixed);
+    const double x = (double)pages * slots / ((double)units * cost.fixed);
     while ((P + 1) * (P + 1) <= x && P < kAutoMaxPartitions) ++P;
   }
   if (P > pages) P = pages;
@@ -309,9 +318,11 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
       const int rows = l.group * q_len;
       const int per_sm = few_rows ? pa::rows_resident_ctas(rows) : mma_decode && !l.fp8 ? 6 : mma_decode ? 4 : 2;
       const bool bf16 = kv_dtype == PA_KV_BF16;
-      const double fixed = few_rows && win.window > 0 && rows > 8 ? 60. : bf16 && mma_decode ? 20. : 38.;
+      SplitCost cost = {38., 14., 1.5};
+      if (bf16) cost = {mma_decode ? 20. : 38., 12., 1.2};  // a page of twice the bytes or more
+      if (few_rows && win.window > 0 && rows > 8) cost.fixed = 60.;
       plan_rows(win.window > 0, (int64_t)num_seqs * num_kv_heads, (int64_t)dev->num_sms * per_sm,
-                ((int64_t)covered + block_size - 1) / block_size, fixed, bf16 ? 1.2 : 0.5, align, &ppp, &nparts);
+                ((int64_t)covered + block_size - 1) / block_size, cost, align, &ppp, &nparts);
     } else {
       st = paged_attn_plan(dev->num_sms, num_seqs, num_kv_heads, covered, block_size, q_len, kv_dtype, &ppp, &nparts);
       if (st != PA_OK) return st;
@@ -356,10 +367,10 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
 }
 
 int run_prefill(const Window& win, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
-                       const int32_t* context_lens, const int32_t* query_start_loc, int num_seqs, int total_q,
-                       int max_q_len, int max_blocks_per_seq, int num_blocks, int max_context_len, int num_q_heads,
-                       int num_kv_heads, int head_dim, int block_size, float scale, int kv_dtype,
-                       const float* k_scale, const float* v_scale, void* out, void* stream) {
+                const int32_t* context_lens, const int32_t* query_start_loc, int num_seqs, int total_q, int max_q_len,
+                int max_blocks_per_seq, int num_blocks, int max_context_len, int num_q_heads, int num_kv_heads,
+                int head_dim, int block_size, float scale, int kv_dtype, const float* k_scale, const float* v_scale,
+                void* out, void* stream) {
   if (!q || !k_cache || !v_cache || !block_table || !context_lens || !query_start_loc || !out)
     return PA_ERR_INVALID_ARG;
   if (num_seqs < 0 || total_q < 0 || max_q_len < 1 || max_blocks_per_seq < 1 || num_blocks < 1 ||
@@ -513,7 +524,7 @@ int paged_attn_plan(int num_sms, int num_seqs, int num_kv_heads, int max_context
   const int64_t units = (int64_t)(num_seqs > 0 ? num_seqs : 1) * num_kv_heads;
   if (kv_dtype == PA_KV_FP4_E2M1 && block_size > 0) {  // the rows kernel's rule, one n-tile
     plan_rows(false, (int64_t)(num_seqs > 0 ? num_seqs : 1) * num_kv_heads, (int64_t)num_sms * pa::rows_resident_ctas(1),
-              ((int64_t)max_context_len + block_size - 1) / block_size, 38., 0.5, 1, pages_per_partition, max_partitions);
+              ((int64_t)max_context_len + block_size - 1) / block_size, {38., 14., 1.5}, 1, pages_per_partition, max_partitions);
     return PA_OK;
   }
   const int64_t target = (int64_t)(kv_dtype == PA_KV_FP8_E4M3 ? kCtasPerSmTargetE4M3 : kCtasPerSmTarget) * num_sms;
