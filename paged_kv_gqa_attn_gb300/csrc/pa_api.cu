@@ -319,7 +319,7 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
       const int per_sm = few_rows ? pa::rows_resident_ctas(rows) : mma_decode && !l.fp8 ? 6 : mma_decode ? 4 : 2;
       const bool bf16 = kv_dtype == PA_KV_BF16;
       SplitCost cost = {38., 14., 1.5};
-      if (bf16) cost = {mma_decode ? 20. : 38., 12., 1.2};  // a page of twice the bytes or more
+      if (bf16) cost = {mma_decode ? 20. : 38., 8., 1.2};  // a page of twice the bytes or more
       if (few_rows && win.window > 0 && rows > 8) cost.fixed = 60.;
       plan_rows(win.window > 0, (int64_t)num_seqs * num_kv_heads, (int64_t)dev->num_sms * per_sm,
                 ((int64_t)covered + block_size - 1) / block_size, cost, align, &ppp, &nparts);
