@@ -257,6 +257,8 @@ def _kv_dtype(k_cache, v_cache, head_dim, k_scale, v_scale):
     _check_cuda("v_cache", v_cache, _E4M3)
     _check_cuda("k_scale", k_scale, _F32)
     _check_cuda("v_scale", v_scale, _F32)
+    if k_cache.dim() == 4 and min(k_scale.numel(), v_scale.numel()) < k_cache.shape[0] * k_cache.shape[1]:
+        raise ValueError("k_scale / v_scale must be [num_blocks, num_kv_heads]")  # (per-head ones are the 4-bit cache's)
     return PA_KV_FP8_E4M3
 
 

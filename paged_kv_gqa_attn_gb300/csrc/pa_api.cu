@@ -346,7 +346,7 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
     }
     // 2-D TMA maps of the pools (bf16: 16 x 64-dim boxes; E4M3: one 16 x d box per page)
     CUtensorMap tk = {}, tv = {};
-    int r1 = PA_OK, r2 = PA_OK;  // (4-bit pages move as plain bulk copies)
+    int r1 = PA_OK, r2 = PA_OK;  // (4-bit pages need no map: 16-byte cp.async pieces)
     if (!fp4) {
       r1 = l.fp8 ? encode_e4m3_pool_map(&tk, k_cache, num_blocks, num_kv_heads, block_size, head_dim)
                  : encode_pool_map(&tk, k_cache, num_blocks, num_kv_heads, block_size, head_dim);

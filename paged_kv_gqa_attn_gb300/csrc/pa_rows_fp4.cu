@@ -4,7 +4,7 @@
 namespace pa {
 
 cudaError_t rows_fp4_form(const AttnParams& p, const Launch& l) {
-  const CUtensorMap none = {};  // 4-bit pages move as plain bulk copies
+  const CUtensorMap none = {};  // 4-bit pages move as 16-byte cp.async pieces
   const bool win = p.window > 0;
   if (l.head_dim == 128)
     return win ? rows_tiles<128, kKvFp4, true>(p, l, none, none) : rows_tiles<128, kKvFp4, false>(p, l, none, none);

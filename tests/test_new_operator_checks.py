@@ -135,3 +135,15 @@ def test_plan_of_4_bit_pages():
     # few contexts are cut finely, many coarsely
     assert pa.plan(152, 1, 8, 8208, kv_dtype=pa.PA_KV_FP4_E2M1)[1] > 16
     assert pa.plan(152, 512, 8, 2048, kv_dtype=pa.PA_KV_FP4_E2M1)[1] == 1
+
+
+def test_an_e4m3_cache_takes_no_per_head_scales(monkeypatch):
+    # the check of the scales' size alone: the tensors are on the host, where the device check would refuse
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(pa, "_check_cuda", lambda name, t, dtypes: None)
+    cache = torch.zeros(5, 2, 16, 128, dtype=torch.uint8)
+    per_page, per_head = torch.ones(5, 2), torch.ones(2)
+    assert pa._kv_dtype(cache, cache, 128, per_page, per_page) == pa.PA_KV_FP8_E4M3
+    for scales in ((per_head, per_head), (per_page, per_head), (per_head, per_page)):
+        with pytest.raises(ValueError, match="num_blocks"):
+            pa._kv_dtype(cache, cache, 128, *scales)
