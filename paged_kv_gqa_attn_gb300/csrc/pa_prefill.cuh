@@ -205,14 +205,14 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
   const int nparts = SPLIT ? (span.count + ppp - 1) / ppp : 1;
   const int nsteps = plast > pfirst ? (plast - pfirst + T::kTP - 1) / T::kTP : 0;
   const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
-  // block-table column of the CTA's page v (-1: past its range, or seen by no row of the tile)
-  auto column = [&](int v) {
-    if (v >= plast) return -1;
+  // block-table column of the CTA's page v; false: past its range, or seen by no row of the tile
+  auto column = [&](int v, int& page) {
+    page = v;
     if constexpr (WIN) {
-      const int page = span.real(v);
-      return page < sink_pages || page >= lo_page ? page : -1;
+      page = span.real(v);
+      return v < plast && (page < sink_pages || page >= lo_page);
     }
-    return v;
+    return v < plast;
   };
   // first token of step s (a step lies on one side of the window's gap)
   auto step_token = [&](int s) { return (WIN ? span.real(pfirst + s * T::kTP) : pfirst + s * T::kTP) * T::kBS; };
@@ -299,9 +299,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     static_assert(2 * kStageFp8 == T::kTile, "fp8 step in the upper half of its f16 tile");
     // block id of page pfirst + s * kTP + (lane & 3) for lanes 0-3 (-1: none, or outside the pool)
     auto step_id = [&](int s, bool flag) {
-      const int page = column(pfirst + s * T::kTP + (lane & 3));
-      int v = -1;
-      if (lane < T::kTP && page >= 0) {
+      int v = -1, page;
+      if (column(pfirst + s * T::kTP + (lane & 3), page) && lane < T::kTP) {
         v = bt[page];
         if (v < 0 || v >= p.num_blocks) {
           if (flag) record_error(p.err, kErrBlockId);
@@ -364,7 +363,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
           const unsigned okm = __ballot_sync(0xffffffffu, step_id(gc, false) >= 0) & ((1u << T::kTP) - 1u);
           const int tok = step_token(gc);
           // token rows [0, rows_ok), but for those between the sinks and the window
-          const int rows_ok = min(n_max - tok, min(T::kTP, plast - pfirst - gc * T::kTP) * T::kBS);
+          const int ps = pfirst + gc * T::kTP;  // (tok is ps's first token but for a window's gap)
+          const int rows_ok = min(n_max - tok + ps * T::kBS, min(ps + T::kTP, plast) * T::kBS) - ps * T::kBS;
           // batches of 32 * kBatch chunks: a batch holds whole token rows, and the f16 write of
           // row t lands on the E4M3 bytes of row t only, so reading the batch before writing it
           // (the warp-wide barrier below) keeps every later batch's bytes intact
@@ -438,9 +438,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     const uint32_t staging = base + T::kOffRaw;
     // block ids of 32 pages (8 steps) in the lanes; -1: no page, or outside the pool
     auto load_ids = [&](int v0) {
-      const int page = column(v0 + lane);
-      int v = -1;
-      if (page >= 0) {
+      int v = -1, page;
+      if (column(v0 + lane, page)) {
         v = bt[page];
         if (v < 0 || v >= p.num_blocks) {
           if (warp == 7) record_error(p.err, kErrBlockId);
@@ -584,9 +583,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     const uint32_t bar_full = is_k ? bar_kfull : bar_vfull;
     const uint32_t bar_free = is_k ? bar_kempty : bar_o_done;
     auto load_ids = [&](int pbase) {
-      const int pg = column(pbase + lane);
-      int v = -1;
-      if (pg >= 0) {
+      int v = -1, pg;
+      if (column(pbase + lane, pg)) {
         v = bt[pg];
         if (v < 0 || v >= p.num_blocks) {
           if (is_k) record_error(p.err, kErrBlockId);
@@ -820,8 +818,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
       for (int pg = 0; pg < T::kTP; ++pg) {
         ksc[pg] = 0.f;
         vsc[pg] = 0.f;
-        const int page = column(pfirst + s * T::kTP + pg);
-        if (page >= 0) {
+        int page;
+        if (column(pfirst + s * T::kTP + pg, page)) {
           const int pb = bt[page];
           if (pb >= 0 && pb < p.num_blocks) okp |= 1u << pg;
         }
@@ -834,8 +832,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     if constexpr (!FP8) {
       unsigned bad = 0;
       for (int pg = pfirst + r; pg < plast; pg += T::kRows) {
-        const int col = column(pg);
-        if (WIN && col < 0) continue;
+        int col;
+        if (!column(pg, col)) continue;
         const int pb = bt[col];
         bad |= (pb < 0 || pb >= p.num_blocks) ? 1u : 0u;
       }
@@ -864,8 +862,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     auto load_ids = [&](int s, int (&ids)[T::kTP]) {
 #pragma unroll
       for (int pg = 0; pg < T::kTP; ++pg) {
-        const int page = column(pfirst + s * T::kTP + pg);
-        ids[pg] = page >= 0 ? bt[page] : -1;
+        int page;
+        ids[pg] = column(pfirst + s * T::kTP + pg, page) ? bt[page] : -1;
       }
     };
     auto scales_of = [&](const int (&ids)[T::kTP], float (&ksc)[T::kTP], float (&vsc)[T::kTP]) {
