@@ -32,7 +32,7 @@
 // 4-bit caches: an eighth warp stages a step's pages (codes and scales) ahead, warp 4 turns K and warp 5 V into
 // the f16 tiles (code * scale is exact in f16).  No scale belongs to a page: the head's K scale is part of
 // the row's score factor and its V scale of the epilogue's, so the softmax runs the bf16 form's raw-score
-// path.  2 x 1024 new tokens behind up to 16384: 621 us (bf16 pages 512): the conversions' stores and the
+// path.  2 x 1024 new tokens behind up to 16384: 614 us (bf16 pages 512): the conversions' stores and the
 // products' operand reads fill most of the shared memory's cycles, and the converting warps slow the softmax
 // warps of their sub-partitions.
 // Sliding window with sinks (WIN): the tile's pages are the sinks' and those from its first row's
