@@ -10,8 +10,9 @@ namespace {
 // heaviest tiles start first and the light ones fill the tail).  One CTA: per-sequence checks,
 // a histogram of step counts, its exclusive scan from the top, a scatter.  tiles[0] = number of
 // pairs, tiles[1 + k] = b | tile << 16.
-// WIN is a parameter because the loop over a sequence's tiles is one thread's: the window's step count as a
-// branch in it cost the dense call 2 us (4 chunks of 2048: 6.7 -> 8.7 us).
+// Up to 32 threads share a sequence's tiles where there are few sequences (4 chunks of 2048: 6.3 -> 4.5 us;
+// one thread walked 64 tiles), and the window's step count is a variant of its own (as a branch it cost the
+// dense call 2 us of 6.7).
 constexpr int kCostBuckets = 8192;
 
 template <bool WIN>
@@ -24,6 +25,8 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnParams p, 
   if (tid == 0) total = 0;
   __syncthreads();
   const int Tt = tiles_per_row;
+  int share = 1;  // threads that share a sequence's tiles
+  while (share < 32 && p.num_seqs <= 512 / share) share *= 2;
   auto seq_info = [&](int b, int& QL, int& first_new) {
     const int qs = p.query_start_loc[b];
     QL = p.query_start_loc[b + 1] - qs;
@@ -45,11 +48,11 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnParams p, 
       steps = (page_span((n_max + 15) / 16, max(0, first_new + t * Tt + 1 - p.window), p.sinks, 4).count + 3) / 4;
     return kCostBuckets - 1 - min(steps, kCostBuckets - 1);  // order index: costliest first
   };
-  for (int b = tid; b < p.num_seqs; b += 1024) {
+  for (int b = tid / share; b < p.num_seqs; b += 1024 / share) {
     int QL, first_new;
     seq_info(b, QL, first_new);
     const int nt = (QL + Tt - 1) / Tt;
-    for (int t = 0; t < nt; ++t) atomicAdd(&hist[cost(QL, first_new, t)], 1);
+    for (int t = tid % share; t < nt; t += share) atomicAdd(&hist[cost(QL, first_new, t)], 1);
   }
   __syncthreads();
   // exclusive scan of the histogram (8 buckets per thread)
@@ -86,11 +89,11 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnParams p, 
   }
   if (tid == 1023) total = run;
   __syncthreads();
-  for (int b = tid; b < p.num_seqs; b += 1024) {
+  for (int b = tid / share; b < p.num_seqs; b += 1024 / share) {
     int QL, first_new;
     seq_info(b, QL, first_new);
     const int nt = (QL + Tt - 1) / Tt;
-    for (int t = 0; t < nt; ++t) {
+    for (int t = tid % share; t < nt; t += share) {
       const int pos = atomicAdd(&hist[cost(QL, first_new, t)], 1);
       tiles[1 + pos] = b | (t << 16);
     }
