@@ -171,7 +171,7 @@ int paged_attn_tree_verify(const void* q, const void* k_cache, const void* v_cac
  * Other arguments as paged_attn_decode.  Limits: bf16 or E4M3 KV (E4M3: k_scale / v_scale
  * required; pages converted exactly to f16 in shared memory, products in f16 with Q rows
  * re-encoded as in paged_attn_verify), head_dim 64 or 128, block_size 16, num_q_heads /
- * num_kv_heads in {1, 2, 4, 8}.  Device-side: a sequence whose rows fall outside
+ * num_kv_heads in {1, 2, 4, 8}, at most 65536 sequences.  Device-side: a sequence whose rows fall outside
  * [0, total_q) or exceed max_q_len is skipped and flagged; rows that see no token (context
  * shorter than the new rows) come out as zeros and are flagged (PA_ERR_DEVICE_BOUNDS from
  * paged_attn_check_device_errors).  Asynchronous on `stream`; its work list (4 bytes per

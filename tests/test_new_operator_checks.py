@@ -127,6 +127,16 @@ def test_window_prefill_checks():
     assert fn(*lead, 5, 2, 0.1, 4, None, None, FAKE, None) == pa.PA_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("kv", [0, 2])
+def test_prefill_takes_at_most_65536_sequences(kv):
+    # the planner packs a sequence and a tile into one word; no rows, so that no accepted call reaches a GPU
+    lib = pa.load_library()
+    for seqs, status in ((65536, pa.PA_OK), (65537, pa.PA_ERR_UNSUPPORTED)):
+        lead = [FAKE] * 6 + [seqs, 0, 1, 4, 8, 64, 8, 2, 128, 16]
+        assert lib.paged_attn_window_prefill(*lead, 5, 2, 0.1, kv, None, None, FAKE, None) == status
+        assert lib.paged_attn_prefill(*lead, 0.1, kv, None, None, FAKE, None) == status
+
+
 def test_plan_of_4_bit_pages():
     pa.set_max_partitions(0)
     for units_b, pages in ((1, 513), (16, 257), (64, 2048), (256, 100), (1, 1)):
