@@ -43,6 +43,7 @@
 
 #include "pa_fp4.cuh"
 #include "pa_kernels.h"
+#include "pa_stage_ring.h"
 #include "pa_tc.cuh"
 
 namespace pa {
@@ -65,13 +66,14 @@ struct PfTraits {
   static constexpr int kOffQ = kOffV + 2 * kTile;
   static constexpr int kOffBar = kOffQ + kQBytes;
   // kfull[2], vfull[2], kempty[2], o_done[2], s_ready[2], p_ready[2], q_ready, final, and for
-  // E4M3 and 4-bit caches kready[2], vready[2] (tile converted to f16), raw_full[3], raw_empty[3] (4-bit:
-  // staged pages landed, and read)
-  static constexpr int kNumBars = 24;
+  // E4M3 and 4-bit caches kready[2], vready[2] (tile converted to f16), and the staging ring's (4-bit:
+  // staged pages landed, and read); an even number keeps kOffRaw 16-byte aligned
+  static constexpr int kNumBars = (18 + StageRing::kFullBars + StageRing::kEmptyBars + 1) / 2 * 2;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem base, abort flag
-  static constexpr int kOffRaw = kOffMisc + 16;            // 4-bit: three slots for a step's K or V pages as they came
+  static constexpr int kOffRaw = kOffMisc + 16;            // 4-bit: slots for a step's K or V pages as they came
+  static_assert(kOffRaw % 16 == 0, "bulk copies land on 16-byte boundaries");
   static constexpr int smem(int kv) {                      // + slack for 1024-byte alignment
-    return kOffRaw + (kv == kKvFp4 ? 3 * kTP * Fp4Page<D>::kBytes : 0) + 1024;
+    return kOffRaw + (kv == kKvFp4 ? StageRing::kSlots * kTP * Fp4Page<D>::kBytes : 0) + 1024;
   }
   static constexpr int kSCol = 0;                          // S/P buffer j: columns 64 j ..
   static constexpr int kOCol = 128;
@@ -166,8 +168,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
   const uint32_t bar_final = bar_q_ready + 8;    // every MMA issued has completed
   const uint32_t bar_kready = bar_final + 8;     // E4M3: + 8 * stage: K tile converted to f16
   const uint32_t bar_vready = bar_kready + 16;   // E4M3: + 8 * stage: V tile converted to f16
-  const uint32_t bar_raw_full = bar_vready + 16;     // 4-bit: + 8 * slot: a step's K or V pages staged
-  const uint32_t bar_raw_empty = bar_raw_full + 24;  // 4-bit: + 8 * slot: and taken into registers
+  const uint32_t bar_raw_full = bar_vready + 16;     // 4-bit: + 8 * full_bar(use): a step's K or V pages staged
+  const uint32_t bar_raw_empty = bar_raw_full + 8 * StageRing::kFullBars;  // + 8 * empty_bar(use): and read
   uint32_t* misc = reinterpret_cast<uint32_t*>(gbase + T::kOffMisc);
   volatile uint32_t* abort_flag = misc + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -246,11 +248,10 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
       mbar_init(bar_kready + 8 * s, 1);
       mbar_init(bar_vready + 8 * s, kKDirect ? 2 : 1);  // head_dim 128: both producer warps convert V
     }
-    if constexpr (FP4)
-      for (int s = 0; s < 3; ++s) {
-        mbar_init(bar_raw_full + 8 * s, 1);
-        mbar_init(bar_raw_empty + 8 * s, 1);
-      }
+    if constexpr (FP4) {
+      for (int s = 0; s < StageRing::kFullBars; ++s) mbar_init(bar_raw_full + 8 * s, 1);
+      for (int s = 0; s < StageRing::kEmptyBars; ++s) mbar_init(bar_raw_empty + 8 * s, 1);
+    }
     mbar_init(bar_q_ready, 4);
     mbar_init(bar_final, 1);
     *abort_flag = 0u;
@@ -430,8 +431,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     __syncwarp();
   } else if (FP4 && warp != 6 && warp >= 4) {
     // ======== 4-bit producers.  Warp 7 stages a step's K pages, then its V pages, by bulk copies into a ring
-    // of three such slots, so copies run ahead of warp 4, which converts K, and warp 5, which converts V: each
-    // writes the f16 tile once QK (PV) of the step two before is done, and gives the slot back.  (Staged in the tile's own space, or one step ahead only,
+    // of three such slots (StageRing), so copies run ahead of warp 4, which converts K, and warp 5, which converts
+    // V: each writes the f16 tile once QK (PV) of the step two before is done, and gives the slot back.  (Staged in the tile's own space, or one step ahead only,
     // the copies' latency was in every step: 651-840 us where this takes 621.)
     using P = Fp4Page<D>;
     constexpr uint32_t kSlot = T::kTP * P::kBytes;
@@ -464,9 +465,11 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           if (lane == 0 && go) {
-            const int slot = u % 3;
-            const uint32_t bar = bar_raw_full + 8 * slot;
-            if (u >= 3) go = wait_or_abort(bar_raw_empty + 8 * slot, (u / 3 - 1) & 1, abort_flag, p.err);
+            const int slot = StageRing::slot(u);
+            const uint32_t bar = bar_raw_full + 8 * StageRing::full_bar(u);
+            if (u >= StageRing::kSlots)
+              go = wait_or_abort(bar_raw_empty + 8 * StageRing::empty_bar(u), StageRing::empty_parity(u), abort_flag,
+                                 p.err);
             if (go) {
               if (npg == 0) {
                 mbar_arrive(bar);
@@ -487,7 +490,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
       }
       // every copy started has landed before the CTA's shared memory can go away
       if (lane == 0)
-        for (int k = max(0, u - 3); k < u; ++k) mbar_wait(bar_raw_full + 8 * (k % 3), (k / 3) & 1);
+        for (int k = max(0, u - StageRing::kSlots); k < u; ++k)
+          mbar_wait(bar_raw_full + 8 * StageRing::full_bar(k), StageRing::full_parity(k));
     } else {
       const bool is_k = warp == 4;
       const uint32_t ring = is_k ? sK : sV;
@@ -503,9 +507,10 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
       constexpr int kRowsPer = 32 / kUnitsRow;  // token rows of one unit of all lanes
       for (int s = 0; s < nsteps; ++s) {
         if (s % 8 == 0) ids = load_ids(pfirst + s * T::kTP);
-        const int u = 2 * s + (is_k ? 0 : 1), slot = u % 3;
+        const int u = StageRing::use(s, !is_k), slot = StageRing::slot(u);
         bool go = true;
-        if (lane == 0) go = wait_or_abort(bar_raw_full + 8 * slot, (u / 3) & 1, abort_flag, p.err);
+        if (lane == 0)
+          go = wait_or_abort(bar_raw_full + 8 * StageRing::full_bar(u), StageRing::full_parity(u), abort_flag, p.err);
         if (!__shfl_sync(0xffffffffu, go, 0)) break;
         if (lane == 0 && s >= 2) go = wait_or_abort(bar_free + 8 * (s & 1), ((s - 2) >> 1) & 1, abort_flag, p.err);
         if (!__shfl_sync(0xffffffffu, go, 0)) break;
@@ -570,7 +575,7 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar_ready + 8 * (s & 1));
-          mbar_arrive(bar_raw_empty + 8 * slot);
+          mbar_arrive(bar_raw_empty + 8 * StageRing::empty_bar(u));
         }
       }
     }
