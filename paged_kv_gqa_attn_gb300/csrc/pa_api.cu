@@ -8,6 +8,7 @@
 
 #include "paged_attn.h"
 #include "pa_kernels.h"
+#include "pa_work_item.h"
 
 // Per-device error word written by the kernels (see pa::kErr*).
 __device__ unsigned int g_pa_error_word;
@@ -388,8 +389,9 @@ int run_prefill(const Window& win, const void* q, const void* k_cache, const voi
   if (block_size != 16 || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
   if (group != 1 && group != 2 && group != 4 && group != 8) return PA_ERR_UNSUPPORTED;
   if ((int64_t)num_seqs * num_kv_heads > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
-  if (num_seqs > 65536) return PA_ERR_UNSUPPORTED;  // a work item is sequence | tile << 16
-  if (((int64_t)max_q_len + 128 / group - 1) / (128 / group) > 65535) return PA_ERR_UNSUPPORTED;  // tile < 2^16
+  // what a work item holds
+  if (num_seqs > pa::kWorkSeqs) return PA_ERR_UNSUPPORTED;
+  if (((int64_t)max_q_len + 128 / group - 1) / (128 / group) > pa::kWorkTiles) return PA_ERR_UNSUPPORTED;
   if ((int64_t)num_seqs * ((max_q_len + 128 / group - 1) / (128 / group)) * num_kv_heads > 0x7fffffffLL)
     return PA_ERR_UNSUPPORTED;  // one CTA per (tile, kv head)
   // TMA row coordinates are signed 32-bit

@@ -9,7 +9,7 @@ namespace {
 // (longest-processing-time order: the block scheduler hands out CTAs in blockIdx order, so the
 // heaviest tiles start first and the light ones fill the tail).  One CTA: per-sequence checks,
 // a histogram of step counts, its exclusive scan from the top, a scatter.  tiles[0] = number of
-// pairs, tiles[1 + k] = b | tile << 16.
+// pairs, tiles[1 + k] = work_item(b, tile).
 // Up to 32 threads share a sequence's tiles where there are few sequences (4 chunks of 2048: 6.3 -> 4.5 us;
 // one thread walked 64 tiles), and the window's step count is a variant of its own (as a branch it cost the
 // dense call 2 us of 6.7).
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnParams p, 
     const int nt = (QL + Tt - 1) / Tt;
     for (int t = tid % share; t < nt; t += share) {
       const int pos = atomicAdd(&hist[cost(QL, first_new, t)], 1);
-      tiles[1 + pos] = b | (t << 16);
+      tiles[1 + pos] = work_item(b, t);
     }
   }
   if (tid == 0) tiles[0] = total;

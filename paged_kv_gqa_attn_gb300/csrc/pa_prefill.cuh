@@ -45,6 +45,7 @@
 #include "pa_kernels.h"
 #include "pa_stage_ring.h"
 #include "pa_tc.cuh"
+#include "pa_work_item.h"
 
 namespace pa {
 namespace {
@@ -147,9 +148,9 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     const int rank = (int)(blockIdx.x / (unsigned)Hkv);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the work list comes from the planner
     if (rank >= tiles[0]) return;                       // fewer tiles than the grid's bound (uniform)
-    const int entry = tiles[1 + rank];
-    b = entry & 0xffff;
-    tile = entry >> 16;
+    const int32_t item = tiles[1 + rank];
+    b = work_seq(item);
+    tile = work_tile(item);
     qs = p.query_start_loc[b];
     QL = p.query_start_loc[b + 1] - qs;
   }
