@@ -880,7 +880,10 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
         okp |= (v ? 1u : 0u) << pg;
         const size_t at = (size_t)(v ? ids[pg] : 0) * Hkv + g;
         ksc[pg] = p.k_scale[at];
-        vsc[pg] = p.v_scale[at];
+        // a page that is not there must not lend a weight of 0 the scale of whatever lies in block 0, which may
+        // be a NaN (K's scale only meets scores that the mask replaces)
+        const float vs = p.v_scale[at];
+        vsc[pg] = v ? vs : 1.f;
       }
       return okp;
     };
