@@ -24,8 +24,8 @@
 // becomes the B fragment of P^T with one movmatrix.trans per 8 tokens.
 //
 // Softmax weights: E4M3 weights are f16 with each page's V scale folded in as an added
-// log2|scale| (and its sign), so that they stay in (0, 2^kTau] for any scale and the running sum
-// takes exp2(score - max) without it; each page's K scale multiplies its scores.  bf16 weights
+// log2|scale| (and its sign; fold_v_scale), so that they stay in (0, 2^kTau] for any scale and the
+// running sum takes exp2(score - max) without it; each page's K scale multiplies its scores.  bf16 weights
 // are a bf16 high part plus the rounded remainder (another bf16 column of the n-tile for G <= 4,
 // a second P.V pass for G = 8): ~16 significant bits.  The running maximum is refreshed (three
 // shuffles per column, the outputs rescaled) only when some score passes it by more than kTau.
@@ -246,6 +246,7 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
 #pragma unroll
   for (int i = 0; i < T::kMTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  float lv_top = kVFoldMin;
 
   int k_done = 0;
   bool timed_out = false;
@@ -307,20 +308,17 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
       }
 
       // ---- online softmax: sc[0] / sc[1] = token gi, columns 2qi / 2qi+1; sc[2] / sc[3] = token gi+8 ----
-      float ksc = p.scale_log2, lv = 0.f, rvs = 1.f;
-      uint32_t neg = 0u;
+      float ksc = p.scale_log2;
+      VScaleFold vf = {0.f, 1.f, 0u};
       if constexpr (FP8) {
         const int o32 = k - wb;  // k is in [wb, wb + 32) here
         const float ks = __shfl_sync(0xffffffffu, ksw0, o32);
-        const float vs = __shfl_sync(0xffffffffu, vsw0, o32);
-        lv = __log2f(fmaxf(fabsf(vs), 0x1p-100f));
-        rvs = fast_exp2(-lv);
-        neg = vs < 0.f ? 0x80008000u : 0u;
+        vf = fold_v_scale(__shfl_sync(0xffffffffu, vsw0, o32), lv_top);
         ksc *= ks;
       }
       const float ksc0 = FP8 ? ksc * qdiv0 : ksc, ksc1 = FP8 ? ksc * qdiv1 : ksc;
-      float x0 = fmaf(sc[0], ksc0, lv), x1 = fmaf(sc[1], ksc1, lv);
-      float x2 = fmaf(sc[2], ksc0, lv), x3 = fmaf(sc[3], ksc1, lv);
+      float x0 = fmaf(sc[0], ksc0, vf.lv), x1 = fmaf(sc[1], ksc1, vf.lv);
+      float x2 = fmaf(sc[2], ksc0, vf.lv), x3 = fmaf(sc[3], ksc1, vf.lv);
       if (!whole) {
         if (!sees(gi)) x0 = x1 = -INFINITY;
         if (!sees(gi + 8)) x2 = x3 = -INFINITY;
@@ -334,10 +332,10 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
         }
         const float n0 = fmaxf(m0, lm0), n1 = fmaxf(m1, lm1);
         const float a0 = fast_exp2(m0 - n0), a1 = fast_exp2(m1 - n1);
+        l0 = FP8 ? scale_exp2(l0, m0 - n0) : l0 * a0;
+        l1 = FP8 ? scale_exp2(l1, m1 - n1) : l1 * a1;
         m0 = n0;
         m1 = n1;
-        l0 *= a0;
-        l1 *= a1;
 #pragma unroll
         for (int i = 0; i < T::kMTiles; ++i) {
           o[i][0] *= a0;
@@ -348,13 +346,13 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
       }
       const float p0 = fast_exp2(x0 - m0), p1 = fast_exp2(x1 - m1);
       const float p2 = fast_exp2(x2 - m0), p3 = fast_exp2(x3 - m1);
-      l0 += (p0 + p2) * rvs;
-      l1 += (p1 + p3) * rvs;
+      l0 += (p0 + p2) * vf.rvs;
+      l1 += (p1 + p3) * vf.rvs;
       // B fragments of P^T: b0 = tokens 2qi, 2qi+1 of column gi, b1 = tokens 2qi+8, 2qi+9
       uint32_t b0, b1, b0l = 0u, b1l = 0u;
       if constexpr (FP8) {
-        b0 = movmatrix_trans(pack_f16(p0, p1) ^ neg);
-        b1 = movmatrix_trans(pack_f16(p2, p3) ^ neg);
+        b0 = movmatrix_trans(pack_f16(p0, p1) ^ vf.neg);
+        b1 = movmatrix_trans(pack_f16(p2, p3) ^ vf.neg);
       } else if constexpr (T::kLowPass) {
         b0 = movmatrix_trans(pack_bf16(p0, p1));
         b1 = movmatrix_trans(pack_bf16(p2, p3));
@@ -471,7 +469,7 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
     if (h1 < G) *reinterpret_cast<float2*>(wacc + (warp * G + h1) * D + dd) = make_float2(o[i][1], o[i][3]);
   }
   __syncthreads();
-  store_partition<G, D, T::kWarps>(p, wacc, wm, wl, b, g, part, nparts);
+  store_partition<G, D, T::kWarps, FP8>(p, wacc, wm, wl, b, g, part, nparts);
 }
 
 template <int D, int G, bool FP8, bool WIN>

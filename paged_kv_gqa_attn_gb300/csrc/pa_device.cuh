@@ -156,6 +156,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// l * 2^x for x down to -252: a row sum whose maximum moved by more than a float's exponents (E4M3 page scales
+// are part of the maximum, but not of the sum).
+__device__ __forceinline__ float scale_exp2(float l, float x) {
+  const float h = fast_exp2(0.5f * x);
+  return l * h * h;
+}
+
 union F2U {
   float2 f;
   unsigned long long u;
@@ -214,7 +221,7 @@ __device__ __forceinline__ int context_len(const AttnParams& p, int b, bool flag
 // warps left in shared memory (wacc [W][G][D] unnormalised outputs, wm [W][G] running maxima and
 // wl [W][G] sums, base 2) and store either the finished bf16 rows (the sequence has one
 // partition) or the normalised partial output and its log2-sum-exp for the merge kernel.
-template <int G, int D, int W>
+template <int G, int D, int W, bool E4M3 = false>
 __device__ __forceinline__ void store_partition(const AttnParams& p, const float* wacc, const float* wm,
                                                 const float* wl, int b, int g, int part, int nparts) {
   const int Hq = p.num_q_heads;
@@ -228,9 +235,15 @@ __device__ __forceinline__ void store_partition(const AttnParams& p, const float
     if (M != -INFINITY) {
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const float f = fast_exp2(wm[w * G + h] - M);
-        lsum += f * wl[w * G + h];
-        o += f * wacc[(w * G + h) * D + dd];
+        if constexpr (E4M3) {  // as scale_exp2
+          const float half = fast_exp2(0.5f * (wm[w * G + h] - M));
+          lsum += half * (half * wl[w * G + h]);
+          o += half * (half * wacc[(w * G + h) * D + dd]);
+        } else {
+          const float f = fast_exp2(wm[w * G + h] - M);
+          lsum += f * wl[w * G + h];
+          o += f * wacc[(w * G + h) * D + dd];
+        }
       }
       o = o / lsum;
     }

@@ -388,6 +388,7 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
     m[nt][0] = m[nt][1] = -INFINITY;
     l[nt][0] = l[nt][1] = 0.f;
   }
+  float lv_top = kVFoldMin;
 
   int k_done = 0;
   bool timed_out = false;
@@ -459,15 +460,12 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
       }
 
       // ---- online softmax: x[..][0..1] = token gi, columns 2qi, 2qi+1; x[..][2..3] = token gi + 8 ----
-      float ks = 1.f, lv = 0.f, rvs = 1.f;
-      uint32_t neg = 0u;
+      float ks = 1.f;
+      VScaleFold vf = {0.f, 1.f, 0u};
       if constexpr (T::kFp8) {
         const int o32 = k - wb;
         ks = __shfl_sync(0xffffffffu, ksw0, o32);
-        const float vs = __shfl_sync(0xffffffffu, vsw0, o32);
-        lv = __log2f(fmaxf(fabsf(vs), 0x1p-100f));
-        rvs = fast_exp2(-lv);
-        neg = vs < 0.f ? 0x80008000u : 0u;
+        vf = fold_v_scale(__shfl_sync(0xffffffffu, vsw0, o32), lv_top);
       }
       bool need = false;
       float top[NT][2];  // the step's largest score of the thread's columns
@@ -477,7 +475,7 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
         for (int pp = 0; pp < T::kPP; ++pp) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            x[pp][nt][e] = T::kFp8 ? fmaf(x[pp][nt][e], mul[nt][e & 1] * ks, lv) : x[pp][nt][e] * mul[nt][e & 1];
+            x[pp][nt][e] = T::kFp8 ? fmaf(x[pp][nt][e], mul[nt][e & 1] * ks, vf.lv) : x[pp][nt][e] * mul[nt][e & 1];
           if (!whole) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -505,8 +503,11 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
             for (int sh = 4; sh < 32; sh <<= 1) lm = fmaxf(lm, __shfl_xor_sync(0xffffffffu, lm, sh));
             const float n = fmaxf(m[nt][e], lm);
             const float al = n == -INFINITY ? 1.f : fast_exp2(m[nt][e] - n);
+            if constexpr (T::kFp8)
+              l[nt][e] = n == -INFINITY ? 0.f : scale_exp2(l[nt][e], m[nt][e] - n);
+            else
+              l[nt][e] *= al;
             m[nt][e] = n;
-            l[nt][e] *= al;
 #pragma unroll
             for (int i = 0; i < T::kMTiles; ++i) {
               o[nt][i][e] *= al;
@@ -527,16 +528,16 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
           if (!whole)  // a column that has seen nothing yet has no maximum
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = x[pp][nt][e] == -INFINITY ? 0.f : w[e];
-          l[nt][0] += (w[0] + w[2]) * rvs;
-          l[nt][1] += (w[1] + w[3]) * rvs;
+          l[nt][0] += (w[0] + w[2]) * vf.rvs;
+          l[nt][1] += (w[1] + w[3]) * vf.rvs;
           if constexpr (T::kBf16) {
             bf[nt][0] = movmatrix_trans(pack_bf16(w[0], w[1]));
             bf[nt][1] = movmatrix_trans(pack_bf16(w[2], w[3]));
             bl[nt][0] = movmatrix_trans(pack_bf16(bf16_rem(w[0]), bf16_rem(w[1])));
             bl[nt][1] = movmatrix_trans(pack_bf16(bf16_rem(w[2]), bf16_rem(w[3])));
           } else {
-            bf[nt][0] = movmatrix_trans(pack_f16(w[0], w[1]) ^ neg);
-            bf[nt][1] = movmatrix_trans(pack_f16(w[2], w[3]) ^ neg);
+            bf[nt][0] = movmatrix_trans(pack_f16(w[0], w[1]) ^ vf.neg);
+            bf[nt][1] = movmatrix_trans(pack_f16(w[2], w[3]) ^ vf.neg);
           }
         }
 
@@ -628,9 +629,10 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
     if (M != -INFINITY) {
 #pragma unroll
       for (int w = 0; w < T::kWarps; ++w) {
-        const float f = fast_exp2(wm[w * T::kCols + c] - M);
+        const float half = fast_exp2(0.5f * (wm[w * T::kCols + c] - M));  // (E4M3: as scale_exp2)
+        const float f = T::kFp8 ? half * half : fast_exp2(wm[w * T::kCols + c] - M);
         const float4 v = *reinterpret_cast<const float4*>(wacc + (w * T::kCols + c) * D + dd);
-        lsum += f * wl[w * T::kCols + c];
+        lsum += T::kFp8 ? half * (half * wl[w * T::kCols + c]) : f * wl[w * T::kCols + c];
         acc.x += f * v.x;
         acc.y += f * v.y;
         acc.z += f * v.z;
