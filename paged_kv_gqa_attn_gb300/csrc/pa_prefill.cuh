@@ -881,9 +881,9 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
         const size_t at = (size_t)(v ? ids[pg] : 0) * Hkv + g;
         ksc[pg] = p.k_scale[at];
         // a page that is not there must not lend a weight of 0 the scale of whatever lies in block 0, which may
-        // be a NaN (K's scale only meets scores that the mask replaces)
+        // be a NaN, nor the outputs' unit its size (K's scale only meets scores that the mask replaces)
         const float vs = p.v_scale[at];
-        vsc[pg] = v ? vs : 1.f;
+        vsc[pg] = v ? vs : 0.f;
       }
       return okp;
     };
@@ -891,6 +891,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     float m_used = -INFINITY, l = 0.f;
     float ks_next[T::kTP], vs_next[T::kTP];
     unsigned pok_next;
+    // E4M3: O is summed in units of v_unit = 2^v_exp (v_unit_exp); chosen in the first step
+    float v_unit = 0.f, v_exp = 0.f;
     if constexpr (FP8) {
       load_ids(0, ids_next);
       pok_next = scales_of(ids_next, ks_next, vs_next);
@@ -971,15 +973,26 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
       float kmul[T::kTP];
 #pragma unroll
       for (int pg = 0; pg < T::kTP; ++pg) kmul[pg] = FP8 ? ksc[pg] * qdiv * p.scale_log2 : rowmul;
+      // E4M3: the outputs' unit, grown (the same for every row) when a scale passes it
+      float v_shrink = 1.f;
+      if constexpr (FP8) {
+        const float top = max_abs(vsc);
+        if (top >= v_unit * kVUnitTop) {
+          const int e = v_unit_exp(top);
+          if (s > 0) v_shrink = exp2_int(max(-126, (int)v_exp - e));
+          v_exp = (float)e;
+          v_unit = exp2_int(e);
+        }
+      }
       // E4M3 full steps with positive scales stay in raw scores too: the page's max of raw scores
       // times its K multiplier is its scaled max, and each weight is ex2(s * kmul - m + log2
       // vscale), the V scale folded into the exponent's packed FMA, the row sum recovered per page
-      // by dividing by the scale.  The V scales must be at least 2^-60: a folded weight then drops
+      // by the same power.  The V scales must be at least 2^-60 units: a folded weight then drops
       // below the smallest normal float (and out of the row sum) only where the weight itself is
       // under 2^-66; a smaller scale would lose the page's weights from the row sum.
       const bool fraw = FP8 && vis == ~0ull && p.scale_log2 > 0.f &&
                         fminf(fminf(ksc[0], ksc[1]), fminf(ksc[2], ksc[3])) > 0.f &&
-                        fminf(fminf(vsc[0], vsc[1]), fminf(vsc[2], vsc[3])) >= 0x1p-60f;
+                        fminf(fminf(vsc[0], vsc[1]), fminf(vsc[2], vsc[3])) >= fmaxf(v_unit * 0x1p-60f, 0x1p-126f);
       float mxs[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) mxs[j] = -INFINITY;
@@ -1008,18 +1021,18 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
       if (raw) mx *= rowmul;
       const float m_new = fmaxf(m_used, mx);
       const bool need = (m_used != -INFINITY) && (m_new > m_used + 8.f);
-      if (__any_sync(0xffffffffu, need)) {
+      if (__any_sync(0xffffffffu, need) || (FP8 && v_shrink != 1.f)) {
         // the O row is rescaled only once PV(s - 1) has landed in it
         if (!(ok = wait_or_abort(bar_o_done + 8 * ((s - 1) & 1), ((s - 1) >> 1) & 1, abort_flag, p.err))) break;
         tc_fence_after();
-        const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;
+        const float alpha = need ? fast_exp2(m_used - m_new) : 1.f, o_alpha = FP8 ? alpha * v_shrink : alpha;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t rw[32];
           tmem_ld_x32(tO + lane_off + c0, rw);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; ++c) rw[c] = __float_as_uint(__uint_as_float(rw[c]) * alpha);
+          for (int c = 0; c < 32; ++c) rw[c] = __float_as_uint(__uint_as_float(rw[c]) * o_alpha);
           tmem_st_x32(tO + lane_off + c0, rw);
         }
         tmem_wait_st();
@@ -1067,11 +1080,12 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
       const float2 nb2 = make_float2(-basev, -basev);
       float lstep = 0.f;
       if (FP8 && fraw) {
+        const float unit_basev = basev + v_exp;
         // pair c lies in page c / 8; acc[page] sums the weights times the page's V scale
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
           const int pg = c / (T::kBS / 2);
-          const float bias = __log2f(vsc[pg]) - basev;
+          const float bias = __log2f(vsc[pg]) - unit_basev;
           const float2 x = ffma2(make_float2(sc[2 * c], sc[2 * c + 1]), make_float2(kmul[pg], kmul[pg]),
                                  make_float2(bias, bias));
           const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
@@ -1079,8 +1093,14 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
           w[c] = pack_f16(e.x, e.y);
         }
 #pragma unroll
-        for (int pg = 0; pg < T::kTP; ++pg) lstep += (acc[pg].x + acc[pg].y) / vsc[pg];
+        for (int pg = 0; pg < T::kTP; ++pg) lstep = fmaf(acc[pg].x + acc[pg].y, fast_exp2(-__log2f(vsc[pg])), lstep);
+        lstep *= v_unit;
       } else {
+        if constexpr (FP8) {
+          const float down = 1.f / v_unit;
+#pragma unroll
+          for (int pg = 0; pg < T::kTP; ++pg) vsc[pg] *= down;
+        }
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
           const float2 x = ffma2(make_float2(sc[2 * c], sc[2 * c + 1]), sc2, nb2);
@@ -1141,7 +1161,7 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
       ok = wait_or_abort(bar_o_done + 8 * (gl & 1), (gl >> 1) & 1, abort_flag, p.err);
       if (ok) {
         tc_fence_after();
-        const float inv = l > 0.f ? (FP4 ? v_head / l : 1.f / l) : 0.f;
+        const float inv = l > 0.f ? (FP4 ? v_head : FP8 ? v_unit : 1.f) / l : 0.f;
         __nv_bfloat16* dst = p.out + ((size_t)(qs + t) * Hq + h) * D;
         // split sequence: the partition's normalised rows and log2-sum-exp for the merge kernel
         const bool partial = SPLIT && nparts > 1;

@@ -910,6 +910,7 @@ __global__ void __launch_bounds__(160, 2) verify_tc_kernel(const AttnParams p, i
       float ks_next[T::kTP] = {}, vs_next[T::kTP] = {};
       unsigned pok_next = 0;
       if constexpr (FP8) pok_next = step_pages_ok(sg, sg.p0, ks_next, vs_next);
+      int v_unit = 0;  // E4M3: a segment's O is summed in units of 2^v_unit (v_unit_exp)
       while (ok) {
         const int L = context_len(p, sg.b, false);
         const int first_new = L - QL;  // the q_len new tokens start here
@@ -922,6 +923,7 @@ __global__ void __launch_bounds__(160, 2) verify_tc_kernel(const AttnParams p, i
         const bool has_next = xnext < rg.x1 && sg_next.p1 > sg_next.p0;
         float m_used = -INFINITY, l = 0.f;
         const float qdiv = qdiv_next;  // 2^-k of this segment's Q row (E4M3)
+        if constexpr (FP8) v_unit = v_unit_exp(max_abs(vs_next));
         for (int pstep = sg.p0; pstep < sg.p1; pstep += T::kTP, ++gs) {
           const bool last = pstep + T::kTP >= sg.p1;
           const uint32_t tS = tS_of(gs) + lane_off;
@@ -933,6 +935,19 @@ __global__ void __launch_bounds__(160, 2) verify_tc_kernel(const AttnParams p, i
           for (int pg = 0; pg < T::kTP; ++pg) {
             ksc[pg] = ks_next[pg];
             vsc[pg] = vs_next[pg];
+          }
+          // E4M3: the scales in the outputs' unit, which grows (the same for every row) when they outgrow it
+          float v_shrink = 1.f;
+          if constexpr (FP8) {
+            const float top = max_abs(vsc);
+            if (top >= exp2_int(v_unit) * kVUnitTop) {
+              const int e = v_unit_exp(top);
+              v_shrink = exp2_int(max(-126, v_unit - e));
+              v_unit = e;
+            }
+            const float down = exp2_int(-v_unit);
+#pragma unroll
+            for (int pg = 0; pg < T::kTP; ++pg) vsc[pg] *= down;
           }
           if constexpr (!FP8) {
             // the step's page record (written by the K producer when it copied the step's K pages)
@@ -1004,7 +1019,7 @@ __global__ void __launch_bounds__(160, 2) verify_tc_kernel(const AttnParams p, i
           const float m_new = fmaxf(m_used, mx);
           const bool need = row_live && (m_used != -INFINITY) && (m_new > m_used + 8.f);
 
-          if (__any_sync(0xffffffffu, need)) {
+          if (__any_sync(0xffffffffu, need) || (FP8 && v_shrink != 1.f)) {
             // the O row is rescaled only once PV(gs - 1) has landed in it
             if (!(ok = wait_or_abort(bar_o_done + 8 * ((gs - 1) & 1), ((gs - 1) >> 1) & 1, abort_flag, p.err)))
               break;
@@ -1016,7 +1031,8 @@ __global__ void __launch_bounds__(160, 2) verify_tc_kernel(const AttnParams p, i
               tmem_ld_x32(tO + lane_off + c0, raw);
               tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < 32; ++c) raw[c] = __float_as_uint(__uint_as_float(raw[c]) * alpha);
+              for (int c = 0; c < 32; ++c)
+                raw[c] = __float_as_uint(__uint_as_float(raw[c]) * (FP8 ? alpha * v_shrink : alpha));
               tmem_st_x32(tO + lane_off + c0, raw);
             }
             tmem_wait_st();
@@ -1086,7 +1102,7 @@ __global__ void __launch_bounds__(160, 2) verify_tc_kernel(const AttnParams p, i
         const int gl = gs - 1;  // this segment's last step
         if (!(ok = wait_or_abort(bar_o_done + 8 * (gl & 1), (gl >> 1) & 1, abort_flag, p.err))) break;
         tc_fence_after();
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l > 0.f ? (FP8 ? exp2_int(v_unit) : 1.f) / l : 0.f;
         const size_t orow = ((size_t)sg.b * QL + ri) * Hq + sg.g * G + rh;
         // partial slot of this segment (see the header): rows of kv head g, sequence b, CTA c
         const size_t slot = (size_t)sg.g * B + sg.b + blockIdx.x;

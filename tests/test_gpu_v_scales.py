@@ -9,9 +9,15 @@ import paged_kv_gqa_attn_gb300 as pa
 
 pytestmark = pytest.mark.gpu
 
-FORMS = [  # on the warp-level instruction: decode, decode with a window, other groups and verify with a window
+FORMS = [
+    # on the warp-level instruction: decode, decode with a window, other groups and verify with a window
     ("decode", 8, 2, [1] * 4, None), ("decode", 8, 2, [1] * 4, 200),
     ("decode", 6, 2, [1] * 4, 200), ("verify", 8, 2, [5] * 4, 200), ("verify", 8, 1, [4] * 4, 200),
+    # 64-row tiles: verify, decode of other groups
+    ("verify", 8, 2, [5] * 4, None), ("decode", 6, 2, [1] * 4, None),
+    # 128-row tiles: split verify and prefill, without and with a window
+    ("verify", 16, 2, [9] * 4, None), ("verify", 16, 2, [9] * 4, 200),
+    ("prefill", 8, 2, [20, 1, 9, 130], None), ("prefill", 8, 1, [20, 1, 9, 130], 200),
 ]
 
 
