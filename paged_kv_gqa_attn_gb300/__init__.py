@@ -266,12 +266,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _made_for(stream, *outs):
-    """Outputs that a call made itself belong to the current stream's memory: where another stream writes
-    them, the allocator keeps them until that stream is done."""
-    if stream is not None:
-        for t in outs:
-            t.record_stream(stream)
+def _new(shape, like, stream, dtype=torch.bfloat16):
+    """An output that a call makes itself.  It comes from the memory of the stream that writes it: a block of
+    the current stream's could still be read there by work that was queued before it was freed, and the
+    given stream does not wait for that.  The caller's stream, which the output is handed to, is recorded."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
 
 
 _WINDOW_FORMS = {"paged_attn_decode": "paged_attn_window_decode", "paged_attn_verify": "paged_attn_window_verify",
@@ -305,8 +309,7 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
     if (d2 != d and kv != PA_KV_FP4_E2M1) or rows != B or context_lens.shape != (B,):
         raise ValueError("shape mismatch between q, caches, block_table and context_lens")
     if out is None:
-        out = torch.empty_like(q)
-        _made_for(stream, out)
+        out = _new(q.shape, q, stream)
     else:
         _check_cuda("out", out, _BF16)
         if out.shape != q.shape:
@@ -381,8 +384,7 @@ def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, sca
     if (d2 != d and kv != PA_KV_FP4_E2M1) or context_lens.shape != (B,) or query_start_loc.shape != (B + 1,):
         raise ValueError("shape mismatch between q, caches, block_table, context_lens, query_start_loc")
     if out is None:
-        out = torch.empty_like(q)
-        _made_for(stream, out)
+        out = _new(q.shape, q, stream)
     else:
         _check_cuda("out", out, _BF16)
         if out.shape != q.shape:
@@ -465,8 +467,7 @@ def read_kv(k_cache, v_cache, block_table, context_lens, n, *, k_scale=None, v_s
     outs = []
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is None:
-            t = torch.empty((B, n, Hkv, d), dtype=torch.bfloat16, device=k_cache.device)
-            _made_for(stream, t)
+            t = _new((B, n, Hkv, d), k_cache, stream)
         else:
             _check_cuda(name, t, _BF16)
             if t.shape != (B, n, Hkv, d):
@@ -523,14 +524,12 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, *, eps=1e-6, inte
     if q_weight.shape != (d,) or k_weight.shape != (d,) or cos_sin.dim() != 2 or positions.shape != (T,):
         raise ValueError("expected weights [d], cos_sin [max_position, rotary_dim], positions [T]")
     if q_out is None:
-        q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
-        _made_for(stream, q_out)
+        q_out = _new(q_shape, q, stream)
         strides.append(Hq * d)
     else:
         strides.append(_token_stride("q_out", q_out, q_shape))
     if k_out is None:
-        k_out = torch.empty(k_shape, dtype=torch.bfloat16, device=k.device)
-        _made_for(stream, k_out)
+        k_out = _new(k_shape, k, stream)
         strides.append(Hkv * d)
     else:
         strides.append(_token_stride("k_out", k_out, k_shape))
@@ -569,9 +568,9 @@ def spec_accept(p, q, draft_tokens, u_accept, u_sample, *, out_tokens=None, num_
     if u_sample.shape != (B,):
         raise ValueError("u_sample must be [B]")
     if out_tokens is None:
-        out_tokens = torch.empty(B, K + 1, dtype=torch.int32, device=p.device)
+        out_tokens = _new((B, K + 1), p, stream, torch.int32)
     if num_accepted is None:
-        num_accepted = torch.empty(B, dtype=torch.int32, device=p.device)
+        num_accepted = _new((B,), p, stream, torch.int32)
     _check_cuda("out_tokens", out_tokens, _I32)
     _check_cuda("num_accepted", num_accepted, _I32)
     if out_tokens.shape != (B, K + 1) or num_accepted.shape != (B,):
