@@ -390,7 +390,8 @@ def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, sca
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
     if max_q_len is None:
-        qsl = query_start_loc.cpu()
+        with torch.cuda.stream(stream):  # (None: the current one) the stream that the offsets are ready on
+            qsl = query_start_loc.cpu()
         max_q_len = int((qsl[1:] - qsl[:-1]).max()) if B else 1
     max_blocks = int(block_table.shape[1])
     if max_context_len is None:
