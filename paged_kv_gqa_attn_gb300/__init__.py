@@ -199,22 +199,23 @@ class _Here:
 _HERE = _Here()
 
 
-def _one_device(stream, *tensors, **named):
+def _one_device(stream, *tensors, names="", **named):
     """Check that every tensor (and the stream, if one is given) is on one CUDA device and return
     a context that makes it the current device for the call: the library launches on the
-    current device."""
+    current device.  names: the tensors' names in order, for the error."""
     if named:
+        names = " ".join([names, *named])
         tensors += tuple(named.values())
-    index = -1
+    index = None
     for t in tensors:
         if t is not None:
             at = t.get_device()
             if at != index:
-                if index >= 0 or at < 0:
-                    where = [str(x.device) for x in tensors if x is not None]
+                if index is not None or at < 0:
+                    where = {n: str(x.device) for n, x in zip(names.split(), tensors) if x is not None}
                     raise ValueError(f"tensors must be on one CUDA device, got {where}")
                 index = at
-    if index < 0:
+    if index is None:
         raise ValueError("tensors must be on one CUDA device, got none")
     if stream is not None and stream.device.index != index:
         raise ValueError(f"stream is on {stream.device}, tensors on cuda:{index}")
@@ -325,7 +326,8 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
         if tree_mask.shape != (B, q_len):
             raise ValueError("tree_mask must be [B, q_len]")
         mask = (tree_mask.data_ptr(),)
-    with _one_device(stream, q, k_cache, v_cache, block_table, context_lens, tree_mask, out, k_scale, v_scale):
+    with _one_device(stream, q, k_cache, v_cache, block_table, context_lens, tree_mask, out, k_scale, v_scale,
+                     names="q k_cache v_cache block_table context_lens tree_mask out k_scale v_scale"):
         st = getattr(lib, fn_name)(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), *mask,
             B, max_blocks, NB, int(max_context_len), q_len, Hq, Hkv, d, bs, *span,
@@ -397,8 +399,8 @@ def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, sca
     if max_context_len is None:
         max_context_len = max_blocks * bs
     fn_name, span = _window("paged_attn_prefill", window, sinks)
-    with _one_device(stream, q, k_cache, v_cache, block_table, context_lens, query_start_loc, out, k_scale,
-                     v_scale):
+    with _one_device(stream, q, k_cache, v_cache, block_table, context_lens, query_start_loc, out, k_scale, v_scale,
+                     names="q k_cache v_cache block_table context_lens query_start_loc out k_scale v_scale"):
         st = getattr(lib, fn_name)(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
             context_lens.data_ptr(), query_start_loc.data_ptr(), B, total_q, max(1, int(max_q_len)),
@@ -432,7 +434,8 @@ def append_kv(k_new, v_new, k_cache, v_cache, block_table, context_lens, *, k_sc
         k_scale = v_scale = None
     if kv == PA_KV_FP8_E4M3 and (k_scale.shape != (NB, Hkv) or v_scale.shape != (NB, Hkv)):
         raise ValueError("k_scale / v_scale must be [num_blocks, num_kv_heads]")
-    with _one_device(stream, k_new, v_new, k_cache, v_cache, block_table, context_lens, k_scale, v_scale):
+    with _one_device(stream, k_new, v_new, k_cache, v_cache, block_table, context_lens, k_scale, v_scale,
+                     names="k_new v_new k_cache v_cache block_table context_lens k_scale v_scale"):
         st = lib.paged_attn_append_kv(
             k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_table.data_ptr(), context_lens.data_ptr(), B, n_new, int(block_table.shape[1]), NB,
@@ -476,7 +479,8 @@ def read_kv(k_cache, v_cache, block_table, context_lens, n, *, k_scale=None, v_s
         outs.append(t)
     if n == 0 or B == 0:
         return tuple(outs)
-    with _one_device(stream, k_cache, v_cache, block_table, context_lens, k_scale, v_scale, *outs):
+    with _one_device(stream, k_cache, v_cache, block_table, context_lens, k_scale, v_scale, *outs,
+                     names="k_cache v_cache block_table context_lens k_scale v_scale k_out v_out"):
         st = lib.paged_attn_read_kv(
             k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), B, n,
             int(block_table.shape[1]), NB, Hkv, d, bs, kv, _ptr(k_scale), _ptr(v_scale), outs[0].data_ptr(),
@@ -537,7 +541,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, *, eps=1e-6, inte
     if T == 0:
         return q_out, k_out
     max_position, rotary = cos_sin.shape
-    with _one_device(stream, q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out):
+    with _one_device(stream, q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out,
+                     names="q k q_weight k_weight cos_sin positions q_out k_out"):
         st = lib.paged_attn_qk_norm_rope(
             q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), cos_sin.data_ptr(),
             positions.data_ptr(), T, Hq, Hkv, d, rotary, 1 if interleaved else 0, max_position, eps, *strides,
