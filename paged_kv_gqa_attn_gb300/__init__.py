@@ -127,6 +127,12 @@ def load_library(build_if_missing: bool = True, timeline: Optional[bool] = None)
     return _lib
 
 
+def _c_int(v) -> int:
+    """An integer argument as the C int it is passed as: beyond the type, its largest (smallest) value, which the
+    library takes or refuses like any other that large.  (ctypes would keep the low 32 bits.)"""
+    return max(-(1 << 31), min((1 << 31) - 1, int(v)))
+
+
 def status_string(status: int) -> str:
     return load_library().paged_attn_status_string(int(status)).decode()
 
@@ -137,7 +143,7 @@ def version() -> int:
 
 def set_max_partitions(p: int) -> None:
     """Force at most p split-KV partitions per sequence (0 = automatic, 1 = no split)."""
-    st = load_library().paged_attn_set_max_partitions(int(p))
+    st = load_library().paged_attn_set_max_partitions(_c_int(p))
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attn_set_max_partitions")
 
@@ -146,8 +152,8 @@ def plan(num_sms: int, num_seqs: int, num_kv_heads: int, max_context_len: int, b
          q_len: int = 1, kv_dtype: int = PA_KV_BF16):
     """(pages_per_partition, max_partitions) the library chooses for this shape."""
     a, b = ctypes.c_int(0), ctypes.c_int(0)
-    st = load_library().paged_attn_plan(num_sms, num_seqs, num_kv_heads, max_context_len, block_size,
-                                        q_len, kv_dtype, ctypes.byref(a), ctypes.byref(b))
+    shape = map(_c_int, (num_sms, num_seqs, num_kv_heads, max_context_len, block_size, q_len, kv_dtype))
+    st = load_library().paged_attn_plan(*shape, ctypes.byref(a), ctypes.byref(b))
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attn_plan")
     return a.value, b.value
@@ -289,7 +295,7 @@ def _window(fn_name, window, sinks):
         if sinks:
             raise ValueError("sinks need a window: without one every token is visible")
         return fn_name, ()
-    return _WINDOW_FORMS[fn_name], (int(window), int(sinks))
+    return _WINDOW_FORMS[fn_name], (_c_int(window), _c_int(sinks))
 
 
 def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_scale=None,
@@ -330,7 +336,7 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
                      names="q k_cache v_cache block_table context_lens tree_mask out k_scale v_scale"):
         st = getattr(lib, fn_name)(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), *mask,
-            B, max_blocks, NB, int(max_context_len), q_len, Hq, Hkv, d, bs, *span,
+            B, max_blocks, NB, _c_int(max_context_len), q_len, Hq, Hkv, d, bs, *span,
             float(scale), kv, _ptr(k_scale), _ptr(v_scale), out.data_ptr(), _stream_handle(stream))
     if st != PA_OK:
         raise PagedAttnError(st, fn_name)
@@ -403,8 +409,8 @@ def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, sca
                      names="q k_cache v_cache block_table context_lens query_start_loc out k_scale v_scale"):
         st = getattr(lib, fn_name)(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-            context_lens.data_ptr(), query_start_loc.data_ptr(), B, total_q, max(1, int(max_q_len)),
-            max_blocks, NB, int(max_context_len), Hq, Hkv, d, bs, *span, float(scale), kv, _ptr(k_scale),
+            context_lens.data_ptr(), query_start_loc.data_ptr(), B, total_q, max(1, _c_int(max_q_len)),
+            max_blocks, NB, _c_int(max_context_len), Hq, Hkv, d, bs, *span, float(scale), kv, _ptr(k_scale),
             _ptr(v_scale), out.data_ptr(), _stream_handle(stream))
     if st != PA_OK:
         raise PagedAttnError(st, fn_name)
