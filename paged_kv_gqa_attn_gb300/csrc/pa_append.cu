@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(128) append_bf16_kernel(const AppendParams p) 
       if (i < total) v[k] = i < per_side ? ksrc[i] : vsrc[i - per_side];
     }
     const int L = p.context_lens[b];
-    if (L < p.n_new || L > p.max_blocks_per_seq * 16) {  // shorter than the new rows, or past the table
+    if (!context_holds(L, p.n_new, p.max_blocks_per_seq)) {  // shorter than the new rows, or past the table
       if (threadIdx.x == 0) record_error(p.err, kErrShortContext);
       return;
     }
@@ -117,11 +117,11 @@ __global__ void __launch_bounds__(128) append_fp8_kernel(const AppendParams p) {
   const int g = blockIdx.x, b = blockIdx.y;
   const bool is_v = blockIdx.z == 1;
   const int L = p.context_lens[b];
-  const int first = L - p.n_new;
-  if (first < 0 || L > p.max_blocks_per_seq * 16) {
+  if (!context_holds(L, p.n_new, p.max_blocks_per_seq)) {
     if (threadIdx.x == 0) record_error(p.err, kErrShortContext);
     return;
   }
+  const int first = L - p.n_new;
   const __nv_bfloat16* src = is_v ? p.v_new : p.k_new;
   uint8_t* cache = is_v ? p.v_cache : p.k_cache;
   float* scales = is_v ? p.v_scale : p.k_scale;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(128) append_fp4_kernel(const AppendParams p) {
     const float* scales = is_v ? p.v_scale : p.k_scale;
     const float s = scales ? scales[g] : 1.f;
     const int L = p.context_lens[b];
-    if (L < p.n_new || L > p.max_blocks_per_seq * 16) {
+    if (!context_holds(L, p.n_new, p.max_blocks_per_seq)) {
       if (threadIdx.x == 0) record_error(p.err, kErrShortContext);
       return;
     }

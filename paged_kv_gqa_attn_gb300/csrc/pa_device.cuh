@@ -206,15 +206,22 @@ __device__ __forceinline__ void record_error(unsigned* err, unsigned bit) {
   if (err) atomicOr(err, bit);
 }
 
+// Whether a context of L tokens has its last n and ends within its block-table row.  L may be any int: nothing
+// here overflows.
+__device__ __forceinline__ bool context_holds(int L, int n, int max_blocks) {
+  return L >= n && L >= 0 && (L >> 4) + ((L & 15) != 0 ? 1 : 0) <= max_blocks;
+}
+
 // context_lens[b], clamped to the host-side bound the grid and scratch were sized for (a longer
-// context would index past its block-table row); thread 0 of partition 0 flags the clamp.
+// context would index past its block-table row); thread 0 of partition 0 flags the clamp.  A negative
+// length, however large, is no token: differences of it would wrap round.
 __device__ __forceinline__ int context_len(const AttnParams& p, int b, bool flag) {
   int L = p.context_lens[b];
   if (L > p.max_context_len) {
     if (flag) record_error(p.err, kErrShortContext);
     L = p.max_context_len;
   }
-  return L;
+  return max(L, 0);
 }
 
 // Last step of a split-KV partition: combine the per-warp online-softmax states that the CTA's

@@ -28,18 +28,19 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const AttnParams p, 
   int share = 1;  // threads that share a sequence's tiles
   while (share < 32 && p.num_seqs <= 512 / share) share *= 2;
   auto seq_info = [&](int b, int& QL, int& first_new) {
-    const int qs = p.query_start_loc[b];
-    QL = p.query_start_loc[b + 1] - qs;
-    if (qs < 0 || QL < 0 || qs + QL > p.total_q || QL > p.q_len) {
+    const int qs = p.query_start_loc[b], qe = p.query_start_loc[b + 1];
+    if (qs < 0 || qe < qs || qe > p.total_q || qe - qs > p.q_len) {  // (in this order no difference wraps)
       record_error(p.err, kErrBadInput);  // rows outside the packed q: the sequence is skipped
       QL = 0;
+    } else {
+      QL = qe - qs;
     }
     int L = p.context_lens[b];
     if (L > p.max_context_len) {
       record_error(p.err, kErrShortContext);
       L = p.max_context_len;
     }
-    first_new = L - QL;
+    first_new = max(L, 0) - QL;
   };
   auto cost = [&](int QL, int first_new, int t) {
     const int n_max = first_new + min((t + 1) * Tt, QL);

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
 
   // a longer context is flagged by the planner (split: by partition 0 of kv head 0)
   const int L = SPLIT ? context_len(p, b, part == 0 && g == 0 && threadIdx.x == 0)
-                      : min(p.context_lens[b], p.max_context_len);
+                      : max(min(p.context_lens[b], p.max_context_len), 0);
   const int t0 = tile * Tt;
   const int first_new = L - QL;                       // cache position of new token 0
   const int n_max = first_new + min(t0 + Tt, QL);     // tokens the tile's last row sees

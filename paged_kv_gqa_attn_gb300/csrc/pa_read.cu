@@ -18,9 +18,10 @@ __global__ void __launch_bounds__(128) read_kv_kernel(const ReadParams p) {
   const int b = row / p.n, t = row - b * p.n;
   const int per_side = p.num_kv_heads * kC;
   const int L = p.context_lens[b];
-  const int j = L - p.n + t;
+  const bool fits = context_holds(L, 0, p.max_blocks_per_seq);
+  const int j = fits ? L - p.n + t : -1;
   int pb = -1;
-  if (j < 0 || L > p.max_blocks_per_seq * 16) {
+  if (j < 0) {
     if (threadIdx.x == 0) record_error(p.err, kErrShortContext);
   } else {
     pb = p.block_table[(size_t)b * p.max_blocks_per_seq + j / 16];
