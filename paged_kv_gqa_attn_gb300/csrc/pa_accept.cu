@@ -255,6 +255,8 @@ __global__ void __launch_bounds__(kThreads) accept_pick_kernel(const AcceptParam
   const int rej = s_rej;
   int32_t* out = a.out_tokens + (size_t)b * (a.K + 1);
   if (rej < 0) {
+    // (this grid must not end before the scan, although nothing of the scan is used here)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int i = threadIdx.x; i <= a.K; i += blockDim.x) out[i] = -1;
     if (threadIdx.x == 0) {
       a.num_accepted[b] = -1;

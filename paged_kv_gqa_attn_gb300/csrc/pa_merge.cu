@@ -59,16 +59,17 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttnParams p) {
   const int Hq = p.num_q_heads;
   const long rows = (long)p.num_seqs * p.q_len * Hq;
   const long row = (long)blockIdx.x * 4 + warp;  // (b, i, h) flattened
-  if (row >= rows) return;
-  const int b = (int)(row / ((long)p.q_len * Hq));
+  const int b = (int)(min(row, rows - 1) / ((long)p.q_len * Hq));
   const int L = context_len(p, b, false);
-  if (L <= 0) return;
   int npages = (L + 15) / 16;
   if (p.window > 0) npages = page_span(npages, max(0, L - p.q_len + 1 - p.window), p.sinks, p.page_align).count;
-  const int nparts = (npages + p.pages_per_partition - 1) / p.pages_per_partition;
-  if (nparts <= 1) return;  // the attention kernel wrote this row directly
-  // launched as a programmatic dependent of the attention kernel: wait for its partials
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int nparts = L > 0 ? (npages + p.pages_per_partition - 1) / p.pages_per_partition : 0;
+  const bool merges = row < rows && nparts > 1;  // (otherwise the attention kernel wrote the row directly)
+  // Launched as a programmatic dependent of the attention kernel: wait for its partials.  CTA 0 waits even with
+  // nothing to merge, so that this grid never ends before the one it depends on: what comes next on the stream
+  // waits for this grid alone.
+  if (merges || blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!merges) return;
   const float* lse = p.part_lse + row * p.max_partitions;
   const float* po = p.part_o + row * p.max_partitions * D;
 

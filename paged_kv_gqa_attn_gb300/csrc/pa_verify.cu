@@ -1244,6 +1244,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) verify_merge_kernel(const At
   // the planner kernel's copy is read after the wait.
   const bool own_plan = p.num_seqs <= kOwnPlanMax;
   if (own_plan) build_plan(p, own, -1);  // every thread of the CTA takes part
+  // CTA 0 waits for the verify kernel even with nothing to merge, so that this grid never ends before the one it
+  // depends on: what comes next on the stream waits for this grid alone
+  if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows) return;
   const int h = (int)(row % Hq);
   const int i = (int)((row / Hq) % QL);
