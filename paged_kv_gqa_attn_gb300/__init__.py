@@ -150,7 +150,8 @@ def set_max_partitions(p: int) -> None:
 
 def plan(num_sms: int, num_seqs: int, num_kv_heads: int, max_context_len: int, block_size: int = 16,
          q_len: int = 1, kv_dtype: int = PA_KV_BF16):
-    """(pages_per_partition, max_partitions) the library chooses for this shape."""
+    """(pages_per_partition, max_partitions) the library chooses for decode of this shape (4-bit caches: groups
+    of up to 8; q_len other than 1 is refused).  See paged_attn_plan."""
     a, b = ctypes.c_int(0), ctypes.c_int(0)
     shape = map(_c_int, (num_sms, num_seqs, num_kv_heads, max_context_len, block_size, q_len, kv_dtype))
     st = load_library().paged_attn_plan(*shape, ctypes.byref(a), ctypes.byref(b))

@@ -230,6 +230,19 @@ void plan_rows(bool windowed, int64_t units, int64_t slots, int64_t pages, const
   *nparts = (int)((pages + per - 1) / per);
 }
 
+// The kernels that take such a split, their resident CTAs an SM and the cost of one in pages.
+enum class Split { kDecode, kRows, kTiles };  // the decode kernel with a window, the rows kernel, split 128-row tiles
+void plan_split(Split kernel, int kv_dtype, int rows, bool windowed, int num_sms, int64_t units, int64_t pages, int align,
+                int* ppp, int* nparts) {
+  const bool decode = kernel == Split::kDecode, few_rows = kernel == Split::kRows;
+  const bool bf16 = kv_dtype == PA_KV_BF16;
+  const int per_sm = few_rows ? pa::rows_resident_ctas(rows) : !decode ? 2 : kv_dtype == PA_KV_FP8_E4M3 ? 4 : 6;
+  SplitCost cost = {38., 14., 1.5};
+  if (bf16) cost = {decode ? 20. : 38., 8., 1.2};  // a page of twice the bytes or more
+  if (few_rows && windowed && rows > 8) cost.fixed = 60.;
+  plan_rows(windowed, units, (int64_t)num_sms * per_sm, pages, cost, align, ppp, nparts);
+}
+
 int run(Form form, const Window& win, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
         const int32_t* context_lens, const uint32_t* tree_mask, int num_seqs, int max_blocks_per_seq,
         int num_blocks, int max_context_len, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
@@ -315,15 +328,9 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
     int ppp = 0, nparts = 0;
     const int covered = visible_context(win, max_context_len, q_len, align);
     if (few_rows || win.window > 0 || fp4) {
-      // resident CTAs per SM and the cost of one in pages, by kernel
-      const int rows = l.group * q_len;
-      const int per_sm = few_rows ? pa::rows_resident_ctas(rows) : mma_decode && !l.fp8 ? 6 : mma_decode ? 4 : 2;
-      const bool bf16 = kv_dtype == PA_KV_BF16;
-      SplitCost cost = {38., 14., 1.5};
-      if (bf16) cost = {mma_decode ? 20. : 38., 8., 1.2};  // a page of twice the bytes or more
-      if (few_rows && win.window > 0 && rows > 8) cost.fixed = 60.;
-      plan_rows(win.window > 0, (int64_t)num_seqs * num_kv_heads, (int64_t)dev->num_sms * per_sm,
-                ((int64_t)covered + block_size - 1) / block_size, cost, align, &ppp, &nparts);
+      plan_split(mma_decode ? Split::kDecode : few_rows ? Split::kRows : Split::kTiles, kv_dtype, l.group * q_len,
+                 win.window > 0, dev->num_sms, (int64_t)num_seqs * num_kv_heads,
+                 ((int64_t)covered + block_size - 1) / block_size, align, &ppp, &nparts);
     } else {
       st = paged_attn_plan(dev->num_sms, num_seqs, num_kv_heads, covered, block_size, q_len, kv_dtype, &ppp, &nparts);
       if (st != PA_OK) return st;
@@ -509,10 +516,11 @@ extern "C" {
 
 int paged_attn_plan(int num_sms, int num_seqs, int num_kv_heads, int max_context_len, int block_size, int q_len,
                     int kv_dtype, int* pages_per_partition, int* max_partitions) {
-  (void)q_len;
   if (!pages_per_partition || !max_partitions || num_sms < 1 || num_seqs < 0 || num_kv_heads < 1 ||
       max_context_len < 0 || block_size < 1)
     return PA_ERR_INVALID_ARG;
+  // 4-bit verify splits by its rows per kv head, of which the group is no argument here
+  if (kv_dtype == PA_KV_FP4_E2M1 && q_len != 1) return PA_ERR_UNSUPPORTED;
   const int64_t max_pages = ((int64_t)max_context_len + block_size - 1) / block_size;
   const int64_t pages = max_pages > 0 ? max_pages : 1;
   int64_t P;
@@ -525,9 +533,8 @@ int paged_attn_plan(int num_sms, int num_seqs, int num_kv_heads, int max_context
     return PA_OK;
   }
   const int64_t units = (int64_t)(num_seqs > 0 ? num_seqs : 1) * num_kv_heads;
-  if (kv_dtype == PA_KV_FP4_E2M1 && block_size > 0) {  // the rows kernel's rule, one n-tile
-    plan_rows(false, (int64_t)(num_seqs > 0 ? num_seqs : 1) * num_kv_heads, (int64_t)num_sms * pa::rows_resident_ctas(1),
-              ((int64_t)max_context_len + block_size - 1) / block_size, {38., 14., 1.5}, 1, pages_per_partition, max_partitions);
+  if (kv_dtype == PA_KV_FP4_E2M1) {  // the rows kernel, one n-tile (groups of up to 8)
+    plan_split(Split::kRows, kv_dtype, 1, false, num_sms, units, pages, 1, pages_per_partition, max_partitions);
     return PA_OK;
   }
   const int64_t target = (int64_t)(kv_dtype == PA_KV_FP8_E4M3 ? kCtasPerSmTargetE4M3 : kCtasPerSmTarget) * num_sms;
@@ -706,7 +713,7 @@ int paged_attn_qk_norm_rope(const void* q, const void* k, const void* q_weight, 
   if (!(eps >= 0.f) || eps > 3.4e38f) return PA_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
   if (rotary_dim < 16 || rotary_dim > head_dim || rotary_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
-  if (num_q_heads > 65536 || num_kv_heads > 65536) return PA_ERR_UNSUPPORTED;  // grid.y of the kernel
+  if (num_q_heads > 65536 || num_kv_heads > 65536) return PA_ERR_UNSUPPORTED;  // far beyond any model: head indices are ints
   const int64_t q_row = (int64_t)num_q_heads * head_dim, k_row = (int64_t)num_kv_heads * head_dim;
   if (q_stride < q_row || q_out_stride < q_row || k_stride < k_row || k_out_stride < k_row) return PA_ERR_INVALID_ARG;
   // rows are moved in 16-byte pieces
