@@ -91,12 +91,12 @@ def measured_peaks():
 
 # Source files each profiled kernel is built and launched from: a traffic figure stays valid
 # while none of them changes.
-COMMON_SOURCES = ("pa_api.cu", "pa_kernels.h", "pa_device.cuh")
+COMMON_SOURCES = ("pa_api.cu", "pa_kernels.h", "pa_device.cuh", "pa_work_item.h")
 KERNEL_SOURCES = {
     "decode": ("pa_decode.cu", "pa_decode_mma.cu", "pa_mma.cuh", "pa_merge.cu", "pa_tc.cuh") + COMMON_SOURCES,
     "verify": ("pa_verify.cu", "pa_tc.cuh") + COMMON_SOURCES,
-    "prefill": ("pa_prefill.cu", "pa_prefill.cuh", "pa_tc.cuh") + COMMON_SOURCES,
-    "append": ("pa_append.cu",) + COMMON_SOURCES,
+    "prefill": ("pa_prefill.cu", "pa_prefill.cuh", "pa_fp4.cuh", "pa_stage_ring.h", "pa_tc.cuh") + COMMON_SOURCES,
+    "append": ("pa_append.cu", "pa_fp4.cuh") + COMMON_SOURCES,
     "accept": ("pa_accept.cu",) + COMMON_SOURCES,
 }
 
