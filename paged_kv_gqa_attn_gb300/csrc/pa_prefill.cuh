@@ -124,7 +124,7 @@ __device__ __forceinline__ void pf_tl_put(int slot, unsigned long long v) {
 // when the sequence has several partitions, writes the normalised partial rows and their
 // log2-sum-exp for the log-sum-exp merge kernel; p.tree_mask, when set, replaces the causal mask.
 template <int D, bool SPLIT, int KV, bool WIN>
-__global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel(const AttnParams p, const int32_t* __restrict__ tiles,
+__global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel(const AttnParams p, const int32_t* tiles,
                                                             const __grid_constant__ CUtensorMap tmk,
                                                             const __grid_constant__ CUtensorMap tmv) {
   using T = PfTraits<D>;
@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
   } else {
     g = (int)(blockIdx.x % (unsigned)Hkv);
     const int rank = (int)(blockIdx.x / (unsigned)Hkv);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the work list comes from the planner
+    // The work list comes from the planner.  (No __restrict__: a read-only pointer's loads may move above the wait.)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (rank >= tiles[0]) return;                       // fewer tiles than the grid's bound (uniform)
     const int32_t item = tiles[1 + rank];
     b = work_seq(item);

@@ -287,7 +287,7 @@ __device__ __forceinline__ void st_put(int step, int slot) {
 #endif
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(160, 2) verify_tc_kernel(const AttnParams p, int32_t* __restrict__ plan_g,
+__global__ void __launch_bounds__(160, 2) verify_tc_kernel(const AttnParams p, int32_t* plan_g,
                                                            const __grid_constant__ CUtensorMap tmk,
                                                            const __grid_constant__ CUtensorMap tmv) {
   using T = TcTraits<D>;
@@ -1232,7 +1232,7 @@ __global__ void __launch_bounds__(1024) verify_plan_kernel(const AttnParams p, i
 // ranges meet the sequence.
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) verify_merge_kernel(const AttnParams p,
-                                                                        const int32_t* __restrict__ plan, int ncta) {
+                                                                        const int32_t* plan, int ncta) {
   constexpr int kDPL = D / 32;
   __shared__ int32_t own[kOwnPlanMax + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1253,6 +1253,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) verify_merge_kernel(const At
   const int b = (int)(row / ((long long)Hq * QL));
   const int g = h / G;
   const int rr = i * G + (h - g * G);  // row within the kv head's group
+  // (plan has no __restrict__: a read-only pointer's loads may move above the wait)
   if (!own_plan) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (own_plan) plan = own;
   const long long TP = plan[0];

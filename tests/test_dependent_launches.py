@@ -41,6 +41,15 @@ def _with_wait(name):
     return ""
 
 
+def test_what_a_dependent_reads_may_not_move_above_its_wait():
+    # loads through a const __restrict__ pointer count as reads of memory that never changes
+    for f, text in _all_sources().items():
+        for head in re.findall(r"__global__[^{;]*\{", text):
+            name = re.search(r"(\w+_kernel)\(", head)
+            if name and WAIT in _with_wait(name.group(1)):
+                assert "__restrict__" not in head, (f, name.group(1))
+
+
 @pytest.mark.parametrize("name", ["merge_kernel", "verify_merge_kernel", "accept_pick_kernel", "prefill_tc_kernel"])
 def test_no_cta_0_returns_before_it_waits(name):
     body = _with_wait(name)

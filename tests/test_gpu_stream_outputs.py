@@ -61,3 +61,27 @@ def test_outputs_lie_in_the_memory_of_the_stream_that_writes_them():
         assert all(torch.equal(g, w) for g, w in zip(copies, want)), name
         assert all(torch.equal(g, w) for g, w in zip(again, want)), name
     assert pa.check_device_errors() == pa.PA_OK
+
+
+def test_a_given_stream_inside_a_capture():
+    c = A.make("fp4", [900, 70], [5, 5], 8, 2, 128, seed=8)
+    dev = {n: (t.cuda() if torch.is_tensor(t) else t) for n, t in c.items()}
+    lens = torch.tensor(c["lens"], dtype=torch.int32, device="cuda")
+    q = dev["q"].view(2, 5, 8, 128)
+    kw = {"k_scale": dev["k_scale"], "v_scale": dev["v_scale"]}
+    want = pa.verify(q, dev["k"], dev["v"], dev["table"], lens, c["scale"], **kw)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        out = pa.verify(q, dev["k"], dev["v"], dev["table"], lens, c["scale"], stream=side, **kw)
+        here.wait_stream(side)
+        after = out * 1
+    for _ in range(5):
+        out.zero_()
+        after.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(after, want)
+    assert pa.check_device_errors() == pa.PA_OK
