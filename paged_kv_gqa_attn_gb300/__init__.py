@@ -322,6 +322,8 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
         _check_cuda("out", out, _BF16)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
+    if B == 0:  # (an empty tensor has no address)
+        return out
     if max_context_len is None:
         max_context_len = max_blocks * bs  # an upper bound known without reading the device
     span = ()
@@ -398,10 +400,12 @@ def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, sca
         _check_cuda("out", out, _BF16)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
+    if B == 0 or total_q == 0:
+        return out
     if max_q_len is None:
         with torch.cuda.stream(stream):  # (None: the current one) the stream that the offsets are ready on
             qsl = query_start_loc.cpu()
-        max_q_len = int((qsl[1:] - qsl[:-1]).max()) if B else 1
+        max_q_len = int((qsl[1:] - qsl[:-1]).max())
     max_blocks = int(block_table.shape[1])
     if max_context_len is None:
         max_context_len = max_blocks * bs
@@ -441,6 +445,8 @@ def append_kv(k_new, v_new, k_cache, v_cache, block_table, context_lens, *, k_sc
         k_scale = v_scale = None
     if kv == PA_KV_FP8_E4M3 and (k_scale.shape != (NB, Hkv) or v_scale.shape != (NB, Hkv)):
         raise ValueError("k_scale / v_scale must be [num_blocks, num_kv_heads]")
+    if B == 0 or n_new == 0:
+        return
     with _one_device(stream, k_new, v_new, k_cache, v_cache, block_table, context_lens, k_scale, v_scale,
                      names="k_new v_new k_cache v_cache block_table context_lens k_scale v_scale"):
         st = lib.paged_attn_append_kv(
@@ -588,6 +594,8 @@ def spec_accept(p, q, draft_tokens, u_accept, u_sample, *, out_tokens=None, num_
     _check_cuda("num_accepted", num_accepted, _I32)
     if out_tokens.shape != (B, K + 1) or num_accepted.shape != (B,):
         raise ValueError("out_tokens must be [B, K+1] and num_accepted [B]")
+    if B == 0:
+        return num_accepted, out_tokens
     ptr = (lambda t: t.data_ptr() if K > 0 else None)
     with _one_device(stream, p=p, u_sample=u_sample, out_tokens=out_tokens, num_accepted=num_accepted,
                      q=q if K > 0 else None, draft_tokens=draft_tokens if K > 0 else None,
