@@ -317,7 +317,7 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
     if (d2 != d and kv != PA_KV_FP4_E2M1) or rows != B or context_lens.shape != (B,):
         raise ValueError("shape mismatch between q, caches, block_table and context_lens")
     if out is None:
-        out = _new(q.shape, q, stream)
+        out = torch.empty_like(q) if stream is None else _new(q.shape, q, stream)  # (a third of the time of empty)
     else:
         _check_cuda("out", out, _BF16)
         if out.shape != q.shape:
@@ -395,7 +395,7 @@ def prefill(q, k_cache, v_cache, block_table, context_lens, query_start_loc, sca
     if (d2 != d and kv != PA_KV_FP4_E2M1) or context_lens.shape != (B,) or query_start_loc.shape != (B + 1,):
         raise ValueError("shape mismatch between q, caches, block_table, context_lens, query_start_loc")
     if out is None:
-        out = _new(q.shape, q, stream)
+        out = torch.empty_like(q) if stream is None else _new(q.shape, q, stream)  # (a third of the time of empty)
     else:
         _check_cuda("out", out, _BF16)
         if out.shape != q.shape:

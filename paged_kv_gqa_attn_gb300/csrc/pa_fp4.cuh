@@ -2,8 +2,8 @@
 //
 // 16 consecutive dims of one token's head row are 16 E2M1 codes (two a byte, the lower dim in the low
 // nibble) and one E4M3 scale; a code's value is e2m1 * scale * (one fp32 scale per kv head).  A
-// (block, head) page holds the codes of its 16 tokens, then their scales: 9 d bytes, one contiguous
-// piece that a single bulk copy moves.  The scale belongs to the token, so storing a token never
+// (block, head) page holds the codes of its 16 tokens, then their scales: 9 d contiguous bytes, which
+// the tile kernel moves as one bulk copy and the rows kernel as 16-byte cp.async pieces.  The scale belongs to the token, so storing a token never
 // re-encodes its neighbours.  e2m1 * e4m3 has at most six significant bits and lies in
 // [2^-10, 2688]: exact in f16.
 #pragma once

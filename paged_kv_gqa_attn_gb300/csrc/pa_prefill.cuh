@@ -32,7 +32,7 @@
 // 4-bit caches: an eighth warp stages a step's pages (codes and scales) ahead, warp 4 turns K and warp 5 V into
 // the f16 tiles (code * scale is exact in f16).  No scale belongs to a page: the head's K scale is part of
 // the row's score factor and its V scale of the epilogue's, so the softmax runs the bf16 form's raw-score
-// path.  2 x 1024 new tokens behind up to 16384: 614 us (bf16 pages 512): the conversions' stores and the
+// path.  2 x 1024 new tokens behind up to 16384: 614 us (bf16 pages 416): the conversions' stores and the
 // products' operand reads fill most of the shared memory's cycles, and the converting warps slow the softmax
 // warps of their sub-partitions.
 // Sliding window with sinks (WIN): the tile's pages are the sinks' and those from its first row's
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     // ======== 4-bit producers.  Warp 7 stages a step's K pages, then its V pages, by bulk copies into a ring
     // of three such slots (StageRing), so copies run ahead of warp 4, which converts K, and warp 5, which converts
     // V: each writes the f16 tile once QK (PV) of the step two before is done, and gives the slot back.  (Staged in the tile's own space, or one step ahead only,
-    // the copies' latency was in every step: 651-840 us where this takes 621.)
+    // the copies' latency was in every step: 651-840 us where this takes 614.)
     using P = Fp4Page<D>;
     constexpr uint32_t kSlot = T::kTP * P::kBytes;
     const uint32_t staging = base + T::kOffRaw;
