@@ -324,7 +324,7 @@ def prepare(case, seed):
     elif case["op"] == "prefix":
         st["starts"] = torch.tensor(_starts(case), dtype=torch.int32, device=dev)
         st["prefix_lens"] = torch.tensor(_prefixes(case)[0], dtype=torch.int32, device=dev)
-        st["max_prefix"] = max(_prefixes(case)[0])
+        st["max_prefix"], st["max_own"] = max(_prefixes(case)[0]), case["own_max"]
     else:  # sums of a few hundred steps: a few tokens have most of the weight
         st["weights"] = torch.exp(2.0 * torch.randn(pool, hkv, BLOCK, generator=rng, device=dev))
         if case["op"] == "evict":
@@ -371,7 +371,8 @@ def _run_own(st):
         more["blocks"] = blocks
         out = (blocks,)
     elif c["op"] == "prefix":
-        more |= {"group_starts": st["starts"], "prefix_lens": st["prefix_lens"], "max_prefix_len": st["max_prefix"]}
+        more |= {"group_starts": st["starts"], "prefix_lens": st["prefix_lens"], "max_prefix_len": st["max_prefix"],
+                 "max_own_len": st["max_own"]}
     else:
         more |= {"weights": _sums(st), "decay": c["decay"]}
         out = (more["weights"],)
