@@ -223,6 +223,162 @@ int paged_attn_window_prefill(const void* q, const void* k_cache, const void* v_
                               const float* k_scale, const float* v_scale, void* out, void* stream);
 
 /*
+ * Bounds of the keys of cache blocks, what paged_attn_select_blocks reads in place of the keys: for each
+ * (block, kv head) the largest and the smallest value of every dim over the block's tokens, as int8 codes
+ * times one power of two.
+ *   e            the smallest integer with max|k| 2^-e <= 127 over the block's tokens and dims (at least
+ *                -126; 0 where every key is 0).
+ *   bounds       [num_blocks, num_kv_heads, 2, head_dim] int8, device, 16-byte aligned: ceil(max 2^-e) of every
+ *                dim, then floor(min 2^-e).
+ *   bound_scale  [num_blocks, num_kv_heads] fp32, device: 2^e.
+ * Both are written for every block that holds one of a sequence's last n tokens (context_lens counts them;
+ * n past the context: all of its blocks), from all of the block's stored tokens; the others stay as they are.
+ * A step calls it after paged_attn_append_kv with the same n, a prompt once with its length.  k_cache, kv_dtype and
+ * k_scale as in paged_attn_decode; the key of a scaled cache is its fp32 value (code, times the 16-dim scale of
+ * a 4-bit one, times k_scale: one rounding).  Keys must be finite: a NaN gives way to the block's other tokens, an
+ * infinity to the largest code.  Out-of-range block ids and contexts past the table are skipped and flagged.
+ * Asynchronous on `stream`; never allocates.  Returns PA_OK (also for num_seqs == 0 or n == 0),
+ * PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED or PA_ERR_CUDA.
+ */
+int paged_attn_block_bounds(const void* k_cache, const int32_t* block_table,
+                            const int32_t* context_lens, int num_seqs, int n,
+                            int max_blocks_per_seq, int num_blocks, int num_kv_heads, int head_dim,
+                            int block_size, int kv_dtype, const float* k_scale, int8_t* bounds,
+                            float* bound_scale, void* stream);
+
+/*
+ * The blocks of each sequence that a step's queries should read, by an upper bound of their scores.  A query
+ * row is rounded (to nearest even) to int8 codes c times 2^f by the rule of the bounds, f from the row's largest
+ * |q|; block j's score for it is 2^f 2^e sum_i max(c_i hi_i, c_i lo_i), and its score for a kv head the
+ * largest over the head's rows (every new token, every query head of the group).  The sum is a whole number
+ * below 2^22: the selection does not depend on the order of the arithmetic.
+ *   q            [num_seqs, q_len, num_q_heads, head_dim] bf16, device, 16-byte aligned, finite.
+ *   bounds, bound_scale  as paged_attn_block_bounds writes them, for every block of the contexts.
+ *   count        blocks to select: the first sink_blocks and the last recent_blocks (together at most count)
+ *                whatever their scores, then the highest, ties to the lowest block.  The blocks that hold new
+ *                tokens should be among the recent ones.
+ *   blocks       [num_seqs, num_kv_heads, count] int32, device, written: columns of the block table, ascending, then -1
+ *                where the context has fewer.
+ * Limits: q_len * (num_q_heads / num_kv_heads) at most 32, head_dim 64 or 128, block_size 16.  A block id out of range is
+ * flagged and comes behind every other.  Scratch: 4 bytes per (block, kv head) of max_context_len.  Asynchronous on
+ * `stream`.  Returns PA_OK (also for num_seqs == 0), PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_NO_MEMORY
+ * or PA_ERR_CUDA.
+ */
+int paged_attn_select_blocks(const void* q, const int8_t* bounds, const float* bound_scale,
+                             const int32_t* block_table, const int32_t* context_lens, int num_seqs,
+                             int max_blocks_per_seq, int num_blocks, int max_context_len, int q_len,
+                             int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                             int count, int sink_blocks, int recent_blocks, int32_t* blocks,
+                             void* stream);
+
+/*
+ * Sparse attention over listed blocks: paged_attn_decode and paged_attn_verify in which a row of kv head g sees,
+ * of the tokens that it would see, those of the blocks that blocks[b][g] lists.
+ *   blocks       [num_seqs, num_kv_heads, num_listed] int32, device: columns of the block table in any order, each at
+ *                most once (a column listed twice counts twice); negative entries are unused.  A column past
+ *                the context is skipped and flagged (PA_ERR_DEVICE_BOUNDS).
+ * Blocks that are not listed are neither looked up nor read.  A row whose list holds nothing that it sees comes out as
+ * zeros.  Same arguments and errors otherwise; limits: q_len * (num_q_heads / num_kv_heads) at most 32,
+ * num_listed in [1, 2^26], max_context_len at most 2^30.  Kernels: the decode kernel (decode, groups of 1, 2, 4 and 8, bf16 and
+ * E4M3) and the rows kernel, split over the list.
+ */
+int paged_attn_sparse_decode(const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_table, const int32_t* context_lens,
+                             const int32_t* blocks, int num_seqs, int max_blocks_per_seq,
+                             int num_blocks, int max_context_len, int q_len, int num_listed,
+                             int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                             float scale, int kv_dtype, const float* k_scale, const float* v_scale,
+                             void* out, void* stream);
+int paged_attn_sparse_verify(const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_table, const int32_t* context_lens,
+                             const int32_t* blocks, int num_seqs, int max_blocks_per_seq,
+                             int num_blocks, int max_context_len, int q_len, int num_listed,
+                             int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                             float scale, int kv_dtype, const float* k_scale, const float* v_scale,
+                             void* out, void* stream);
+
+/*
+ * Attention of a batch whose sequences share prefixes (prefix caching: one system prompt, one document, in
+ * the same blocks for many sequences): the results of paged_attn_decode and paged_attn_verify, with the keys
+ * and values of a shared prefix read once for all of its sequences.
+ *   group_starts   [num_groups + 1] int32, device, non-decreasing: sequences group_starts[i] .. group_starts[i + 1]
+ *                  - 1 share a prefix.  Sequences outside every group share nothing.
+ *   prefix_lens    [num_groups] int32, device: tokens that group i shares, rounded down to whole blocks (what is left
+ *                  is read from each sequence's own row).  Those blocks are looked up in the row of the group's first
+ *                  sequence; the other rows' entries for them are not read.
+ *   max_prefix_len host-side bound of prefix_lens, at most max_blocks_per_seq * 16.
+ *   max_own_len    host-side bound of what a sequence has behind its prefix (context_lens[b] - prefix).  Both size grids
+ *                  and scratch only.
+ * The new tokens lie behind the prefix: a sequence with context_lens[b] < prefix + q_len, or with more of its own
+ * than max_own_len, comes out as zeros and is flagged (PA_ERR_DEVICE_BOUNDS).  A prefix longer than its bound is cut to
+ * it and flagged; group offsets that do not fit are flagged, their group shares nothing, and outputs of
+ * sequences that two groups claim are undefined.  Same arguments and errors otherwise; limits: max_context_len at
+ * most 2^30, and the 128-row tiles of all groups (num_seqs * q_len rows of 128 / group tokens, one more a group) at most 65535.
+ * Kernels: the tile kernel of paged_attn_prefill over the rows of all of a group's sequences (the prefix, split into
+ * partitions), the window forms' kernels over the own tokens, one merge.
+ */
+int paged_attn_prefix_decode(const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_table, const int32_t* context_lens,
+                             const int32_t* group_starts, const int32_t* prefix_lens, int num_seqs,
+                             int max_blocks_per_seq, int num_blocks, int max_context_len, int q_len,
+                             int num_groups, int max_prefix_len, int max_own_len, int num_q_heads,
+                             int num_kv_heads, int head_dim, int block_size, float scale,
+                             int kv_dtype, const float* k_scale, const float* v_scale, void* out,
+                             void* stream);
+int paged_attn_prefix_verify(const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_table, const int32_t* context_lens,
+                             const int32_t* group_starts, const int32_t* prefix_lens, int num_seqs,
+                             int max_blocks_per_seq, int num_blocks, int max_context_len, int q_len,
+                             int num_groups, int max_prefix_len, int max_own_len, int num_q_heads,
+                             int num_kv_heads, int head_dim, int block_size, float scale,
+                             int kv_dtype, const float* k_scale, const float* v_scale, void* out,
+                             void* stream);
+
+/*
+ * Decode that also keeps the attention weight each cached token has received: paged_attn_decode, and
+ *   weights[block, g, slot] = decay * weights[block, g, slot] + sum_h softmax(s_h)_j
+ * for every token j of every sequence, h over the query heads of kv head g; the step's own token, j =
+ * context_lens[b] - 1, has no sum yet and its slot is set to its weight.
+ *   weights      [num_blocks, num_kv_heads, 16] fp32, device: caller-owned, laid out as the cache (the sums of a prompt's tokens
+ *                start at what the caller stores, zeros for instance).  Slots past a context are not touched.
+ *   decay        finite; 0 overwrites without reading, 1 adds, less than 1 forgets.
+ * Blocks that two sequences of the call share would get both sums in an undefined order: their sums are undefined.
+ * Same arguments and errors otherwise; limits: num_q_heads / num_kv_heads at most 32, max_context_len at most 2^30.
+ * Scratch: 4 bytes per (query head, token) of num_seqs * max_context_len beside the split's.
+ */
+int paged_attn_weighted_decode(const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_table, const int32_t* context_lens,
+                               float* weights, int num_seqs, int max_blocks_per_seq, int num_blocks,
+                               int max_context_len, int q_len, int num_q_heads, int num_kv_heads,
+                               int head_dim, int block_size, float decay, float scale, int kv_dtype,
+                               const float* k_scale, const float* v_scale, void* out, void* stream);
+
+/*
+ * Eviction by accumulated attention weight: each (sequence, kv head) keeps min(context_lens[b], keep) tokens -- the first
+ * `sinks`, the last `recent` (together at most keep) and the others of the largest sums, ties to the earliest, a NaN
+ * below everything -- and they move in their order, with their sums, to the blocks of new_table.
+ *   k_cache, v_cache, k_scale, v_scale, kv_dtype, block_table, context_lens, max_context_len as in paged_attn_decode
+ *                (4-bit caches: the scales are not used and may be NULL).
+ *   weights      [num_blocks, num_kv_heads, 16] fp32, device, as paged_attn_weighted_decode keeps them.
+ *   new_table    [num_seqs, new_blocks_per_seq] int32, device, new_blocks_per_seq * 16 >= keep: blocks that hold no
+ *                token of any of the call's sequences, each once.  Blocks past the kept tokens are not touched.
+ *   new_lens     [num_seqs] int32, device, written: the new context lengths.
+ * The old blocks are only read, so they may be shared, and the caller gives them back afterwards.  bf16 and 4-bit rows move as they
+ * are; E4M3 pages get the scale amax / 448 of their tokens and are re-encoded as paged_attn_append_kv does.  Different
+ * heads keep different tokens: a slot no longer stands for one position, so attention over what is left uses keys
+ * rotated before (the caller counts positions on its own).  Out-of-range ids are flagged: a token that cannot be read
+ * counts as sum 0 and becomes zeros, a page that cannot be written is left out.  Scratch: 4 bytes per (kept token, kv
+ * head), and 4 per (token, kv head) where max_context_len exceeds 50000.  Asynchronous on `stream`.  Returns PA_OK
+ * (also for num_seqs == 0), PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_NO_MEMORY or PA_ERR_CUDA.
+ */
+int paged_attn_evict(void* k_cache, void* v_cache, float* weights, const int32_t* block_table,
+                     const int32_t* context_lens, const int32_t* new_table, int num_seqs,
+                     int max_blocks_per_seq, int new_blocks_per_seq, int num_blocks,
+                     int max_context_len, int num_kv_heads, int head_dim, int block_size,
+                     int kv_dtype, float* k_scale, float* v_scale, int keep, int sinks, int recent,
+                     int32_t* new_lens, void* stream);
+
+/*
  * KV append: store the new tokens' K and V in the paged cache, the step that precedes the
  * attention call of each decode or verify step (studybook fde-roadmap ch.10, sections 10.2.2
  * and 10.3.2: the step's K/V join the cache; section 10.12.2 and aegloslab servingai 5.3.7:

@@ -25,6 +25,9 @@ __all__ = [
     "prefill",
     "append_kv",
     "read_kv",
+    "block_bounds",
+    "select_blocks",
+    "evict",
     "qk_norm_rope",
     "spec_accept",
     "check_device_errors",
@@ -106,6 +109,22 @@ def load_library(build_if_missing: bool = True, timeline: Optional[bool] = None)
             lib.paged_attn_append_kv.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P]
             lib.paged_attn_read_kv.restype = I
             lib.paged_attn_read_kv.argtypes = [P, P, P, P, I, I, I, I, I, I, I, I, P, P, P, P, P]
+            for name in ("paged_attn_sparse_decode", "paged_attn_sparse_verify"):
+                fn = getattr(lib, name)
+                fn.restype = I
+                fn.argtypes = attn_args[:5] + [P] + attn_args[5:10] + [I] + attn_args[10:]
+            for name in ("paged_attn_prefix_decode", "paged_attn_prefix_verify"):
+                fn = getattr(lib, name)
+                fn.restype = I
+                fn.argtypes = attn_args[:5] + [P, P] + attn_args[5:10] + [I, I, I] + attn_args[10:]
+            lib.paged_attn_weighted_decode.restype = I
+            lib.paged_attn_weighted_decode.argtypes = attn_args[:5] + [P] + attn_args[5:14] + [F] + attn_args[14:]
+            lib.paged_attn_block_bounds.restype = I
+            lib.paged_attn_block_bounds.argtypes = [P, P, P, I, I, I, I, I, I, I, I, P, P, P, P]
+            lib.paged_attn_select_blocks.restype = I
+            lib.paged_attn_select_blocks.argtypes = [P, P, P, P, P] + [I] * 12 + [P, P]
+            lib.paged_attn_evict.restype = I
+            lib.paged_attn_evict.argtypes = [P] * 6 + [I] * 9 + [P, P] + [I] * 3 + [P, P]
             L = ctypes.c_int64
             lib.paged_attn_qk_norm_rope.restype = I
             lib.paged_attn_qk_norm_rope.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, F, L, L, L, L, P, P, P]
@@ -240,6 +259,7 @@ def _check_cuda(name, t, dtypes):
 
 # (names of the accepted types, made once: every call passes them)
 _BF16, _I32, _F32, _BYTES = (torch.bfloat16,), (torch.int32,), (torch.float32,), (torch.uint8,)
+_I8 = (torch.int8,)
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 
 
@@ -299,8 +319,53 @@ def _window(fn_name, window, sinks):
     return _WINDOW_FORMS[fn_name], (_c_int(window), _c_int(sinks))
 
 
+_EXTRA_FORMS = {
+    "blocks": {"paged_attn_decode": "paged_attn_sparse_decode", "paged_attn_verify": "paged_attn_sparse_verify"},
+    "prefix": {"paged_attn_decode": "paged_attn_prefix_decode", "paged_attn_verify": "paged_attn_prefix_verify"},
+    "weights": {"paged_attn_decode": "paged_attn_weighted_decode"},
+}
+
+
+def _extra(fn_name, shape, cache_shape, max_context_len, blocks, group_starts, prefix_lens, max_prefix_len, max_own_len,
+           weights, decay, window):
+    """The C entry of a call over listed blocks, with shared prefixes or with sums of the weights; its pointers behind
+    the context lengths, its integers behind q_len, its floats before the scale, and the tensors to check the device of."""
+    given = [n for n, t in (("blocks", blocks), ("prefix", group_starts), ("weights", weights)) if t is not None]
+    if window is not None:
+        given.append("window")
+    if len(given) > 1:
+        raise ValueError(f"a call takes one of blocks, group_starts, weights and window, got {given}")
+    if group_starts is None and (prefix_lens is not None or max_prefix_len is not None or max_own_len is not None):
+        raise ValueError("prefix_lens, max_prefix_len and max_own_len need group_starts")
+    if weights is None and decay != 1.0:
+        raise ValueError("decay needs weights")
+    form = given[0]
+    if fn_name not in _EXTRA_FORMS[form]:
+        raise ValueError(f"{fn_name} takes no {form}")
+    name = _EXTRA_FORMS[form][fn_name]
+    B, NB, Hkv = shape[0], cache_shape[0], cache_shape[1]
+    if form == "blocks":
+        _check_cuda("blocks", blocks, _I32)
+        if blocks.dim() != 3 or blocks.shape[:2] != (B, Hkv):
+            raise ValueError("blocks must be [B, num_kv_heads, count]")
+        return name, (blocks.data_ptr(),), (blocks.shape[2],), (), {"blocks": blocks}
+    if form == "prefix":
+        _check_cuda("group_starts", group_starts, _I32)
+        _check_cuda("prefix_lens", prefix_lens, _I32)
+        if group_starts.dim() != 1 or prefix_lens.shape != (group_starts.shape[0] - 1,):
+            raise ValueError("group_starts must be [num_groups + 1] and prefix_lens [num_groups]")
+        bounds = [max_context_len if v is None else v for v in (max_prefix_len, max_own_len)]
+        return (name, (group_starts.data_ptr(), prefix_lens.data_ptr()), (prefix_lens.shape[0], *map(_c_int, bounds)), (),
+                {"group_starts": group_starts, "prefix_lens": prefix_lens})
+    _check_cuda("weights", weights, _F32)
+    if weights.shape != (NB, Hkv, 16):
+        raise ValueError("weights must be [num_blocks, num_kv_heads, 16]")
+    return name, (weights.data_ptr(),), (), (float(decay),), {"weights": weights}
+
+
 def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_scale=None,
-          v_scale=None, max_context_len=None, out=None, stream=None, tree_mask=None, window=None, sinks=0):
+          v_scale=None, max_context_len=None, out=None, stream=None, tree_mask=None, window=None, sinks=0, blocks=None,
+          group_starts=None, prefix_lens=None, max_prefix_len=None, max_own_len=None, weights=None, decay=1.0):
     lib = load_library()
     _check_cuda("q", q, _BF16)
     cache_shape = k_cache.shape
@@ -329,7 +394,12 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
     span = ()
     if window is not None or sinks:
         fn_name, span = _window(fn_name, window, sinks)
+    counts, floats, more = (), (), {}
     mask = ()
+    if not (blocks is group_starts is weights is prefix_lens is max_prefix_len is max_own_len is None) or decay != 1.0:
+        fn_name, mask, counts, floats, more = _extra(fn_name, q.shape, cache_shape, max_context_len, blocks, group_starts,
+                                                     prefix_lens, max_prefix_len, max_own_len, weights, decay, window)
+        _one_device(None, q=q, **more)  # (the check alone: the call's own is below)
     if fn_name == "paged_attn_tree_verify":
         _check_cuda("tree_mask", tree_mask, _I32)
         if tree_mask.shape != (B, q_len):
@@ -339,7 +409,7 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
                      names="q k_cache v_cache block_table context_lens tree_mask out k_scale v_scale"):
         st = getattr(lib, fn_name)(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), *mask,
-            B, max_blocks, NB, _c_int(max_context_len), q_len, Hq, Hkv, d, bs, *span,
+            B, max_blocks, NB, _c_int(max_context_len), q_len, *counts, Hq, Hkv, d, bs, *span, *floats,
             float(scale), kv, _ptr(k_scale), _ptr(v_scale), out.data_ptr(), _stream_handle(stream))
     if st != PA_OK:
         raise PagedAttnError(st, fn_name)
@@ -348,15 +418,19 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
 
 def decode(q, k_cache, v_cache, block_table, context_lens, scale, **kw):
     """Single-token paged GQA decode; q [B, 1, Hq, d] bf16.  With window=W (and sinks=S) the token sees
-    the last W tokens, itself included, and the first S.  See paged_attn_decode,
-    paged_attn_window_decode."""
+    the last W tokens, itself included, and the first S.  With blocks [B, Hkv, count] int32 each kv head
+    reads the listed blocks only (select_blocks).  With group_starts [n + 1] and prefix_lens [n] int32 the
+    sequences of a group share their first tokens' blocks, which are read once (max_prefix_len and max_own_len: host-side
+    bounds of the shared and the own tokens).  With weights [NB, Hkv, 16] fp32 the step's softmax weights join the sums
+    kept there, in place: decay * sum + weight.  One of the four a call.  See paged_attn_decode,
+    paged_attn_window_decode, paged_attn_sparse_decode, paged_attn_prefix_decode, paged_attn_weighted_decode."""
     return _call("paged_attn_decode", q, k_cache, v_cache, block_table, context_lens, scale, **kw)
 
 
 def verify(q, k_cache, v_cache, block_table, context_lens, scale, **kw):
     """(K+1)-row causal speculative-verify attention; q [B, K+1, Hq, d] bf16.  window and sinks as in
-    decode, each row's window ending at its own token.  See paged_attn_verify,
-    paged_attn_window_verify."""
+    decode, each row's window ending at its own token; blocks, group_starts and prefix_lens as in decode.  See
+    paged_attn_verify, paged_attn_window_verify, paged_attn_sparse_verify, paged_attn_prefix_verify."""
     return _call("paged_attn_verify", q, k_cache, v_cache, block_table, context_lens, scale, **kw)
 
 
@@ -364,8 +438,9 @@ def tree_verify(q, k_cache, v_cache, block_table, context_lens, tree_mask, scale
     """Verify over a tree of drafts: tree_mask int32 [B, q_len] ancestor bitmasks over the new
     tokens (bit t of row i: row i sees new token t).  It takes no window.  See
     paged_attn_tree_verify."""
-    if kw.get("window") is not None:
-        raise ValueError("tree_verify takes no window")
+    for name in ("window", "blocks", "group_starts", "weights"):
+        if kw.get(name) is not None:
+            raise ValueError(f"tree_verify takes no {name}")
     return _call("paged_attn_tree_verify", q, k_cache, v_cache, block_table, context_lens, scale,
                  tree_mask=tree_mask, **kw)
 
@@ -501,6 +576,131 @@ def read_kv(k_cache, v_cache, block_table, context_lens, n, *, k_scale=None, v_s
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attn_read_kv")
     return tuple(outs)
+
+
+def block_bounds(k_cache, block_table, context_lens, n, bounds, bound_scale, *, k_scale=None, stream=None):
+    """Bounds of the keys of every block that holds one of a sequence's last n tokens, in place: bounds [NB, Hkv, 2, d]
+    int8 and bound_scale [NB, Hkv] fp32, what select_blocks reads.  Called after append_kv with the same n, or
+    once for a prompt with its length.  k_cache and k_scale of any cache type.  See paged_attn_block_bounds."""
+    lib = load_library()
+    _check_cuda("bounds", bounds, _I8)
+    _check_cuda("bound_scale", bound_scale, _F32)
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or bounds.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("expected k_cache [NB, Hkv, bs, d], bounds [NB, Hkv, 2, d] and block_table [B, M]")
+    NB, Hkv, bs, last = k_cache.shape
+    d = bounds.shape[3]
+    # (the value cache's checks are the key cache's: there is none here)
+    fp4 = k_cache.dtype is torch.uint8 and 16 * last == 9 * d
+    kv = _kv_dtype(k_cache, k_cache, d, k_scale, k_scale)
+    _check_cuda("block_table", block_table, _I32)
+    _check_cuda("context_lens", context_lens, _I32)
+    B, n = block_table.shape[0], int(n)
+    if (last != d and not fp4) or bounds.shape != (NB, Hkv, 2, d) or bound_scale.shape != (NB, Hkv) \
+            or context_lens.shape != (B,) or n < 0:
+        raise ValueError("shape mismatch between k_cache, bounds, bound_scale, block_table, context_lens and n")
+    if kv == PA_KV_BF16:
+        k_scale = None
+    if B == 0 or n == 0:
+        return
+    with _one_device(stream, k_cache=k_cache, block_table=block_table, context_lens=context_lens, k_scale=k_scale,
+                     bounds=bounds, bound_scale=bound_scale):
+        st = lib.paged_attn_block_bounds(
+            k_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), B, _c_int(n), block_table.shape[1], NB, Hkv, d,
+            bs, kv, _ptr(k_scale), bounds.data_ptr(), bound_scale.data_ptr(), _stream_handle(stream))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attn_block_bounds")
+
+
+def select_blocks(q, bounds, bound_scale, block_table, context_lens, count, *, sink_blocks=1, recent_blocks=2,
+                  max_context_len=None, out=None, stream=None):
+    """The `count` blocks of each sequence and kv head that the rows q [B, q_len, Hq, d] bf16 score highest by the
+    bounds of block_bounds, the first sink_blocks and last recent_blocks always among them: int32 [B, Hkv, count], columns
+    of the block table, ascending, -1 where there are fewer.  For decode(blocks=) and verify(blocks=).  See
+    paged_attn_select_blocks."""
+    lib = load_library()
+    _check_cuda("q", q, _BF16)
+    _check_cuda("bounds", bounds, _I8)
+    _check_cuda("bound_scale", bound_scale, _F32)
+    _check_cuda("block_table", block_table, _I32)
+    _check_cuda("context_lens", context_lens, _I32)
+    if q.dim() != 4 or bounds.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("expected q [B, q_len, Hq, d], bounds [NB, Hkv, 2, d] and block_table [B, M]")
+    B, q_len, Hq, d = q.shape
+    NB, Hkv = bounds.shape[:2]
+    count = int(count)
+    if bounds.shape != (NB, Hkv, 2, d) or bound_scale.shape != (NB, Hkv) or block_table.shape[0] != B \
+            or context_lens.shape != (B,):
+        raise ValueError("shape mismatch between q, bounds, bound_scale, block_table and context_lens")
+    if count < 1:
+        raise ValueError("count must be at least 1")
+    if out is None:
+        out = _new((B, Hkv, count), q, stream, torch.int32)
+    else:
+        _check_cuda("out", out, _I32)
+        if out.shape != (B, Hkv, count):
+            raise ValueError("out must be [B, num_kv_heads, count]")
+    if B == 0:
+        return out
+    if max_context_len is None:
+        max_context_len = block_table.shape[1] * 16
+    with _one_device(stream, q=q, bounds=bounds, bound_scale=bound_scale, block_table=block_table,
+                     context_lens=context_lens, out=out):
+        st = lib.paged_attn_select_blocks(
+            q.data_ptr(), bounds.data_ptr(), bound_scale.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), B,
+            block_table.shape[1], NB, _c_int(max_context_len), q_len, Hq, Hkv, d, 16, _c_int(count), _c_int(sink_blocks),
+            _c_int(recent_blocks), out.data_ptr(), _stream_handle(stream))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attn_select_blocks")
+    return out
+
+
+def evict(k_cache, v_cache, weights, block_table, context_lens, new_table, keep, *, sinks=0, recent=0, k_scale=None,
+          v_scale=None, max_context_len=None, head_dim=None, new_lens=None, stream=None):
+    """Keep of every sequence and kv head the first `sinks` tokens, the last `recent` and, up to `keep` in all, those of
+    the largest sums in weights [NB, Hkv, 16] fp32 (decode(weights=)); they move in order, with their sums, to the
+    blocks of new_table [B, M2] int32, which must hold no token of the batch.  Returns the new lengths [B] int32; the old blocks
+    stay as they are for the caller to give back.  head_dim as in read_kv.  See paged_attn_evict."""
+    lib = load_library()
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or k_cache.shape != v_cache.shape \
+            or block_table.dim() != 2 or new_table.dim() != 2:
+        raise ValueError("expected caches [NB, Hkv, bs, d], block_table [B, M] and new_table [B, M2]")
+    NB, Hkv, bs, last = k_cache.shape
+    if head_dim is None:
+        head_dim = {36: 64, 72: 128}.get(last, last) if k_cache.dtype == torch.uint8 else last
+    d = int(head_dim)
+    kv = _kv_dtype(k_cache, v_cache, d, k_scale, v_scale)
+    _check_cuda("weights", weights, _F32)
+    _check_cuda("block_table", block_table, _I32)
+    _check_cuda("context_lens", context_lens, _I32)
+    _check_cuda("new_table", new_table, _I32)
+    B = block_table.shape[0]
+    if context_lens.shape != (B,) or new_table.shape[0] != B or weights.shape != (NB, Hkv, 16) \
+            or (last != d and kv != PA_KV_FP4_E2M1):
+        raise ValueError("shape mismatch between caches, weights, block_table, context_lens, new_table and head_dim")
+    if kv == PA_KV_FP8_E4M3 and (k_scale.shape != (NB, Hkv) or v_scale.shape != (NB, Hkv)):
+        raise ValueError("k_scale / v_scale must be [num_blocks, num_kv_heads]")
+    if kv == PA_KV_BF16:
+        k_scale = v_scale = None
+    if new_lens is None:
+        new_lens = _new((B,), k_cache, stream, torch.int32)
+    else:
+        _check_cuda("new_lens", new_lens, _I32)
+        if new_lens.shape != (B,):
+            raise ValueError("new_lens must be [B]")
+    if B == 0:
+        return new_lens
+    if max_context_len is None:
+        max_context_len = block_table.shape[1] * bs
+    with _one_device(stream, k_cache=k_cache, v_cache=v_cache, weights=weights, block_table=block_table,
+                     context_lens=context_lens, new_table=new_table, new_lens=new_lens, k_scale=k_scale, v_scale=v_scale):
+        st = lib.paged_attn_evict(
+            k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(),
+            new_table.data_ptr(), B, block_table.shape[1], new_table.shape[1], NB, _c_int(max_context_len), Hkv, d, bs, kv,
+            _ptr(k_scale), _ptr(v_scale), _c_int(keep), _c_int(sinks), _c_int(recent), new_lens.data_ptr(),
+            _stream_handle(stream))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attn_evict")
+    return new_lens
 
 
 def _token_stride(name, t, heads_dims):

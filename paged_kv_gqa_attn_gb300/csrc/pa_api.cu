@@ -243,15 +243,55 @@ void plan_split(Split kernel, int kv_dtype, int rows, bool windowed, int num_sms
   plan_rows(windowed, units, (int64_t)num_sms * per_sm, pages, cost, align, ppp, nparts);
 }
 
+// What a form other than a window's needs beside the ordinary arguments.
+struct Extra {
+  int form = pa::kFormAll;
+  const int32_t* blocks = nullptr;  // kFormBlocks
+  int num_listed = 0;
+  const int32_t* group_starts = nullptr;  // kFormOwn
+  const int32_t* prefix_lens = nullptr;
+  int num_groups = 0, max_prefix_len = 0, max_own_len = 0;
+  float* weights = nullptr;  // kFormScores
+  float decay = 0.f;
+};
+
+// The arguments of those forms; the kernels' position arithmetic is 32-bit, as with a window.
+int check_extra(const Extra& x, Form form, int num_seqs, int max_blocks_per_seq, int max_context_len, int q_len,
+                int num_q_heads, int num_kv_heads) {
+  const int rows = num_kv_heads > 0 && q_len <= 16 ? num_q_heads / num_kv_heads * q_len : 0;
+  if (x.form == pa::kFormBlocks) {
+    if (!x.blocks || x.num_listed < 1) return PA_ERR_INVALID_ARG;
+    if (x.num_listed > (1 << 26) || rows > pa::kRowsMax) return PA_ERR_UNSUPPORTED;
+  } else if (x.form == pa::kFormOwn) {
+    if (x.num_groups < 0 || x.max_prefix_len < 0 || x.max_own_len < 0) return PA_ERR_INVALID_ARG;
+    if (x.num_groups > 0 && (!x.group_starts || !x.prefix_lens)) return PA_ERR_INVALID_ARG;
+    if ((int64_t)x.max_prefix_len > (int64_t)max_blocks_per_seq * 16) return PA_ERR_INVALID_ARG;
+    if (x.num_groups > 65535) return PA_ERR_UNSUPPORTED;
+    if (rows > 0 && rows <= 128 && num_seqs >= 0 && num_seqs <= 65535 && x.num_groups > 0 &&
+        pa::prefix_tiles(num_seqs, q_len, num_q_heads / num_kv_heads, x.num_groups) > 65535)
+      return PA_ERR_UNSUPPORTED;  // a grid dimension
+  } else {
+    if (!x.weights || !(x.decay >= -3.4e38f && x.decay <= 3.4e38f)) return PA_ERR_INVALID_ARG;
+    if (rows > pa::kRowsMax) return PA_ERR_UNSUPPORTED;
+  }
+  return max_context_len > (1 << 30) ? PA_ERR_UNSUPPORTED : PA_OK;
+}
+
+size_t round_up(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
 int run(Form form, const Window& win, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
         const int32_t* context_lens, const uint32_t* tree_mask, int num_seqs, int max_blocks_per_seq,
         int num_blocks, int max_context_len, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
         int block_size, float scale, int kv_dtype, const float* k_scale, const float* v_scale, void* out,
-        void* stream) {
+        void* stream, const Extra& x = Extra()) {
   int st = validate(form, q, k_cache, v_cache, block_table, context_lens, num_seqs, max_blocks_per_seq,
                     num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim, block_size,
                     kv_dtype, k_scale, v_scale, out);
   if (st != PA_OK) return st;
+  if (x.form != pa::kFormAll) {
+    st = check_extra(x, form, num_seqs, max_blocks_per_seq, max_context_len, q_len, num_q_heads, num_kv_heads);
+    if (st != PA_OK) return st;
+  }
   if (num_seqs == 0) return PA_OK;
   DeviceState* dev = nullptr;
   st = device_state(&dev);
@@ -284,6 +324,7 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
   l.fp8 = kv_dtype == PA_KV_FP8_E4M3;
   l.kv = kv_dtype;
   l.stream = s;
+  l.form = x.form != pa::kFormAll ? x.form : win.window > 0 ? pa::kFormWindow : pa::kFormAll;
 
   cudaError_t e;
   void* scratch = nullptr;
@@ -295,13 +336,16 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
   // 4-bit caches, and the window forms but decode's, take the rows kernel up to its 32 rows per kv head and
   // the split prefill kernel beyond; bf16 pages, which cost neither a conversion, only up to 16 (32
   // sequences of up to 2048 + 16 visible tokens, 8 kv heads: 12 rows 49 / 55 us, 20 rows 59 / 55, 32 rows
-  // 77 / 54; E4M3 44 / 87, 51 / 86, 60 / 80; 4-bit, 8192 tokens: 79 / 152, 95 / 154, 125 / 150).
+  // 77 / 54; E4M3 44 / 87, 51 / 86, 60 / 80; 4-bit, 8192 tokens: 79 / 152, 95 / 154, 125 / 150).  The forms
+  // over listed blocks and with kept scores, which the tile kernel has not, take the rows kernel up to its 32 rows.
   const bool mma_group = l.group == 1 || l.group == 2 || l.group == 4 || l.group == 8;
   const bool fp4 = kv_dtype == PA_KV_FP4_E2M1;
   const bool mma_decode = form == Form::kDecode && mma_group && !fp4;
-  const bool few_rows = !mma_decode && (win.window > 0 || fp4) &&
-                        l.group * q_len <= (kv_dtype == PA_KV_BF16 ? pa::kRowsMaxBf16 : pa::kRowsMax);
-  const bool split_tiles = !mma_decode && !few_rows && (l.group * q_len > 64 || win.window > 0 || fp4);
+  const bool special = l.form != pa::kFormAll;  // (a window among them)
+  const bool rows_only = l.form == pa::kFormBlocks || l.form == pa::kFormScores;
+  const bool few_rows = !mma_decode && (special || fp4) &&
+                        l.group * q_len <= (kv_dtype == PA_KV_BF16 && !rows_only ? pa::kRowsMaxBf16 : pa::kRowsMax);
+  const bool split_tiles = !mma_decode && !few_rows && (l.group * q_len > 64 || special || fp4);
   const bool on_tensor_cores = !mma_decode && !few_rows && !split_tiles;
   const int align = split_tiles ? 4 : 1;  // the split prefill kernel walks whole 64-token steps
   set_window(&p, win, max_context_len, align);
@@ -325,12 +369,39 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
     }
     e = (r1 == PA_OK && r2 == PA_OK) ? pa::launch_verify_tc(p, l, scratch, ncta, tk, tv) : cudaErrorInvalidValue;
   } else {
-    int ppp = 0, nparts = 0;
-    const int covered = visible_context(win, max_context_len, q_len, align);
-    if (few_rows || win.window > 0 || fp4) {
-      plan_split(mma_decode ? Split::kDecode : few_rows ? Split::kRows : Split::kTiles, kv_dtype, l.group * q_len,
-                 win.window > 0, dev->num_sms, (int64_t)num_seqs * num_kv_heads,
-                 ((int64_t)covered + block_size - 1) / block_size, align, &ppp, &nparts);
+    int ppp = 0, nparts = 0, prefix_parts = 0;
+    int covered = visible_context(win, max_context_len, q_len, align);
+    if (l.form == pa::kFormBlocks) {
+      covered = x.num_listed * block_size;
+      p.blocks = x.blocks;
+      p.num_listed = x.num_listed;
+    } else if (l.form == pa::kFormOwn) {
+      // the prefixes: one unit for each tile of rows and kv head; then the own tokens, as a window of them
+      p.group_starts = x.group_starts;
+      p.prefix_lens = x.prefix_lens;
+      p.max_prefix_len = x.max_prefix_len < max_context_len ? x.max_prefix_len : max_context_len;
+      p.num_groups = p.max_prefix_len >= block_size ? x.num_groups : 0;
+      p.max_own_len = x.max_own_len < max_context_len ? x.max_own_len : max_context_len;
+      p.window = 1 << 30;  // no row's window ends in front of its sequence
+      p.page_align = align;
+      p.prefix_ppp = 1;
+      if (p.num_groups > 0)
+        plan_split(Split::kTiles, kv_dtype, 128, true, dev->num_sms,
+                   (int64_t)pa::prefix_tiles(num_seqs, q_len, l.group, p.num_groups) * num_kv_heads,
+                   p.max_prefix_len / block_size, 4, &p.prefix_ppp, &prefix_parts);
+      const int64_t own = (int64_t)p.max_own_len + (align - 1) * block_size;  // (its first pages rounded down)
+      covered = (int)(own < max_context_len ? own : max_context_len);
+    }
+    if (few_rows || special || fp4) {
+      const bool scores_dense = l.form == pa::kFormScores && mma_decode;
+      if (scores_dense) {
+        st = paged_attn_plan(dev->num_sms, num_seqs, num_kv_heads, covered, block_size, q_len, kv_dtype, &ppp, &nparts);
+        if (st != PA_OK) return st;
+      } else {
+        plan_split(mma_decode ? Split::kDecode : few_rows ? Split::kRows : Split::kTiles, kv_dtype, l.group * q_len,
+                   special && l.form != pa::kFormScores, dev->num_sms, (int64_t)num_seqs * num_kv_heads,
+                   ((int64_t)covered + block_size - 1) / block_size, align, &ppp, &nparts);
+      }
     } else {
       st = paged_attn_plan(dev->num_sms, num_seqs, num_kv_heads, covered, block_size, q_len, kv_dtype, &ppp, &nparts);
       if (st != PA_OK) return st;
@@ -341,16 +412,25 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
       }
     }
     p.pages_per_partition = ppp;
+    p.own_partitions = nparts;
+    nparts += prefix_parts;
     p.max_partitions = nparts;
-    if (nparts > 1) {
-      const size_t rows = (size_t)num_seqs * q_len * num_q_heads * nparts;
-      const size_t bytes = rows * head_dim * sizeof(float) + rows * sizeof(float);
+    if (nparts > 1 || l.form == pa::kFormScores) {
+      const size_t rows = nparts > 1 ? (size_t)num_seqs * q_len * num_q_heads * nparts : 0;
+      const size_t part_bytes = rows * head_dim * sizeof(float) + rows * sizeof(float);
+      const size_t score_bytes = l.form == pa::kFormScores
+                                     ? (size_t)num_seqs * num_q_heads * max_context_len * sizeof(float)
+                                     : 0;
+      const size_t lse_bytes = l.form == pa::kFormScores ? (size_t)num_seqs * num_q_heads * sizeof(float) : 0;
+      const size_t bytes = lse_bytes ? round_up(part_bytes) + round_up(score_bytes) + lse_bytes : part_bytes;
       if (cudaMallocFromPoolAsync(&scratch, bytes, dev->pool, s) != cudaSuccess) {
         cudaGetLastError();
         return PA_ERR_NO_MEMORY;
       }
       p.part_o = static_cast<float*>(scratch);
       p.part_lse = p.part_o + rows * head_dim;
+      p.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + round_up(part_bytes));
+      p.lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.scores) + round_up(score_bytes));
     }
     // 2-D TMA maps of the pools (bf16: 16 x 64-dim boxes; E4M3: one 16 x d box per page)
     CUtensorMap tk = {}, tv = {};
@@ -363,12 +443,23 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
     }
     if (r1 != PA_OK || r2 != PA_OK)
       e = cudaErrorInvalidValue;
-    else
-      e = split_tiles        ? pa::launch_verify_split(p, l, tk, tv)
-          : few_rows && fp4 ? pa::rows_fp4_form(p, l)
-          : few_rows        ? pa::rows_window_form(p, l, tk, tv)
-                            : pa::launch_decode_mma(p, l, tk, tv);
+    else {
+      e = prefix_parts > 0 ? pa::launch_prefix(p, l, tk, tv) : cudaSuccess;
+      if (e == cudaSuccess)
+        e = split_tiles                               ? pa::launch_verify_split(p, l, tk, tv)
+            : !few_rows                               ? pa::launch_decode_mma(p, l, tk, tv)
+            : l.form == pa::kFormBlocks               ? pa::rows_blocks_form(p, l, tk, tv)
+            : l.form == pa::kFormOwn                  ? pa::rows_own_form(p, l, tk, tv)
+            : l.form == pa::kFormScores               ? pa::rows_scores_form(p, l, tk, tv)
+            : fp4                                     ? pa::rows_fp4_form(p, l)
+                                                      : pa::rows_window_form(p, l, tk, tv);
+    }
     if (e == cudaSuccess && nparts > 1) e = pa::launch_merge(p, l);
+    if (e == cudaSuccess && l.form == pa::kFormScores) {
+      const pa::WeightParams w = {p.scores, p.lse, x.weights, block_table, context_lens, num_seqs, num_kv_heads, l.group,
+                                  max_blocks_per_seq, num_blocks, max_context_len, x.decay};
+      e = pa::launch_fold_weights(w, s);
+    }
   }
   if (scratch) cudaFreeAsync(scratch, s);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
@@ -503,6 +594,10 @@ cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, int smem, cudaStre
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+cudaError_t launch_dependent(const void* fn, dim3 grid, dim3 block, int smem, cudaStream_t st, void** args) {
+  return launch_pdl(fn, grid, block, smem, st, args);
+}
+
 cudaError_t error_word_address(unsigned** out) {
   void* ptr = nullptr;
   cudaError_t e = cudaGetSymbolAddress(&ptr, g_pa_error_word);
@@ -600,6 +695,229 @@ int paged_attn_window_verify(const void* q, const void* k_cache, const void* v_c
   return run(Form::kVerify, win, q, k_cache, v_cache, block_table, context_lens, nullptr, num_seqs, max_blocks_per_seq,
              num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim, block_size, scale, kv_dtype,
              k_scale, v_scale, out, stream);
+}
+
+int paged_attn_sparse_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                             const int32_t* context_lens, const int32_t* blocks, int num_seqs, int max_blocks_per_seq,
+                             int num_blocks, int max_context_len, int q_len, int num_listed, int num_q_heads,
+                             int num_kv_heads, int head_dim, int block_size, float scale, int kv_dtype,
+                             const float* k_scale, const float* v_scale, void* out, void* stream) {
+  Extra x;
+  x.form = pa::kFormBlocks;
+  x.blocks = blocks;
+  x.num_listed = num_listed;
+  return run(Form::kDecode, kNoWindow, q, k_cache, v_cache, block_table, context_lens, nullptr, num_seqs, max_blocks_per_seq,
+             num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim, block_size, scale, kv_dtype,
+             k_scale, v_scale, out, stream, x);
+}
+
+int paged_attn_sparse_verify(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                             const int32_t* context_lens, const int32_t* blocks, int num_seqs, int max_blocks_per_seq,
+                             int num_blocks, int max_context_len, int q_len, int num_listed, int num_q_heads,
+                             int num_kv_heads, int head_dim, int block_size, float scale, int kv_dtype,
+                             const float* k_scale, const float* v_scale, void* out, void* stream) {
+  Extra x;
+  x.form = pa::kFormBlocks;
+  x.blocks = blocks;
+  x.num_listed = num_listed;
+  return run(Form::kVerify, kNoWindow, q, k_cache, v_cache, block_table, context_lens, nullptr, num_seqs, max_blocks_per_seq,
+             num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim, block_size, scale, kv_dtype,
+             k_scale, v_scale, out, stream, x);
+}
+
+int paged_attn_prefix_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                             const int32_t* context_lens, const int32_t* group_starts, const int32_t* prefix_lens,
+                             int num_seqs, int max_blocks_per_seq, int num_blocks, int max_context_len, int q_len,
+                             int num_groups, int max_prefix_len, int max_own_len, int num_q_heads, int num_kv_heads,
+                             int head_dim, int block_size, float scale, int kv_dtype, const float* k_scale,
+                             const float* v_scale, void* out, void* stream) {
+  Extra x;
+  x.form = pa::kFormOwn;
+  x.group_starts = group_starts;
+  x.prefix_lens = prefix_lens;
+  x.num_groups = num_groups;
+  x.max_prefix_len = max_prefix_len;
+  x.max_own_len = max_own_len;
+  return run(Form::kDecode, kNoWindow, q, k_cache, v_cache, block_table, context_lens, nullptr, num_seqs, max_blocks_per_seq,
+             num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim, block_size, scale, kv_dtype,
+             k_scale, v_scale, out, stream, x);
+}
+
+int paged_attn_prefix_verify(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                             const int32_t* context_lens, const int32_t* group_starts, const int32_t* prefix_lens,
+                             int num_seqs, int max_blocks_per_seq, int num_blocks, int max_context_len, int q_len,
+                             int num_groups, int max_prefix_len, int max_own_len, int num_q_heads, int num_kv_heads,
+                             int head_dim, int block_size, float scale, int kv_dtype, const float* k_scale,
+                             const float* v_scale, void* out, void* stream) {
+  Extra x;
+  x.form = pa::kFormOwn;
+  x.group_starts = group_starts;
+  x.prefix_lens = prefix_lens;
+  x.num_groups = num_groups;
+  x.max_prefix_len = max_prefix_len;
+  x.max_own_len = max_own_len;
+  return run(Form::kVerify, kNoWindow, q, k_cache, v_cache, block_table, context_lens, nullptr, num_seqs, max_blocks_per_seq,
+             num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim, block_size, scale, kv_dtype,
+             k_scale, v_scale, out, stream, x);
+}
+
+int paged_attn_weighted_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                               const int32_t* context_lens, float* weights, int num_seqs, int max_blocks_per_seq,
+                               int num_blocks, int max_context_len, int q_len, int num_q_heads, int num_kv_heads,
+                               int head_dim, int block_size, float decay, float scale, int kv_dtype,
+                               const float* k_scale, const float* v_scale, void* out, void* stream) {
+  Extra x;
+  x.form = pa::kFormScores;
+  x.weights = weights;
+  x.decay = decay;
+  return run(Form::kDecode, kNoWindow, q, k_cache, v_cache, block_table, context_lens, nullptr, num_seqs, max_blocks_per_seq,
+             num_blocks, max_context_len, q_len, num_q_heads, num_kv_heads, head_dim, block_size, scale, kv_dtype,
+             k_scale, v_scale, out, stream, x);
+}
+
+int paged_attn_block_bounds(const void* k_cache, const int32_t* block_table, const int32_t* context_lens, int num_seqs, int n,
+                            int max_blocks_per_seq, int num_blocks, int num_kv_heads, int head_dim, int block_size,
+                            int kv_dtype, const float* k_scale, int8_t* bounds, float* bound_scale, void* stream) {
+  if (!k_cache || !block_table || !context_lens || !bounds || !bound_scale) return PA_ERR_INVALID_ARG;
+  if (num_seqs < 0 || n < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || num_kv_heads < 1 || head_dim < 1 ||
+      block_size < 1)
+    return PA_ERR_INVALID_ARG;
+  if (!known_kv_dtype(kv_dtype)) return PA_ERR_INVALID_ARG;
+  if (kv_dtype == PA_KV_FP8_E4M3 && !k_scale) return PA_ERR_INVALID_ARG;
+  if (block_size != 16 || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)max_blocks_per_seq * block_size > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+  if (!aligned(k_cache, 16) || !aligned(bounds, 16)) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || n == 0) return PA_OK;
+  DeviceState* dev = nullptr;
+  const int st = device_state(&dev);
+  if (st != PA_OK) return st;
+  pa::BoundsParams p = {};
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.block_table = block_table;
+  p.context_lens = context_lens;
+  p.k_scale = k_scale;
+  p.bounds = bounds;
+  p.bound_scale = bound_scale;
+  p.err = dev->err;
+  p.num_seqs = num_seqs;
+  const int most = max_blocks_per_seq * block_size;  // (more tokens than the table holds: all of them)
+  p.n = n < most ? n : most;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.num_kv_heads = num_kv_heads;
+  return pa::launch_block_bounds(p, head_dim, kv_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                                          : PA_ERR_CUDA;
+}
+
+int paged_attn_select_blocks(const void* q, const int8_t* bounds, const float* bound_scale, const int32_t* block_table,
+                             const int32_t* context_lens, int num_seqs, int max_blocks_per_seq, int num_blocks,
+                             int max_context_len, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                             int block_size, int count, int sink_blocks, int recent_blocks, int32_t* blocks,
+                             void* stream) {
+  if (!q || !bounds || !bound_scale || !block_table || !context_lens || !blocks) return PA_ERR_INVALID_ARG;
+  if (num_seqs < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || max_context_len < 0 || q_len < 1 || num_q_heads < 1 ||
+      num_kv_heads < 1 || head_dim < 1 || block_size < 1)
+    return PA_ERR_INVALID_ARG;
+  if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+  if (count < 1 || sink_blocks < 0 || recent_blocks < 0 || (int64_t)sink_blocks + recent_blocks > count)
+    return PA_ERR_INVALID_ARG;
+  if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(bounds, 16)) return PA_ERR_INVALID_ARG;
+  if (block_size != 16 || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || num_kv_heads > 65535 || max_context_len > (1 << 30)) return PA_ERR_UNSUPPORTED;
+  if (q_len > pa::kSelectMaxRows || num_q_heads / num_kv_heads > pa::kSelectMaxRows ||
+      num_q_heads / num_kv_heads * q_len > pa::kSelectMaxRows)
+    return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  DeviceState* dev = nullptr;
+  const int st = device_state(&dev);
+  if (st != PA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* scratch = nullptr;
+  if (cudaMallocFromPoolAsync(&scratch, pa::select_scratch_bytes(num_seqs, num_kv_heads, max_context_len), dev->pool, s) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return PA_ERR_NO_MEMORY;
+  }
+  pa::SelectParams p = {};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.bounds = bounds;
+  p.bound_scale = bound_scale;
+  p.block_table = block_table;
+  p.context_lens = context_lens;
+  p.blocks = blocks;
+  p.scores = static_cast<float*>(scratch);
+  p.err = dev->err;
+  p.num_seqs = num_seqs;
+  p.q_len = q_len;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.max_context_len = max_context_len;
+  p.max_cols = (max_context_len + block_size - 1) / block_size;
+  p.count = count;
+  p.sinks = sink_blocks;
+  p.recent = recent_blocks;
+  const cudaError_t e = pa::launch_select_blocks(p, head_dim, dev->num_sms, s);
+  cudaFreeAsync(scratch, s);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int paged_attn_evict(void* k_cache, void* v_cache, float* weights, const int32_t* block_table, const int32_t* context_lens,
+                     const int32_t* new_table, int num_seqs, int max_blocks_per_seq, int new_blocks_per_seq, int num_blocks,
+                     int max_context_len, int num_kv_heads, int head_dim, int block_size, int kv_dtype, float* k_scale,
+                     float* v_scale, int keep, int sinks, int recent, int32_t* new_lens, void* stream) {
+  if (!k_cache || !v_cache || !weights || !block_table || !context_lens || !new_table || !new_lens)
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs < 0 || max_blocks_per_seq < 1 || new_blocks_per_seq < 1 || num_blocks < 1 || max_context_len < 0 ||
+      num_kv_heads < 1 || head_dim < 1 || block_size < 1)
+    return PA_ERR_INVALID_ARG;
+  if (!known_kv_dtype(kv_dtype)) return PA_ERR_INVALID_ARG;
+  if (kv_dtype == PA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  if (keep < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep) return PA_ERR_INVALID_ARG;
+  if ((int64_t)keep > (int64_t)new_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
+  if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return PA_ERR_INVALID_ARG;
+  if (block_size != 16 || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || num_kv_heads > 65535 || max_context_len > (1 << 30)) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  if (keep > max_context_len) keep = max_context_len > 0 ? max_context_len : 1;  // (every token of every sequence)
+  DeviceState* dev = nullptr;
+  const int st = device_state(&dev);
+  if (st != PA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* scratch = nullptr;
+  if (cudaMallocFromPoolAsync(&scratch, pa::evict_scratch_bytes(num_seqs, num_kv_heads, keep, max_context_len), dev->pool,
+                              s) != cudaSuccess) {
+    cudaGetLastError();
+    return PA_ERR_NO_MEMORY;
+  }
+  pa::EvictParams p = {};
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.weights = weights;
+  p.block_table = block_table;
+  p.context_lens = context_lens;
+  p.new_table = new_table;
+  p.new_lens = new_lens;
+  p.kept = static_cast<int32_t*>(scratch);
+  p.err = dev->err;
+  p.num_seqs = num_seqs;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.new_blocks = new_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.num_kv_heads = num_kv_heads;
+  p.max_context_len = max_context_len;
+  p.keep = keep;
+  p.sinks = sinks;
+  p.recent = recent;
+  const cudaError_t e = pa::launch_evict(p, head_dim, kv_dtype, s);
+  cudaFreeAsync(scratch, s);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 int paged_attn_tree_verify(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,

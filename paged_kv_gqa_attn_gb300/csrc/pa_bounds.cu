@@ -1,0 +1,200 @@
+// Bounds of the keys of cache blocks: what the selection of blocks reads in place of their keys.
+//
+// For each (block, kv head) the largest and the smallest value of every dim over the block's tokens, as int8 codes times
+// one power of two 2^e: the smallest e with amax 2^-e <= 127, upper codes rounded up and lower ones down, so that
+// q . k <= sum_i max(q_i hi_i, q_i lo_i) holds for every token.  Scaling by a power of two is exact, so the codes do
+// not depend on how they are computed.  2 d + 4 bytes stand for the 32 d of a bf16 block's keys.
+//
+// A pass over the keys bound by their bytes: one warp takes the page of one (block, head), all of its loads in flight
+// at once (bf16, d = 128: eight 16-byte pieces a lane), and folds rows in packed 16-bit maxima and minima: E4M3 codes and
+// 4-bit codes times their scales are exact in f16, and the page's (head's) fp32 scale is applied once, at the end, as
+// rounding a product is monotone in its factor.
+#include "pa_fp4.cuh"
+#include "pa_kernels.h"
+#include "pa_tc.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kBoundsWarps = 8;
+
+// Folds of 16-bit pairs; a NaN gives way to the other operand.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (BF16)
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t min_pair(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (BF16)
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+template <int D, int KV>
+struct BoundsTraits {
+  static constexpr bool kBf16 = KV == kKvBf16;
+  static constexpr int kRowBytes = kBf16 ? 2 * D : KV == kKvE4m3 ? D : D / 2;  // of codes
+  static constexpr int kPieces = kRowBytes / 16;   // 16-byte pieces of a row: a lane each
+  static constexpr int kRowsAtOnce = 32 / kPieces;
+  static constexpr int kLoads = 16 / kRowsAtOnce;
+  static constexpr int kDims = D / kPieces;        // dims of a lane: 8, 16 or 32
+  static constexpr int kPairs = kDims / 2;
+  static constexpr int kPageBytes = KV == kKvFp4 ? Fp4Page<D>::kBytes : 16 * kRowBytes;
+};
+
+template <int D, int KV>
+__global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const BoundsParams p) {
+  using T = BoundsTraits<D, KV>;
+  constexpr uint32_t kLowest = T::kBf16 ? 0xff80ff80u : 0xfc00fc00u, kHighest = T::kBf16 ? 0x7f807f80u : 0x7c007c00u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.y;
+  const int L = p.context_lens[b];
+  if (!context_holds(L, 0, p.max_blocks_per_seq)) {
+    if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) record_error(p.err, kErrShortContext);
+    return;
+  }
+  const int col = max(0, L - p.n) / 16 + blockIdx.x;
+  if (col * 16 >= L) return;
+  const int pb = p.block_table[(size_t)b * p.max_blocks_per_seq + col];
+  if (pb < 0 || pb >= p.num_blocks) {
+    if (blockIdx.z == 0 && threadIdx.x == 0) record_error(p.err, kErrBlockId);
+    return;
+  }
+  const int valid = min(16, L - col * 16);
+  const int piece = lane % T::kPieces, row0 = lane / T::kPieces;
+  for (int g = blockIdx.z * kBoundsWarps + warp; g < p.num_kv_heads; g += gridDim.z * kBoundsWarps) {
+    const size_t page = (size_t)pb * p.num_kv_heads + g;
+    const uint8_t* src = p.k_cache + page * T::kPageBytes;
+    uint4 x[T::kLoads];
+    uint32_t sc[T::kLoads];
+#pragma unroll
+    for (int i = 0; i < T::kLoads; ++i) {
+      const int r = row0 + i * T::kRowsAtOnce;
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      sc[i] = 0u;
+      if (r < valid) {
+        x[i] = *reinterpret_cast<const uint4*>(src + r * T::kRowBytes + piece * 16);
+        if constexpr (KV == kKvFp4)
+          sc[i] = *reinterpret_cast<const uint16_t*>(src + Fp4Page<D>::kCodeBytes + r * Fp4Page<D>::kScaleRow + piece * 2);
+      }
+    }
+    float s = 1.f;
+    if constexpr (KV == kKvE4m3) s = p.k_scale[page];
+    if constexpr (KV == kKvFp4) s = p.k_scale ? p.k_scale[g] : 1.f;
+    uint32_t hi[T::kPairs], lo[T::kPairs];
+#pragma unroll
+    for (int j = 0; j < T::kPairs; ++j) {
+      hi[j] = kLowest;
+      lo[j] = kHighest;
+    }
+#pragma unroll
+    for (int i = 0; i < T::kLoads; ++i) {
+      if (row0 + i * T::kRowsAtOnce >= valid) continue;
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t v[T::kPairs];
+      if constexpr (KV == kKvBf16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = w[j];
+      } else if constexpr (KV == kKvE4m3) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[2 * j] = e4m3x2_to_f16x2(w[j]);
+          v[2 * j + 1] = e4m3x2_to_f16x2(w[j] >> 16);
+        }
+      } else {
+        const uint32_t s2 = e4m3x2_to_f16x2(sc[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t h[4];
+          e2m1x8_to_f16x2(w[j], h);
+          const uint32_t sp = __byte_perm(s2, s2, j < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * j + e] = mul_f16x2(h[e], sp);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < T::kPairs; ++j) {
+        hi[j] = max_pair<T::kBf16>(hi[j], v[j]);
+        lo[j] = min_pair<T::kBf16>(lo[j], v[j]);
+      }
+    }
+#pragma unroll
+    for (int o = T::kPieces; o < 32; o <<= 1) {
+#pragma unroll
+      for (int j = 0; j < T::kPairs; ++j) {
+        hi[j] = max_pair<T::kBf16>(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], o));
+        lo[j] = min_pair<T::kBf16>(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], o));
+      }
+    }
+    // the value of a pair's element, times the fp32 scale; a negative scale turns the ends round
+    auto value = [&](uint32_t pair, int e) {
+      if constexpr (T::kBf16) return e ? __uint_as_float(pair & 0xffff0000u) : __uint_as_float(pair << 16);
+      const __half2 h = *reinterpret_cast<const __half2*>(&pair);
+      return s * (e ? __high2float(h) : __low2float(h));
+    };
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < T::kPairs; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) amax = fmaxf(amax, fmaxf(fabsf(value(hi[j], e)), fabsf(value(lo[j], e))));
+#pragma unroll
+    for (int o = 1; o < T::kPieces; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const uint32_t bits = __float_as_uint(fminf(amax, 3.4028235e38f));  // (a key of infinity: the widest bounds)
+    int e = (int)(bits >> 23) - 127 - 6 + ((bits & 0x7fffffu) > 0x7e0000u ? 1 : 0);  // above 127 / 64: one more
+    e = bits == 0 ? 0 : max(e, -126);
+    const float down = exp2_int(-e);
+    // lanes of row 0 write the upper codes, those of the last rows the lower ones
+    const bool upper = row0 == 0, lower = row0 == T::kRowsAtOnce - 1;
+    auto code = [&](int j, int e2, bool up) {
+      const float a = value(hi[j], e2) * down, c = value(lo[j], e2) * down;
+      const float y = up ? ceilf(fmaxf(a, c)) : floorf(fminf(a, c));
+      return (uint32_t)(int)fminf(fmaxf(y, -127.f), 127.f) & 0xffu;
+    };
+    int8_t* dst = p.bounds + page * (2 * D) + piece * T::kDims;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      if (side == 0 ? !upper : !lower) continue;
+      uint32_t out[T::kPairs / 2];
+#pragma unroll
+      for (int j = 0; j < T::kPairs / 2; ++j)
+        out[j] = code(2 * j, 0, side == 0) | (code(2 * j, 1, side == 0) << 8) | (code(2 * j + 1, 0, side == 0) << 16) |
+                 (code(2 * j + 1, 1, side == 0) << 24);
+#pragma unroll
+      for (int j = 0; j < T::kPairs / 2; j += 2)
+        *reinterpret_cast<uint2*>(dst + side * D + 4 * j) = make_uint2(out[j], out[j + 1]);
+    }
+    if (lane == 0) p.bound_scale[page] = exp2_int(e);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const BoundsParams& p, int kv, cudaStream_t st) {
+  const int cols = min((p.n + 14) / 16 + 1, p.max_blocks_per_seq);  // columns that n tokens touch at most
+  const int z = min((p.num_kv_heads + kBoundsWarps - 1) / kBoundsWarps, 64);
+  const dim3 grid(cols, p.num_seqs, z);
+  if (kv == kKvBf16)
+    block_bounds_kernel<D, kKvBf16><<<grid, kBoundsWarps * 32, 0, st>>>(p);
+  else if (kv == kKvE4m3)
+    block_bounds_kernel<D, kKvE4m3><<<grid, kBoundsWarps * 32, 0, st>>>(p);
+  else
+    block_bounds_kernel<D, kKvFp4><<<grid, kBoundsWarps * 32, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_block_bounds(const BoundsParams& p, int head_dim, int kv_dtype, cudaStream_t st) {
+  if (head_dim == 128) return launch_d<128>(p, kv_dtype, st);
+  if (head_dim == 64) return launch_d<64>(p, kv_dtype, st);
+  return cudaErrorInvalidConfiguration;
+}
+
+}  // namespace pa

@@ -23,6 +23,15 @@ constexpr uint32_t kSpinLimit = 1u << 22;
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// What an attention kernel reads of a sequence, and what it writes beside the rows (a template parameter, so
+// that a form costs the others nothing).
+constexpr int kFormAll = 0;     // every token
+constexpr int kFormWindow = 1;  // a window of the last tokens, and the first ones
+constexpr int kFormBlocks = 2;  // the blocks that a list names for each (sequence, kv head)
+constexpr int kFormOwn = 3;     // what lies behind the prefix that a group of sequences shares
+constexpr int kFormPrefix = 4;  // the shared prefix, for the rows of all of its group's sequences (tile kernel)
+constexpr int kFormScores = 5;  // every token; the scores are kept for the tokens' weights
+
 // Arguments of every attention kernel.  Pointers are device pointers.
 struct AttnParams {
   const __nv_bfloat16* q;       // [B, q_len, Hq, d]
@@ -52,7 +61,55 @@ struct AttnParams {
   int window;                   // tokens a row sees up to its own, past the sinks; 0: all
   int sinks;                    // first tokens that stay visible (with a window)
   int page_align;               // window: pages that page_span rounds its edges to (see there)
+  const int32_t* blocks;        // kFormBlocks: [B, Hkv, num_listed] block-table columns
+  int num_listed;
+  const int32_t* group_starts;  // kFormOwn, kFormPrefix: [num_groups + 1] first sequence of each group
+  const int32_t* prefix_lens;   // [num_groups] tokens that the sequences of a group share
+  int num_groups;
+  int max_prefix_len;           // host-side bounds; longer ones are clamped (prefix) or refused (own), and flagged
+  int max_own_len;
+  int own_partitions;           // partial slots [0, own_partitions) of a row: its own tokens; the rest: the prefix
+  int prefix_ppp;               // pages per partition of the prefix
+  float* scores;                // kFormScores: [B, Hkv, max_context_len, G] base-2 scores
+  float* lse;                   // [B, Hq] log2 of each row's softmax mass
 };
+
+constexpr int kNoBlock = -0x7fffffff - 1;  // kFormBlocks: an unused entry of the list, in place of a block id
+
+// The group of sequences [first, last) that share `tokens` prefix tokens, a whole number of blocks.
+struct PrefixGroup {
+  int first, last, tokens;
+};
+// Group i, with every bound checked: offsets that do not fit leave it empty.  Flags what it finds wrong when asked.
+__device__ __forceinline__ PrefixGroup prefix_group(const AttnParams& p, int i, unsigned& wrong) {
+  PrefixGroup r = {p.group_starts[i], p.group_starts[i + 1], p.prefix_lens[i]};
+  if (r.first < 0 || r.last < r.first || r.last > p.num_seqs) {
+    wrong |= kErrBadInput;
+    r.first = r.last = 0;
+  }
+  if (r.tokens > p.max_prefix_len) {
+    wrong |= kErrShortContext;
+    r.tokens = p.max_prefix_len;
+  }
+  r.tokens = max(r.tokens, 0) / 16 * 16;
+  return r;
+}
+// Whether a sequence's new rows all lie behind its prefix, and no more than the bound does.
+__device__ __forceinline__ bool own_tokens_fit(const AttnParams& p, int L, int prefix) {
+  return (prefix == 0 || L - p.q_len >= prefix) && L - prefix <= p.max_own_len;
+}
+// Prefix tokens of sequence b: those of the first group that holds it, or 0.  Whole warp.
+__device__ __forceinline__ int prefix_of(const AttnParams& p, int b) {
+  const int lane = threadIdx.x & 31;
+  for (int i0 = 0; i0 < p.num_groups; i0 += 32) {
+    PrefixGroup r = {0, 0, 0};
+    unsigned wrong = 0;
+    if (i0 + lane < p.num_groups) r = prefix_group(p, i0 + lane, wrong);
+    const unsigned in = __ballot_sync(0xffffffffu, b >= r.first && b < r.last);
+    if (in) return __shfl_sync(0xffffffffu, r.tokens, __ffs(in) - 1);
+  }
+  return 0;
+}
 
 // The pages of a sequence (or tile) that a window with sinks leaves, numbered without the gap: page v
 // of [0, count) is column v of the block table before `head` and column v + gap from there on.  With
@@ -228,7 +285,7 @@ __device__ __forceinline__ int context_len(const AttnParams& p, int b, bool flag
 // warps left in shared memory (wacc [W][G][D] unnormalised outputs, wm [W][G] running maxima and
 // wl [W][G] sums, base 2) and store either the finished bf16 rows (the sequence has one
 // partition) or the normalised partial output and its log2-sum-exp for the merge kernel.
-template <int G, int D, int W, bool E4M3 = false>
+template <int G, int D, int W, bool E4M3 = false, int FORM = kFormAll>
 __device__ __forceinline__ void store_partition(const AttnParams& p, const float* wacc, const float* wm,
                                                 const float* wl, int b, int g, int part, int nparts) {
   const int Hq = p.num_q_heads;
@@ -257,6 +314,7 @@ __device__ __forceinline__ void store_partition(const AttnParams& p, const float
     const int qh = g * G + h;
     if (nparts == 1) {
       p.out[((size_t)b * Hq + qh) * D + dd] = __float2bfloat16(o);
+      if (FORM == kFormScores && dd == 0) p.lse[(size_t)b * Hq + qh] = M + __log2f(lsum);
     } else {
       const size_t row = ((size_t)b * Hq + qh) * p.max_partitions + part;
       p.part_o[row * D + dd] = o;

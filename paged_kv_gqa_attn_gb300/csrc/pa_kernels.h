@@ -18,6 +18,7 @@ struct Launch {
   bool fp8;
   cudaStream_t stream;
   int kv = kKvBf16;  // cache type (fp8: kv == kKvE4m3)
+  int form = kFormAll;
 };
 
 // Each returns cudaSuccess or the launch error.  Unsupported combinations return
@@ -61,6 +62,19 @@ constexpr int kRowsMax = 32, kRowsMaxBf16 = 16;
 constexpr int rows_resident_ctas(int rows) { return rows <= 8 ? 4 : rows <= 16 ? 3 : 2; }
 cudaError_t rows_fp4_form(const AttnParams& p, const Launch& l);
 cudaError_t rows_window_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
+// The forms over listed blocks, over what lies behind a shared prefix and with kept scores: of the decode kernel, the
+// rows kernel (every cache type) and the tile kernel (more rows than that takes).
+cudaError_t decode_blocks_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
+cudaError_t decode_own_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
+cudaError_t decode_scores_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
+cudaError_t rows_blocks_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
+cudaError_t rows_own_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
+cudaError_t rows_scores_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
+cudaError_t tiles_own_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
+// The shared prefixes of p.num_groups groups, in at most prefix_tiles(...) tiles of 128 rows per kv head (a bound
+// without the groups' sizes: each but one may leave a tile part full).
+int prefix_tiles(int num_seqs, int q_len, int group, int num_groups);
+cudaError_t launch_prefix(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
 // KV append (bf16 scatter, fp8 with per-(block, head) rescaling, or E2M1 codes with a scale for each
 // 16 dims of a token); arguments already checked.
 cudaError_t launch_append(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
@@ -82,6 +96,66 @@ struct ReadParams {
   int num_seqs, n, max_blocks_per_seq, num_blocks, num_kv_heads;
 };
 cudaError_t launch_read_kv(const ReadParams& p, int head_dim, int kv_dtype, cudaStream_t st);
+
+// Bounds of the keys of each block that holds one of a sequence's last n tokens; arguments already checked.
+struct BoundsParams {
+  const uint8_t* k_cache;
+  const int32_t* block_table;
+  const int32_t* context_lens;
+  const float* k_scale;   // as the cache type's (E2M1: [Hkv] or null)
+  int8_t* bounds;         // [NB, Hkv, 2, d]: codes of the largest, then of the smallest
+  float* bound_scale;     // [NB, Hkv]: a power of two
+  unsigned* err;
+  int num_seqs, n, max_blocks_per_seq, num_blocks, num_kv_heads;
+};
+cudaError_t launch_block_bounds(const BoundsParams& p, int head_dim, int kv_dtype, cudaStream_t st);
+
+// The highest-scoring blocks of each (sequence, kv head).  scratch holds select_scratch_bytes(...) bytes.
+struct SelectParams {
+  const __nv_bfloat16* q;       // [B, q_len, Hq, d]
+  const int8_t* bounds;
+  const float* bound_scale;
+  const int32_t* block_table;
+  const int32_t* context_lens;
+  int32_t* blocks;              // [B, Hkv, count]
+  float* scores;                // [B, Hkv, max_cols]
+  unsigned* err;
+  int num_seqs, q_len, num_q_heads, num_kv_heads, max_blocks_per_seq, num_blocks, max_context_len, max_cols;
+  int count, sinks, recent;     // in blocks
+};
+constexpr int kSelectMaxRows = 32;  // q_len * group
+size_t select_scratch_bytes(int num_seqs, int num_kv_heads, int max_context_len);
+cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, int num_sms, cudaStream_t st);
+
+// The step's softmax weights from the kept scores and the rows' log2-sum-exps, folded into the tokens' sums.
+struct WeightParams {
+  const float* scores;          // [B, Hkv, max_context_len, G]
+  const float* lse;             // [B, Hq]
+  float* weights;               // [NB, Hkv, 16]
+  const int32_t* block_table;
+  const int32_t* context_lens;
+  int num_seqs, num_kv_heads, group, max_blocks_per_seq, num_blocks, max_context_len;
+  float decay;
+};
+cudaError_t launch_fold_weights(const WeightParams& p, cudaStream_t st);
+
+// Eviction: the tokens of the largest sums move to the blocks of new_table.  scratch holds evict_scratch_bytes(...).
+struct EvictParams {
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  float* k_scale;               // E4M3: [NB, Hkv]
+  float* v_scale;
+  float* weights;               // [NB, Hkv, 16]
+  const int32_t* block_table;
+  const int32_t* context_lens;
+  const int32_t* new_table;     // [B, new_blocks]
+  int32_t* new_lens;            // [B]
+  int32_t* kept;                // scratch: [B, Hkv, keep] positions, then the keys of long contexts
+  unsigned* err;
+  int num_seqs, max_blocks_per_seq, new_blocks, num_blocks, num_kv_heads, max_context_len, keep, sinks, recent;
+};
+size_t evict_scratch_bytes(int num_seqs, int num_kv_heads, int keep, int max_context_len);
+cudaError_t launch_evict(const EvictParams& p, int head_dim, int kv_dtype, cudaStream_t st);
 
 // RMS norm and rotation of the query and key head rows; strides in elements between tokens.
 struct RopeParams {
@@ -109,6 +183,10 @@ cudaError_t launch_accept(const float* p, const float* q, const int32_t* draft, 
 // Programmatic dependent launch of `fn` on `st` (cudaLaunchKernelExC with the
 // programmatic-stream-serialisation attribute).
 cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, int smem, cudaStream_t st, void** args);
+
+// launch_pdl for kernels whose every CTA waits (griddepcontrol.wait) before its first read of what the kernel before
+// it wrote, and before it returns.
+cudaError_t launch_dependent(const void* fn, dim3 grid, dim3 block, int smem, cudaStream_t st, void** args);
 
 // Raise a kernel's dynamic shared-memory limit on the current device (first call per device
 // and kernel only; later calls are a table lookup).

@@ -51,7 +51,9 @@ __device__ __forceinline__ void merge_partitions(const float* lse, const float* 
   }
 }
 
-template <int D>
+// FORM: kFormAll (a window too), kFormBlocks, kFormOwn (the partials of a sequence's own tokens and, in the slots
+// behind them, of its group's prefix) or kFormScores (the row's log2-sum-exp is kept as well).
+template <int D, int FORM>
 __global__ void __launch_bounds__(128) merge_kernel(const AttnParams p) {
   constexpr int kDPL = D / 32;
   const int warp = threadIdx.x >> 5;
@@ -62,9 +64,20 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttnParams p) {
   const int b = (int)(min(row, rows - 1) / ((long)p.q_len * Hq));
   const int L = context_len(p, b, false);
   int npages = (L + 15) / 16;
-  if (p.window > 0) npages = page_span(npages, max(0, L - p.q_len + 1 - p.window), p.sinks, p.page_align).count;
-  const int nparts = L > 0 ? (npages + p.pages_per_partition - 1) / p.pages_per_partition : 0;
-  const bool merges = row < rows && nparts > 1;  // (otherwise the attention kernel wrote the row directly)
+  int prefix_parts = 0;
+  bool some = L > 0;
+  if constexpr (FORM == kFormOwn) {
+    const int prefix = prefix_of(p, b);
+    some = some && own_tokens_fit(p, L, prefix);
+    prefix_parts = some ? (prefix / 16 + p.prefix_ppp - 1) / p.prefix_ppp : 0;
+    npages = page_span(npages, prefix, 0, p.page_align).count;
+  } else if constexpr (FORM == kFormBlocks) {
+    npages = p.num_listed;
+  } else {
+    if (p.window > 0) npages = page_span(npages, max(0, L - p.q_len + 1 - p.window), p.sinks, p.page_align).count;
+  }
+  const int nparts = some ? (npages + p.pages_per_partition - 1) / p.pages_per_partition : 0;
+  const bool merges = row < rows && nparts + prefix_parts > 1;  // (otherwise the attention kernel wrote the row directly)
   // Launched as a programmatic dependent of the attention kernel: wait for its partials.  CTA 0 waits even with
   // nothing to merge, so that this grid never ends before the one it depends on: what comes next on the stream
   // waits for this grid alone.
@@ -82,6 +95,11 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttnParams p) {
     merge_partitions<D, 8>(lse, po, nparts, lane, M, wsum, acc);
   else
     merge_partitions<D, 32>(lse, po, nparts, lane, M, wsum, acc);
+  if constexpr (FORM == kFormOwn) {
+    if (prefix_parts > 0)
+      merge_partitions<D, 8>(lse + p.own_partitions, po + (size_t)p.own_partitions * D, prefix_parts, lane, M, wsum, acc);
+  }
+  if (FORM == kFormScores && lane == 0) p.lse[row] = M + __log2f(wsum);
   __nv_bfloat16* dst = p.out + row * D + lane * kDPL;
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
 #pragma unroll
@@ -107,9 +125,22 @@ cudaError_t launch_merge(const AttnParams& p, const Launch& l) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (l.head_dim == 128) return cudaLaunchKernelEx(&cfg, merge_kernel<128>, p);
-  if (l.head_dim == 64) return cudaLaunchKernelEx(&cfg, merge_kernel<64>, p);
-  return cudaErrorInvalidConfiguration;
+  if (l.head_dim != 128 && l.head_dim != 64) return cudaErrorInvalidConfiguration;
+  const bool wide = l.head_dim == 128;
+  switch (l.form) {
+    case kFormBlocks:
+      return wide ? cudaLaunchKernelEx(&cfg, merge_kernel<128, kFormBlocks>, p)
+                  : cudaLaunchKernelEx(&cfg, merge_kernel<64, kFormBlocks>, p);
+    case kFormOwn:
+      return wide ? cudaLaunchKernelEx(&cfg, merge_kernel<128, kFormOwn>, p)
+                  : cudaLaunchKernelEx(&cfg, merge_kernel<64, kFormOwn>, p);
+    case kFormScores:
+      return wide ? cudaLaunchKernelEx(&cfg, merge_kernel<128, kFormScores>, p)
+                  : cudaLaunchKernelEx(&cfg, merge_kernel<64, kFormScores>, p);
+    default:
+      return wide ? cudaLaunchKernelEx(&cfg, merge_kernel<128, kFormAll>, p)
+                  : cudaLaunchKernelEx(&cfg, merge_kernel<64, kFormAll>, p);
+  }
 }
 
 }  // namespace pa

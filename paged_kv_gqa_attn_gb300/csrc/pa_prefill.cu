@@ -119,16 +119,17 @@ namespace {
 cudaError_t dense_form(const AttnParams& p, const Launch& l, int max_q_len, int32_t* tiles, const CUtensorMap& tk,
                        const CUtensorMap& tv) {
   if (l.head_dim == 128)
-    return l.kv == kKvE4m3 ? prefill_form<128, kKvE4m3, false>(p, l, max_q_len, tiles, tk, tv)
-                           : prefill_form<128, kKvBf16, false>(p, l, max_q_len, tiles, tk, tv);
+    return l.kv == kKvE4m3 ? prefill_form<128, kKvE4m3, kFormAll>(p, l, max_q_len, tiles, tk, tv)
+                           : prefill_form<128, kKvBf16, kFormAll>(p, l, max_q_len, tiles, tk, tv);
   if (l.head_dim == 64)
-    return l.kv == kKvE4m3 ? prefill_form<64, kKvE4m3, false>(p, l, max_q_len, tiles, tk, tv)
-                           : prefill_form<64, kKvBf16, false>(p, l, max_q_len, tiles, tk, tv);
+    return l.kv == kKvE4m3 ? prefill_form<64, kKvE4m3, kFormAll>(p, l, max_q_len, tiles, tk, tv)
+                           : prefill_form<64, kKvBf16, kFormAll>(p, l, max_q_len, tiles, tk, tv);
   return cudaErrorInvalidConfiguration;
 }
 
 cudaError_t any_form(const AttnParams& p, const Launch& l, int max_q_len, int32_t* tiles, const CUtensorMap& tk,
                      const CUtensorMap& tv) {
+  if (l.form == kFormOwn) return tiles_own_form(p, l, tk, tv);
   if (l.kv == kKvFp4) return prefill_fp4_form(p, l, max_q_len, tiles);
   if (p.window > 0) return prefill_window_form(p, l, max_q_len, tiles, tk, tv);
   return dense_form(p, l, max_q_len, tiles, tk, tv);

@@ -39,6 +39,10 @@
 // window on, numbered without the gap between (page_span; both edges on whole steps, so that a step
 // never straddles the gap); pages of a step that no row of the tile sees are neither looked up nor
 // copied, and each row masks the tokens between its sinks and its window.
+// Shared prefix (kFormPrefix, split): the rows are those of all of a group's sequences, which are neighbours in q,
+// 128 / G tokens a tile; every row sees the whole prefix, read through the first sequence's table, once for each
+// tile.  The rows' own tokens (kFormOwn, split) are the window form's with the window's begin where the prefix ends;
+// both leave partials.
 #pragma once
 
 #include "pa_fp4.cuh"
@@ -123,20 +127,53 @@ __device__ __forceinline__ void pf_tl_put(int slot, unsigned long long v) {
 // plan of decode -- the CTA walks the pages [part * ppp, part * ppp + ppp) of its sequence and,
 // when the sequence has several partitions, writes the normalised partial rows and their
 // log2-sum-exp for the log-sum-exp merge kernel; p.tree_mask, when set, replaces the causal mask.
-template <int D, bool SPLIT, int KV, bool WIN>
+template <int D, bool SPLIT, int KV, int FORM>
 __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel(const AttnParams p, const int32_t* tiles,
                                                             const __grid_constant__ CUtensorMap tmk,
                                                             const __grid_constant__ CUtensorMap tmv) {
   using T = PfTraits<D>;
   constexpr bool FP8 = KV == kKvE4m3, FP4 = KV == kKvFp4;
+  constexpr bool PREFIX = FORM == kFormPrefix, OWN = FORM == kFormOwn;
+  constexpr bool WIN = FORM == kFormWindow || OWN;  // pages numbered with a gap
+  static_assert(SPLIT || !(PREFIX || OWN), "both leave partials");
   constexpr bool kConv = FP8 || FP4;  // operands converted to f16 in shared memory
   // E4M3 with head_dim 128: Q.K^T on the E4M3 codes of K (kind::f8f6f4, Q split into two E4M3
   // terms), P.V on f16; head_dim 64: both products on f16 (K and V converted)
   constexpr bool kKDirect = FP8 && D == 128;
   const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, G = Hq / Hkv;
   const int Tt = T::kRows / G;  // new tokens per tile
-  int g, b, tile, qs, QL, part = 0;
-  if constexpr (SPLIT) {
+  int g, b, tile, qs, QL, part = 0, prefix = 0;
+  if constexpr (PREFIX) {  // tile blockIdx.z of the groups' tiles, laid end to end
+    part = (int)blockIdx.x;
+    g = (int)blockIdx.y;
+    const int lane = threadIdx.x & 31, z = (int)blockIdx.z;
+    b = -1;
+    tile = QL = 0;
+    int before = 0;
+    for (int i0 = 0; i0 < p.num_groups && b < 0; i0 += 32) {
+      PrefixGroup r = {0, 0, 0};
+      unsigned wrong = 0;
+      if (i0 + lane < p.num_groups) r = prefix_group(p, i0 + lane, wrong);
+      if (wrong && z == 0 && g == 0 && part == 0 && threadIdx.x < 32) record_error(p.err, wrong);
+      const int tiles_here = r.tokens > 0 ? ((r.last - r.first) * p.q_len + Tt - 1) / Tt : 0;
+      int upto = tiles_here;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, z < before + upto);
+      const int at = past ? __ffs(past) - 1 : 31;
+      if (past) {
+        b = __shfl_sync(0xffffffffu, r.first, at);
+        QL = (__shfl_sync(0xffffffffu, r.last, at) - b) * p.q_len;
+        prefix = __shfl_sync(0xffffffffu, r.tokens, at);
+        tile = z - before - __shfl_sync(0xffffffffu, upto - tiles_here, at);
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    qs = b * p.q_len;
+  } else if constexpr (SPLIT) {
     part = (int)blockIdx.x;
     g = (int)blockIdx.y;
     b = (int)blockIdx.z;
@@ -155,6 +192,7 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     qs = p.query_start_loc[b];
     QL = p.query_start_loc[b + 1] - qs;
   }
+  if (PREFIX && b < 0) return;  // fewer tiles than the grid's bound
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -190,23 +228,28 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
 #endif
 
   // a longer context is flagged by the planner (split: by partition 0 of kv head 0)
-  const int L = SPLIT ? context_len(p, b, part == 0 && g == 0 && threadIdx.x == 0)
-                      : max(min(p.context_lens[b], p.max_context_len), 0);
+  int L = PREFIX  ? prefix
+          : SPLIT ? context_len(p, b, part == 0 && g == 0 && threadIdx.x == 0)
+                  : max(min(p.context_lens[b], p.max_context_len), 0);
+  if constexpr (OWN) {
+    prefix = prefix_of(p, b);
+    if (!own_tokens_fit(p, L, prefix)) L = 0;
+  }
   const int t0 = tile * Tt;
   const int first_new = L - QL;                       // cache position of new token 0
-  const int n_max = first_new + min(t0 + Tt, QL);     // tokens the tile's last row sees
+  const int n_max = PREFIX ? L : first_new + min(t0 + Tt, QL);  // tokens the tile's last row sees
   const int npages = n_max > 0 ? (n_max + T::kBS - 1) / T::kBS : 0;
   // window: the first position the tile's first row sees past the sinks, and the pages in between left out
-  const int win_lo = WIN ? max(0, first_new + t0 + 1 - p.window) : 0;
+  const int win_lo = OWN ? prefix : WIN ? max(0, first_new + t0 + 1 - p.window) : 0;
   const int lo_page = win_lo / T::kBS;
   const int sink_pages = WIN ? (p.sinks + T::kBS - 1) / T::kBS : 0;
   PageSpan span = {npages, 0, npages};
   if constexpr (WIN) span = page_span(npages, win_lo, p.sinks, T::kTP);
   // the CTA's pages [pfirst, plast): all of them, or its partition (a whole number of steps)
-  const int ppp = SPLIT ? p.pages_per_partition : 0;
+  const int ppp = PREFIX ? p.prefix_ppp : SPLIT ? p.pages_per_partition : 0;
   const int pfirst = SPLIT ? part * ppp : 0;
   const int plast = SPLIT ? min(span.count, pfirst + ppp) : span.count;
-  const int nparts = SPLIT ? (span.count + ppp - 1) / ppp : 1;
+  const int nparts = SPLIT ? (span.count + ppp - 1) / ppp + (OWN && prefix > 0 ? 1 : 0) : 1;
   const int nsteps = plast > pfirst ? (plast - pfirst + T::kTP - 1) / T::kTP : 0;
   const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
   // block-table column of the CTA's page v; false: past its range, or seen by no row of the tile
@@ -221,7 +264,7 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
   // first token of step s (a step lies on one side of the window's gap)
   auto step_token = [&](int s) { return (WIN ? span.real(pfirst + s * T::kTP) : pfirst + s * T::kTP) * T::kBS; };
 
-  if (first_new + t0 + 1 <= 0 && part == 0) {
+  if (!PREFIX && first_new + t0 + 1 <= 0 && part == 0) {
     // the tile's first row sees no token (context shorter than the new tokens): its rows that see
     // nothing come out as zeros
     if (threadIdx.x == 0) record_error(p.err, kErrShortContext);
@@ -744,11 +787,12 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     const int t = t0 + r / G;          // new-token index of this row
     const int h = g * G + r % G;       // its query head
-    const bool row_live = t < QL;
-    const int n_r = row_live ? max(first_new + t + 1, 0) : 0;  // tokens this row sees
+    // (with a group that does not divide 128 the tile's last rows would be the next tile's first)
+    const bool row_live = t < QL && (!PREFIX || r < Tt * G);
+    const int n_r = !row_live ? 0 : PREFIX ? L : max(first_new + t + 1, 0);  // tokens this row sees
     // tree verify (split mode only): the new tokens the row sees are its ancestor bits; the chain
     // mask (bits 0 .. t) gives the causal row exactly
-    const bool tree = SPLIT && p.tree_mask != nullptr;
+    const bool tree = SPLIT && !PREFIX && p.tree_mask != nullptr;
     const uint32_t anc = (tree && row_live) ? p.tree_mask[(size_t)b * QL + t] : 0u;
     // Q row r: bf16, K-major 128-byte swizzle (halves of 64 dims, 8-row groups 1024 B apart).
     // E4M3: the row scaled by a power of two 2^k first (exact, no overflow for any bf16 q) and its
@@ -1165,8 +1209,8 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
         const float inv = l > 0.f ? (FP4 ? v_head : FP8 ? v_unit : 1.f) / l : 0.f;
         __nv_bfloat16* dst = p.out + ((size_t)(qs + t) * Hq + h) * D;
         // split sequence: the partition's normalised rows and log2-sum-exp for the merge kernel
-        const bool partial = SPLIT && nparts > 1;
-        const size_t prow = ((size_t)(qs + t) * Hq + h) * p.max_partitions + part;
+        const bool partial = PREFIX || (SPLIT && nparts > 1);
+        const size_t prow = ((size_t)(qs + t) * Hq + h) * p.max_partitions + (PREFIX ? p.own_partitions : 0) + part;
         if (partial && row_live) p.part_lse[prow] = l > 0.f ? m_used + __log2f(l) : -INFINITY;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -1183,14 +1227,16 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
                               __uint_as_float(raw[c + 2]) * inv, __uint_as_float(raw[c + 3]) * inv);
             continue;
           }
+          if constexpr (!PREFIX) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 8) {
-            uint4 v;
-            v.x = pack_bf16(__uint_as_float(raw[c + 0]) * inv, __uint_as_float(raw[c + 1]) * inv);
-            v.y = pack_bf16(__uint_as_float(raw[c + 2]) * inv, __uint_as_float(raw[c + 3]) * inv);
-            v.z = pack_bf16(__uint_as_float(raw[c + 4]) * inv, __uint_as_float(raw[c + 5]) * inv);
-            v.w = pack_bf16(__uint_as_float(raw[c + 6]) * inv, __uint_as_float(raw[c + 7]) * inv);
-            *reinterpret_cast<uint4*>(dst + c0 + c) = v;
+            for (int c = 0; c < 32; c += 8) {
+              uint4 v;
+              v.x = pack_bf16(__uint_as_float(raw[c + 0]) * inv, __uint_as_float(raw[c + 1]) * inv);
+              v.y = pack_bf16(__uint_as_float(raw[c + 2]) * inv, __uint_as_float(raw[c + 3]) * inv);
+              v.z = pack_bf16(__uint_as_float(raw[c + 4]) * inv, __uint_as_float(raw[c + 5]) * inv);
+              v.w = pack_bf16(__uint_as_float(raw[c + 6]) * inv, __uint_as_float(raw[c + 7]) * inv);
+              *reinterpret_cast<uint4*>(dst + c0 + c) = v;
+            }
           }
         }
       }
@@ -1208,11 +1254,11 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
 #endif
 }
 
-template <int D, int KV, bool WIN>
+template <int D, int KV, int FORM>
 cudaError_t prefill_tiles(const AttnParams& p, int max_q_len, int group, int32_t* tiles, const CUtensorMap& tk,
                           const CUtensorMap& tv, cudaStream_t st) {
   using T = PfTraits<D>;
-  const void* fn = reinterpret_cast<const void*>(prefill_tc_kernel<D, false, KV, WIN>);
+  const void* fn = reinterpret_cast<const void*>(prefill_tc_kernel<D, false, KV, FORM>);
   cudaError_t e = set_smem_once(fn, T::smem(KV));
   if (e != cudaSuccess) return e;
   const int tt = T::kRows / group;
@@ -1227,22 +1273,41 @@ cudaError_t prefill_tiles(const AttnParams& p, int max_q_len, int group, int32_t
   return launch_pdl(fn, dim3((unsigned)(bound * p.num_kv_heads)), dim3(T::threads(KV)), T::smem(KV), st, args);
 }
 
-template <int D, int KV, bool WIN>
+template <int D, int KV, int FORM>
 cudaError_t prefill_split(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   using T = PfTraits<D>;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(prefill_tc_kernel<D, true, KV, WIN>), T::smem(KV));
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(prefill_tc_kernel<D, true, KV, FORM>), T::smem(KV));
   if (e != cudaSuccess) return e;
-  dim3 grid(p.max_partitions, p.num_kv_heads, p.num_seqs);
-  prefill_tc_kernel<D, true, KV, WIN><<<grid, T::threads(KV), T::smem(KV), st>>>(p, nullptr, tk, tv);
+  dim3 grid(FORM == kFormOwn ? p.own_partitions : p.max_partitions, p.num_kv_heads, p.num_seqs);
+  if constexpr (FORM == kFormPrefix) {
+    grid.x = p.max_partitions - p.own_partitions;
+    grid.z = prefix_tiles(p.num_seqs, p.q_len, p.num_q_heads / p.num_kv_heads, p.num_groups);
+  }
+  prefill_tc_kernel<D, true, KV, FORM><<<grid, T::threads(KV), T::smem(KV), st>>>(p, nullptr, tk, tv);
   return cudaGetLastError();
 }
 
 // One head_dim of a launch, split (verify rows) or in the planner's tiles.
-template <int D, int KV, bool WIN>
+template <int D, int KV, int FORM>
 cudaError_t prefill_form(const AttnParams& p, const Launch& l, int max_q_len, int32_t* tiles, const CUtensorMap& tk,
                          const CUtensorMap& tv) {
-  return tiles ? prefill_tiles<D, KV, WIN>(p, max_q_len, l.group, tiles, tk, tv, l.stream)
-               : prefill_split<D, KV, WIN>(p, tk, tv, l.stream);
+  return tiles ? prefill_tiles<D, KV, FORM>(p, max_q_len, l.group, tiles, tk, tv, l.stream)
+               : prefill_split<D, KV, FORM>(p, tk, tv, l.stream);
+}
+
+// One split form, for its cache type and head_dim.
+template <int FORM>
+cudaError_t split_any(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv) {
+  const bool wide = l.head_dim == 128;
+  if (!wide && l.head_dim != 64) return cudaErrorInvalidConfiguration;
+  switch (l.kv) {
+    case kKvBf16:
+      return wide ? prefill_split<128, kKvBf16, FORM>(p, tk, tv, l.stream) : prefill_split<64, kKvBf16, FORM>(p, tk, tv, l.stream);
+    case kKvE4m3:
+      return wide ? prefill_split<128, kKvE4m3, FORM>(p, tk, tv, l.stream) : prefill_split<64, kKvE4m3, FORM>(p, tk, tv, l.stream);
+    default:
+      return wide ? prefill_split<128, kKvFp4, FORM>(p, tk, tv, l.stream) : prefill_split<64, kKvFp4, FORM>(p, tk, tv, l.stream);
+  }
 }
 
 }  // namespace

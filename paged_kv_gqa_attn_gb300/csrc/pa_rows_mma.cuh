@@ -29,6 +29,8 @@
 // Masks: a page that every row sees whole is the fast path; pages at the causal edge, at an edge of the
 // window or of the sinks, and tree masks test each (row, token).  Tokens that no row sees have their V
 // zeroed, whatever is stored there.
+//
+// Listed blocks, a sequence's own tokens behind a shared prefix, kept scores: as in the decode kernel.
 #pragma once
 
 #include "pa_fp4.cuh"
@@ -199,11 +201,14 @@ struct RowsMask {
   }
 };
 
-template <int D, int NT, int KV, bool WIN>
+template <int D, int NT, int KV, int FORM>
 __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits<D, NT, KV>::kMinBlocks))
     rows_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv) {
   using T = RowsTraits<D, NT, KV>;
+  constexpr bool LIST = FORM == kFormBlocks, OWN = FORM == kFormOwn, SCORES = FORM == kFormScores;
+  constexpr bool WIN = FORM == kFormWindow || OWN;  // pages numbered with a gap
+  constexpr bool kIdsAhead = !WIN && !LIST;         // the first block ids depend on the partition only
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -218,9 +223,14 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
   const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
   // without a window the first block ids depend on the partition only: load them with the length
   const int row0 = page_no(lane), row1 = page_no(32 + lane);
-  const int raw0 = !WIN && row0 < p.max_blocks_per_seq ? bt[row0] : -1;
-  const int raw1 = !WIN && row1 < p.max_blocks_per_seq ? bt[row1] : -1;
-  const int L = context_len(p, b, part == 0 && g == 0 && threadIdx.x == 0);
+  const int raw0 = kIdsAhead && row0 < p.max_blocks_per_seq ? bt[row0] : -1;
+  const int raw1 = kIdsAhead && row1 < p.max_blocks_per_seq ? bt[row1] : -1;
+  int L = context_len(p, b, part == 0 && g == 0 && threadIdx.x == 0);
+  int prefix = 0;
+  if constexpr (OWN) {
+    prefix = prefix_of(p, b);
+    if (!own_tokens_fit(p, L, prefix)) L = 0;
+  }
   const int first_new = L - p.q_len;
 
   if (first_new < 0 && part == 0 && threadIdx.x == 0) record_error(p.err, kErrShortContext);
@@ -232,14 +242,16 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
       }
     return;
   }
-  const int lo_first = WIN ? max(0, first_new + 1 - p.window) : 0;  // window begin of the first row
-  const int lo_last = WIN ? max(0, L - p.window) : 0;               // and of the last
-  PageSpan span = {0, 0, (L + T::kBS - 1) / T::kBS};
+  const int lo_first = OWN ? prefix : WIN ? max(0, first_new + 1 - p.window) : 0;  // window begin of the first row
+  const int lo_last = OWN ? prefix : WIN ? max(0, L - p.window) : 0;               // and of the last
+  const int ncols = (L + T::kBS - 1) / T::kBS;
+  PageSpan span = {0, 0, ncols};
   if constexpr (WIN) span = page_span(span.count, lo_first, p.sinks, 1);
-  const int npages = span.count;  // pages that some row sees
+  const int npages = LIST ? p.num_listed : span.count;  // pages that some row sees (or that the list has room for)
   if (pbeg >= npages) return;
   const int pend = min(npages, pbeg + ppp);
-  const int nparts = (npages + ppp - 1) / ppp;
+  const int nparts = (npages + ppp - 1) / ppp + (OWN && prefix > 0 ? 1 : 0);  // (with a prefix: always partial)
+  const int32_t* list = LIST ? p.blocks + ((size_t)b * Hkv + g) * p.num_listed : nullptr;
   RowsMask mask = {p.tree_mask ? p.tree_mask + (size_t)b * p.q_len : nullptr, first_new, p.sinks, p.window};
 
   if (!T::kFp4 && threadIdx.x == 0) {
@@ -258,16 +270,22 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
   __syncwarp();
 
   // block ids (E4M3: and scales) of the warp's pages, two windows of 32 in lane registers
-  auto load_window = [&](int jb) {
+  auto load_window = [&](int jb, int& col) {
     const int v = page_no(jb + lane);
+    if constexpr (LIST) {
+      col = v < pend ? list[v] : -1;
+      if (col < 0) return kNoBlock;
+      return col < ncols ? max(bt[col], -1) : -1;
+    }
     return v < pend ? bt[WIN ? span.real(v) : v] : -1;
   };
   auto load_scale = [&](const float* sc, int id) {
     return (T::kFp8 && id >= 0 && id < p.num_blocks) ? sc[(size_t)id * Hkv + g] : 1.f;
   };
   int wb = 0;
-  int idw0 = WIN ? load_window(0) : row0 < pend ? raw0 : -1;
-  int idw1 = WIN ? load_window(32) : row1 < pend ? raw1 : -1;
+  int col0 = -1, col1 = -1;  // listed blocks: the columns
+  int idw0 = !kIdsAhead ? load_window(0, col0) : row0 < pend ? raw0 : -1;
+  int idw1 = !kIdsAhead ? load_window(32, col1) : row1 < pend ? raw1 : -1;
   float ksw0 = load_scale(p.k_scale, idw0), vsw0 = load_scale(p.v_scale, idw0);
   float ksw1 = load_scale(p.k_scale, idw1), vsw1 = load_scale(p.v_scale, idw1);
   auto id_of = [&](int j) {  // j in [wb, wb + 64), warp-uniform
@@ -289,7 +307,8 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
     for (int pp = 0; pp < T::kPP; ++pp) {
       ids[pp] = id_of(k * T::kPP + pp);
       ok[pp] = (unsigned)ids[pp] < (unsigned)p.num_blocks;
-      if (!ok[pp] && lane == 0 && page_no(k * T::kPP + pp) < pend) record_error(p.err, kErrBlockId);
+      if (!ok[pp] && lane == 0 && page_no(k * T::kPP + pp) < pend && (!LIST || ids[pp] != kNoBlock))
+        record_error(p.err, kErrBlockId);
     }
     const int s = k % T::kStages;
     const uint32_t stage = smem_addr(stages + s * T::kStageBytes);
@@ -408,7 +427,8 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
     if (k * T::kPP == wb + 32) {  // slide the windows (the issue below looks at most kStages ahead)
       wb += 32;
       idw0 = idw1;
-      idw1 = load_window(wb + 32);
+      col0 = col1;
+      idw1 = load_window(wb + 32, col1);
       if constexpr (T::kFp8) {
         ksw0 = ksw1;
         vsw0 = vsw1;
@@ -426,7 +446,9 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
       const int pb = id_of(k * T::kPP + pp);
       const bool ok = pb >= 0 && pb < p.num_blocks;
       const int v_at = page_no(k * T::kPP + pp);
-      tok0[pp] = (WIN ? span.real(v_at) : v_at) * T::kBS;
+      int col = WIN ? span.real(v_at) : v_at;
+      if constexpr (LIST) col = __shfl_sync(0xffffffffu, col0, k * T::kPP + pp - wb);
+      tok0[pp] = col * T::kBS;
       const bool all = ok && tok0[pp] + T::kBS <= first_new + (mask.tree ? 0 : 1) &&
                        (!WIN || tok0[pp] >= lo_last || tok0[pp] + T::kBS <= p.sinks);
       live[pp] = 0xffffu;
@@ -474,8 +496,15 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
 #pragma unroll
         for (int pp = 0; pp < T::kPP; ++pp) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (SCORES) {  // (no new row but the last: every token before the context's end is seen)
+              const int c = 8 * nt + 2 * qi + (e & 1), t = gi + 8 * (e >> 1);
+              if (((live[pp] >> t) & 1u) && c < R)
+                p.scores[(((size_t)b * Hkv + g) * p.max_context_len + tok0[pp] + t) * G + c] =
+                    x[pp][nt][e] * (T::kFp8 ? mul[nt][e & 1] * ks : mul[nt][e & 1]);
+            }
             x[pp][nt][e] = T::kFp8 ? fmaf(x[pp][nt][e], mul[nt][e & 1] * ks, vf.lv) : x[pp][nt][e] * mul[nt][e & 1];
+          }
           if (!whole) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -644,6 +673,7 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
     const size_t row = ((size_t)b * p.q_len + c / G) * Hq + g * G + c % G;
     if (nparts == 1) {
       *reinterpret_cast<uint2*>(p.out + row * D + dd) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+      if (SCORES && dd == 0) p.lse[row] = M + __log2f(lsum);
     } else {
       const size_t at = row * p.max_partitions + part;
       *reinterpret_cast<float4*>(p.part_o + at * D + dd) = acc;
@@ -652,26 +682,39 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
   }
 }
 
-template <int D, int NT, int KV, bool WIN>
+template <int D, int NT, int KV, int FORM>
 cudaError_t rows_launch(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   using T = RowsTraits<D, NT, KV>;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(rows_mma_kernel<D, NT, KV, WIN>), T::kSmem);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(rows_mma_kernel<D, NT, KV, FORM>), T::kSmem);
   if (e != cudaSuccess) return e;
-  dim3 grid(p.max_partitions, p.num_kv_heads, p.num_seqs);
-  rows_mma_kernel<D, NT, KV, WIN><<<grid, T::kThreads, T::kSmem, st>>>(p, tk, tv);
+  dim3 grid(FORM == kFormOwn ? p.own_partitions : p.max_partitions, p.num_kv_heads, p.num_seqs);
+  rows_mma_kernel<D, NT, KV, FORM><<<grid, T::kThreads, T::kSmem, st>>>(p, tk, tv);
   return cudaGetLastError();
 }
 
-template <int D, int KV, bool WIN>
+template <int D, int KV, int FORM>
 cudaError_t rows_tiles(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv) {
   const int nt = (l.group * p.q_len + 7) / 8;
-  if (nt == 1) return rows_launch<D, 1, KV, WIN>(p, tk, tv, l.stream);
-  if (nt == 2) return rows_launch<D, 2, KV, WIN>(p, tk, tv, l.stream);
-  if constexpr (KV != kKvBf16) {  // (more bf16 rows run the tile kernel)
-    if (nt == 3) return rows_launch<D, 3, KV, WIN>(p, tk, tv, l.stream);
-    if (nt == 4) return rows_launch<D, 4, KV, WIN>(p, tk, tv, l.stream);
+  if (nt == 1) return rows_launch<D, 1, KV, FORM>(p, tk, tv, l.stream);
+  if (nt == 2) return rows_launch<D, 2, KV, FORM>(p, tk, tv, l.stream);
+  // (more bf16 rows run the tile kernel, which takes no list and keeps no scores)
+  if constexpr (KV != kKvBf16 || FORM == kFormBlocks || FORM == kFormScores) {
+    if (nt == 3) return rows_launch<D, 3, KV, FORM>(p, tk, tv, l.stream);
+    if (nt == 4) return rows_launch<D, 4, KV, FORM>(p, tk, tv, l.stream);
   }
   return cudaErrorInvalidConfiguration;
+}
+
+// One form of the rows kernel, for its cache type and head_dim.
+template <int FORM>
+cudaError_t rows_any(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv) {
+  const bool wide = l.head_dim == 128;
+  if (!wide && l.head_dim != 64) return cudaErrorInvalidConfiguration;
+  switch (l.kv) {
+    case kKvBf16: return wide ? rows_tiles<128, kKvBf16, FORM>(p, l, tk, tv) : rows_tiles<64, kKvBf16, FORM>(p, l, tk, tv);
+    case kKvE4m3: return wide ? rows_tiles<128, kKvE4m3, FORM>(p, l, tk, tv) : rows_tiles<64, kKvE4m3, FORM>(p, l, tk, tv);
+    default: return wide ? rows_tiles<128, kKvFp4, FORM>(p, l, tk, tv) : rows_tiles<64, kKvFp4, FORM>(p, l, tk, tv);
+  }
 }
 
 }  // namespace

@@ -6,9 +6,9 @@ namespace pa {
 
 cudaError_t rows_window_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv) {
   if (l.head_dim == 128)
-    return l.fp8 ? rows_tiles<128, kKvE4m3, true>(p, l, tk, tv) : rows_tiles<128, kKvBf16, true>(p, l, tk, tv);
+    return l.fp8 ? rows_tiles<128, kKvE4m3, kFormWindow>(p, l, tk, tv) : rows_tiles<128, kKvBf16, kFormWindow>(p, l, tk, tv);
   if (l.head_dim == 64)
-    return l.fp8 ? rows_tiles<64, kKvE4m3, true>(p, l, tk, tv) : rows_tiles<64, kKvBf16, true>(p, l, tk, tv);
+    return l.fp8 ? rows_tiles<64, kKvE4m3, kFormWindow>(p, l, tk, tv) : rows_tiles<64, kKvBf16, kFormWindow>(p, l, tk, tv);
   return cudaErrorInvalidConfiguration;
 }
 

@@ -1,0 +1,223 @@
+// Selection of the cache blocks that a step's queries should read: a cheap score for each block, the highest kept.
+//
+// A query row is rounded to int8 codes times a power of two 2^f, a block's bounds are int8 codes times 2^e
+// (pa_bounds.cu), and its score for the row is 2^f 2^e sum_i max(c_i hi_i, c_i lo_i): with c+ = max(c, 0) and c- = min(c, 0)
+// a product of [c+ | c-] with [hi | lo], 2 d long.  That is a matrix product of 16 blocks by 8 rows on the tensor
+// cores' int8 form, exact in int32 and, below 2^22, exact in fp32: no rounding anywhere, so the selection does not depend
+// on how it is computed.  A block counts for a kv head with its best row.
+//
+// Scores: a warp takes 16 blocks of one (sequence, kv head) at a time, straight from global memory into A fragments (the
+// contraction's order is free: a lane reads whole 16-byte pieces, and the rows' codes are laid out alike once per warp).
+// Bound by the bounds' bytes.  Selection: one CTA per (sequence, kv head), see pa_topk.cuh.
+#include "pa_kernels.h"
+#include "pa_tc.cuh"
+#include "pa_topk.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kScoreWarps = 4;
+
+// D[16x8] += A[16x32] . B[32x8], int8 operands, int32 accumulators (warp-collective).
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// e of the int8 codes of numbers up to amax: the smallest with amax 2^-e <= 127, at least -126.
+__device__ __forceinline__ int code_exp(float amax) {
+  const uint32_t bits = __float_as_uint(fminf(amax, 3.4028235e38f));
+  const int e = (int)(bits >> 23) - 127 - 6 + ((bits & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+  return bits == 0 ? 0 : max(e, -126);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const SelectParams p, int tiles_per_warp) {
+  constexpr int kChunks = D / 64;  // 16-byte pieces of a lane in each half ([hi] and [lo]) of a row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gi = lane >> 2, qi = lane & 3;
+  const int g = blockIdx.y, b = blockIdx.z;
+  const int Hkv = p.num_kv_heads, G = p.num_q_heads / Hkv, R = p.q_len * G;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int L = max(0, min(p.context_lens[b], p.max_context_len));
+  if (p.context_lens[b] > p.max_context_len && blockIdx.x == 0 && g == 0 && threadIdx.x == 0)
+    record_error(p.err, kErrShortContext);
+  const int ncols = (L + 15) / 16;
+  const int tile0 = (blockIdx.x * kScoreWarps + warp) * tiles_per_warp;
+  if (tile0 * 16 >= ncols) return;
+
+  // B fragments: the codes of row gi of each n-tile, pieces qi and qi + 4 of its d dims, positive and negative parts
+  uint32_t qp[NT][kChunks][4], qn[NT][kChunks][4];
+  float up[NT][2];  // 2^f of rows 2qi, 2qi + 1
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int c = 8 * nt + gi;
+    const bool real = c < R;
+    const __nv_bfloat16* row =
+        p.q + (((size_t)b * p.q_len + (real ? c / G : 0)) * p.num_q_heads + g * G + (real ? c % G : 0)) * D;
+    uint32_t x[kChunks][8];
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const uint4* src = reinterpret_cast<const uint4*>(row + (qi + 4 * k) * 16);
+      const uint4 a = real ? src[0] : make_uint4(0u, 0u, 0u, 0u), d = real ? src[1] : make_uint4(0u, 0u, 0u, 0u);
+      x[k][0] = a.x; x[k][1] = a.y; x[k][2] = a.z; x[k][3] = a.w;
+      x[k][4] = d.x; x[k][5] = d.y; x[k][6] = d.z; x[k][7] = d.w;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 f = bf16x2_to_f2(x[k][j]);
+        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int f = code_exp(amax);
+    const float down = exp2_int(-f);
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t pos = 0u, neg = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = bf16x2_to_f2(x[k][2 * w + e / 2]);
+          const int code = (int)fminf(fmaxf(rintf((e & 1 ? v.y : v.x) * down), -127.f), 127.f);
+          pos |= (uint32_t)(max(code, 0) & 0xff) << (8 * e);
+          neg |= (uint32_t)(min(code, 0) & 0xff) << (8 * e);
+        }
+        qp[nt][k][w] = pos;
+        qn[nt][k][w] = neg;
+      }
+    up[nt][0] = exp2_int(__shfl_sync(0xffffffffu, f, (2 * qi) * 4));
+    up[nt][1] = exp2_int(__shfl_sync(0xffffffffu, f, (2 * qi + 1) * 4));
+  }
+
+  const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
+  float* out = p.scores + ((size_t)b * Hkv + g) * p.max_cols;
+  auto id_at = [&](int col) { return col < ncols ? bt[col] : -1; };
+  int id0 = id_at(tile0 * 16 + gi), id1 = id_at(tile0 * 16 + gi + 8);
+  for (int t = 0; t < tiles_per_warp; ++t) {
+    const int col0 = (tile0 + t) * 16;
+    if (col0 >= ncols) break;
+    const bool ok0 = id0 >= 0 && id0 < p.num_blocks, ok1 = id1 >= 0 && id1 < p.num_blocks;
+    if (((!ok0 && col0 + gi < ncols) || (!ok1 && col0 + gi + 8 < ncols)) && qi == 0) record_error(p.err, kErrBlockId);
+    const size_t page0 = (size_t)(ok0 ? id0 : 0) * Hkv + g, page1 = (size_t)(ok1 ? id1 : 0) * Hkv + g;
+    const uint4* r0 = reinterpret_cast<const uint4*>(p.bounds + page0 * (2 * D)) + qi;
+    const uint4* r1 = reinterpret_cast<const uint4*>(p.bounds + page1 * (2 * D)) + qi;
+    uint4 a0[2 * kChunks], a1[2 * kChunks];
+#pragma unroll
+    for (int k = 0; k < 2 * kChunks; ++k) {  // upper, then lower codes: pieces qi, qi + 4, ...
+      a0[k] = r0[4 * k];
+      a1[k] = r1[4 * k];
+    }
+    const float s0 = p.bound_scale[page0], s1 = p.bound_scale[page1];
+    id0 = id_at(col0 + 16 + gi);
+    id1 = id_at(col0 + 24 + gi);
+    float best0 = -INFINITY, best1 = -INFINITY;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      int acc[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < 2 * kChunks; ++k) {
+        const uint32_t(&q)[4] = k < kChunks ? qp[nt][k] : qn[nt][k - kChunks];
+        mma_s8(acc, a0[k].x, a1[k].x, a0[k].y, a1[k].y, q[0], q[1]);
+        mma_s8(acc, a0[k].z, a1[k].z, a0[k].w, a1[k].w, q[2], q[3]);
+      }
+      // acc[0..1]: block gi, rows 2qi, 2qi + 1; acc[2..3]: block gi + 8
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (8 * nt + 2 * qi + e < R) {
+          best0 = fmaxf(best0, (float)acc[e] * up[nt][e]);
+          best1 = fmaxf(best1, (float)acc[e + 2] * up[nt][e]);
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      best0 = fmaxf(best0, __shfl_xor_sync(0xffffffffu, best0, o));
+      best1 = fmaxf(best1, __shfl_xor_sync(0xffffffffu, best1, o));
+    }
+    if (qi == 0) {  // (a block that is not there comes last)
+      if (col0 + gi < ncols) out[col0 + gi] = ok0 ? best0 * s0 : -INFINITY;
+      if (col0 + gi + 8 < ncols) out[col0 + gi + 8] = ok1 ? best1 * s1 : -INFINITY;
+    }
+  }
+}
+
+// One CTA per (kv head, sequence).  IN_SMEM: the keys are kept in shared memory, else turned in place in the scores.
+template <bool IN_SMEM>
+__global__ void __launch_bounds__(1024) block_pick_kernel(const SelectParams p) {
+  extern __shared__ uint32_t smem_keys[];
+  __shared__ TopkShared sh;
+  const int g = blockIdx.x, b = blockIdx.y;
+  const int L = max(0, min(p.context_lens[b], p.max_context_len));
+  const int n = (L + 15) / 16;
+  int32_t* out = p.blocks + ((size_t)b * p.num_kv_heads + g) * p.count;
+  const int k = min(n, p.count);
+  for (int i = k + threadIdx.x; i < p.count; i += blockDim.x) out[i] = -1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (n <= p.count) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) out[i] = i;
+    return;
+  }
+  float* scores = p.scores + ((size_t)b * p.num_kv_heads + g) * p.max_cols;
+  uint32_t* keys = IN_SMEM ? smem_keys : reinterpret_cast<uint32_t*>(scores);
+  for (int i = threadIdx.x; i < n; i += blockDim.x)
+    keys[i] = i < p.sinks || i >= n - p.recent ? kKeyAlways : order_key(scores[i]);
+  __syncthreads();
+  topk_in_order(keys, n, k, sh, [&](int at, int i) { out[at] = i; });
+}
+
+constexpr int kPickSmemCols = 50000;  // keys that fit in shared memory
+
+template <int D, int NT>
+cudaError_t score(const SelectParams& p, int num_sms, cudaStream_t st) {
+  // enough warps to fill the device several times over where there are that many blocks; else a tile a warp
+  const int64_t tiles = (p.max_cols + 15) / 16, units = (int64_t)p.num_seqs * p.num_kv_heads;
+  int64_t per = tiles * units / ((int64_t)num_sms * 32);
+  per = per < 1 ? 1 : per > 8 ? 8 : per;
+  const dim3 grid((unsigned)((tiles + per * kScoreWarps - 1) / (per * kScoreWarps)), p.num_kv_heads, p.num_seqs);
+  block_score_kernel<D, NT><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)per);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t score_rows(const SelectParams& p, int num_sms, cudaStream_t st) {
+  switch ((p.q_len * (p.num_q_heads / p.num_kv_heads) + 7) / 8) {
+    case 1: return score<D, 1>(p, num_sms, st);
+    case 2: return score<D, 2>(p, num_sms, st);
+    case 3: return score<D, 3>(p, num_sms, st);
+    case 4: return score<D, 4>(p, num_sms, st);
+    default: return cudaErrorInvalidConfiguration;
+  }
+}
+
+}  // namespace
+
+size_t select_scratch_bytes(int num_seqs, int num_kv_heads, int max_context_len) {
+  return (size_t)num_seqs * num_kv_heads * (((size_t)max_context_len + 15) / 16 + 1) * sizeof(float);
+}
+
+cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, int num_sms, cudaStream_t st) {
+  if (p.max_cols > 0) {
+    const cudaError_t e = head_dim == 128 ? score_rows<128>(p, num_sms, st)
+                          : head_dim == 64 ? score_rows<64>(p, num_sms, st)
+                                           : cudaErrorInvalidConfiguration;
+    if (e != cudaSuccess) return e;
+  }
+  const bool in_smem = p.max_cols <= kPickSmemCols;
+  const void* fn = in_smem ? reinterpret_cast<const void*>(block_pick_kernel<true>)
+                           : reinterpret_cast<const void*>(block_pick_kernel<false>);
+  const int smem = in_smem ? p.max_cols * 4 : 0;
+  if (in_smem) {
+    const cudaError_t e = set_smem_once(fn, kPickSmemCols * 4);
+    if (e != cudaSuccess) return e;
+  }
+  const int threads = p.max_cols <= 1024 ? 256 : p.max_cols <= 4096 ? 512 : 1024;
+  SelectParams pp = p;
+  void* args[] = {&pp};
+  return launch_dependent(fn, dim3(p.num_kv_heads, p.num_seqs), dim3(threads), smem, st, args);
+}
+
+}  // namespace pa
