@@ -249,7 +249,7 @@ int paged_attn_block_bounds(const void* k_cache, const int32_t* block_table,
 /*
  * The blocks of each sequence that a step's queries should read, by an upper bound of their scores.  A query
  * row is rounded (to nearest even) to int8 codes c times 2^f by the rule of the bounds, f from the row's largest
- * |q|; block j's score for it is 2^f 2^e sum_i max(c_i hi_i, c_i lo_i), and its score for a kv head the
+ * |q|; block j's score for it is 2^f 2^e sum_i (c_i > 0 ? c_i hi_i : c_i lo_i), and its score for a kv head the
  * largest over the head's rows (every new token, every query head of the group).  The sum is a whole number
  * below 2^22: the selection does not depend on the order of the arithmetic.
  *   q            [num_seqs, q_len, num_q_heads, head_dim] bf16, device, 16-byte aligned, finite.
