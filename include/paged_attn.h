@@ -339,7 +339,7 @@ int paged_attn_prefix_verify(const void* q, const void* k_cache, const void* v_c
  *   weights[block, g, slot] = decay * weights[block, g, slot] + sum_h softmax(s_h)_j
  * for every token j of every sequence, h over the query heads of kv head g; the step's own token, j =
  * context_lens[b] - 1, has no sum yet and its slot is set to its weight.
- *   weights      [num_blocks, num_kv_heads, 16] fp32, device: caller-owned, laid out as the cache (the sums of a prompt's tokens
+ *   weights      [num_blocks, num_kv_heads, 16] fp32, device, 16-byte aligned: caller-owned, laid out as the cache (the sums of a prompt's tokens
  *                start at what the caller stores, zeros for instance).  Slots past a context are not touched.
  *   decay        finite; 0 overwrites without reading, 1 adds, less than 1 forgets.
  * Blocks that two sequences of the call share would get both sums in an undefined order: their sums are undefined.

@@ -8,7 +8,9 @@
 // A pass over the keys bound by their bytes: one warp takes the page of one (block, head), all of its loads in flight
 // at once (bf16, d = 128: eight 16-byte pieces a lane), and folds rows in packed 16-bit maxima and minima: E4M3 codes and
 // 4-bit codes times their scales are exact in f16, and the page's (head's) fp32 scale is applied once, at the end, as
-// rounding a product is monotone in its factor.
+// rounding a product is monotone in its factor.  The lanes that hold the same dims of different rows then halve the dims
+// between them at every exchange, so that each ends with d / 32 dims of its own to round (all of them ending with all dims
+// cost 700 instructions a page where this takes 300, and more than half the time).
 #include "pa_fp4.cuh"
 #include "pa_kernels.h"
 #include "pa_tc.cuh"
@@ -48,6 +50,8 @@ struct BoundsTraits {
   static constexpr int kDims = D / kPieces;        // dims of a lane: 8, 16 or 32
   static constexpr int kPairs = kDims / 2;
   static constexpr int kPageBytes = KV == kKvFp4 ? Fp4Page<D>::kBytes : 16 * kRowBytes;
+  static constexpr int kOwnPairs = D / 64;         // of a lane in the end
+  static_assert(kPairs / kRowsAtOnce == kOwnPairs, "the lanes of a piece share its dims");
 };
 
 template <int D, int KV>
@@ -126,50 +130,59 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const B
         lo[j] = min_pair<T::kBf16>(lo[j], v[j]);
       }
     }
+    // lanes of the same piece, o apart: each keeps one half of the pairs it still has and gets the other's of it
+    int kept = 0;  // first pair that the lane keeps
 #pragma unroll
-    for (int o = T::kPieces; o < 32; o <<= 1) {
+    for (int o = 16, left = T::kPairs / 2; o >= T::kPieces; o >>= 1, left >>= 1) {
+      const bool top = (lane & o) != 0;
 #pragma unroll
-      for (int j = 0; j < T::kPairs; ++j) {
-        hi[j] = max_pair<T::kBf16>(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], o));
-        lo[j] = min_pair<T::kBf16>(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], o));
+      for (int j = 0; j < left; ++j) {
+        const uint32_t give_hi = top ? hi[j] : hi[left + j], give_lo = top ? lo[j] : lo[left + j];
+        hi[j] = max_pair<T::kBf16>(top ? hi[left + j] : hi[j], __shfl_xor_sync(0xffffffffu, give_hi, o));
+        lo[j] = min_pair<T::kBf16>(top ? lo[left + j] : lo[j], __shfl_xor_sync(0xffffffffu, give_lo, o));
       }
+      if (top) kept += left;
     }
-    // the value of a pair's element, times the fp32 scale; a negative scale turns the ends round
-    auto value = [&](uint32_t pair, int e) {
-      if constexpr (T::kBf16) return e ? __uint_as_float(pair & 0xffff0000u) : __uint_as_float(pair << 16);
-      const __half2 h = *reinterpret_cast<const __half2*>(&pair);
-      return s * (e ? __high2float(h) : __low2float(h));
-    };
+    // the lane's dims, times the fp32 scale; a negative scale turns the ends round
+    float top[2 * T::kOwnPairs], bottom[2 * T::kOwnPairs];
     float amax = 0.f;
 #pragma unroll
-    for (int j = 0; j < T::kPairs; ++j)
+    for (int j = 0; j < T::kOwnPairs; ++j) {
+      float2 a, c;
+      if constexpr (T::kBf16) {
+        a = bf16x2_to_f2(hi[j]);
+        c = bf16x2_to_f2(lo[j]);
+      } else {
+        a = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
+        c = __half22float2(*reinterpret_cast<const __half2*>(&lo[j]));
+        a = make_float2(a.x * s, a.y * s);
+        c = make_float2(c.x * s, c.y * s);
+      }
+      top[2 * j] = fmaxf(a.x, c.x);
+      top[2 * j + 1] = fmaxf(a.y, c.y);
+      bottom[2 * j] = fminf(a.x, c.x);
+      bottom[2 * j + 1] = fminf(a.y, c.y);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) amax = fmaxf(amax, fmaxf(fabsf(value(hi[j], e)), fabsf(value(lo[j], e))));
-#pragma unroll
-    for (int o = 1; o < T::kPieces; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const uint32_t bits = __float_as_uint(fminf(amax, 3.4028235e38f));  // (a key of infinity: the widest bounds)
+      for (int i = 2 * j; i < 2 * j + 2; ++i) amax = fmaxf(amax, fmaxf(fabsf(top[i]), fabsf(bottom[i])));
+    }
+    // (magnitudes in the order of their bits; an infinity: the widest bounds)
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(fminf(amax, 3.4028235e38f)));
     int e = (int)(bits >> 23) - 127 - 6 + ((bits & 0x7fffffu) > 0x7e0000u ? 1 : 0);  // above 127 / 64: one more
     e = bits == 0 ? 0 : max(e, -126);
     const float down = exp2_int(-e);
-    // lanes of row 0 write the upper codes, those of the last rows the lower ones
-    const bool upper = row0 == 0, lower = row0 == T::kRowsAtOnce - 1;
-    auto code = [&](int j, int e2, bool up) {
-      const float a = value(hi[j], e2) * down, c = value(lo[j], e2) * down;
-      const float y = up ? ceilf(fmaxf(a, c)) : floorf(fminf(a, c));
-      return (uint32_t)(int)fminf(fmaxf(y, -127.f), 127.f) & 0xffu;
-    };
-    int8_t* dst = p.bounds + page * (2 * D) + piece * T::kDims;
+    uint32_t upper = 0u, lower = 0u;
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      if (side == 0 ? !upper : !lower) continue;
-      uint32_t out[T::kPairs / 2];
-#pragma unroll
-      for (int j = 0; j < T::kPairs / 2; ++j)
-        out[j] = code(2 * j, 0, side == 0) | (code(2 * j, 1, side == 0) << 8) | (code(2 * j + 1, 0, side == 0) << 16) |
-                 (code(2 * j + 1, 1, side == 0) << 24);
-#pragma unroll
-      for (int j = 0; j < T::kPairs / 2; j += 2)
-        *reinterpret_cast<uint2*>(dst + side * D + 4 * j) = make_uint2(out[j], out[j + 1]);
+    for (int i = 0; i < 2 * T::kOwnPairs; ++i) {
+      upper |= (uint32_t)(max(-127, min(127, __float2int_ru(top[i] * down))) & 0xff) << (8 * i);
+      lower |= (uint32_t)(max(-127, min(127, __float2int_rd(bottom[i] * down))) & 0xff) << (8 * i);
+    }
+    int8_t* dst = p.bounds + page * (2 * D) + piece * T::kDims + 2 * kept;
+    if constexpr (T::kOwnPairs == 2) {
+      *reinterpret_cast<uint32_t*>(dst) = upper;
+      *reinterpret_cast<uint32_t*>(dst + D) = lower;
+    } else {
+      *reinterpret_cast<uint16_t*>(dst) = (uint16_t)upper;
+      *reinterpret_cast<uint16_t*>(dst + D) = (uint16_t)lower;
     }
     if (lane == 0) p.bound_scale[page] = exp2_int(e);
   }

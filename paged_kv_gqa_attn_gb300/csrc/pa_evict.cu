@@ -60,8 +60,27 @@ __global__ void __launch_bounds__(1024) evict_pick_kernel(const EvictParams p, u
     return;
   }
   uint32_t* keys = keys_global ? keys_global + unit * p.max_context_len : smem_keys;
-  for (int i = threadIdx.x; i < L; i += blockDim.x)
-    keys[i] = i < p.sinks || i >= L - p.recent ? kKeyAlways : order_key(sum_at(i));
+  // the sums, kBatch of a thread in flight at once (their addresses wait for the table)
+  constexpr int kBatch = 8;
+  const int threads = blockDim.x;
+  for (int i0 = threadIdx.x; i0 < L; i0 += kBatch * threads) {
+    int pb[kBatch];
+    float w[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) pb[j] = i0 + j * threads < L ? bt[(i0 + j * threads) / 16] : 0;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * threads;
+      const bool there = pb[j] >= 0 && pb[j] < p.num_blocks;
+      if (!there) record_error(p.err, kErrBlockId);
+      w[j] = there && i < L ? p.weights[((size_t)pb[j] * p.num_kv_heads + g) * 16 + i % 16] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * threads;
+      if (i < L) keys[i] = i < p.sinks || i >= L - p.recent ? kKeyAlways : order_key(w[j]);
+    }
+  }
   __syncthreads();
   if (k > 0) topk_in_order(keys, L, k, sh, take);
 }

@@ -7,8 +7,8 @@
 // on how it is computed.  A block counts for a kv head with its best row.
 //
 // Scores: a warp takes 16 blocks of one (sequence, kv head) at a time, straight from global memory into A fragments (the
-// contraction's order is free: a lane reads whole 16-byte pieces, and the rows' codes are laid out alike once per warp).
-// Bound by the bounds' bytes.  Selection: one CTA per (sequence, kv head), see pa_topk.cuh.
+// contraction's order is free: a lane reads whole 16-byte pieces, and the rows' codes are laid out alike, once for the CTA's
+// warps, in shared memory).  Bound by the bounds' bytes: a warp's next tile is loaded before this one's products.  Selection: one CTA per (sequence, kv head), see pa_topk.cuh.
 #include "pa_kernels.h"
 #include "pa_tc.cuh"
 #include "pa_topk.cuh"
@@ -37,6 +37,8 @@ __device__ __forceinline__ int code_exp(float amax) {
 template <int D, int NT>
 __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const SelectParams p, int tiles_per_warp) {
   constexpr int kChunks = D / 64;  // 16-byte pieces of a lane in each half ([hi] and [lo]) of a row
+  __shared__ uint4 q_frag[NT][2 * kChunks][32];  // B fragments: positive parts, then negative ones
+  __shared__ float q_up[8 * NT];                 // 2^f of each row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gi = lane >> 2, qi = lane & 3;
   const int g = blockIdx.y, b = blockIdx.z;
   const int Hkv = p.num_kv_heads, G = p.num_q_heads / Hkv, R = p.q_len * G;
@@ -45,14 +47,37 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const Sel
   if (p.context_lens[b] > p.max_context_len && blockIdx.x == 0 && g == 0 && threadIdx.x == 0)
     record_error(p.err, kErrShortContext);
   const int ncols = (L + 15) / 16;
-  const int tile0 = (blockIdx.x * kScoreWarps + warp) * tiles_per_warp;
-  if (tile0 * 16 >= ncols) return;
+  if (blockIdx.x * kScoreWarps * tiles_per_warp * 16 >= ncols) return;
 
-  // B fragments: the codes of row gi of each n-tile, pieces qi and qi + 4 of its d dims, positive and negative parts
-  uint32_t qp[NT][kChunks][4], qn[NT][kChunks][4];
-  float up[NT][2];  // 2^f of rows 2qi, 2qi + 1
+  // the warp's tiles, dealt out in turn; the first one's loads start before the rows are rounded
+  const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
+  const int tile0 = blockIdx.x * kScoreWarps * tiles_per_warp + warp;
+  struct Tile {
+    uint4 a0[2 * kChunks], a1[2 * kChunks];  // blocks gi and gi + 8: upper, then lower codes, pieces qi, qi + 4, ...
+    float s0, s1;
+    bool ok0, ok1;
+  };
+  auto id_at = [&](int col) { return col < ncols ? bt[col] : -1; };
+  auto load = [&](Tile& t, int id0, int id1) {
+    t.ok0 = id0 >= 0 && id0 < p.num_blocks;
+    t.ok1 = id1 >= 0 && id1 < p.num_blocks;
+    const size_t page0 = (size_t)(t.ok0 ? id0 : 0) * Hkv + g, page1 = (size_t)(t.ok1 ? id1 : 0) * Hkv + g;
+    const uint4* r0 = reinterpret_cast<const uint4*>(p.bounds + page0 * (2 * D)) + qi;
+    const uint4* r1 = reinterpret_cast<const uint4*>(p.bounds + page1 * (2 * D)) + qi;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+    for (int k = 0; k < 2 * kChunks; ++k) {
+      t.a0[k] = t.ok0 ? r0[4 * k] : make_uint4(0u, 0u, 0u, 0u);
+      t.a1[k] = t.ok1 ? r1[4 * k] : make_uint4(0u, 0u, 0u, 0u);
+    }
+    t.s0 = p.bound_scale[page0];
+    t.s1 = p.bound_scale[page1];
+  };
+  Tile cur;
+  load(cur, id_at(tile0 * 16 + gi), id_at(tile0 * 16 + gi + 8));
+  int id0 = id_at((tile0 + kScoreWarps) * 16 + gi), id1 = id_at((tile0 + kScoreWarps) * 16 + gi + 8);
+
+  // the codes of row gi of each n-tile, pieces qi and qi + 4 of its d dims, positive and negative parts
+  for (int nt = warp; nt < NT; nt += kScoreWarps) {
     const int c = 8 * nt + gi;
     const bool real = c < R;
     const __nv_bfloat16* row =
@@ -76,54 +101,54 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const Sel
     const int f = code_exp(amax);
     const float down = exp2_int(-f);
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k)
+    for (int k = 0; k < kChunks; ++k) {
+      uint32_t pos[4], neg[4];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        uint32_t pos = 0u, neg = 0u;
+        pos[w] = neg[w] = 0u;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 v = bf16x2_to_f2(x[k][2 * w + e / 2]);
-          const int code = (int)fminf(fmaxf(rintf((e & 1 ? v.y : v.x) * down), -127.f), 127.f);
-          pos |= (uint32_t)(max(code, 0) & 0xff) << (8 * e);
-          neg |= (uint32_t)(min(code, 0) & 0xff) << (8 * e);
+          const int code = max(-127, min(127, __float2int_rn((e & 1 ? v.y : v.x) * down)));
+          pos[w] |= (uint32_t)(max(code, 0) & 0xff) << (8 * e);
+          neg[w] |= (uint32_t)(min(code, 0) & 0xff) << (8 * e);
         }
-        qp[nt][k][w] = pos;
-        qn[nt][k][w] = neg;
       }
-    up[nt][0] = exp2_int(__shfl_sync(0xffffffffu, f, (2 * qi) * 4));
-    up[nt][1] = exp2_int(__shfl_sync(0xffffffffu, f, (2 * qi + 1) * 4));
+      q_frag[nt][k][lane] = make_uint4(pos[0], pos[1], pos[2], pos[3]);
+      q_frag[nt][kChunks + k][lane] = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+    }
+    if (qi == 0) q_up[c] = exp2_int(f);
+  }
+  __syncthreads();
+  float up[NT][2];  // of rows 2qi, 2qi + 1
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    up[nt][0] = q_up[8 * nt + 2 * qi];
+    up[nt][1] = q_up[8 * nt + 2 * qi + 1];
   }
 
-  const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
   float* out = p.scores + ((size_t)b * Hkv + g) * p.max_cols;
-  auto id_at = [&](int col) { return col < ncols ? bt[col] : -1; };
-  int id0 = id_at(tile0 * 16 + gi), id1 = id_at(tile0 * 16 + gi + 8);
   for (int t = 0; t < tiles_per_warp; ++t) {
-    const int col0 = (tile0 + t) * 16;
+    const int col0 = (tile0 + t * kScoreWarps) * 16;
     if (col0 >= ncols) break;
-    const bool ok0 = id0 >= 0 && id0 < p.num_blocks, ok1 = id1 >= 0 && id1 < p.num_blocks;
-    if (((!ok0 && col0 + gi < ncols) || (!ok1 && col0 + gi + 8 < ncols)) && qi == 0) record_error(p.err, kErrBlockId);
-    const size_t page0 = (size_t)(ok0 ? id0 : 0) * Hkv + g, page1 = (size_t)(ok1 ? id1 : 0) * Hkv + g;
-    const uint4* r0 = reinterpret_cast<const uint4*>(p.bounds + page0 * (2 * D)) + qi;
-    const uint4* r1 = reinterpret_cast<const uint4*>(p.bounds + page1 * (2 * D)) + qi;
-    uint4 a0[2 * kChunks], a1[2 * kChunks];
-#pragma unroll
-    for (int k = 0; k < 2 * kChunks; ++k) {  // upper, then lower codes: pieces qi, qi + 4, ...
-      a0[k] = r0[4 * k];
-      a1[k] = r1[4 * k];
+    Tile next;
+    const bool more = t + 1 < tiles_per_warp && col0 + kScoreWarps * 16 < ncols;
+    if (more) {
+      load(next, id0, id1);
+      id0 = id_at(col0 + 2 * kScoreWarps * 16 + gi);
+      id1 = id_at(col0 + 2 * kScoreWarps * 16 + gi + 8);
     }
-    const float s0 = p.bound_scale[page0], s1 = p.bound_scale[page1];
-    id0 = id_at(col0 + 16 + gi);
-    id1 = id_at(col0 + 24 + gi);
+    if (((!cur.ok0 && col0 + gi < ncols) || (!cur.ok1 && col0 + gi + 8 < ncols)) && qi == 0)
+      record_error(p.err, kErrBlockId);
     float best0 = -INFINITY, best1 = -INFINITY;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       int acc[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < 2 * kChunks; ++k) {
-        const uint32_t(&q)[4] = k < kChunks ? qp[nt][k] : qn[nt][k - kChunks];
-        mma_s8(acc, a0[k].x, a1[k].x, a0[k].y, a1[k].y, q[0], q[1]);
-        mma_s8(acc, a0[k].z, a1[k].z, a0[k].w, a1[k].w, q[2], q[3]);
+        const uint4 q = q_frag[nt][k][lane];
+        mma_s8(acc, cur.a0[k].x, cur.a1[k].x, cur.a0[k].y, cur.a1[k].y, q.x, q.y);
+        mma_s8(acc, cur.a0[k].z, cur.a1[k].z, cur.a0[k].w, cur.a1[k].w, q.z, q.w);
       }
       // acc[0..1]: block gi, rows 2qi, 2qi + 1; acc[2..3]: block gi + 8
 #pragma unroll
@@ -139,9 +164,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const Sel
       best1 = fmaxf(best1, __shfl_xor_sync(0xffffffffu, best1, o));
     }
     if (qi == 0) {  // (a block that is not there comes last)
-      if (col0 + gi < ncols) out[col0 + gi] = ok0 ? best0 * s0 : -INFINITY;
-      if (col0 + gi + 8 < ncols) out[col0 + gi + 8] = ok1 ? best1 * s1 : -INFINITY;
+      if (col0 + gi < ncols) out[col0 + gi] = cur.ok0 ? best0 * cur.s0 : -INFINITY;
+      if (col0 + gi + 8 < ncols) out[col0 + gi + 8] = cur.ok1 ? best1 * cur.s1 : -INFINITY;
     }
+    if (more) cur = next;
   }
 }
 
@@ -173,10 +199,10 @@ constexpr int kPickSmemCols = 50000;  // keys that fit in shared memory
 
 template <int D, int NT>
 cudaError_t score(const SelectParams& p, int num_sms, cudaStream_t st) {
-  // enough warps to fill the device several times over where there are that many blocks; else a tile a warp
+  // enough warps to fill the device twice over where there are that many blocks; else a tile a warp
   const int64_t tiles = (p.max_cols + 15) / 16, units = (int64_t)p.num_seqs * p.num_kv_heads;
   int64_t per = tiles * units / ((int64_t)num_sms * 32);
-  per = per < 1 ? 1 : per > 8 ? 8 : per;
+  per = per < 1 ? 1 : per > 16 ? 16 : per;
   const dim3 grid((unsigned)((tiles + per * kScoreWarps - 1) / (per * kScoreWarps)), p.num_kv_heads, p.num_seqs);
   block_score_kernel<D, NT><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)per);
   return cudaGetLastError();

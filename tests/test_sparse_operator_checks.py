@@ -86,6 +86,7 @@ def test_prefix_tiles_fit_a_grid_dimension():
 
 @pytest.mark.parametrize("over,status", COMMON + [
     (dict(lead=(None,)), pa.PA_ERR_INVALID_ARG),
+    (dict(lead=(FAKE + 4,)), pa.PA_ERR_INVALID_ARG),
     (dict(tail=(float("nan"),)), pa.PA_ERR_INVALID_ARG),
     (dict(tail=(float("inf"),)), pa.PA_ERR_INVALID_ARG),
     (dict(tail=(-0.5,)), pa.PA_OK),
