@@ -386,7 +386,7 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
       p.page_align = align;
       p.prefix_ppp = 1;
       if (p.num_groups > 0)
-        plan_split(Split::kTiles, kv_dtype, 128, true, dev->num_sms,
+        plan_split(Split::kTiles, kv_dtype, 128, p.num_groups == 1, dev->num_sms,
                    (int64_t)pa::prefix_tiles(num_seqs, q_len, l.group, p.num_groups) * num_kv_heads,
                    p.max_prefix_len / block_size, 4, &p.prefix_ppp, &prefix_parts);
       const int64_t own = (int64_t)p.max_own_len + (align - 1) * block_size;  // (its first pages rounded down)
@@ -399,7 +399,7 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
         if (st != PA_OK) return st;
       } else {
         plan_split(mma_decode ? Split::kDecode : few_rows ? Split::kRows : Split::kTiles, kv_dtype, l.group * q_len,
-                   special && l.form != pa::kFormScores, dev->num_sms, (int64_t)num_seqs * num_kv_heads,
+                   l.form == pa::kFormWindow || l.form == pa::kFormBlocks, dev->num_sms, (int64_t)num_seqs * num_kv_heads,
                    ((int64_t)covered + block_size - 1) / block_size, align, &ppp, &nparts);
       }
     } else {
@@ -444,15 +444,14 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
     if (r1 != PA_OK || r2 != PA_OK)
       e = cudaErrorInvalidValue;
     else {
-      e = prefix_parts > 0 ? pa::launch_prefix(p, l, tk, tv) : cudaSuccess;
-      if (e == cudaSuccess)
-        e = split_tiles                               ? pa::launch_verify_split(p, l, tk, tv)
-            : !few_rows                               ? pa::launch_decode_mma(p, l, tk, tv)
-            : l.form == pa::kFormBlocks               ? pa::rows_blocks_form(p, l, tk, tv)
-            : l.form == pa::kFormOwn                  ? pa::rows_own_form(p, l, tk, tv)
-            : l.form == pa::kFormScores               ? pa::rows_scores_form(p, l, tk, tv)
-            : fp4                                     ? pa::rows_fp4_form(p, l)
-                                                      : pa::rows_window_form(p, l, tk, tv);
+      e = split_tiles                               ? pa::launch_verify_split(p, l, tk, tv)
+          : !few_rows                               ? pa::launch_decode_mma(p, l, tk, tv)
+          : l.form == pa::kFormBlocks               ? pa::rows_blocks_form(p, l, tk, tv)
+          : l.form == pa::kFormOwn                  ? pa::rows_own_form(p, l, tk, tv)
+          : l.form == pa::kFormScores               ? pa::rows_scores_form(p, l, tk, tv)
+          : fp4                                     ? pa::rows_fp4_form(p, l)
+                                                    : pa::rows_window_form(p, l, tk, tv);
+      if (e == cudaSuccess && prefix_parts > 0) e = pa::launch_prefix(p, l, tk, tv);
     }
     if (e == cudaSuccess && nparts > 1) e = pa::launch_merge(p, l);
     if (e == cudaSuccess && l.form == pa::kFormScores) {

@@ -19,6 +19,7 @@ namespace pa {
 namespace {
 
 constexpr int kBoundsWarps = 8;
+constexpr int kBoundsCols = 4;  // columns of a CTA at most
 
 // Folds of 16-bit pairs; a NaN gives way to the other operand.
 template <bool BF16>
@@ -55,7 +56,7 @@ struct BoundsTraits {
 };
 
 template <int D, int KV>
-__global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const BoundsParams p) {
+__global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const BoundsParams p, int cols) {
   using T = BoundsTraits<D, KV>;
   constexpr uint32_t kLowest = T::kBf16 ? 0xff80ff80u : 0xfc00fc00u, kHighest = T::kBf16 ? 0x7f807f80u : 0x7c007c00u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -65,34 +66,47 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const B
     if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) record_error(p.err, kErrShortContext);
     return;
   }
-  const int col = max(0, L - p.n) / 16 + blockIdx.x;
-  if (col * 16 >= L) return;
-  const int pb = p.block_table[(size_t)b * p.max_blocks_per_seq + col];
-  if (pb < 0 || pb >= p.num_blocks) {
-    if (blockIdx.z == 0 && threadIdx.x == 0) record_error(p.err, kErrBlockId);
-    return;
+  const int col0 = max(0, L - p.n) / 16 + blockIdx.x * cols;  // the CTA's columns [col0, col0 + count)
+  const int count = min(cols, (L + 15) / 16 - col0);
+  if (count <= 0) return;
+  int ids[kBoundsCols];
+#pragma unroll
+  for (int c = 0; c < kBoundsCols; ++c) {
+    ids[c] = c < count ? p.block_table[(size_t)b * p.max_blocks_per_seq + col0 + c] : 0;
+    if (ids[c] < 0 || ids[c] >= p.num_blocks) {
+      ids[c] = -1;
+      if (blockIdx.z == 0 && threadIdx.x == 0) record_error(p.err, kErrBlockId);
+    }
   }
-  const int valid = min(16, L - col * 16);
   const int piece = lane % T::kPieces, row0 = lane / T::kPieces;
-  for (int g = blockIdx.z * kBoundsWarps + warp; g < p.num_kv_heads; g += gridDim.z * kBoundsWarps) {
-    const size_t page = (size_t)pb * p.num_kv_heads + g;
-    const uint8_t* src = p.k_cache + page * T::kPageBytes;
+  // a page's loads: its codes (4-bit: and their scales)
+  struct Page {
     uint4 x[T::kLoads];
-    uint32_t sc[T::kLoads];
+    uint32_t sc[KV == kKvFp4 ? T::kLoads : 1];
+    float s;
+  };
+  auto load = [&](Page& q, int c, int g) {
+    const size_t page = (size_t)max(ids[c], 0) * p.num_kv_heads + g;
+    const uint8_t* src = p.k_cache + page * T::kPageBytes;
+    const int valid = ids[c] < 0 ? 0 : min(16, L - (col0 + c) * 16);
 #pragma unroll
     for (int i = 0; i < T::kLoads; ++i) {
       const int r = row0 + i * T::kRowsAtOnce;
-      x[i] = make_uint4(0u, 0u, 0u, 0u);
-      sc[i] = 0u;
       if (r < valid) {
-        x[i] = *reinterpret_cast<const uint4*>(src + r * T::kRowBytes + piece * 16);
+        q.x[i] = *reinterpret_cast<const uint4*>(src + r * T::kRowBytes + piece * 16);
         if constexpr (KV == kKvFp4)
-          sc[i] = *reinterpret_cast<const uint16_t*>(src + Fp4Page<D>::kCodeBytes + r * Fp4Page<D>::kScaleRow + piece * 2);
+          q.sc[i] = *reinterpret_cast<const uint16_t*>(src + Fp4Page<D>::kCodeBytes + r * Fp4Page<D>::kScaleRow + piece * 2);
       }
     }
-    float s = 1.f;
-    if constexpr (KV == kKvE4m3) s = p.k_scale[page];
-    if constexpr (KV == kKvFp4) s = p.k_scale ? p.k_scale[g] : 1.f;
+    q.s = 1.f;
+    if constexpr (KV == kKvE4m3) q.s = p.k_scale[page];
+    if constexpr (KV == kKvFp4) q.s = p.k_scale ? p.k_scale[g] : 1.f;
+  };
+  auto bounds_of = [&](const Page& q, int c, int g) {
+    if (ids[c] < 0) return;
+    const size_t page = (size_t)ids[c] * p.num_kv_heads + g;
+    const int valid = min(16, L - (col0 + c) * 16);
+    const float s = q.s;
     uint32_t hi[T::kPairs], lo[T::kPairs];
 #pragma unroll
     for (int j = 0; j < T::kPairs; ++j) {
@@ -102,7 +116,7 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const B
 #pragma unroll
     for (int i = 0; i < T::kLoads; ++i) {
       if (row0 + i * T::kRowsAtOnce >= valid) continue;
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      const uint32_t w[4] = {q.x[i].x, q.x[i].y, q.x[i].z, q.x[i].w};
       uint32_t v[T::kPairs];
       if constexpr (KV == kKvBf16) {
 #pragma unroll
@@ -114,7 +128,7 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const B
           v[2 * j + 1] = e4m3x2_to_f16x2(w[j] >> 16);
         }
       } else {
-        const uint32_t s2 = e4m3x2_to_f16x2(sc[i]);
+        const uint32_t s2 = e4m3x2_to_f16x2(q.sc[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t h[4];
@@ -185,20 +199,33 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const B
       *reinterpret_cast<uint16_t*>(dst + D) = (uint16_t)lower;
     }
     if (lane == 0) p.bound_scale[page] = exp2_int(e);
+  };
+  for (int g = blockIdx.z * kBoundsWarps + warp; g < p.num_kv_heads; g += gridDim.z * kBoundsWarps) {
+    Page cur, next;
+    load(cur, 0, g);
+#pragma unroll
+    for (int c = 0; c < kBoundsCols; ++c) {  // the next page's loads before this one's arithmetic
+      if (c >= count) break;
+      if (c + 1 < kBoundsCols && c + 1 < count) load(next, c + 1 < kBoundsCols ? c + 1 : 0, g);
+      bounds_of(cur, c, g);
+      cur = next;
+    }
   }
 }
 
 template <int D>
 cudaError_t launch_d(const BoundsParams& p, int kv, cudaStream_t st) {
-  const int cols = min((p.n + 14) / 16 + 1, p.max_blocks_per_seq);  // columns that n tokens touch at most
+  const int touched = min((p.n + 14) / 16 + 1, p.max_blocks_per_seq);  // columns that n tokens touch at most
   const int z = min((p.num_kv_heads + kBoundsWarps - 1) / kBoundsWarps, 64);
-  const dim3 grid(cols, p.num_seqs, z);
+  // several columns a CTA where there are enough of them to fill the device all the same (152 SMs of three or four CTAs)
+  const int cols = (int64_t)touched * p.num_seqs * z >= 152 * 4 * kBoundsCols ? kBoundsCols : 1;
+  const dim3 grid((touched + cols - 1) / cols, p.num_seqs, z);
   if (kv == kKvBf16)
-    block_bounds_kernel<D, kKvBf16><<<grid, kBoundsWarps * 32, 0, st>>>(p);
+    block_bounds_kernel<D, kKvBf16><<<grid, kBoundsWarps * 32, 0, st>>>(p, cols);
   else if (kv == kKvE4m3)
-    block_bounds_kernel<D, kKvE4m3><<<grid, kBoundsWarps * 32, 0, st>>>(p);
+    block_bounds_kernel<D, kKvE4m3><<<grid, kBoundsWarps * 32, 0, st>>>(p, cols);
   else
-    block_bounds_kernel<D, kKvFp4><<<grid, kBoundsWarps * 32, 0, st>>>(p);
+    block_bounds_kernel<D, kKvFp4><<<grid, kBoundsWarps * 32, 0, st>>>(p, cols);
   return cudaGetLastError();
 }
 

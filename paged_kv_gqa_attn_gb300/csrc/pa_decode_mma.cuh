@@ -110,6 +110,8 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
   const int part = blockIdx.x;
   const int g = blockIdx.y;
   const int b = blockIdx.z;
+  // the kernel over the prefixes, or the merge, may take the room that this grid leaves
+  if constexpr (OWN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int Hq = p.num_q_heads;
   // The first two windows of block ids (below) depend only on the partition, not on the context
   // length: load them together with it, bounded by the table row, and mask them once it arrives.
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
   }
 
   // the merge kernel (launched as a programmatic dependent) may start its prologue now
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (!OWN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // sums over the 8 row groups (each thread summed its own tokens)
 #pragma unroll

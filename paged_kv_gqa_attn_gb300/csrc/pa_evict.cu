@@ -41,28 +41,41 @@ __global__ void __launch_bounds__(1024) evict_pick_kernel(const EvictParams p, u
     if (p.context_lens[b] > p.max_context_len) record_error(p.err, kErrShortContext);
   }
   int32_t* kept = p.kept + unit * p.keep;
-  auto sum_at = [&](int i) {
-    const int pb = bt[i / 16];
-    if (pb < 0 || pb >= p.num_blocks) {
-      record_error(p.err, kErrBlockId);
-      return 0.f;
+  // the sums of k kept positions (pos(at) ascending) go to the new blocks, kMoves of a thread in flight at once
+  constexpr int kMoves = 4;
+  const int threads = blockDim.x;
+  auto move_sums = [&](auto pos) {
+    for (int a0 = threadIdx.x; a0 < k; a0 += kMoves * threads) {
+      int from[kMoves], i[kMoves];
+      float w[kMoves];
+#pragma unroll
+      for (int j = 0; j < kMoves; ++j) i[j] = a0 + j * threads < k ? pos(a0 + j * threads) : 0;
+#pragma unroll
+      for (int j = 0; j < kMoves; ++j) from[j] = bt[i[j] / 16];
+#pragma unroll
+      for (int j = 0; j < kMoves; ++j) {
+        const bool there = from[j] >= 0 && from[j] < p.num_blocks;
+        if (!there) record_error(p.err, kErrBlockId);
+        w[j] = there ? p.weights[((size_t)from[j] * p.num_kv_heads + g) * 16 + i[j] % 16] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kMoves; ++j) {
+        const int at = a0 + j * threads;
+        if (at >= k) continue;
+        const int pb = to[at / 16];
+        if (pb >= 0 && pb < p.num_blocks)  // (out of range: flagged by the kernel that moves the rows)
+          p.weights[((size_t)pb * p.num_kv_heads + g) * 16 + at % 16] = w[j];
+      }
     }
-    return p.weights[((size_t)pb * p.num_kv_heads + g) * 16 + i % 16];
-  };
-  auto take = [&](int at, int i) {
-    kept[at] = i;
-    const int pb = to[at / 16];
-    if (pb >= 0 && pb < p.num_blocks)  // (out of range: flagged by the kernel that moves the rows)
-      p.weights[((size_t)pb * p.num_kv_heads + g) * 16 + at % 16] = sum_at(i);
   };
   if (L <= p.keep) {
-    for (int i = threadIdx.x; i < L; i += blockDim.x) take(i, i);
+    for (int i = threadIdx.x; i < L; i += threads) kept[i] = i;
+    move_sums([](int at) { return at; });
     return;
   }
   uint32_t* keys = keys_global ? keys_global + unit * p.max_context_len : smem_keys;
   // the sums, kBatch of a thread in flight at once (their addresses wait for the table)
   constexpr int kBatch = 8;
-  const int threads = blockDim.x;
   for (int i0 = threadIdx.x; i0 < L; i0 += kBatch * threads) {
     int pb[kBatch];
     float w[kBatch];
@@ -82,7 +95,9 @@ __global__ void __launch_bounds__(1024) evict_pick_kernel(const EvictParams p, u
     }
   }
   __syncthreads();
-  if (k > 0) topk_in_order(keys, L, k, sh, take);
+  topk_in_order(keys, L, k, sh, [&](int at, int i) { kept[at] = i; });
+  __syncthreads();  // (the CTA's own writes)
+  move_sums([&](int at) { return kept[at]; });
 }
 
 // A warp moves the page (new block, head): lane t < 16 knows where token t comes from.

@@ -96,8 +96,12 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttnParams p) {
   else
     merge_partitions<D, 32>(lse, po, nparts, lane, M, wsum, acc);
   if constexpr (FORM == kFormOwn) {
-    if (prefix_parts > 0)
-      merge_partitions<D, 8>(lse + p.own_partitions, po + (size_t)p.own_partitions * D, prefix_parts, lane, M, wsum, acc);
+    lse += p.own_partitions;
+    po += (size_t)p.own_partitions * D;
+    if (prefix_parts > 8)
+      merge_partitions<D, 32>(lse, po, prefix_parts, lane, M, wsum, acc);
+    else if (prefix_parts > 0)
+      merge_partitions<D, 8>(lse, po, prefix_parts, lane, M, wsum, acc);
   }
   if (FORM == kFormScores && lane == 0) p.lse[row] = M + __log2f(wsum);
   __nv_bfloat16* dst = p.out + row * D + lane * kDPL;

@@ -192,7 +192,16 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     qs = p.query_start_loc[b];
     QL = p.query_start_loc[b + 1] - qs;
   }
-  if (PREFIX && b < 0) return;  // fewer tiles than the grid's bound
+  // Shared prefixes: a programmatic dependent of the grid over the own tokens, which it does not read from; its first CTA
+  // ends after that grid, so that what waits for this one (the merge) has both.
+  auto after_own_tokens = [&] {
+    if (PREFIX && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
+  if (PREFIX && b < 0) {  // fewer tiles than the grid's bound
+    after_own_tokens();
+    return;
+  }
+  if constexpr (OWN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -1249,6 +1258,7 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(T::kTmemCols) : "memory");
   }
+  after_own_tokens();
 #ifdef PA_TIMELINE
   if (threadIdx.x == 0) pf_tl_put(1, pf_gtime());
 #endif
@@ -1276,12 +1286,18 @@ cudaError_t prefill_tiles(const AttnParams& p, int max_q_len, int group, int32_t
 template <int D, int KV, int FORM>
 cudaError_t prefill_split(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   using T = PfTraits<D>;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(prefill_tc_kernel<D, true, KV, FORM>), T::smem(KV));
+  const void* fn = reinterpret_cast<const void*>(prefill_tc_kernel<D, true, KV, FORM>);
+  cudaError_t e = set_smem_once(fn, T::smem(KV));
   if (e != cudaSuccess) return e;
   dim3 grid(FORM == kFormOwn ? p.own_partitions : p.max_partitions, p.num_kv_heads, p.num_seqs);
   if constexpr (FORM == kFormPrefix) {
     grid.x = p.max_partitions - p.own_partitions;
     grid.z = prefix_tiles(p.num_seqs, p.q_len, p.num_q_heads / p.num_kv_heads, p.num_groups);
+    AttnParams pp = p;
+    const int32_t* none = nullptr;
+    CUtensorMap k = tk, v = tv;
+    void* args[] = {&pp, &none, &k, &v};
+    return launch_pdl(fn, grid, dim3(T::threads(KV)), T::smem(KV), st, args);
   }
   prefill_tc_kernel<D, true, KV, FORM><<<grid, T::threads(KV), T::smem(KV), st>>>(p, nullptr, tk, tv);
   return cudaGetLastError();

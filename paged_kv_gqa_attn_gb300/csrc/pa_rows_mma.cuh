@@ -214,6 +214,8 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gi = lane >> 2, qi = lane & 3;
   const int part = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+  // the kernel over the prefixes, or the merge, may take the room that this grid leaves
+  if constexpr (OWN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, G = Hq / Hkv;
   const int R = p.q_len * G;  // columns in use
   const int ppp = p.pages_per_partition;
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
     __syncwarp();
   }
   // the merge kernel (launched as a programmatic dependent) may start its prologue now
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (!OWN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   __syncthreads();  // every warp is done with its stages
   float* wacc = reinterpret_cast<float*>(smem);   // [kWarps][kCols][D]

@@ -1,12 +1,11 @@
 // The k largest of n numbers by one CTA, in the order of their indices (sm_103a).
 //
-// Numbers become unsigned keys of the same order.  The k-th largest key is found eight bits at a time from the top:
-// a histogram of the next digit over the keys that agree with what is known so far, in shared memory with four counters
-// a digit (a lane takes one by its number, so that keys of one digit, the usual case in the first pass, meet a quarter
-// as often), and one warp's scan from the highest digit down.  A digit whose keys are all taken ends it early; equal keys at the
-// border run to the last digit and are then taken from the lowest index on.  Counts are whole numbers: nothing depends on an
-// order of atomics.  (Two bits a round by counting keys at or above three candidates: 20 us where this takes 9, 512
-// lists of up to 2048 keys; 80 and 30 for 128 of up to 32768.)
+// Numbers become unsigned keys of the same order.  The k-th largest key is found eight bits at a time, from the highest bit
+// in which the keys differ (scores of one query have the same sign and nearly the same exponent: from bit 31 all of
+// them would meet in one counter): a histogram of the next digit over the keys that agree with what is known so far, in
+// shared memory with four counters a digit (a lane takes one by its number), and one warp's scan from the highest digit down.  A
+// digit whose keys are all taken ends it early; equal keys at the border run to the last bit and are then taken from
+// the lowest index on.  Counts are whole numbers: nothing depends on an order of atomics.
 #pragma once
 
 #include <stdint.h>
@@ -24,23 +23,57 @@ struct TopkShared {
   alignas(16) int hist[256 * 4];
   int warp_gt[32], warp_eq[32];
   int digit, above, at;  // the digit of the k-th key, and how many candidates lie above it and at it
+  uint32_t top, bottom;  // the largest and the smallest key that is not kKeyAlways, and how many are
+  int always;
 };
 
 // keys[0, n) in shared or global memory, written before a barrier; every thread of the CTA (a multiple of 32, at most
-// 1024) calls this with 0 < k < n.  Calls take(position, index) for each key taken, positions 0 .. k - 1 in
-// the order of the indices.
+// 1024) calls this with 0 < k < n, and at most k keys kKeyAlways.  Calls take(position, index) for each key taken, positions
+// 0 .. k - 1 in the order of the indices.
 template <class Take>
 __device__ __forceinline__ void topk_in_order(const uint32_t* keys, int n, int k, TopkShared& sh, Take take) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
-  uint32_t low = 0u, known = 0u;  // the k-th key's known digits, and their bits
-  int need = k;                   // keys to take among those that agree with them
-  bool exact = false;             // all of those are taken
-  for (int shift = 24; shift >= 0 && !exact; shift -= 8) {
+  if (tid == 0) {
+    sh.top = 0u;
+    sh.bottom = kKeyAlways;
+    sh.always = 0;
+  }
+  __syncthreads();
+  {
+    uint32_t top = 0u, bottom = kKeyAlways;
+    int always = 0;
+    for (int i = tid; i < n; i += threads) {
+      const uint32_t x = keys[i];
+      always += x == kKeyAlways;
+      top = max(top, x == kKeyAlways ? 0u : x);
+      bottom = min(bottom, x);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    bottom = __reduce_min_sync(0xffffffffu, bottom);
+    always = __reduce_add_sync(0xffffffffu, always);
+    if (lane == 0) {
+      atomicMax(&sh.top, top);
+      atomicMin(&sh.bottom, bottom);
+      atomicAdd(&sh.always, always);
+    }
+  }
+  __syncthreads();
+  int need = k - sh.always;  // keys to take among the candidates: those that agree with low in the known bits
+  const int differ = 32 - __clz(sh.top ^ sh.bottom);  // bits from the highest that differs down
+  uint32_t known = differ >= 32 ? 0u : ~0u << differ, low = sh.top & known;
+  bool exact = false;  // all candidates are taken (those above low, and at it)
+  if (need <= 0) {
+    low = kKeyAlways;
+    exact = true;
+  }
+  int shift = differ;
+  while (shift > 0 && !exact) {
+    shift = max(shift - 8, 0);
     for (int i = tid; i < 256 * 4; i += threads) sh.hist[i] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += threads) {
       const uint32_t x = keys[i];
-      if ((x & known) == low) atomicAdd(&sh.hist[((x >> shift) & 255u) * 4 + (lane & 3)], 1);
+      if ((x & known) == low && x != kKeyAlways) atomicAdd(&sh.hist[((x & ~known) >> shift) * 4 + (lane & 3)], 1);
     }
     __syncthreads();
     if (warp == 0) {  // lane l: digits 255 - 8 l down to 248 - 8 l
@@ -74,7 +107,7 @@ __device__ __forceinline__ void topk_in_order(const uint32_t* keys, int n, int k
     }
     __syncthreads();
     low |= (uint32_t)sh.digit << shift;
-    known |= 255u << shift;
+    known = ~0u << shift;
     need -= sh.above;
     exact = sh.at == need;  // (what is not known of low is zeros: every candidate is at or above it)
   }
