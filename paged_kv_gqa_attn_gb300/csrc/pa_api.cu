@@ -231,15 +231,17 @@ void plan_rows(bool windowed, int64_t units, int64_t slots, int64_t pages, const
 }
 
 // The kernels that take such a split, their resident CTAs an SM and the cost of one in pages.
-enum class Split { kDecode, kRows, kTiles };  // the decode kernel with a window, the rows kernel, split 128-row tiles
+// (the decode kernel with a window, or behind a shared prefix; the rows kernel; split 128-row tiles)
+enum class Split { kDecode, kOwnDecode, kRows, kTiles };
 void plan_split(Split kernel, int kv_dtype, int rows, bool windowed, int num_sms, int64_t units, int64_t pages, int align,
                 int* ppp, int* nparts) {
-  const bool decode = kernel == Split::kDecode, few_rows = kernel == Split::kRows;
+  const bool decode = kernel == Split::kDecode || kernel == Split::kOwnDecode, few_rows = kernel == Split::kRows;
   const bool bf16 = kv_dtype == PA_KV_BF16;
   const int per_sm = few_rows ? pa::rows_resident_ctas(rows) : !decode ? 2 : kv_dtype == PA_KV_FP8_E4M3 ? 4 : 6;
   SplitCost cost = {38., 14., 1.5};
   if (bf16) cost = {decode ? 20. : 38., 8., 1.2};  // a page of twice the bytes or more
   if (few_rows && windowed && rows > 8) cost.fixed = 60.;
+  if (kernel == Split::kOwnDecode) cost.fixed *= 0.5;  // beside the prefixes' CTAs, which take room of some SMs only
   plan_rows(windowed, units, (int64_t)num_sms * per_sm, pages, cost, align, ppp, nparts);
 }
 
@@ -278,6 +280,27 @@ int check_extra(const Extra& x, Form form, int num_seqs, int max_blocks_per_seq,
 }
 
 size_t round_up(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+// The split of shared prefixes of `pages` pages at most, in `units` (tile, kv head) pairs.  One CTA an SM or fewer: a
+// tile's shared memory leaves room for three CTAs over own tokens beside one, for none beside two.  As the ragged split
+// above, with the SMs as slots and CTAs whose start and end cost 90 pages where all are equally long, 38 where they are
+// not.  Measured (with the own tokens at their best split; partitions: us): 64 sequences behind 8192 tokens, bf16: 3 51.5, 6 43.6,
+// 9 47.1, 12 48.6, 19 53.1; 128 in 5 groups behind up to 16384, E4M3: 4 143, 8 119, 11 124, 16 133; 8 x 5 rows
+// behind 2048, 4-bit: 2 32.8, 4 26.9, 8 28.7, 16 34.4.
+void plan_prefix(bool one_group, int num_sms, int64_t units, int64_t pages, int* ppp, int* nparts) {
+  int64_t P = 1;
+  const int forced = g_forced_partitions.load();
+  if (forced > 0) {
+    P = forced;
+  } else {
+    const double x = (double)pages * num_sms / ((double)units * (one_group ? 90. : 38.));
+    while ((P + 0.5) * (P + 0.5) <= x && P < kAutoMaxPartitions) ++P;
+  }
+  if (P > pages) P = pages;
+  const int64_t per = ((pages + P - 1) / P + 3) / 4 * 4;  // whole 64-token steps
+  *ppp = (int)per;
+  *nparts = (int)((pages + per - 1) / per);
+}
 
 int run(Form form, const Window& win, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
         const int32_t* context_lens, const uint32_t* tree_mask, int num_seqs, int max_blocks_per_seq,
@@ -386,9 +409,9 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
       p.page_align = align;
       p.prefix_ppp = 1;
       if (p.num_groups > 0)
-        plan_split(Split::kTiles, kv_dtype, 128, p.num_groups == 1, dev->num_sms,
-                   (int64_t)pa::prefix_tiles(num_seqs, q_len, l.group, p.num_groups) * num_kv_heads,
-                   p.max_prefix_len / block_size, 4, &p.prefix_ppp, &prefix_parts);
+        plan_prefix(p.num_groups == 1, dev->num_sms,
+                    (int64_t)pa::prefix_tiles(num_seqs, q_len, l.group, p.num_groups) * num_kv_heads,
+                    p.max_prefix_len / block_size, &p.prefix_ppp, &prefix_parts);
       const int64_t own = (int64_t)p.max_own_len + (align - 1) * block_size;  // (its first pages rounded down)
       covered = (int)(own < max_context_len ? own : max_context_len);
     }
@@ -398,7 +421,7 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
         st = paged_attn_plan(dev->num_sms, num_seqs, num_kv_heads, covered, block_size, q_len, kv_dtype, &ppp, &nparts);
         if (st != PA_OK) return st;
       } else {
-        plan_split(mma_decode ? Split::kDecode : few_rows ? Split::kRows : Split::kTiles, kv_dtype, l.group * q_len,
+        plan_split(mma_decode ? (l.form == pa::kFormOwn ? Split::kOwnDecode : Split::kDecode) : few_rows ? Split::kRows : Split::kTiles, kv_dtype, l.group * q_len,
                    l.form == pa::kFormWindow || l.form == pa::kFormBlocks, dev->num_sms, (int64_t)num_seqs * num_kv_heads,
                    ((int64_t)covered + block_size - 1) / block_size, align, &ppp, &nparts);
       }
@@ -444,14 +467,15 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
     if (r1 != PA_OK || r2 != PA_OK)
       e = cudaErrorInvalidValue;
     else {
-      e = split_tiles                               ? pa::launch_verify_split(p, l, tk, tv)
-          : !few_rows                               ? pa::launch_decode_mma(p, l, tk, tv)
-          : l.form == pa::kFormBlocks               ? pa::rows_blocks_form(p, l, tk, tv)
-          : l.form == pa::kFormOwn                  ? pa::rows_own_form(p, l, tk, tv)
-          : l.form == pa::kFormScores               ? pa::rows_scores_form(p, l, tk, tv)
-          : fp4                                     ? pa::rows_fp4_form(p, l)
-                                                    : pa::rows_window_form(p, l, tk, tv);
-      if (e == cudaSuccess && prefix_parts > 0) e = pa::launch_prefix(p, l, tk, tv);
+      e = prefix_parts > 0 ? pa::launch_prefix(p, l, tk, tv) : cudaSuccess;
+      if (e == cudaSuccess)
+        e = split_tiles                     ? pa::launch_verify_split(p, l, tk, tv)
+            : !few_rows                     ? pa::launch_decode_mma(p, l, tk, tv)
+            : l.form == pa::kFormBlocks     ? pa::rows_blocks_form(p, l, tk, tv)
+            : l.form == pa::kFormOwn        ? pa::rows_own_form(p, l, tk, tv)
+            : l.form == pa::kFormScores     ? pa::rows_scores_form(p, l, tk, tv)
+            : fp4                           ? pa::rows_fp4_form(p, l)
+                                            : pa::rows_window_form(p, l, tk, tv);
     }
     if (e == cudaSuccess && nparts > 1) e = pa::launch_merge(p, l);
     if (e == cudaSuccess && l.form == pa::kFormScores) {

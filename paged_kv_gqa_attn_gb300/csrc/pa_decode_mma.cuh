@@ -110,8 +110,6 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
   const int part = blockIdx.x;
   const int g = blockIdx.y;
   const int b = blockIdx.z;
-  // the kernel over the prefixes, or the merge, may take the room that this grid leaves
-  if constexpr (OWN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int Hq = p.num_q_heads;
   // The first two windows of block ids (below) depend only on the partition, not on the context
   // length: load them together with it, bounded by the table row, and mask them once it arrives.
@@ -135,6 +133,7 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
         p.out[((size_t)b * Hq + g * G) * D + idx] = __float2bfloat16(0.f);
       if (threadIdx.x == 0) record_error(p.err, kErrShortContext);
     }
+    if constexpr (OWN) after_prefixes();
     return;
   }
   const int win_lo = OWN ? prefix : WIN ? max(0, L - p.window) : 0;
@@ -461,7 +460,7 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
   }
 
   // the merge kernel (launched as a programmatic dependent) may start its prologue now
-  if constexpr (!OWN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // sums over the 8 row groups (each thread summed its own tokens)
 #pragma unroll
@@ -508,6 +507,7 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
   }
   __syncthreads();
   store_partition<G, D, T::kWarps, FP8, FORM>(p, wacc, wm, wl, b, g, part, nparts);
+  if constexpr (OWN) after_prefixes();
 }
 
 template <int D, int G, bool FP8, int FORM>
@@ -516,6 +516,13 @@ cudaError_t decode_form(const AttnParams& p, cudaStream_t stream, const CUtensor
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(decode_mma_kernel<D, G, FP8, FORM>), T::kSmem);
   if (e != cudaSuccess) return e;
   dim3 grid(FORM == kFormOwn ? p.own_partitions : p.max_partitions, p.num_kv_heads, p.num_seqs);
+  if (FORM == kFormOwn && p.max_partitions > p.own_partitions) {  // beside the prefixes
+    AttnParams pp = p;
+    CUtensorMap k = tk, v = tv;
+    void* args[] = {&pp, &k, &v};
+    return launch_dependent(reinterpret_cast<const void*>(decode_mma_kernel<D, G, FP8, FORM>), grid, dim3(T::kThreads),
+                            T::kSmem, stream, args);
+  }
   decode_mma_kernel<D, G, FP8, FORM><<<grid, T::kThreads, T::kSmem, stream>>>(p, tk, tv);
   return cudaGetLastError();
 }

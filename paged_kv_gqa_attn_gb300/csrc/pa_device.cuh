@@ -94,6 +94,12 @@ __device__ __forceinline__ PrefixGroup prefix_group(const AttnParams& p, int i, 
   r.tokens = max(r.tokens, 0) / 16 * 16;
   return r;
 }
+// The grid over the own tokens is a programmatic dependent of the one over the prefixes, which it does not read from: they
+// share the SMs.  Its first CTA ends after that grid, so that what waits for this one (the merge) has both.  Called
+// on every way out of a kernel's first CTA.
+__device__ __forceinline__ void after_prefixes() {
+  if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 // Whether a sequence's new rows all lie behind its prefix, and no more than the bound does.
 __device__ __forceinline__ bool own_tokens_fit(const AttnParams& p, int L, int prefix) {
   return (prefix == 0 || L - p.q_len >= prefix) && L - prefix <= p.max_own_len;

@@ -192,16 +192,9 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     qs = p.query_start_loc[b];
     QL = p.query_start_loc[b + 1] - qs;
   }
-  // Shared prefixes: a programmatic dependent of the grid over the own tokens, which it does not read from; its first CTA
-  // ends after that grid, so that what waits for this one (the merge) has both.
-  auto after_own_tokens = [&] {
-    if (PREFIX && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-  };
-  if (PREFIX && b < 0) {  // fewer tiles than the grid's bound
-    after_own_tokens();
-    return;
-  }
-  if constexpr (OWN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // the grid over the own tokens may take the room that this one leaves
+  if constexpr (PREFIX) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (PREFIX && b < 0) return;  // fewer tiles than the grid's bound
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -287,6 +280,7 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
       __nv_bfloat16* dst = p.out + ((size_t)(qs + t) * Hq + g * G + r % G) * D;
       for (int c = 0; c < D; ++c) dst[c] = __float2bfloat16(0.f);
     }
+    if constexpr (OWN) after_prefixes();
     return;
   }
 
@@ -1258,7 +1252,7 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(T::kTmemCols) : "memory");
   }
-  after_own_tokens();
+  if constexpr (OWN) after_prefixes();
 #ifdef PA_TIMELINE
   if (threadIdx.x == 0) pf_tl_put(1, pf_gtime());
 #endif
@@ -1293,6 +1287,8 @@ cudaError_t prefill_split(const AttnParams& p, const CUtensorMap& tk, const CUte
   if constexpr (FORM == kFormPrefix) {
     grid.x = p.max_partitions - p.own_partitions;
     grid.z = prefix_tiles(p.num_seqs, p.q_len, p.num_q_heads / p.num_kv_heads, p.num_groups);
+  }
+  if (FORM == kFormOwn && p.max_partitions > p.own_partitions) {  // beside the prefixes
     AttnParams pp = p;
     const int32_t* none = nullptr;
     CUtensorMap k = tk, v = tv;

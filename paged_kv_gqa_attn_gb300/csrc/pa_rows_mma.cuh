@@ -214,8 +214,6 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gi = lane >> 2, qi = lane & 3;
   const int part = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
-  // the kernel over the prefixes, or the merge, may take the room that this grid leaves
-  if constexpr (OWN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, G = Hq / Hkv;
   const int R = p.q_len * G;  // columns in use
   const int ppp = p.pages_per_partition;
@@ -242,6 +240,7 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
         const int c = idx / D;
         p.out[(((size_t)b * p.q_len + c / G) * Hq + g * G + c % G) * D + idx % D] = __float2bfloat16(0.f);
       }
+    if constexpr (OWN) after_prefixes();
     return;
   }
   const int lo_first = OWN ? prefix : WIN ? max(0, first_new + 1 - p.window) : 0;  // window begin of the first row
@@ -624,7 +623,7 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
     __syncwarp();
   }
   // the merge kernel (launched as a programmatic dependent) may start its prologue now
-  if constexpr (!OWN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   __syncthreads();  // every warp is done with its stages
   float* wacc = reinterpret_cast<float*>(smem);   // [kWarps][kCols][D]
@@ -682,6 +681,7 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
       if (dd == 0) p.part_lse[at] = M == -INFINITY ? -INFINITY : M + __log2f(lsum);
     }
   }
+  if constexpr (OWN) after_prefixes();
 }
 
 template <int D, int NT, int KV, int FORM>
@@ -690,6 +690,13 @@ cudaError_t rows_launch(const AttnParams& p, const CUtensorMap& tk, const CUtens
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(rows_mma_kernel<D, NT, KV, FORM>), T::kSmem);
   if (e != cudaSuccess) return e;
   dim3 grid(FORM == kFormOwn ? p.own_partitions : p.max_partitions, p.num_kv_heads, p.num_seqs);
+  if (FORM == kFormOwn && p.max_partitions > p.own_partitions) {  // beside the prefixes
+    AttnParams pp = p;
+    CUtensorMap k = tk, v = tv;
+    void* args[] = {&pp, &k, &v};
+    return launch_dependent(reinterpret_cast<const void*>(rows_mma_kernel<D, NT, KV, FORM>), grid, dim3(T::kThreads),
+                            T::kSmem, st, args);
+  }
   rows_mma_kernel<D, NT, KV, FORM><<<grid, T::kThreads, T::kSmem, st>>>(p, tk, tv);
   return cudaGetLastError();
 }

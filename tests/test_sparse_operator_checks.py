@@ -192,24 +192,43 @@ def test_evict_checks(over, status):
 
 
 DEPENDENTS = {"block_pick_kernel", "fold_weights_kernel", "evict_move_kernel"}
+BESIDE = {"decode_mma_kernel", "rows_mma_kernel", "prefill_tc_kernel"}  # over own tokens, beside the prefixes
+
+
+def _without_lambdas(body):
+    return re.sub(r"\[&\]\([^)]*\)\s*\{[^{}]*\}", "", body)
 
 
 def test_every_dependent_waits_before_it_returns():
-    """What is launched by launch_dependent: each kernel's wait stands in front of its first return, whatever the data."""
+    """What launch_dependent launches behind a kernel whose outputs it reads: the wait stands in front of the first return,
+    whatever the data."""
     found = set()
     for name, text in _all_sources().items():
-        if "return launch_dependent(" not in text or name == "pa_api.cu":
+        if "launch_dependent(" not in text or name in ("pa_api.cu", "pa_kernels.h"):
             continue
-        for kernel in re.findall(r"__global__[^{;]*?\b(\w+_kernel)\(", text):
-            body = _body(text, kernel)
-            if WAIT not in body:
-                continue
-            found.add(kernel)
-            lambdas = re.sub(r"\[&\]\([^)]*\)\s*\{[^{}]*\}", "", body)
-            assert WAIT in lambdas[: lambdas.index("return")] if "return" in lambdas else True, kernel
-            head = text[text.index("__global__", text.rindex("template", 0, text.index(kernel + "("))):][:400]
-            assert "__restrict__" not in head, kernel
+        for kernel in re.findall(r"__global__[^;{]*?\b(\w+_kernel)\(", text):
+            body = _without_lambdas(_body(text, kernel))
+            if WAIT in body:
+                found.add(kernel)
+                assert "return" not in body[: body.index(WAIT)], kernel
+                head = re.search(r"__global__[^;{]*?\b%s\([^{;]*\{" % kernel, text).group(0)
+                assert "__restrict__" not in head, kernel
     assert found == DEPENDENTS
+
+
+@pytest.mark.parametrize("kernel", sorted(BESIDE))
+def test_the_first_cta_over_own_tokens_ends_after_the_prefixes(kernel):
+    """They read nothing of the prefixes' grid; the merge that waits for them reads both.  Every way out of their first CTA
+    (partition 0, which none of the returns for a partition past the pages concerns) passes the wait, and it is last."""
+    text = next(t for t in _all_sources().values() if re.search(r"__global__[^;{]*\b%s\(" % kernel, t))
+    body = _body(text, kernel)
+    assert body.rstrip().rstrip("}").rstrip().splitlines()[-1].strip() in (
+        "if constexpr (OWN) after_prefixes();", "#endif"), kernel
+    zeros = body.index("__float2bfloat16(0.f);")  # the rows of a sequence without tokens
+    assert body[zeros: body.index("return;", zeros)].count("after_prefixes()") == 1
+    device = _all_sources()["pa_device.cuh"]
+    at = device.index("void after_prefixes()")
+    assert "blockIdx.x | blockIdx.y | blockIdx.z) == 0" in device[at: at + 200] and WAIT in device[at: at + 200]
 
 
 def test_the_oracle_on_closed_cases():
