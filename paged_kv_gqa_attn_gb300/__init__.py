@@ -183,11 +183,12 @@ def plan(num_sms: int, num_seqs: int, num_kv_heads: int, max_context_len: int, b
 # the index of the current device.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
     if stream is None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return int(stream.cuda_stream)
 
 
@@ -245,7 +246,7 @@ def _one_device(stream, *tensors, names="", **named):
         raise ValueError("tensors must be on one CUDA device, got none")
     if stream is not None and stream.device.index != index:
         raise ValueError(f"stream is on {stream.device}, tensors on cuda:{index}")
-    return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
+    return _HERE if _current_device() == index else torch.cuda.device(index)
 
 
 def _check_cuda(name, t, dtypes):

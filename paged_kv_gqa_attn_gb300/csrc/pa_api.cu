@@ -434,17 +434,37 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
         nparts = pages > 0 ? (pages + ppp - 1) / ppp : 1;
       }
     }
+    // Few partitions of a form that may: one cluster for each (sequence, kv head) joins them in shared memory.  With kept
+    // scores it cuts each sequence's own pages evenly and keeps the scores there too.
+    const bool scores = l.form == pa::kFormScores;
+    if (l.form == pa::kFormBlocks) {
+      l.join = nparts <= pa::kJoinCtas;
+    } else if (scores) {
+      const int64_t pages = ((int64_t)max_context_len + block_size - 1) / block_size;
+      const int64_t fit = pa::kJoinScores / (block_size * l.group * (int64_t)sizeof(float));  // pages of a CTA at most
+      int64_t parts = (pages + fit - 1) / fit;
+      if (parts < nparts) parts = nparts;
+      if (parts > pa::kJoinCtas) parts = pa::kJoinCtas;
+      const int64_t per = (pages + parts - 1) / parts;
+      // (more partitions than a cluster has, of few sequences: they are spread over the device instead)
+      l.join = per <= fit && (nparts <= pa::kJoinCtas || (int64_t)num_seqs * num_kv_heads * parts >= dev->num_sms);
+      if (l.join) {
+        nparts = (int)parts;
+        ppp = (int)per;
+        p.weights = x.weights;
+        p.decay = x.decay;
+      }
+    }
     p.pages_per_partition = ppp;
     p.own_partitions = nparts;
     nparts += prefix_parts;
     p.max_partitions = nparts;
-    if (nparts > 1 || l.form == pa::kFormScores) {
+    const bool kept = scores && !l.join;  // scores in scratch
+    if ((nparts > 1 && !l.join) || kept) {
       const size_t rows = nparts > 1 ? (size_t)num_seqs * q_len * num_q_heads * nparts : 0;
       const size_t part_bytes = rows * head_dim * sizeof(float) + rows * sizeof(float);
-      const size_t score_bytes = l.form == pa::kFormScores
-                                     ? (size_t)num_seqs * num_q_heads * max_context_len * sizeof(float)
-                                     : 0;
-      const size_t lse_bytes = l.form == pa::kFormScores ? (size_t)num_seqs * num_q_heads * sizeof(float) : 0;
+      const size_t score_bytes = kept ? (size_t)num_seqs * num_q_heads * max_context_len * sizeof(float) : 0;
+      const size_t lse_bytes = kept ? (size_t)num_seqs * num_q_heads * sizeof(float) : 0;
       const size_t bytes = lse_bytes ? round_up(part_bytes) + round_up(score_bytes) + lse_bytes : part_bytes;
       if (cudaMallocFromPoolAsync(&scratch, bytes, dev->pool, s) != cudaSuccess) {
         cudaGetLastError();
@@ -477,8 +497,8 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
             : fp4                           ? pa::rows_fp4_form(p, l)
                                             : pa::rows_window_form(p, l, tk, tv);
     }
-    if (e == cudaSuccess && nparts > 1) e = pa::launch_merge(p, l);
-    if (e == cudaSuccess && l.form == pa::kFormScores) {
+    if (e == cudaSuccess && nparts > 1 && !l.join) e = pa::launch_merge(p, l);
+    if (e == cudaSuccess && kept) {
       const pa::WeightParams w = {p.scores, p.lse, x.weights, block_table, context_lens, num_seqs, num_kv_heads, l.group,
                                   max_blocks_per_seq, num_blocks, max_context_len, x.decay};
       e = pa::launch_fold_weights(w, s);
@@ -619,6 +639,21 @@ cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, int smem, cudaStre
 
 cudaError_t launch_dependent(const void* fn, dim3 grid, dim3 block, int smem, cudaStream_t st, void** args) {
   return launch_pdl(fn, grid, block, smem, st, args);
+}
+
+cudaError_t launch_clusters(const void* fn, dim3 grid, dim3 block, int smem, int ctas, cudaStream_t st, void** args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 cudaError_t error_word_address(unsigned** out) {
@@ -858,8 +893,8 @@ int paged_attn_select_blocks(const void* q, const int8_t* bounds, const float* b
   if (st != PA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* scratch = nullptr;
-  if (cudaMallocFromPoolAsync(&scratch, pa::select_scratch_bytes(num_seqs, num_kv_heads, max_context_len), dev->pool, s) !=
-      cudaSuccess) {
+  const size_t bytes = pa::select_scratch_bytes(num_seqs, num_kv_heads, max_context_len, dev->num_sms);
+  if (bytes > 0 && cudaMallocFromPoolAsync(&scratch, bytes, dev->pool, s) != cudaSuccess) {
     cudaGetLastError();
     return PA_ERR_NO_MEMORY;
   }
@@ -884,7 +919,7 @@ int paged_attn_select_blocks(const void* q, const int8_t* bounds, const float* b
   p.sinks = sink_blocks;
   p.recent = recent_blocks;
   const cudaError_t e = pa::launch_select_blocks(p, head_dim, dev->num_sms, s);
-  cudaFreeAsync(scratch, s);
+  if (scratch) cudaFreeAsync(scratch, s);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

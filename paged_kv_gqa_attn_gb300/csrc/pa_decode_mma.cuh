@@ -42,6 +42,9 @@
 // Behind a shared prefix (kFormOwn): the window form whose window begins where the prefix ends.
 // Scores kept (kFormScores): each score also goes to memory in base-2 units, 4 G bytes a token beside the 2 d or
 // more that its key and value take, for the pass that turns them into weights.
+// Joined (JOIN, listed blocks and kept scores): the partitions of a (sequence, kv head) are one cluster, whose CTAs read each
+// other's partials from shared memory: no scratch and no second kernel.  Kept scores then stay in shared memory too: once
+// the rows' masses are known, each CTA folds its own tokens' weights into the sums.
 #pragma once
 
 #include "pa_kernels.h"
@@ -92,7 +95,7 @@ __device__ __forceinline__ float bf16_part(float p, int c) {
   return c < G ? p : bf16_rem(p);
 }
 
-template <int D, int G, bool FP8, int FORM>
+template <int D, int G, bool FP8, int FORM, bool JOIN>
 __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDecodeTraits<D, G, FP8>::kMinBlocks))
     decode_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv) {
@@ -100,7 +103,9 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
   constexpr int RB = T::kRowBytes;
   constexpr bool LIST = FORM == kFormBlocks, OWN = FORM == kFormOwn, SCORES = FORM == kFormScores;
   constexpr bool WIN = FORM == kFormWindow || OWN;  // pages numbered with a gap
-  constexpr bool kIdsAhead = !WIN && !LIST;         // the first block ids depend on the partition only
+  constexpr bool kIdsAhead = !WIN && !LIST && !JOIN;  // the first block ids depend on the partition only
+  constexpr bool kEven = JOIN && SCORES;              // the cluster cuts the sequence's own pages evenly
+  static_assert(!JOIN || LIST || SCORES, "forms that clusters join");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5;
@@ -113,9 +118,9 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
   const int Hq = p.num_q_heads;
   // The first two windows of block ids (below) depend only on the partition, not on the context
   // length: load them together with it, bounded by the table row, and mask them once it arrives.
-  const int ppp = p.pages_per_partition;
-  const int pbeg = part * ppp;
-  const int first = pbeg + warp;
+  int ppp = p.pages_per_partition;
+  int pbeg = part * ppp;
+  int first = pbeg + warp;
   const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
   const int row0 = first + T::kWarps * lane, row1 = first + T::kWarps * (32 + lane);
   const int raw0 = kIdsAhead && row0 < p.max_blocks_per_seq ? bt[row0] : -1;
@@ -141,8 +146,13 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
   PageSpan span = {0, 0, ncols};
   if constexpr (WIN) span = page_span(span.count, win_lo, p.sinks, 1);
   const int npages = LIST ? p.num_listed : span.count;  // pages that the row sees (or that the list has room for)
-  if (pbeg >= npages) return;
-  const int pend = min(npages, pbeg + ppp);
+  if constexpr (kEven) {
+    ppp = (npages + (int)gridDim.x - 1) / (int)gridDim.x;
+    pbeg = min(part * ppp, npages);
+    first = pbeg + warp;
+  }
+  if (!JOIN && pbeg >= npages) return;
+  const int pend = max(pbeg, min(npages, pbeg + ppp));  // (joined: a partition may be empty)
   const int nparts = (npages + ppp - 1) / ppp + (OWN && prefix > 0 ? 1 : 0);  // (with a prefix: always partial)
   const int32_t* list = LIST ? p.blocks + ((size_t)b * p.num_kv_heads + g) * p.num_listed : nullptr;
 
@@ -152,6 +162,7 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
   }
   uint8_t* stages = smem + warp * T::kStages * T::kStageBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::kStageRegion) + warp * T::kStages;
+  float* kept = reinterpret_cast<float*>(smem + T::kStageRegion + T::kBarRegion);  // joined: scores [tokens][G]
 
   const int nk = first < pend ? (pend - first + T::kWarps - 1) / T::kWarps : 0;
 
@@ -347,7 +358,8 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
       float x0 = fmaf(sc[0], ksc0, vf.lv), x1 = fmaf(sc[1], ksc1, vf.lv);
       float x2 = fmaf(sc[2], ksc0, vf.lv), x3 = fmaf(sc[3], ksc1, vf.lv);
       if constexpr (SCORES) {  // tokens past the last are never read back
-        float* dst = p.scores + (((size_t)b * p.num_kv_heads + g) * p.max_context_len + page * T::kBS) * G + 2 * qi;
+        float* dst = JOIN ? kept + (page - pbeg) * T::kBS * G + 2 * qi
+                          : p.scores + (((size_t)b * p.num_kv_heads + g) * p.max_context_len + page * T::kBS) * G + 2 * qi;
         if constexpr (G == 1) {
           if (qi == 0 && gi < valid) dst[gi] = sc[0] * ksc0;
           if (qi == 0 && gi + 8 < valid) dst[gi + 8] = sc[2] * ksc0;
@@ -506,45 +518,63 @@ __global__ void __launch_bounds__((MmaDecodeTraits<D, G, FP8>::kThreads), (MmaDe
     if (h1 < G) *reinterpret_cast<float2*>(wacc + (warp * G + h1) * D + dd) = make_float2(o[i][1], o[i][3]);
   }
   __syncthreads();
+  if constexpr (JOIN) {
+    static_assert((T::kWarps + 1) * G * D * 4 + (2 * T::kWarps + 4) * G * 4 <= T::kStageRegion, "partials to join fit");
+    float* part_o = wl + T::kWarps * G;     // [G][D] (16-byte aligned: the parts before it are multiples of 4 G floats)
+    Mass* part_mass = reinterpret_cast<Mass*>(part_o + G * D);  // [G]
+    Mass* joined = part_mass + G;                               // [G]
+    store_partition<G, D, T::kWarps, FP8, FORM, true>(p, wacc, wm, wl, b, g, part, nparts, part_o, part_mass);
+    join_partitions<D, SCORES>(part_o, part_mass, G, joined,
+                               [&](int h) { return p.out + ((size_t)b * Hq + g * G + h) * D; });
+    if constexpr (SCORES) {
+      __syncthreads();
+      fold_weights(p, b, g, G, pbeg * T::kBS, min(pend * T::kBS, L), L, kept, joined);
+    }
+    cluster_wait();  // nobody reads this CTA's shared memory any more
+    return;
+  }
   store_partition<G, D, T::kWarps, FP8, FORM>(p, wacc, wm, wl, b, g, part, nparts);
   if constexpr (OWN) after_prefixes();
 }
 
-template <int D, int G, bool FP8, int FORM>
+template <int D, int G, bool FP8, int FORM, bool JOIN>
 cudaError_t decode_form(const AttnParams& p, cudaStream_t stream, const CUtensorMap& tk, const CUtensorMap& tv) {
   using T = MmaDecodeTraits<D, G, FP8>;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(decode_mma_kernel<D, G, FP8, FORM>), T::kSmem);
+  constexpr int kKept = JOIN && FORM == kFormScores ? kJoinScores : 0;
+  const void* fn = reinterpret_cast<const void*>(decode_mma_kernel<D, G, FP8, FORM, JOIN>);
+  cudaError_t e = set_smem_once(fn, T::kSmem + kKept);
   if (e != cudaSuccess) return e;
   dim3 grid(FORM == kFormOwn ? p.own_partitions : p.max_partitions, p.num_kv_heads, p.num_seqs);
-  if (FORM == kFormOwn && p.max_partitions > p.own_partitions) {  // beside the prefixes
+  if (JOIN || (FORM == kFormOwn && p.max_partitions > p.own_partitions)) {
     AttnParams pp = p;
     CUtensorMap k = tk, v = tv;
     void* args[] = {&pp, &k, &v};
-    return launch_dependent(reinterpret_cast<const void*>(decode_mma_kernel<D, G, FP8, FORM>), grid, dim3(T::kThreads),
-                            T::kSmem, stream, args);
+    const int smem = T::kSmem + (kKept ? p.pages_per_partition * T::kBS * G * 4 : 0);
+    if (JOIN) return launch_clusters(fn, grid, dim3(T::kThreads), smem, (int)grid.x, stream, args);
+    return launch_dependent(fn, grid, dim3(T::kThreads), T::kSmem, stream, args);  // beside the prefixes
   }
-  decode_mma_kernel<D, G, FP8, FORM><<<grid, T::kThreads, T::kSmem, stream>>>(p, tk, tv);
+  decode_mma_kernel<D, G, FP8, FORM, JOIN><<<grid, T::kThreads, T::kSmem, stream>>>(p, tk, tv);
   return cudaGetLastError();
 }
 
-template <int FORM, int D, bool FP8>
+template <int FORM, bool JOIN, int D, bool FP8>
 cudaError_t decode_group(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv) {
   switch (l.group) {
-    case 1: return decode_form<D, 1, FP8, FORM>(p, l.stream, tk, tv);
-    case 2: return decode_form<D, 2, FP8, FORM>(p, l.stream, tk, tv);
-    case 4: return decode_form<D, 4, FP8, FORM>(p, l.stream, tk, tv);
-    case 8: return decode_form<D, 8, FP8, FORM>(p, l.stream, tk, tv);
+    case 1: return decode_form<D, 1, FP8, FORM, JOIN>(p, l.stream, tk, tv);
+    case 2: return decode_form<D, 2, FP8, FORM, JOIN>(p, l.stream, tk, tv);
+    case 4: return decode_form<D, 4, FP8, FORM, JOIN>(p, l.stream, tk, tv);
+    case 8: return decode_form<D, 8, FP8, FORM, JOIN>(p, l.stream, tk, tv);
     default: return cudaErrorInvalidConfiguration;
   }
 }
 
 // One form of the decode kernel, for its head_dim, cache type and group.
-template <int FORM>
+template <int FORM, bool JOIN = false>
 cudaError_t decode_any(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv) {
   if (l.head_dim == 128)
-    return l.fp8 ? decode_group<FORM, 128, true>(p, l, tk, tv) : decode_group<FORM, 128, false>(p, l, tk, tv);
+    return l.fp8 ? decode_group<FORM, JOIN, 128, true>(p, l, tk, tv) : decode_group<FORM, JOIN, 128, false>(p, l, tk, tv);
   if (l.head_dim == 64)
-    return l.fp8 ? decode_group<FORM, 64, true>(p, l, tk, tv) : decode_group<FORM, 64, false>(p, l, tk, tv);
+    return l.fp8 ? decode_group<FORM, JOIN, 64, true>(p, l, tk, tv) : decode_group<FORM, JOIN, 64, false>(p, l, tk, tv);
   return cudaErrorInvalidConfiguration;
 }
 

@@ -4,7 +4,7 @@
 namespace pa {
 
 cudaError_t decode_scores_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv) {
-  return decode_any<kFormScores>(p, l, tk, tv);
+  return l.join ? decode_any<kFormScores, true>(p, l, tk, tv) : decode_any<kFormScores>(p, l, tk, tv);
 }
 
 }  // namespace pa

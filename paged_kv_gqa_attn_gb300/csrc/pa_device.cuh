@@ -72,8 +72,11 @@ struct AttnParams {
   int prefix_ppp;               // pages per partition of the prefix
   float* scores;                // kFormScores: [B, Hkv, max_context_len, G] base-2 scores
   float* lse;                   // [B, Hq] log2 of each row's softmax mass
+  float* weights;               // kFormScores, joined: [NB, Hkv, 16] sums of the tokens' weights
+  float decay;
 };
 
+constexpr int kJoinMax = 8;  // partitions of a cluster at most
 constexpr int kNoBlock = -0x7fffffff - 1;  // kFormBlocks: an unused entry of the list, in place of a block id
 
 // The group of sequences [first, last) that share `tokens` prefix tokens, a whole number of blocks.
@@ -287,13 +290,142 @@ __device__ __forceinline__ int context_len(const AttnParams& p, int b, bool flag
   return max(L, 0);
 }
 
+// ---- partitions of a row as one cluster ---------------------------------------------------------
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// The address of a CTA's shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float cluster_ld(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
+// A row's softmax mass: sum * 2^top.  (Kept apart: a log2-sum-exp of large sums loses more than the fp32 sum does.)
+struct Mass {
+  float top, sum;
+};
+
+// The cluster's CTAs are the partitions of `rows` rows; each has left its normalised rows [rows][D] and their masses
+// [rows] in shared memory (the same offsets in all).  Each joins a share of the outputs and stores them, out_row(r) being
+// row r's place, and, with ROWS, every row's (top, 1 / sum) in joined[r].  Ends with the CTA's arrival: it may not
+// leave before cluster_wait().  All threads; a barrier of the CTA must follow before `joined` is read.
+template <int D, bool ROWS, class OutRow>
+__device__ __forceinline__ void join_partitions(const float* part_o, const Mass* part_mass, int rows, Mass* joined,
+                                                OutRow out_row) {
+  const int parts = gridDim.x, rank = blockIdx.x;
+  const uint32_t o_at = smem_addr(part_o), m_at = smem_addr(part_mass);
+  cluster_arrive();
+  cluster_wait();
+  for (int i = rank * blockDim.x + threadIdx.x; i < rows * (D / 4); i += parts * blockDim.x) {
+    const int r = i / (D / 4), dd = i % (D / 4) * 4;
+    float m[kJoinMax], l[kJoinMax], M = -INFINITY;
+    float4 o[kJoinMax];
+#pragma unroll
+    for (int q = 0; q < kJoinMax; ++q) {  // all loads in flight together
+      m[q] = -INFINITY;
+      if (q < parts) {
+        m[q] = cluster_ld(cluster_addr(m_at + r * 8, q));
+        l[q] = cluster_ld(cluster_addr(m_at + r * 8 + 4, q));
+        o[q] = cluster_ld4(cluster_addr(o_at + (r * D + dd) * 4, q));
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kJoinMax; ++q) M = fmaxf(M, m[q]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < kJoinMax; ++q) {
+      if (q >= parts || m[q] == -INFINITY) continue;
+      const float w = scale_exp2(l[q], m[q] - M);
+      sum += w;
+      acc.x += w * o[q].x;
+      acc.y += w * o[q].y;
+      acc.z += w * o[q].z;
+      acc.w += w * o[q].w;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;  // (nothing seen: zeros)
+    __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), c = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(out_row(r) + dd) =
+        make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&c));
+  }
+  if constexpr (ROWS) {
+    for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+      float M = -INFINITY, sum = 0.f;
+      for (int q = 0; q < parts; ++q) M = fmaxf(M, cluster_ld(cluster_addr(m_at + r * 8, q)));
+      for (int q = 0; q < parts; ++q)
+        sum += scale_exp2(cluster_ld(cluster_addr(m_at + r * 8 + 4, q)), cluster_ld(cluster_addr(m_at + r * 8, q)) - M);
+      joined[r] = {M, 1.f / sum};
+    }
+  }
+  cluster_arrive();
+}
+
+// The step's weights of the CTA's tokens [t0, t1) of (b, g), from their scores [t1 - t0][G] and the rows' (top, 1 / sum),
+// both in shared memory, folded into the sums (L: the context's length; t0 a block's first token).  A thread takes a quarter
+// of a block's tokens at a time, two of them in flight.
+__device__ __forceinline__ void fold_weights(const AttnParams& p, int b, int g, int G, int t0, int t1, int L,
+                                             const float* scores, const Mass* rows) {
+  constexpr int kFlight = 2;
+  const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
+  const int step = 4 * blockDim.x;
+  for (int u = t0 + 4 * threadIdx.x; u < t1; u += kFlight * step) {
+    int pb[kFlight];
+    float4 old[kFlight];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) pb[f] = u + f * step < t1 ? bt[(u + f * step) / 16] : -1;
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      if (pb[f] >= p.num_blocks) pb[f] = -1;  // (flagged by the attention)
+      old[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (pb[f] >= 0 && p.decay != 0.f)
+        old[f] = *reinterpret_cast<const float4*>(p.weights + ((size_t)pb[f] * p.num_kv_heads + g) * 16 + (u + f * step) % 16);
+    }
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int t = u + f * step;
+      if (t >= t1 || pb[f] < 0) continue;
+      const float o4[4] = {old[f].x, old[f].y, old[f].z, old[f].w};
+      float w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = 0.f;
+        const float* x = scores + (t + i - t0) * G;
+        if (t + i < t1)
+          for (int h = 0; h < G; ++h) w[i] += fast_exp2(x[h] - rows[h].top) * rows[h].sum;
+        if (t + i < L - 1 && p.decay != 0.f) w[i] += o4[i] * p.decay;  // (one rounding at the size of the sum)
+      }
+      float* dst = p.weights + ((size_t)pb[f] * p.num_kv_heads + g) * 16 + t % 16;
+      if (t + 4 <= t1) {
+        *reinterpret_cast<float4*>(dst) = make_float4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (t + i < t1) dst[i] = w[i];
+      }
+    }
+  }
+}
+
 // Last step of a split-KV partition: combine the per-warp online-softmax states that the CTA's
 // warps left in shared memory (wacc [W][G][D] unnormalised outputs, wm [W][G] running maxima and
 // wl [W][G] sums, base 2) and store either the finished bf16 rows (the sequence has one
 // partition) or the normalised partial output and its log2-sum-exp for the merge kernel.
-template <int G, int D, int W, bool E4M3 = false, int FORM = kFormAll>
+// JOIN: the partial goes to shared memory for join_partitions, whatever nparts is.
+template <int G, int D, int W, bool E4M3 = false, int FORM = kFormAll, bool JOIN = false>
 __device__ __forceinline__ void store_partition(const AttnParams& p, const float* wacc, const float* wm,
-                                                const float* wl, int b, int g, int part, int nparts) {
+                                                const float* wl, int b, int g, int part, int nparts,
+                                                float* join_o = nullptr, Mass* join_mass = nullptr) {
   const int Hq = p.num_q_heads;
   for (int idx = threadIdx.x; idx < G * D; idx += blockDim.x) {
     const int h = idx / D;
@@ -318,6 +450,11 @@ __device__ __forceinline__ void store_partition(const AttnParams& p, const float
       o = o / lsum;
     }
     const int qh = g * G + h;
+    if constexpr (JOIN) {
+      join_o[idx] = o;
+      if (dd == 0) join_mass[h] = {M, lsum};
+      continue;
+    }
     if (nparts == 1) {
       p.out[((size_t)b * Hq + qh) * D + dd] = __float2bfloat16(o);
       if (FORM == kFormScores && dd == 0) p.lse[(size_t)b * Hq + qh] = M + __log2f(lsum);

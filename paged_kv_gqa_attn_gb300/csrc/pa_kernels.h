@@ -19,7 +19,10 @@ struct Launch {
   cudaStream_t stream;
   int kv = kKvBf16;  // cache type (fp8: kv == kKvE4m3)
   int form = kFormAll;
+  bool join = false;  // a row's partitions are one cluster, which joins them (no partials, no merge)
 };
+constexpr int kJoinCtas = kJoinMax;      // partitions of a cluster at most (the portable size)
+constexpr int kJoinScores = 48 << 10;    // bytes of kept scores of a CTA at most
 
 // Each returns cudaSuccess or the launch error.  Unsupported combinations return
 // cudaErrorInvalidConfiguration (the caller has already checked them).
@@ -124,7 +127,7 @@ struct SelectParams {
   int count, sinks, recent;     // in blocks
 };
 constexpr int kSelectMaxRows = 32;  // q_len * group
-size_t select_scratch_bytes(int num_seqs, int num_kv_heads, int max_context_len);
+size_t select_scratch_bytes(int num_seqs, int num_kv_heads, int max_context_len, int num_sms);
 cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, int num_sms, cudaStream_t st);
 
 // The step's softmax weights from the kept scores and the rows' log2-sum-exps, folded into the tokens' sums.
@@ -187,6 +190,9 @@ cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, int smem, cudaStre
 // launch_pdl for kernels whose every CTA waits (griddepcontrol.wait) before its first read of what the kernel before
 // it wrote, and before it returns.
 cudaError_t launch_dependent(const void* fn, dim3 grid, dim3 block, int smem, cudaStream_t st, void** args);
+
+// Launch in clusters of `ctas` along x (at most 8).
+cudaError_t launch_clusters(const void* fn, dim3 grid, dim3 block, int smem, int ctas, cudaStream_t st, void** args);
 
 // Raise a kernel's dynamic shared-memory limit on the current device (first call per device
 // and kernel only; later calls are a table lookup).

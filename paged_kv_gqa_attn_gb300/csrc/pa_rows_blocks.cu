@@ -4,7 +4,7 @@
 namespace pa {
 
 cudaError_t rows_blocks_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv) {
-  return rows_any<kFormBlocks>(p, l, tk, tv);
+  return l.join ? rows_any<kFormBlocks, true>(p, l, tk, tv) : rows_any<kFormBlocks>(p, l, tk, tv);
 }
 
 }  // namespace pa

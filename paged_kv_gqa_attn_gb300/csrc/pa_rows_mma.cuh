@@ -30,7 +30,7 @@
 // window or of the sinks, and tree masks test each (row, token).  Tokens that no row sees have their V
 // zeroed, whatever is stored there.
 //
-// Listed blocks, a sequence's own tokens behind a shared prefix, kept scores: as in the decode kernel.
+// Listed blocks, a sequence's own tokens behind a shared prefix, kept scores, joined partitions: as in the decode kernel.
 #pragma once
 
 #include "pa_fp4.cuh"
@@ -59,7 +59,7 @@ struct RowsTraits {
   static constexpr int kMTiles = D / 16;
   static constexpr int kMerge = kWarps * kCols * (D + 2) * 4;  // per-warp outputs, maxima, sums
   static constexpr int kStageRegion = kWarps * kStages * kStageBytes;
-  static constexpr int kDataRegion = kStageRegion > kMerge ? kStageRegion : kMerge;
+  static constexpr int kDataRegion = kStageRegion > kMerge + kCols * (D + 4) * 4 ? kStageRegion : kMerge + kCols * (D + 4) * 4;
   static constexpr int kBarRegion = kWarps * kStages * 8;  // (a multiple of 16: kWarps is even)
   static constexpr int kQRegion = NT * (kKSteps / 2) * 32 * 16;
   static constexpr int kSmem = 1024 + kDataRegion + kBarRegion + kQRegion;  // 1 KiB: alignment of the swizzle
@@ -201,14 +201,16 @@ struct RowsMask {
   }
 };
 
-template <int D, int NT, int KV, int FORM>
+template <int D, int NT, int KV, int FORM, bool JOIN>
 __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits<D, NT, KV>::kMinBlocks))
     rows_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv) {
   using T = RowsTraits<D, NT, KV>;
   constexpr bool LIST = FORM == kFormBlocks, OWN = FORM == kFormOwn, SCORES = FORM == kFormScores;
   constexpr bool WIN = FORM == kFormWindow || OWN;  // pages numbered with a gap
-  constexpr bool kIdsAhead = !WIN && !LIST;         // the first block ids depend on the partition only
+  constexpr bool kIdsAhead = !WIN && !LIST && !JOIN;  // the first block ids depend on the partition only
+  constexpr bool kEven = JOIN && SCORES;              // the cluster cuts the sequence's own pages evenly
+  static_assert(!JOIN || LIST || SCORES, "forms that clusters join");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -216,8 +218,8 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
   const int part = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int Hq = p.num_q_heads, Hkv = p.num_kv_heads, G = Hq / Hkv;
   const int R = p.q_len * G;  // columns in use
-  const int ppp = p.pages_per_partition;
-  const int pbeg = part * ppp;
+  int ppp = p.pages_per_partition;
+  int pbeg = part * ppp;
   // the warp's j-th page: steps of kPP consecutive pages, dealt to the warps in turn
   auto page_no = [&](int j) { return pbeg + (warp + T::kWarps * (j / T::kPP)) * T::kPP + j % T::kPP; };
   const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
@@ -249,8 +251,12 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
   PageSpan span = {0, 0, ncols};
   if constexpr (WIN) span = page_span(span.count, lo_first, p.sinks, 1);
   const int npages = LIST ? p.num_listed : span.count;  // pages that some row sees (or that the list has room for)
-  if (pbeg >= npages) return;
-  const int pend = min(npages, pbeg + ppp);
+  if constexpr (kEven) {
+    ppp = (npages + (int)gridDim.x - 1) / (int)gridDim.x;
+    pbeg = min(part * ppp, npages);
+  }
+  if (!JOIN && pbeg >= npages) return;
+  const int pend = max(pbeg, min(npages, pbeg + ppp));  // (joined: a partition may be empty)
   const int nparts = (npages + ppp - 1) / ppp + (OWN && prefix > 0 ? 1 : 0);  // (with a prefix: always partial)
   const int32_t* list = LIST ? p.blocks + ((size_t)b * Hkv + g) * p.num_listed : nullptr;
   RowsMask mask = {p.tree_mask ? p.tree_mask + (size_t)b * p.q_len : nullptr, first_new, p.sinks, p.window};
@@ -363,6 +369,7 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
   // row scaled by a power of two before its f16 re-encoding; mul[nt][e] = what turns a raw score of column
   // 2qi + e into base-2 units.
   uint4* q_frag = reinterpret_cast<uint4*>(smem + T::kDataRegion + T::kBarRegion);
+  float* kept = reinterpret_cast<float*>(smem + T::kDataRegion + T::kBarRegion + T::kQRegion);  // joined: scores [tokens][G]
   float mul[NT][2];
   const float head_mul = p.scale_log2 * (T::kFp4 && p.k_scale ? p.k_scale[g] : 1.f);
 #pragma unroll
@@ -501,7 +508,8 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
             if constexpr (SCORES) {  // (no new row but the last: every token before the context's end is seen)
               const int c = 8 * nt + 2 * qi + (e & 1), t = gi + 8 * (e >> 1);
               if (((live[pp] >> t) & 1u) && c < R)
-                p.scores[(((size_t)b * Hkv + g) * p.max_context_len + tok0[pp] + t) * G + c] =
+                *(JOIN ? kept + (tok0[pp] + t - pbeg * T::kBS) * G + c
+                       : p.scores + (((size_t)b * Hkv + g) * p.max_context_len + tok0[pp] + t) * G + c) =
                     x[pp][nt][e] * (T::kFp8 ? mul[nt][e & 1] * ks : mul[nt][e & 1]);
             }
             x[pp][nt][e] = T::kFp8 ? fmaf(x[pp][nt][e], mul[nt][e & 1] * ks, vf.lv) : x[pp][nt][e] * mul[nt][e & 1];
@@ -649,6 +657,9 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
   __syncthreads();
   // combine the warps; store finished rows, or the partition's normalised rows and log2-sum-exps
   const float v_head = T::kFp4 && p.v_scale ? p.v_scale[g] : 1.f;
+  float* part_o = wl + T::kWarps * T::kCols;  // joined: [kCols][D], [kCols], [kCols]
+  Mass* part_mass = reinterpret_cast<Mass*>(part_o + T::kCols * D);
+  Mass* joined = part_mass + T::kCols;
   for (int idx = threadIdx.x; idx < R * (D / 4); idx += T::kThreads) {
     const int c = idx / (D / 4), dd = (idx % (D / 4)) * 4;
     float M = -INFINITY;
@@ -672,6 +683,11 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
       acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     }
     const size_t row = ((size_t)b * p.q_len + c / G) * Hq + g * G + c % G;
+    if constexpr (JOIN) {
+      *reinterpret_cast<float4*>(part_o + c * D + dd) = acc;
+      if (dd == 0) part_mass[c] = {M, lsum};
+      continue;
+    }
     if (nparts == 1) {
       *reinterpret_cast<uint2*>(p.out + row * D + dd) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
       if (SCORES && dd == 0) p.lse[row] = M + __log2f(lsum);
@@ -681,48 +697,63 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
       if (dd == 0) p.part_lse[at] = M == -INFINITY ? -INFINITY : M + __log2f(lsum);
     }
   }
+  if constexpr (JOIN) {
+    join_partitions<D, SCORES>(part_o, part_mass, R, joined, [&](int c) {
+      return p.out + (((size_t)b * p.q_len + c / G) * Hq + g * G + c % G) * D;
+    });
+    if constexpr (SCORES) {
+      __syncthreads();
+      fold_weights(p, b, g, G, pbeg * T::kBS, min(pend * T::kBS, L), L, kept, joined);
+    }
+    cluster_wait();  // nobody reads this CTA's shared memory any more
+  }
   if constexpr (OWN) after_prefixes();
 }
 
-template <int D, int NT, int KV, int FORM>
+template <int D, int NT, int KV, int FORM, bool JOIN>
 cudaError_t rows_launch(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   using T = RowsTraits<D, NT, KV>;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(rows_mma_kernel<D, NT, KV, FORM>), T::kSmem);
+  constexpr int kKept = JOIN && FORM == kFormScores ? kJoinScores : 0;
+  const void* fn = reinterpret_cast<const void*>(rows_mma_kernel<D, NT, KV, FORM, JOIN>);
+  cudaError_t e = set_smem_once(fn, T::kSmem + kKept);
   if (e != cudaSuccess) return e;
   dim3 grid(FORM == kFormOwn ? p.own_partitions : p.max_partitions, p.num_kv_heads, p.num_seqs);
-  if (FORM == kFormOwn && p.max_partitions > p.own_partitions) {  // beside the prefixes
+  if (JOIN || (FORM == kFormOwn && p.max_partitions > p.own_partitions)) {
     AttnParams pp = p;
     CUtensorMap k = tk, v = tv;
     void* args[] = {&pp, &k, &v};
-    return launch_dependent(reinterpret_cast<const void*>(rows_mma_kernel<D, NT, KV, FORM>), grid, dim3(T::kThreads),
-                            T::kSmem, st, args);
+    const int smem = T::kSmem + (kKept ? p.pages_per_partition * T::kBS * (p.num_q_heads / p.num_kv_heads) * 4 : 0);
+    if (JOIN) return launch_clusters(fn, grid, dim3(T::kThreads), smem, (int)grid.x, st, args);
+    return launch_dependent(fn, grid, dim3(T::kThreads), T::kSmem, st, args);  // beside the prefixes
   }
-  rows_mma_kernel<D, NT, KV, FORM><<<grid, T::kThreads, T::kSmem, st>>>(p, tk, tv);
+  rows_mma_kernel<D, NT, KV, FORM, JOIN><<<grid, T::kThreads, T::kSmem, st>>>(p, tk, tv);
   return cudaGetLastError();
 }
 
-template <int D, int KV, int FORM>
+template <int D, int KV, int FORM, bool JOIN = false>
 cudaError_t rows_tiles(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv) {
   const int nt = (l.group * p.q_len + 7) / 8;
-  if (nt == 1) return rows_launch<D, 1, KV, FORM>(p, tk, tv, l.stream);
-  if (nt == 2) return rows_launch<D, 2, KV, FORM>(p, tk, tv, l.stream);
+  if (nt == 1) return rows_launch<D, 1, KV, FORM, JOIN>(p, tk, tv, l.stream);
+  if (nt == 2) return rows_launch<D, 2, KV, FORM, JOIN>(p, tk, tv, l.stream);
   // (more bf16 rows run the tile kernel, which takes no list and keeps no scores)
   if constexpr (KV != kKvBf16 || FORM == kFormBlocks || FORM == kFormScores) {
-    if (nt == 3) return rows_launch<D, 3, KV, FORM>(p, tk, tv, l.stream);
-    if (nt == 4) return rows_launch<D, 4, KV, FORM>(p, tk, tv, l.stream);
+    if (nt == 3) return rows_launch<D, 3, KV, FORM, JOIN>(p, tk, tv, l.stream);
+    if (nt == 4) return rows_launch<D, 4, KV, FORM, JOIN>(p, tk, tv, l.stream);
   }
   return cudaErrorInvalidConfiguration;
 }
 
 // One form of the rows kernel, for its cache type and head_dim.
-template <int FORM>
+template <int FORM, bool JOIN = false>
 cudaError_t rows_any(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv) {
   const bool wide = l.head_dim == 128;
   if (!wide && l.head_dim != 64) return cudaErrorInvalidConfiguration;
   switch (l.kv) {
-    case kKvBf16: return wide ? rows_tiles<128, kKvBf16, FORM>(p, l, tk, tv) : rows_tiles<64, kKvBf16, FORM>(p, l, tk, tv);
-    case kKvE4m3: return wide ? rows_tiles<128, kKvE4m3, FORM>(p, l, tk, tv) : rows_tiles<64, kKvE4m3, FORM>(p, l, tk, tv);
-    default: return wide ? rows_tiles<128, kKvFp4, FORM>(p, l, tk, tv) : rows_tiles<64, kKvFp4, FORM>(p, l, tk, tv);
+    case kKvBf16:
+      return wide ? rows_tiles<128, kKvBf16, FORM, JOIN>(p, l, tk, tv) : rows_tiles<64, kKvBf16, FORM, JOIN>(p, l, tk, tv);
+    case kKvE4m3:
+      return wide ? rows_tiles<128, kKvE4m3, FORM, JOIN>(p, l, tk, tv) : rows_tiles<64, kKvE4m3, FORM, JOIN>(p, l, tk, tv);
+    default: return wide ? rows_tiles<128, kKvFp4, FORM, JOIN>(p, l, tk, tv) : rows_tiles<64, kKvFp4, FORM, JOIN>(p, l, tk, tv);
   }
 }
 

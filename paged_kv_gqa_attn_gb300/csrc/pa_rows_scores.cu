@@ -4,7 +4,7 @@
 namespace pa {
 
 cudaError_t rows_scores_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv) {
-  return rows_any<kFormScores>(p, l, tk, tv);
+  return l.join ? rows_any<kFormScores, true>(p, l, tk, tv) : rows_any<kFormScores>(p, l, tk, tv);
 }
 
 }  // namespace pa

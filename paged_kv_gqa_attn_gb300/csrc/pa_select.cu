@@ -8,7 +8,12 @@
 //
 // Scores: a warp takes 16 blocks of one (sequence, kv head) at a time, straight from global memory into A fragments (the
 // contraction's order is free: a lane reads whole 16-byte pieces, and the rows' codes are laid out alike, once for the CTA's
-// warps, in shared memory).  Bound by the bounds' bytes: a warp's next tile is loaded before this one's products.  Selection: one CTA per (sequence, kv head), see pa_topk.cuh.
+// warps, in shared memory).  Bound by the bounds' bytes: a warp's next tile is loaded before this one's products.
+//
+// Selection (pa_topk.cuh): up to one wave of clusters, contexts of up to 4096 blocks take one kernel, a cluster of eight CTAs
+// for each (sequence, kv head), whose scores meet as keys in the first CTA's shared memory: one launch, no scratch.  Else
+// two: scores in scratch, then one CTA per (sequence, kv head).  With bounds and attention, 4 contexts of up to 16384
+// tokens take 24.6 us in one kernel and 26.6 in two, 64 of up to 32768 152 and 141: a cluster's CTAs leave together.
 #include "pa_kernels.h"
 #include "pa_tc.cuh"
 #include "pa_topk.cuh"
@@ -35,23 +40,22 @@ __device__ __forceinline__ int code_exp(float amax) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const SelectParams p, int tiles_per_warp) {
-  constexpr int kChunks = D / 64;  // 16-byte pieces of a lane in each half ([hi] and [lo]) of a row
-  __shared__ uint4 q_frag[NT][2 * kChunks][32];  // B fragments: positive parts, then negative ones
-  __shared__ float q_up[8 * NT];                 // 2^f of each row
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gi = lane >> 2, qi = lane & 3;
-  const int g = blockIdx.y, b = blockIdx.z;
-  const int Hkv = p.num_kv_heads, G = p.num_q_heads / Hkv, R = p.q_len * G;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int L = max(0, min(p.context_lens[b], p.max_context_len));
-  if (p.context_lens[b] > p.max_context_len && blockIdx.x == 0 && g == 0 && threadIdx.x == 0)
-    record_error(p.err, kErrShortContext);
-  const int ncols = (L + 15) / 16;
-  if (blockIdx.x * kScoreWarps * tiles_per_warp * 16 >= ncols) return;
+struct ScoreShared {
+  static constexpr int kChunks = D / 64;  // 16-byte pieces of a lane in each half ([hi] and [lo]) of a row
+  uint4 q_frag[NT][2 * kChunks][32];      // B fragments: positive parts, then negative ones
+  float q_up[8 * NT];                     // 2^f of each row
+};
 
-  // the warp's tiles, dealt out in turn; the first one's loads start before the rows are rounded
+// Scores of 16-block tiles first, first + stride, ... (at most `most` of them, below ncols blocks) of (b, g) by each warp of
+// a CTA: sink(column, score) for every block.  Blocks that are not there score -infinity and are flagged.
+template <int D, int NT, class Sink>
+__device__ __forceinline__ void score_tiles(const SelectParams& p, int b, int g, int ncols, int first, int stride, int most,
+                                            ScoreShared<D, NT>& sh, Sink sink) {
+  constexpr int kChunks = D / 64;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gi = lane >> 2, qi = lane & 3;
+  const int Hkv = p.num_kv_heads, G = p.num_q_heads / Hkv, R = p.q_len * G;
+  // the first tile's loads start before the rows are rounded
   const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
-  const int tile0 = blockIdx.x * kScoreWarps * tiles_per_warp + warp;
   struct Tile {
     uint4 a0[2 * kChunks], a1[2 * kChunks];  // blocks gi and gi + 8: upper, then lower codes, pieces qi, qi + 4, ...
     float s0, s1;
@@ -73,8 +77,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const Sel
     t.s1 = p.bound_scale[page1];
   };
   Tile cur;
-  load(cur, id_at(tile0 * 16 + gi), id_at(tile0 * 16 + gi + 8));
-  int id0 = id_at((tile0 + kScoreWarps) * 16 + gi), id1 = id_at((tile0 + kScoreWarps) * 16 + gi + 8);
+  load(cur, id_at(first * 16 + gi), id_at(first * 16 + gi + 8));
+  int id0 = id_at((first + stride) * 16 + gi), id1 = id_at((first + stride) * 16 + gi + 8);
 
   // the codes of row gi of each n-tile, pieces qi and qi + 4 of its d dims, positive and negative parts
   for (int nt = warp; nt < NT; nt += kScoreWarps) {
@@ -114,29 +118,28 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const Sel
           neg[w] |= (uint32_t)(min(code, 0) & 0xff) << (8 * e);
         }
       }
-      q_frag[nt][k][lane] = make_uint4(pos[0], pos[1], pos[2], pos[3]);
-      q_frag[nt][kChunks + k][lane] = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+      sh.q_frag[nt][k][lane] = make_uint4(pos[0], pos[1], pos[2], pos[3]);
+      sh.q_frag[nt][kChunks + k][lane] = make_uint4(neg[0], neg[1], neg[2], neg[3]);
     }
-    if (qi == 0) q_up[c] = exp2_int(f);
+    if (qi == 0) sh.q_up[c] = exp2_int(f);
   }
   __syncthreads();
   float up[NT][2];  // of rows 2qi, 2qi + 1
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    up[nt][0] = q_up[8 * nt + 2 * qi];
-    up[nt][1] = q_up[8 * nt + 2 * qi + 1];
+    up[nt][0] = sh.q_up[8 * nt + 2 * qi];
+    up[nt][1] = sh.q_up[8 * nt + 2 * qi + 1];
   }
 
-  float* out = p.scores + ((size_t)b * Hkv + g) * p.max_cols;
-  for (int t = 0; t < tiles_per_warp; ++t) {
-    const int col0 = (tile0 + t * kScoreWarps) * 16;
+  for (int t = 0; t < most; ++t) {
+    const int col0 = (first + t * stride) * 16;
     if (col0 >= ncols) break;
     Tile next;
-    const bool more = t + 1 < tiles_per_warp && col0 + kScoreWarps * 16 < ncols;
+    const bool more = t + 1 < most && col0 + stride * 16 < ncols;
     if (more) {
       load(next, id0, id1);
-      id0 = id_at(col0 + 2 * kScoreWarps * 16 + gi);
-      id1 = id_at(col0 + 2 * kScoreWarps * 16 + gi + 8);
+      id0 = id_at(col0 + 2 * stride * 16 + gi);
+      id1 = id_at(col0 + 2 * stride * 16 + gi + 8);
     }
     if (((!cur.ok0 && col0 + gi < ncols) || (!cur.ok1 && col0 + gi + 8 < ncols)) && qi == 0)
       record_error(p.err, kErrBlockId);
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const Sel
       int acc[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < 2 * kChunks; ++k) {
-        const uint4 q = q_frag[nt][k][lane];
+        const uint4 q = sh.q_frag[nt][k][lane];
         mma_s8(acc, cur.a0[k].x, cur.a1[k].x, cur.a0[k].y, cur.a1[k].y, q.x, q.y);
         mma_s8(acc, cur.a0[k].z, cur.a1[k].z, cur.a0[k].w, cur.a1[k].w, q.z, q.w);
       }
@@ -164,11 +167,67 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const Sel
       best1 = fmaxf(best1, __shfl_xor_sync(0xffffffffu, best1, o));
     }
     if (qi == 0) {  // (a block that is not there comes last)
-      if (col0 + gi < ncols) out[col0 + gi] = cur.ok0 ? best0 * cur.s0 : -INFINITY;
-      if (col0 + gi + 8 < ncols) out[col0 + gi + 8] = cur.ok1 ? best1 * cur.s1 : -INFINITY;
+      if (col0 + gi < ncols) sink(col0 + gi, cur.ok0 ? best0 * cur.s0 : -INFINITY);
+      if (col0 + gi + 8 < ncols) sink(col0 + gi + 8, cur.ok1 ? best1 * cur.s1 : -INFINITY);
     }
     if (more) cur = next;
   }
+}
+
+// The sequence's blocks, its length cut to the bound (and flagged by one thread).
+__device__ __forceinline__ int select_cols(const SelectParams& p, int b, bool flag) {
+  const int L = p.context_lens[b];
+  if (flag && L > p.max_context_len) record_error(p.err, kErrShortContext);
+  return (max(0, min(L, p.max_context_len)) + 15) / 16;
+}
+
+constexpr int kClusterCtas = 8;
+constexpr int kClusterCols = 4096;  // keys in the first CTA's shared memory
+
+// Whether a call takes the one kernel.
+bool in_clusters(int num_seqs, int num_kv_heads, int max_context_len, int num_sms) {
+  return max_context_len <= kClusterCols * 16 && (int64_t)num_seqs * num_kv_heads <= num_sms;
+}
+
+template <int D, int NT>
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kScoreWarps * 32)
+    block_select_kernel(const SelectParams p) {
+  extern __shared__ uint32_t smem_keys[];  // of the first CTA: one for each block
+  __shared__ ScoreShared<D, NT> sh;
+  __shared__ TopkShared top;
+  const int rank = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+  const int ncols = select_cols(p, b, rank == 0 && g == 0 && threadIdx.x == 0);
+  int32_t* out = p.blocks + ((size_t)b * p.num_kv_heads + g) * p.count;
+  if (ncols <= p.count) {  // (the whole cluster) every block
+    if (rank == 0)
+      for (int i = threadIdx.x; i < p.count; i += blockDim.x) out[i] = i < ncols ? i : -1;
+    return;
+  }
+  cluster_arrive();
+  uint32_t keys0;  // the first CTA's keys
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(keys0) : "r"(smem_addr(smem_keys)), "r"(0));
+  cluster_wait();  // every CTA runs: its shared memory may be written
+  const int first = rank * kScoreWarps + (threadIdx.x >> 5);
+  score_tiles<D, NT>(p, b, g, ncols, first, kClusterCtas * kScoreWarps, kClusterCols, sh, [&](int col, float score) {
+    const uint32_t key = col < p.sinks || col >= ncols - p.recent ? kKeyAlways : order_key(score);
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys0 + col * 4), "r"(key) : "memory");
+  });
+  cluster_arrive();
+  cluster_wait();
+  if (rank == 0) topk_in_order(smem_keys, ncols, p.count, top, [&](int at, int i) { out[at] = i; });
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const SelectParams p, int tiles_per_warp) {
+  __shared__ ScoreShared<D, NT> sh;
+  const int g = blockIdx.y, b = blockIdx.z;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int ncols = select_cols(p, b, blockIdx.x == 0 && g == 0 && threadIdx.x == 0);
+  const int first = blockIdx.x * kScoreWarps * tiles_per_warp;
+  if (first * 16 >= ncols) return;
+  float* out = p.scores + ((size_t)b * p.num_kv_heads + g) * p.max_cols;
+  score_tiles<D, NT>(p, b, g, ncols, first + (threadIdx.x >> 5), kScoreWarps, tiles_per_warp, sh,
+                     [&](int col, float score) { out[col] = score; });
 }
 
 // One CTA per (kv head, sequence).  IN_SMEM: the keys are kept in shared memory, else turned in place in the scores.
@@ -177,8 +236,7 @@ __global__ void __launch_bounds__(1024) block_pick_kernel(const SelectParams p) 
   extern __shared__ uint32_t smem_keys[];
   __shared__ TopkShared sh;
   const int g = blockIdx.x, b = blockIdx.y;
-  const int L = max(0, min(p.context_lens[b], p.max_context_len));
-  const int n = (L + 15) / 16;
+  const int n = select_cols(p, b, false);
   int32_t* out = p.blocks + ((size_t)b * p.num_kv_heads + g) * p.count;
   const int k = min(n, p.count);
   for (int i = k + threadIdx.x; i < p.count; i += blockDim.x) out[i] = -1;
@@ -199,6 +257,10 @@ constexpr int kPickSmemCols = 50000;  // keys that fit in shared memory
 
 template <int D, int NT>
 cudaError_t score(const SelectParams& p, int num_sms, cudaStream_t st) {
+  if (in_clusters(p.num_seqs, p.num_kv_heads, p.max_context_len, num_sms)) {  // scored and selected
+    block_select_kernel<D, NT><<<dim3(kClusterCtas, p.num_kv_heads, p.num_seqs), kScoreWarps * 32, p.max_cols * 4, st>>>(p);
+    return cudaGetLastError();
+  }
   // a tile a warp until there are several waves of warps; then up to eight, so that a warp's loads run ahead (64 contexts
   // of 8000 to 32768 tokens, 8 heads, with selection and attention: 1 tile 156 us, 2 144, 4 140, 8 138, 13 143)
   const int64_t tiles = (p.max_cols + 15) / 16, units = (int64_t)p.num_seqs * p.num_kv_heads;
@@ -222,28 +284,28 @@ cudaError_t score_rows(const SelectParams& p, int num_sms, cudaStream_t st) {
 
 }  // namespace
 
-size_t select_scratch_bytes(int num_seqs, int num_kv_heads, int max_context_len) {
-  return (size_t)num_seqs * num_kv_heads * (((size_t)max_context_len + 15) / 16 + 1) * sizeof(float);
+size_t select_scratch_bytes(int num_seqs, int num_kv_heads, int max_context_len, int num_sms) {
+  const size_t cols = ((size_t)max_context_len + 15) / 16;
+  return in_clusters(num_seqs, num_kv_heads, max_context_len, num_sms) ? 0
+                                                                       : (size_t)num_seqs * num_kv_heads * cols * sizeof(float);
 }
 
 cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, int num_sms, cudaStream_t st) {
-  if (p.max_cols > 0) {
-    const cudaError_t e = head_dim == 128 ? score_rows<128>(p, num_sms, st)
-                          : head_dim == 64 ? score_rows<64>(p, num_sms, st)
-                                           : cudaErrorInvalidConfiguration;
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = head_dim == 128 ? score_rows<128>(p, num_sms, st)
+                        : head_dim == 64 ? score_rows<64>(p, num_sms, st)
+                                         : cudaErrorInvalidConfiguration;
+  if (e != cudaSuccess || in_clusters(p.num_seqs, p.num_kv_heads, p.max_context_len, num_sms)) return e;
   const bool in_smem = p.max_cols <= kPickSmemCols;
   const void* fn = in_smem ? reinterpret_cast<const void*>(block_pick_kernel<true>)
                            : reinterpret_cast<const void*>(block_pick_kernel<false>);
   const int smem = in_smem ? p.max_cols * 4 : 0;
   if (in_smem) {
-    const cudaError_t e = set_smem_once(fn, kPickSmemCols * 4);
-    if (e != cudaSuccess) return e;
+    const cudaError_t e2 = set_smem_once(fn, kPickSmemCols * 4);
+    if (e2 != cudaSuccess) return e2;
   }
-  const int threads = p.max_cols <= 1024 ? 256 : p.max_cols <= 4096 ? 512 : 1024;
   SelectParams pp = p;
   void* args[] = {&pp};
+  const int threads = p.max_cols <= 4096 ? 512 : 1024;
   return launch_dependent(fn, dim3(p.num_kv_heads, p.num_seqs), dim3(threads), smem, st, args);
 }
 

@@ -25,7 +25,10 @@ def _sums(c, seed=1):
 def _hold_weights(c, before, after, decay, dots, probs):
     """The sums' bound, relative to the step's weight of each head: twice the error of a score (as in
     form_cases.check; the row's log2-sum-exp has it as well), four roundings of a base-2 score, the row sum's n
-    additions, and the exponentials' and the logarithm's own (2^-19); then decay * sum + weight in fp32 (2^-23 of it)."""
+    additions, and the exponentials' own (2^-19); where partial rows meet in memory also the log2-sum-exps that they are
+    kept as, of a part and of the row: the logarithm of a sum below 2^16 is below 16, so that two units in its last place
+    (2^-20) are 2^-19, and the sum with the maximum, below 32, rounds by 2^-20, twice each and times ln 2 < 0.7; then
+    decay * sum + weight in fp32 (2^-23 of it)."""
     want = before.double().numpy().copy()
     slack = np.zeros(want.shape)
     hkv, d = want.shape[1], c["d"]
@@ -34,7 +37,8 @@ def _hold_weights(c, before, after, decay, dots, probs):
         for h in range(hkv):
             p = probs[b][h, 0]  # [G, n]
             y = dots[b, 0, h * g: (h + 1) * g]
-            rel = 4 * d * 2.0 ** -24 * y + 4 * 2.0 ** -22 * y + n * 2.0 ** -24 + 2.0 ** -19
+            rel = 4 * d * 2.0 ** -24 * y + 4 * 2.0 ** -22 * y + n * 2.0 ** -24 + 2.0 ** -19 + \
+                0.7 * 2 * (2.0 ** -19 + 2.0 ** -20)
             for j in range(n):
                 at = (int(c["table"][b, j // 16]), h, j % 16)
                 old = 0.0 if j == n - 1 else decay * want[at] if decay else 0.0
