@@ -22,7 +22,9 @@ struct Launch {
   bool join = false;  // a row's partitions are one cluster, which joins them (no partials, no merge)
 };
 constexpr int kJoinCtas = kJoinMax;      // partitions of a cluster at most (the portable size)
-constexpr int kJoinScores = 48 << 10;    // bytes of kept scores of a CTA at most
+// Bytes of kept scores of a CTA at most: they take room from the ring stages of other CTAs (64 contexts of up to 16384
+// tokens, bf16, 32 KB of scores a CTA: 428 us where scores in scratch take 392).
+constexpr int kJoinScores = 8 << 10;
 
 // Each returns cudaSuccess or the launch error.  Unsupported combinations return
 // cudaErrorInvalidConfiguration (the caller has already checked them).

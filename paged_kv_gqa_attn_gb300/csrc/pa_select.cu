@@ -181,7 +181,7 @@ __device__ __forceinline__ int select_cols(const SelectParams& p, int b, bool fl
   return (max(0, min(L, p.max_context_len)) + 15) / 16;
 }
 
-constexpr int kClusterCtas = 8;
+constexpr int kClusterCtas = 8;     // at most
 constexpr int kClusterCols = 4096;  // keys in the first CTA's shared memory
 
 // Whether a call takes the one kernel.
@@ -190,8 +190,7 @@ bool in_clusters(int num_seqs, int num_kv_heads, int max_context_len, int num_sm
 }
 
 template <int D, int NT>
-__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kScoreWarps * 32)
-    block_select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kScoreWarps * 32) block_select_kernel(const SelectParams p) {
   extern __shared__ uint32_t smem_keys[];  // of the first CTA: one for each block
   __shared__ ScoreShared<D, NT> sh;
   __shared__ TopkShared top;
@@ -208,7 +207,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kScoreWar
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(keys0) : "r"(smem_addr(smem_keys)), "r"(0));
   cluster_wait();  // every CTA runs: its shared memory may be written
   const int first = rank * kScoreWarps + (threadIdx.x >> 5);
-  score_tiles<D, NT>(p, b, g, ncols, first, kClusterCtas * kScoreWarps, kClusterCols, sh, [&](int col, float score) {
+  score_tiles<D, NT>(p, b, g, ncols, first, gridDim.x * kScoreWarps, kClusterCols, sh, [&](int col, float score) {
     const uint32_t key = col < p.sinks || col >= ncols - p.recent ? kKeyAlways : order_key(score);
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys0 + col * 4), "r"(key) : "memory");
   });
@@ -258,8 +257,14 @@ constexpr int kPickSmemCols = 50000;  // keys that fit in shared memory
 template <int D, int NT>
 cudaError_t score(const SelectParams& p, int num_sms, cudaStream_t st) {
   if (in_clusters(p.num_seqs, p.num_kv_heads, p.max_context_len, num_sms)) {  // scored and selected
-    block_select_kernel<D, NT><<<dim3(kClusterCtas, p.num_kv_heads, p.num_seqs), kScoreWarps * 32, p.max_cols * 4, st>>>(p);
-    return cudaGetLastError();
+    // CTAs of a cluster: no more than there are tiles for, nor than one wave of four CTAs an SM holds
+    const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads, tiles = (p.max_cols + 15) / 16;
+    int ctas = kClusterCtas;
+    while (ctas > 1 && (units * ctas > 4 * (int64_t)num_sms || (ctas / 2) * kScoreWarps >= tiles)) ctas /= 2;
+    const void* fn = reinterpret_cast<const void*>(block_select_kernel<D, NT>);
+    SelectParams pp = p;
+    void* args[] = {&pp};
+    return launch_clusters(fn, dim3(ctas, p.num_kv_heads, p.num_seqs), dim3(kScoreWarps * 32), p.max_cols * 4, ctas, st, args);
   }
   // a tile a warp until there are several waves of warps; then up to eight, so that a warp's loads run ahead (64 contexts
   // of 8000 to 32768 tokens, 8 heads, with selection and attention: 1 tile 156 us, 2 144, 4 140, 8 138, 13 143)

@@ -15,7 +15,8 @@ constexpr int kFoldTokens = 4;  // of a thread: a quarter of a block's (one a th
 template <int G>  // 0: any group
 __global__ void __launch_bounds__(256) fold_weights_kernel(const WeightParams p) {
   const int group = G > 0 ? G : p.group;
-  const int g = blockIdx.y, b = blockIdx.z;
+  // the sequences whose scores were written last come first: they are still in the L2
+  const int g = blockIdx.y, b = gridDim.z - 1 - blockIdx.z;
   const int L = max(0, min(p.context_lens[b], p.max_context_len));
   const int t = (blockIdx.x * 256 + threadIdx.x) * kFoldTokens;
   int pb = -1;
