@@ -368,7 +368,7 @@ int paged_attn_weighted_decode(const void* q, const void* k_cache, const void* v
  * heads keep different tokens: a slot no longer stands for one position, so attention over what is left uses keys
  * rotated before (the caller counts positions on its own).  Out-of-range ids are flagged: a token that cannot be read
  * counts as sum 0 and becomes zeros, a page that cannot be written is left out.  Scratch: 4 bytes per (kept token, kv
- * head), and 4 per (token, kv head) where max_context_len exceeds 50000.  Asynchronous on `stream`.  Returns PA_OK
+ * head), and 4 per (token, kv head) where max_context_len exceeds 98304.  Asynchronous on `stream`.  Returns PA_OK
  * (also for num_seqs == 0), PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_NO_MEMORY or PA_ERR_CUDA.
  */
 int paged_attn_evict(void* k_cache, void* v_cache, float* weights, const int32_t* block_table,

@@ -973,7 +973,7 @@ int paged_attn_evict(void* k_cache, void* v_cache, float* weights, const int32_t
   p.keep = keep;
   p.sinks = sinks;
   p.recent = recent;
-  const cudaError_t e = pa::launch_evict(p, head_dim, kv_dtype, s);
+  const cudaError_t e = pa::launch_evict(p, head_dim, kv_dtype, dev->num_sms, s);
   cudaFreeAsync(scratch, s);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

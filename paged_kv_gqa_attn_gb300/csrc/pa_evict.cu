@@ -5,11 +5,17 @@
 // table; the old blocks are only read, so blocks that other sequences share stay whole, every row moves
 // independently of the others, and the caller gives the old ones back afterwards.
 //
-// Two kernels.  The first finds the kept positions: one CTA per (kv head, sequence), the sums as keys in shared memory
-// (pa_topk.cuh), and moves the sums.  The second moves rows: a warp for each new (block, head) page, all of a page's K and
-// V loads in flight at once.  bf16 rows and 4-bit rows (codes and their scales belong to the token) move as they
-// are; E4M3 pages get the scale amax / 448 of their new tokens, values times the old scales re-encoded in fp32 to
-// nearest even as the append does.  Bound by the kept rows' bytes, read and written once.
+// Contexts of up to 98304 tokens are selected by a cluster of eight CTAs for each (sequence, kv head), a share of the sums in
+// each one's shared memory as keys.  The k-th largest is found digit by digit (as in pa_topk.cuh), each CTA adding its counters to
+// everybody's, and the kept positions go to scratch.  Few (sequence, kv head) pairs are moved by the same cluster
+// after a barrier; many by a second kernel, whose warps spread over the device (16 contexts of up to 32768 tokens, 8 heads, 4096
+// kept: 116 us; moved by the clusters 147, as they all select, then all move; selected by one CTA each 120; with the
+// second kernel's CTAs started early, to wait on the SMs for the first's, 131).  Longer contexts are selected by one CTA each, with the keys in scratch.  A page is moved by a warp with all of its K and V
+// loads in flight.
+//
+// bf16 rows and 4-bit rows (codes and their scales belong to the token) move as they are; E4M3 pages get the scale amax /
+// 448 of their new tokens, values times the old scales re-encoded in fp32 to nearest even as the append does.  Bound by
+// the kept rows' bytes, read and written once.
 #include "pa_fp4.cuh"
 #include "pa_kernels.h"
 #include "pa_tc.cuh"
@@ -18,7 +24,6 @@
 namespace pa {
 namespace {
 
-constexpr int kKeySmem = 50000;  // sums that are kept in shared memory
 constexpr int kMoveWarps = 4;
 
 // The sequence's length inside its table row.
@@ -26,9 +31,8 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int b) {
   return max(0, min(p.context_lens[b], p.max_context_len));
 }
 
-// keys_global: [B, Hkv, max_context_len] where the sums do not fit in shared memory, else null.
-__global__ void __launch_bounds__(1024) evict_pick_kernel(const EvictParams p, uint32_t* keys_global) {
-  extern __shared__ uint32_t smem_keys[];
+// Contexts past the cluster's shared memory: one CTA per (kv head, sequence), all_keys [B, Hkv, max_context_len].
+__global__ void __launch_bounds__(1024) evict_pick_kernel(const EvictParams p, uint32_t* all_keys) {
   __shared__ TopkShared sh;
   const int g = blockIdx.x, b = blockIdx.y;
   const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
@@ -73,7 +77,7 @@ __global__ void __launch_bounds__(1024) evict_pick_kernel(const EvictParams p, u
     move_sums([](int at) { return at; });
     return;
   }
-  uint32_t* keys = keys_global ? keys_global + unit * p.max_context_len : smem_keys;
+  uint32_t* keys = all_keys + unit * p.max_context_len;
   // the sums, kBatch of a thread in flight at once (their addresses wait for the table)
   constexpr int kBatch = 8;
   for (int i0 = threadIdx.x; i0 < L; i0 += kBatch * threads) {
@@ -102,17 +106,12 @@ __global__ void __launch_bounds__(1024) evict_pick_kernel(const EvictParams p, u
 
 // A warp moves the page (new block, head): lane t < 16 knows where token t comes from.
 template <int D, int KV>
-__global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const EvictParams p) {
+__device__ __forceinline__ void move_page(const EvictParams& p, int b, int g, int page, int k) {
   constexpr int kRowBytes = KV == kKvBf16 ? 2 * D : KV == kKvE4m3 ? D : D / 2;  // of codes
   constexpr int kPageBytes = KV == kKvFp4 ? Fp4Page<D>::kBytes : 16 * kRowBytes;
   constexpr int kPieces = kRowBytes / 16;           // 16-byte pieces of a row
   constexpr int kRowsAtOnce = 32 / kPieces, kLoads = 16 / kRowsAtOnce;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int page = blockIdx.x, b = blockIdx.y;
-  const int g = blockIdx.z * kMoveWarps + warp;
-  const int k = min(evict_len(p, b), p.keep);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (g >= p.num_kv_heads || page * 16 >= k) return;
+  const int lane = threadIdx.x & 31;
   const int valid = min(16, k - page * 16);
   const int nb = p.new_table[(size_t)b * p.new_blocks + page];
   if (nb < 0 || nb >= p.num_blocks) {
@@ -122,7 +121,8 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const Evict
   const size_t dst_page = (size_t)nb * p.num_kv_heads + g;
   int src_block = -1, src_slot = 0;
   if (lane < valid) {
-    const int at = p.kept[((size_t)b * p.num_kv_heads + g) * p.keep + page * 16 + lane];
+    // (from the L2: other CTAs of the cluster wrote it)
+    const int at = __ldcg(&p.kept[((size_t)b * p.num_kv_heads + g) * p.keep + page * 16 + lane]);
     src_block = p.block_table[(size_t)b * p.max_blocks_per_seq + at / 16];
     src_slot = at % 16;
     if (src_block < 0 || src_block >= p.num_blocks) src_block = -1;  // its row becomes zeros (flagged with its sum)
@@ -204,6 +204,264 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const Evict
   }
 }
 
+template <int D, int KV>
+__global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const EvictParams p) {
+  const int page = blockIdx.x, b = blockIdx.y, g = blockIdx.z * kMoveWarps + (threadIdx.x >> 5);
+  const int k = min(evict_len(p, b), p.keep);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (g < p.num_kv_heads && page * 16 < k) move_page<D, KV>(p, b, g, page, k);
+}
+
+constexpr int kEvictCtas = 8, kEvictThreads = 256;  // CTAs of a cluster at most
+constexpr int kEvictKeys = 12288;  // keys of a CTA at most
+
+struct EvictShared {
+  alignas(16) int hist[256 * 4];  // this CTA's counters, four a digit
+  int total[2][256];              // the cluster's: every CTA adds its own to all of them; of every other digit
+  uint32_t top, bottom;           // of the cluster's keys that are not forced, and how many are
+  int always;
+  int digit, above, at;
+  int gt[kEvictCtas], eq[kEvictCtas];  // of the CTAs
+  int warp_gt[kEvictThreads / 32], warp_eq[kEvictThreads / 32];
+};
+
+__device__ __forceinline__ void cluster_add(uint32_t addr, int v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+
+// One cluster per (sequence, kv head).  CTA r has the keys of tokens [r * share, r * share + share).  MOVE: the cluster moves
+// the rows as well (D, KV: of the caches).
+template <int D, int KV, bool MOVE>
+__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams p) {
+  extern __shared__ uint32_t keys[];
+  __shared__ EvictShared sh;
+  const int ctas = gridDim.x, rank = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
+  const int32_t* to = p.new_table + (size_t)b * p.new_blocks;
+  const int L = evict_len(p, b), k = min(L, p.keep);
+  const size_t unit = (size_t)b * p.num_kv_heads + g;
+  int32_t* kept = p.kept + unit * p.keep;
+  if (rank == 0 && g == 0 && tid == 0) {
+    p.new_lens[b] = k;
+    if (p.context_lens[b] > p.max_context_len) record_error(p.err, kErrShortContext);
+  }
+  auto sums = [&](auto pos, int n, auto use) {  // use(i, pos(i), its sum) for i of [0, n), kBatch of a thread in flight
+    constexpr int kBatch = 8;
+    for (int i0 = tid; i0 < n; i0 += kBatch * kEvictThreads) {
+      int pb[kBatch], at[kBatch];
+      float w[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) at[j] = i0 + j * kEvictThreads < n ? pos(i0 + j * kEvictThreads) : -1;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) pb[j] = at[j] >= 0 ? bt[at[j] / 16] : 0;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const bool there = pb[j] >= 0 && pb[j] < p.num_blocks;
+        if (!there) record_error(p.err, kErrBlockId);
+        w[j] = there && at[j] >= 0 ? p.weights[((size_t)pb[j] * p.num_kv_heads + g) * 16 + at[j] % 16] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (at[j] >= 0) use(i0 + j * kEvictThreads, at[j], w[j]);
+    }
+  };
+  auto place = [&](int at, float w) {  // of kept token `at`
+    const int pb = to[at / 16];
+    if (pb >= 0 && pb < p.num_blocks)  // (out of range: flagged with the rows)
+      p.weights[((size_t)pb * p.num_kv_heads + g) * 16 + at % 16] = w;
+  };
+  const int share = (L + ctas * 16 - 1) / (ctas * 16) * 16;
+  const int begin = min(rank * share, L), n = min(share, L - begin);
+  if (L <= p.keep) {  // (the whole cluster) every token
+    sums([&](int i) { return begin + i; }, n, [&](int i, int at, float w) {
+      kept[at] = at;
+      place(at, w);
+    });
+  } else {
+    static_assert(kEvictThreads == 256, "a thread a digit");
+    sh.total[0][tid] = sh.total[1][tid] = 0;
+    if (tid == 0) {
+      sh.top = 0u;
+      sh.bottom = kKeyAlways;
+      sh.always = 0;
+    }
+    cluster_arrive();
+    const uint32_t here = smem_addr(&sh);
+    auto in_cta = [&](int r, const void* member) { return cluster_addr(here, r) + (smem_addr(member) - here); };
+    // the keys, a quarter of a block's of a thread at a time, kQuads in flight
+    constexpr int kQuads = 4;
+    uint32_t top = 0u, bottom = kKeyAlways;
+    int always = 0;
+    for (int i0 = 4 * tid; i0 < n; i0 += kQuads * 4 * kEvictThreads) {
+      int pb[kQuads];
+      float4 w[kQuads];
+#pragma unroll
+      for (int j = 0; j < kQuads; ++j) {
+        const int i = i0 + j * 4 * kEvictThreads;
+        pb[j] = i < n ? bt[(begin + i) / 16] : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kQuads; ++j) {
+        const int i = i0 + j * 4 * kEvictThreads;
+        const bool there = pb[j] >= 0 && pb[j] < p.num_blocks;
+        if (!there) record_error(p.err, kErrBlockId);
+        w[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (there && i < n)
+          w[j] = *reinterpret_cast<const float4*>(p.weights + ((size_t)pb[j] * p.num_kv_heads + g) * 16 + (begin + i) % 16);
+      }
+#pragma unroll
+      for (int j = 0; j < kQuads; ++j) {
+        const float w4[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = i0 + j * 4 * kEvictThreads + e;
+          if (i >= n) break;
+          const bool forced = begin + i < p.sinks || begin + i >= L - p.recent;
+          const uint32_t x = forced ? kKeyAlways : order_key(w4[e]);
+          keys[i] = x;
+          always += forced;
+          top = max(top, forced ? 0u : x);
+          bottom = min(bottom, x);
+        }
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    bottom = __reduce_min_sync(0xffffffffu, bottom);
+    always = __reduce_add_sync(0xffffffffu, always);
+    cluster_wait();  // every CTA runs, and its counters are clear
+    if (lane < ctas) {  // (a lane a CTA)
+      asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(in_cta(lane, &sh.top)), "r"(top) : "memory");
+      asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(in_cta(lane, &sh.bottom)), "r"(bottom)
+                   : "memory");
+      if (always) cluster_add(in_cta(lane, &sh.always), always);
+    }
+    cluster_sync();
+    int need = k - sh.always;  // keys to take among the candidates: those that agree with low in the known bits
+    const int differ = 32 - __clz(sh.top ^ sh.bottom);
+    uint32_t known = differ >= 32 ? 0u : ~0u << differ, low = sh.top & known;
+    bool exact = need <= 0;  // all candidates are taken
+    if (exact) low = kKeyAlways;
+    for (int shift = differ, turn = 0; shift > 0 && !exact; turn ^= 1) {  // (the same in every CTA)
+      shift = max(shift - 8, 0);
+      for (int i = tid; i < 256; i += kEvictThreads) *reinterpret_cast<int4*>(&sh.hist[4 * i]) = make_int4(0, 0, 0, 0);
+      __syncthreads();
+      for (int i = tid; i < n; i += kEvictThreads) {
+        const uint32_t x = keys[i];
+        if ((x & known) == low && x != kKeyAlways) atomicAdd(&sh.hist[((x & ~known) >> shift) * 4 + (lane & 3)], 1);
+      }
+      __syncthreads();
+      const int4 c = *reinterpret_cast<const int4*>(&sh.hist[4 * tid]);
+      const int mine = (c.x + c.y) + (c.z + c.w);
+      if (mine)
+        for (int r = 0; r < ctas; ++r) cluster_add(in_cta(r, &sh.total[turn][tid]), mine);
+      cluster_sync();
+      if (warp == 0) {  // lane l: digits 255 - 8 l down to 248 - 8 l
+        int count[8], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          count[j] = sh.total[turn][255 - 8 * lane - j];
+          sh.total[turn][255 - 8 * lane - j] = 0;  // for the digit after the next, a barrier of the cluster away
+          sum += count[j];
+        }
+        int upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
+        const unsigned reached = __ballot_sync(0xffffffffu, upto >= need);  // (never empty: need candidates are there)
+        if (lane == __ffs(reached) - 1) {
+          int above = upto - sum;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (above + count[j] >= need) {
+              sh.digit = 255 - 8 * lane - j;
+              sh.above = above;
+              sh.at = count[j];
+              break;
+            }
+            above += count[j];
+          }
+        }
+      }
+      __syncthreads();
+      low |= (uint32_t)sh.digit << shift;
+      known = ~0u << shift;
+      need -= sh.above;
+      exact = sh.at == need;  // (what is not known of low is zeros)
+    }
+    // which keys are taken: each warp a run of them, 32 at a time; how many before it, in the CTAs before and in this one
+    const int per = (n + kEvictThreads - 1) / kEvictThreads * 32;
+    const int from = min(n, warp * per), till = min(n, from + per);
+    auto above_at = [&](int i, bool& above, bool& at) {
+      const uint32_t x = i < till ? keys[i] : 0u;
+      above = i < till && (exact ? x >= low : x > low);
+      at = i < till && !exact && x == low;
+    };
+    int gt = 0, eq = 0;
+    for (int i0 = from; i0 < till; i0 += 32) {
+      bool above, at;
+      above_at(i0 + lane, above, at);
+      gt += __popc(__ballot_sync(0xffffffffu, above));
+      eq += __popc(__ballot_sync(0xffffffffu, at));
+    }
+    if (lane == 0) {
+      sh.warp_gt[warp] = gt;
+      sh.warp_eq[warp] = eq;
+    }
+    __syncthreads();
+    int gt_before = 0, eq_before = 0, gt_cta = 0, eq_cta = 0;
+    for (int w = 0; w < kEvictThreads / 32; ++w) {
+      gt_cta += sh.warp_gt[w];
+      eq_cta += sh.warp_eq[w];
+      if (w < warp) {
+        gt_before += sh.warp_gt[w];
+        eq_before += sh.warp_eq[w];
+      }
+    }
+    if (tid < ctas) {  // to every CTA
+      const uint32_t there = cluster_addr(smem_addr(&sh), tid) - smem_addr(&sh);
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there + smem_addr(&sh.gt[rank])), "r"(gt_cta) : "memory");
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there + smem_addr(&sh.eq[rank])), "r"(eq_cta) : "memory");
+    }
+    cluster_sync();
+    int gt_all = 0;
+    for (int r = 0; r < ctas; ++r) {
+      gt_all += sh.gt[r];
+      if (r < rank) {
+        gt_before += sh.gt[r];
+        eq_before += sh.eq[r];
+      }
+    }
+    const int room = k - gt_all;  // keys equal to low that are taken, the earliest
+    const unsigned before = (1u << lane) - 1u;
+    for (int i0 = from; i0 < till; i0 += 32) {
+      bool above, at;
+      above_at(i0 + lane, above, at);
+      const unsigned ga = __ballot_sync(0xffffffffu, above), ea = __ballot_sync(0xffffffffu, at);
+      const int my_gt = gt_before + __popc(ga & before), my_eq = eq_before + __popc(ea & before);
+      if (above || (at && my_eq < room)) kept[my_gt + min(my_eq, room)] = begin + i0 + lane;
+      gt_before += __popc(ga);
+      eq_before += __popc(ea);
+    }
+  }
+  cluster_sync();  // the kept positions, written by all of the cluster
+  if constexpr (MOVE) {
+    const int pages = (k + 15) / 16;
+    for (int page = rank * (kEvictThreads / 32) + warp; page < pages; page += ctas * (kEvictThreads / 32))
+      move_page<D, KV>(p, b, g, page, k);
+  }
+  if (L > p.keep) {  // the sums of this CTA's share of the kept tokens
+    const int part = (k + ctas - 1) / ctas, a0 = rank * part;
+    sums([&](int i) { return __ldcg(&kept[a0 + i]); }, min(part, k - a0), [&](int i, int at, float w) { place(a0 + i, w); });
+  }
+}
+
 template <int D>
 const void* move_kernel(int kv) {
   return kv == kKvBf16   ? reinterpret_cast<const void*>(evict_move_kernel<D, kKvBf16>)
@@ -211,30 +469,49 @@ const void* move_kernel(int kv) {
                          : reinterpret_cast<const void*>(evict_move_kernel<D, kKvFp4>);
 }
 
+template <int D>
+const void* cluster_kernel(int kv) {
+  return kv == kKvBf16   ? reinterpret_cast<const void*>(evict_kernel<D, kKvBf16, true>)
+         : kv == kKvE4m3 ? reinterpret_cast<const void*>(evict_kernel<D, kKvE4m3, true>)
+                         : reinterpret_cast<const void*>(evict_kernel<D, kKvFp4, true>);
+}
+
 }  // namespace
 
 // The kept positions, then (contexts too long for shared memory) the keys.
 size_t evict_scratch_bytes(int num_seqs, int num_kv_heads, int keep, int max_context_len) {
   const size_t units = (size_t)num_seqs * num_kv_heads;
-  return units * keep * sizeof(int32_t) + (max_context_len > kKeySmem ? units * max_context_len * sizeof(uint32_t) : 0);
+  const bool two = max_context_len > kEvictCtas * kEvictKeys;
+  return units * keep * sizeof(int32_t) + (two ? units * max_context_len * sizeof(uint32_t) : 0);
 }
 
-cudaError_t launch_evict(const EvictParams& p, int head_dim, int kv_dtype, cudaStream_t st) {
-  const bool in_smem = p.max_context_len <= kKeySmem;
-  const void* pick = reinterpret_cast<const void*>(evict_pick_kernel);
-  cudaError_t e = set_smem_once(pick, kKeySmem * 4);
-  if (e != cudaSuccess) return e;
-  const int threads = p.max_context_len <= 2048 ? 256 : p.max_context_len <= 4096 ? 512 : 1024;
-  uint32_t* keys = in_smem ? nullptr : reinterpret_cast<uint32_t*>(p.kept + (size_t)p.num_seqs * p.num_kv_heads * p.keep);
-  evict_pick_kernel<<<dim3(p.num_kv_heads, p.num_seqs), threads, in_smem ? p.max_context_len * 4 : 0, st>>>(p, keys);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int pages = (min(p.keep, p.max_context_len) + 15) / 16;
-  if (pages == 0) return cudaSuccess;
+cudaError_t launch_evict(const EvictParams& p, int head_dim, int kv_dtype, int num_sms, cudaStream_t st) {
+  if (head_dim != 128 && head_dim != 64) return cudaErrorInvalidConfiguration;
   EvictParams pp = p;
   void* args[] = {&pp};
+  if (p.max_context_len <= kEvictCtas * kEvictKeys) {
+    // moved by the clusters as well while all of their CTAs are resident at once, two an SM
+    const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads;
+    const bool move = units * kEvictCtas <= 2 * (int64_t)num_sms;
+    int ctas = kEvictCtas;  // one wave of four CTAs an SM where the keys fit
+    while (ctas > 1 && units * ctas > 4 * (int64_t)num_sms && (ctas / 2) * kEvictKeys >= p.max_context_len) ctas /= 2;
+    const void* fn = !move               ? reinterpret_cast<const void*>(evict_kernel<64, kKvBf16, false>)
+                     : head_dim == 128 ? cluster_kernel<128>(kv_dtype)
+                                       : cluster_kernel<64>(kv_dtype);
+    cudaError_t e = set_smem_once(fn, kEvictKeys * 4);
+    if (e != cudaSuccess) return e;
+    const int share = (p.max_context_len + ctas * 16 - 1) / (ctas * 16) * 16;
+    e = launch_clusters(fn, dim3(ctas, p.num_kv_heads, p.num_seqs), dim3(kEvictThreads), share * 4, ctas, st, args);
+    if (move || e != cudaSuccess) return e;
+  } else {
+    uint32_t* keys = reinterpret_cast<uint32_t*>(p.kept + (size_t)p.num_seqs * p.num_kv_heads * p.keep);
+    evict_pick_kernel<<<dim3(p.num_kv_heads, p.num_seqs), 1024, 0, st>>>(p, keys);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  const int pages = (min(p.keep, p.max_context_len) + 15) / 16;
+  if (pages == 0) return cudaSuccess;
   const dim3 grid(pages, p.num_seqs, (p.num_kv_heads + kMoveWarps - 1) / kMoveWarps);
-  if (head_dim != 128 && head_dim != 64) return cudaErrorInvalidConfiguration;
   return launch_dependent(head_dim == 128 ? move_kernel<128>(kv_dtype) : move_kernel<64>(kv_dtype), grid,
                           dim3(kMoveWarps * 32), 0, st, args);
 }

@@ -160,7 +160,7 @@ struct EvictParams {
   int num_seqs, max_blocks_per_seq, new_blocks, num_blocks, num_kv_heads, max_context_len, keep, sinks, recent;
 };
 size_t evict_scratch_bytes(int num_seqs, int num_kv_heads, int keep, int max_context_len);
-cudaError_t launch_evict(const EvictParams& p, int head_dim, int kv_dtype, cudaStream_t st);
+cudaError_t launch_evict(const EvictParams& p, int head_dim, int kv_dtype, int num_sms, cudaStream_t st);
 
 // RMS norm and rotation of the query and key head rows; strides in elements between tokens.
 struct RopeParams {

@@ -47,8 +47,9 @@ struct ScoreShared {
 };
 
 // Scores of 16-block tiles first, first + stride, ... (at most `most` of them, below ncols blocks) of (b, g) by each warp of
-// a CTA: sink(column, score) for every block.  Blocks that are not there score -infinity and are flagged.
-template <int D, int NT, class Sink>
+// a CTA: sink(column, score) for every block.  Blocks that are not there score -infinity and are flagged.  WARP: the warp
+// alone works on (b, g), and sh is its own.
+template <int D, int NT, bool WARP, class Sink>
 __device__ __forceinline__ void score_tiles(const SelectParams& p, int b, int g, int ncols, int first, int stride, int most,
                                             ScoreShared<D, NT>& sh, Sink sink) {
   constexpr int kChunks = D / 64;
@@ -81,7 +82,7 @@ __device__ __forceinline__ void score_tiles(const SelectParams& p, int b, int g,
   int id0 = id_at((first + stride) * 16 + gi), id1 = id_at((first + stride) * 16 + gi + 8);
 
   // the codes of row gi of each n-tile, pieces qi and qi + 4 of its d dims, positive and negative parts
-  for (int nt = warp; nt < NT; nt += kScoreWarps) {
+  for (int nt = WARP ? 0 : warp; nt < NT; nt += WARP ? 1 : kScoreWarps) {
     const int c = 8 * nt + gi;
     const bool real = c < R;
     const __nv_bfloat16* row =
@@ -123,7 +124,10 @@ __device__ __forceinline__ void score_tiles(const SelectParams& p, int b, int g,
     }
     if (qi == 0) sh.q_up[c] = exp2_int(f);
   }
-  __syncthreads();
+  if constexpr (WARP)
+    __syncwarp();
+  else
+    __syncthreads();
   float up[NT][2];  // of rows 2qi, 2qi + 1
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_select_kernel(const Se
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(keys0) : "r"(smem_addr(smem_keys)), "r"(0));
   cluster_wait();  // every CTA runs: its shared memory may be written
   const int first = rank * kScoreWarps + (threadIdx.x >> 5);
-  score_tiles<D, NT>(p, b, g, ncols, first, gridDim.x * kScoreWarps, kClusterCols, sh, [&](int col, float score) {
+  score_tiles<D, NT, false>(p, b, g, ncols, first, gridDim.x * kScoreWarps, kClusterCols, sh, [&](int col, float score) {
     const uint32_t key = col < p.sinks || col >= ncols - p.recent ? kKeyAlways : order_key(score);
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys0 + col * 4), "r"(key) : "memory");
   });
@@ -216,17 +220,23 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_select_kernel(const Se
   if (rank == 0) topk_in_order(smem_keys, ncols, p.count, top, [&](int at, int i) { out[at] = i; });
 }
 
-template <int D, int NT>
+// HEADS: the warps take neighbouring kv heads of the same blocks, whose bounds are neighbours in memory (kScoreWarps
+// or more heads); else the tiles of one head in turn.
+template <int D, int NT, bool HEADS>
 __global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const SelectParams p, int tiles_per_warp) {
-  __shared__ ScoreShared<D, NT> sh;
-  const int g = blockIdx.y, b = blockIdx.z;
+  __shared__ ScoreShared<D, NT> sh[HEADS ? kScoreWarps : 1];
+  const int warp = threadIdx.x >> 5, b = blockIdx.z;
+  const int g = HEADS ? blockIdx.y * kScoreWarps + warp : blockIdx.y;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int ncols = select_cols(p, b, blockIdx.x == 0 && g == 0 && threadIdx.x == 0);
-  const int first = blockIdx.x * kScoreWarps * tiles_per_warp;
-  if (first * 16 >= ncols) return;
+  const int first = blockIdx.x * (HEADS ? 1 : kScoreWarps) * tiles_per_warp;
+  if (first * 16 >= ncols || g >= p.num_kv_heads) return;  // (the whole CTA, or a warp that works alone)
   float* out = p.scores + ((size_t)b * p.num_kv_heads + g) * p.max_cols;
-  score_tiles<D, NT>(p, b, g, ncols, first + (threadIdx.x >> 5), kScoreWarps, tiles_per_warp, sh,
-                     [&](int col, float score) { out[col] = score; });
+  auto sink = [&](int col, float score) { out[col] = score; };
+  if constexpr (HEADS)
+    score_tiles<D, NT, true>(p, b, g, ncols, first, 1, tiles_per_warp, sh[warp], sink);
+  else
+    score_tiles<D, NT, false>(p, b, g, ncols, first + warp, kScoreWarps, tiles_per_warp, sh[0], sink);
 }
 
 // One CTA per (kv head, sequence).  IN_SMEM: the keys are kept in shared memory, else turned in place in the scores.
@@ -266,13 +276,19 @@ cudaError_t score(const SelectParams& p, int num_sms, cudaStream_t st) {
     void* args[] = {&pp};
     return launch_clusters(fn, dim3(ctas, p.num_kv_heads, p.num_seqs), dim3(kScoreWarps * 32), p.max_cols * 4, ctas, st, args);
   }
-  // a tile a warp until there are several waves of warps; then up to eight, so that a warp's loads run ahead (64 contexts
-  // of 8000 to 32768 tokens, 8 heads, with selection and attention: 1 tile 156 us, 2 144, 4 140, 8 138, 13 143)
+  // a tile a warp until there are several waves of warps; then up to sixteen, so that a warp's loads run ahead (64 contexts
+  // of 8000 to 32768 tokens, 8 heads, with selection and attention: 2 tiles 147 us, 4 143, 8 141, 16 139, 32 155)
   const int64_t tiles = (p.max_cols + 15) / 16, units = (int64_t)p.num_seqs * p.num_kv_heads;
-  int64_t per = tiles * units / ((int64_t)num_sms * 64);
-  per = per < 1 ? 1 : per > 8 ? 8 : per;
-  const dim3 grid((unsigned)((tiles + per * kScoreWarps - 1) / (per * kScoreWarps)), p.num_kv_heads, p.num_seqs);
-  block_score_kernel<D, NT><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)per);
+  int64_t per = tiles * units / ((int64_t)num_sms * 32);
+  per = per < 1 ? 1 : per > 16 ? 16 : per;
+  const bool heads = p.num_kv_heads >= kScoreWarps;
+  const int64_t cover = per * (heads ? 1 : kScoreWarps);
+  const dim3 grid((unsigned)((tiles + cover - 1) / cover),
+                  heads ? (p.num_kv_heads + kScoreWarps - 1) / kScoreWarps : p.num_kv_heads, p.num_seqs);
+  if (heads)
+    block_score_kernel<D, NT, true><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)per);
+  else
+    block_score_kernel<D, NT, false><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)per);
   return cudaGetLastError();
 }
 
@@ -310,7 +326,7 @@ cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, int num_sm
   }
   SelectParams pp = p;
   void* args[] = {&pp};
-  const int threads = p.max_cols <= 4096 ? 512 : 1024;
+  const int threads = p.max_cols <= 4096 ? 256 : 1024;  // (512 lists of up to 2048: 512 threads cost 4 us more)
   return launch_dependent(fn, dim3(p.num_kv_heads, p.num_seqs), dim3(threads), smem, st, args);
 }
 

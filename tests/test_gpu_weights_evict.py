@@ -242,7 +242,7 @@ def test_infinities_nans_and_negative_sums():
         _evict(dict(c), sums.clone(), keep, 4, 8)
 
 
-@pytest.mark.parametrize("n", [2048, 2049, 4097, 50000, 50016, 70000])
+@pytest.mark.parametrize("n", [2048, 2049, 4097, 50016, 98304, 98305, 120000])
 def test_lengths_of_every_variant(n):
     c = A.make("bf16", [n, 100], [1] * 2, 1, 1, 64, seed=5, junk=False)
     _evict(c, _sums(c), 500, 4, 100, max_context_len=n)
