@@ -18,7 +18,7 @@
 namespace pa {
 namespace {
 
-constexpr int kBoundsWarps = 8;
+constexpr int kBoundsWarps = 4;
 constexpr int kBoundsCols = 4;  // columns of a CTA at most
 
 // Folds of 16-bit pairs; a NaN gives way to the other operand.
@@ -217,8 +217,8 @@ template <int D>
 cudaError_t launch_d(const BoundsParams& p, int kv, cudaStream_t st) {
   const int touched = min((p.n + 14) / 16 + 1, p.max_blocks_per_seq);  // columns that n tokens touch at most
   const int z = min((p.num_kv_heads + kBoundsWarps - 1) / kBoundsWarps, 64);
-  // several columns a CTA where there are enough of them to fill the device all the same (152 SMs of three or four CTAs)
-  const int cols = (int64_t)touched * p.num_seqs * z >= 152 * 4 * kBoundsCols ? kBoundsCols : 1;
+  // several columns a CTA where there are enough of them to fill the device all the same (152 SMs of six to eight CTAs)
+  const int cols = (int64_t)touched * p.num_seqs * z >= 152 * 8 * kBoundsCols ? kBoundsCols : 1;
   const dim3 grid((touched + cols - 1) / cols, p.num_seqs, z);
   if (kv == kKvBf16)
     block_bounds_kernel<D, kKvBf16><<<grid, kBoundsWarps * 32, 0, st>>>(p, cols);
