@@ -231,7 +231,6 @@ def _one_device(stream, *tensors, names="", **named):
     a context that makes it the current device for the call: the library launches on the
     current device.  names: the tensors' names in order, for the error."""
     if named:
-        names = " ".join([names, *named])
         tensors += tuple(named.values())
     index = None
     for t in tensors:
@@ -239,6 +238,7 @@ def _one_device(stream, *tensors, names="", **named):
             at = t.get_device()
             if at != index:
                 if index is not None or at < 0:
+                    names = " ".join([names, *named])
                     where = {n: str(x.device) for n, x in zip(names.split(), tensors) if x is not None}
                     raise ValueError(f"tensors must be on one CUDA device, got {where}")
                 index = at
@@ -250,12 +250,13 @@ def _one_device(stream, *tensors, names="", **named):
 
 
 def _check_cuda(name, t, dtypes):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 # (names of the accepted types, made once: every call passes them)
@@ -400,7 +401,10 @@ def _call(fn_name, q, k_cache, v_cache, block_table, context_lens, scale, *, k_s
     if not (blocks is group_starts is weights is prefix_lens is max_prefix_len is max_own_len is None) or decay != 1.0:
         fn_name, mask, counts, floats, more = _extra(fn_name, q.shape, cache_shape, max_context_len, blocks, group_starts,
                                                      prefix_lens, max_prefix_len, max_own_len, weights, decay, window)
-        _one_device(None, q=q, **more)  # (the check alone: the call's own is below)
+        index = q.get_device()
+        for t in more.values():
+            if t.get_device() != index:
+                _one_device(None, q=q, **more)  # (names them; the others are checked below)
     if fn_name == "paged_attn_tree_verify":
         _check_cuda("tree_mask", tree_mask, _I32)
         if tree_mask.shape != (B, q_len):
@@ -590,13 +594,16 @@ def block_bounds(k_cache, block_table, context_lens, n, bounds, bound_scale, *, 
         raise ValueError("expected k_cache [NB, Hkv, bs, d], bounds [NB, Hkv, 2, d] and block_table [B, M]")
     NB, Hkv, bs, last = k_cache.shape
     d = bounds.shape[3]
-    # (the value cache's checks are the key cache's: there is none here)
-    fp4 = k_cache.dtype is torch.uint8 and 16 * last == 9 * d
-    kv = _kv_dtype(k_cache, k_cache, d, k_scale, k_scale)
+    if k_cache.dtype is torch.bfloat16:
+        _check_cuda("k_cache", k_cache, _BF16)
+        kv = PA_KV_BF16
+    else:  # (the value cache's checks are the key cache's: there is none here)
+        kv = _kv_dtype(k_cache, k_cache, d, k_scale, k_scale)
     _check_cuda("block_table", block_table, _I32)
     _check_cuda("context_lens", context_lens, _I32)
-    B, n = block_table.shape[0], int(n)
-    if (last != d and not fp4) or bounds.shape != (NB, Hkv, 2, d) or bound_scale.shape != (NB, Hkv) \
+    B, M = block_table.shape
+    n = int(n)
+    if (last != d and kv != PA_KV_FP4_E2M1) or bounds.shape != (NB, Hkv, 2, d) or bound_scale.shape != (NB, Hkv) \
             or context_lens.shape != (B,) or n < 0:
         raise ValueError("shape mismatch between k_cache, bounds, bound_scale, block_table, context_lens and n")
     if kv == PA_KV_BF16:
@@ -606,7 +613,7 @@ def block_bounds(k_cache, block_table, context_lens, n, bounds, bound_scale, *, 
     with _one_device(stream, k_cache=k_cache, block_table=block_table, context_lens=context_lens, k_scale=k_scale,
                      bounds=bounds, bound_scale=bound_scale):
         st = lib.paged_attn_block_bounds(
-            k_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), B, _c_int(n), block_table.shape[1], NB, Hkv, d,
+            k_cache.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), B, _c_int(n), M, NB, Hkv, d,
             bs, kv, _ptr(k_scale), bounds.data_ptr(), bound_scale.data_ptr(), _stream_handle(stream))
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attn_block_bounds")
@@ -627,10 +634,10 @@ def select_blocks(q, bounds, bound_scale, block_table, context_lens, count, *, s
     if q.dim() != 4 or bounds.dim() != 4 or block_table.dim() != 2:
         raise ValueError("expected q [B, q_len, Hq, d], bounds [NB, Hkv, 2, d] and block_table [B, M]")
     B, q_len, Hq, d = q.shape
-    NB, Hkv = bounds.shape[:2]
+    NB, Hkv, ends, d2 = bounds.shape
+    rows, M = block_table.shape
     count = int(count)
-    if bounds.shape != (NB, Hkv, 2, d) or bound_scale.shape != (NB, Hkv) or block_table.shape[0] != B \
-            or context_lens.shape != (B,):
+    if ends != 2 or d2 != d or bound_scale.shape != (NB, Hkv) or rows != B or context_lens.shape != (B,):
         raise ValueError("shape mismatch between q, bounds, bound_scale, block_table and context_lens")
     if count < 1:
         raise ValueError("count must be at least 1")
@@ -643,12 +650,12 @@ def select_blocks(q, bounds, bound_scale, block_table, context_lens, count, *, s
     if B == 0:
         return out
     if max_context_len is None:
-        max_context_len = block_table.shape[1] * 16
+        max_context_len = M * 16
     with _one_device(stream, q=q, bounds=bounds, bound_scale=bound_scale, block_table=block_table,
                      context_lens=context_lens, out=out):
         st = lib.paged_attn_select_blocks(
             q.data_ptr(), bounds.data_ptr(), bound_scale.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(), B,
-            block_table.shape[1], NB, _c_int(max_context_len), q_len, Hq, Hkv, d, 16, _c_int(count), _c_int(sink_blocks),
+            M, NB, _c_int(max_context_len), q_len, Hq, Hkv, d, 16, _c_int(count), _c_int(sink_blocks),
             _c_int(recent_blocks), out.data_ptr(), _stream_handle(stream))
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attn_select_blocks")
