@@ -2,19 +2,24 @@
 //
 // A query row is rounded to int8 codes times a power of two 2^f, a block's bounds are int8 codes times 2^e
 // (pa_bounds.cu), and its score for the row is 2^f 2^e sum_i max(c_i hi_i, c_i lo_i): with c+ = max(c, 0) and c- = min(c, 0)
-// a product of [c+ | c-] with [hi | lo], 2 d long.  That is a matrix product of 16 blocks by 8 rows on the tensor
-// cores' int8 form, exact in int32 and, below 2^22, exact in fp32: no rounding anywhere, so the selection does not depend
-// on how it is computed.  A block counts for a kv head with its best row.
+// a product of [c+ | c-] with [hi | lo], 2 d long: a matrix product of 16 blocks by 8 rows on the tensor cores, whose
+// partial sums are whole numbers below 2^22.  No rounding anywhere, so the selection does not depend on how it is computed: up to
+// eight rows take the int8 form of the instruction, more the f16 form (codes are exact in f16, sums in fp32), as int8 runs
+// at a small part of f16's rate here and its pipe was the bound (20 rows a head: 2 us a tile; a step with them 50 us in
+// int8, 45 in f16), while turning bytes into f16 costs the few-row form more than it saves (151 us against 140, 64
+// contexts of up to 32768).  A block counts for a kv head with its best row.
 //
 // Scores: a warp takes 16 blocks of one (sequence, kv head) at a time, straight from global memory into A fragments (the
 // contraction's order is free: a lane reads whole 16-byte pieces, and the rows' codes are laid out alike, once for the CTA's
-// warps, in shared memory).  Bound by the bounds' bytes: a warp's next tile is loaded before this one's products.
+// warps, in shared memory).  Bound by the bounds' bytes: a warp's next tile is loaded before this one's products.  (A
+// ring of cp.async copies in shared memory, two tiles ahead, measured no faster: its room leaves fewer warps.)
 //
 // Selection (pa_topk.cuh): up to one wave of clusters, contexts of up to 4096 blocks take one kernel, a cluster of eight CTAs
 // for each (sequence, kv head), whose scores meet as keys in the first CTA's shared memory: one launch, no scratch.  Else
 // two: scores in scratch, then one CTA per (sequence, kv head).  With bounds and attention, 4 contexts of up to 16384
 // tokens take 24.6 us in one kernel and 26.6 in two, 64 of up to 32768 152 and 141: a cluster's CTAs leave together.
 #include "pa_kernels.h"
+#include "pa_mma.cuh"
 #include "pa_tc.cuh"
 #include "pa_topk.cuh"
 
@@ -32,6 +37,15 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Four signed bytes -> two f16 pairs, exactly: biased by 128 they are the low bits of 1024 + x.
+__device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  const uint32_t bias = 0x64806480u;  // 1024 + 128
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(bias));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(bias));
+}
+
 // e of the int8 codes of numbers up to amax: the smallest with amax 2^-e <= 127, at least -126.
 __device__ __forceinline__ int code_exp(float amax) {
   const uint32_t bits = __float_as_uint(fminf(amax, 3.4028235e38f));
@@ -41,9 +55,11 @@ __device__ __forceinline__ int code_exp(float amax) {
 
 template <int D, int NT>
 struct ScoreShared {
+  static constexpr bool kInt8 = NT == 1;
   static constexpr int kChunks = D / 64;  // 16-byte pieces of a lane in each half ([hi] and [lo]) of a row
-  uint4 q_frag[NT][2 * kChunks][32];      // B fragments: positive parts, then negative ones
-  float q_up[8 * NT];                     // 2^f of each row
+  // B fragments (for 16 codes one 16-byte piece in int8, two in f16): positive parts, then negative ones
+  uint4 q_frag[NT][2 * kChunks][kInt8 ? 1 : 2][32];
+  float q_up[8 * NT];  // 2^f of each row
 };
 
 // Scores of 16-block tiles first, first + stride, ... (at most `most` of them, below ncols blocks) of (b, g) by each warp of
@@ -52,7 +68,8 @@ struct ScoreShared {
 template <int D, int NT, bool WARP, class Sink>
 __device__ __forceinline__ void score_tiles(const SelectParams& p, int b, int g, int ncols, int first, int stride, int most,
                                             ScoreShared<D, NT>& sh, Sink sink) {
-  constexpr int kChunks = D / 64;
+  using S = ScoreShared<D, NT>;
+  constexpr int kChunks = S::kChunks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gi = lane >> 2, qi = lane & 3;
   const int Hkv = p.num_kv_heads, G = p.num_q_heads / Hkv, R = p.q_len * G;
   // the first tile's loads start before the rows are rounded
@@ -107,20 +124,33 @@ __device__ __forceinline__ void score_tiles(const SelectParams& p, int b, int g,
     const float down = exp2_int(-f);
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
-      uint32_t pos[4], neg[4];
+      uint32_t pos[8], neg[8];
+      if constexpr (S::kInt8) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        pos[w] = neg[w] = 0u;
+        for (int w = 0; w < 4; ++w) {
+          pos[w] = neg[w] = 0u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 v = bf16x2_to_f2(x[k][2 * w + e / 2]);
-          const int code = max(-127, min(127, __float2int_rn((e & 1 ? v.y : v.x) * down)));
-          pos[w] |= (uint32_t)(max(code, 0) & 0xff) << (8 * e);
-          neg[w] |= (uint32_t)(min(code, 0) & 0xff) << (8 * e);
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = bf16x2_to_f2(x[k][2 * w + e / 2]);
+            const int code = max(-127, min(127, __float2int_rn((e & 1 ? v.y : v.x) * down)));
+            pos[w] |= (uint32_t)(max(code, 0) & 0xff) << (8 * e);
+            neg[w] |= (uint32_t)(min(code, 0) & 0xff) << (8 * e);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          const float2 v = bf16x2_to_f2(x[k][w]);
+          const float a = fminf(fmaxf(rintf(v.x * down), -127.f), 127.f), d = fminf(fmaxf(rintf(v.y * down), -127.f), 127.f);
+          pos[w] = pack_f16(fmaxf(a, 0.f), fmaxf(d, 0.f));
+          neg[w] = pack_f16(fminf(a, 0.f), fminf(d, 0.f));
         }
       }
-      sh.q_frag[nt][k][lane] = make_uint4(pos[0], pos[1], pos[2], pos[3]);
-      sh.q_frag[nt][kChunks + k][lane] = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+#pragma unroll
+      for (int h = 0; h < (S::kInt8 ? 1 : 2); ++h) {
+        sh.q_frag[nt][k][h][lane] = make_uint4(pos[4 * h], pos[4 * h + 1], pos[4 * h + 2], pos[4 * h + 3]);
+        sh.q_frag[nt][kChunks + k][h][lane] = make_uint4(neg[4 * h], neg[4 * h + 1], neg[4 * h + 2], neg[4 * h + 3]);
+      }
     }
     if (qi == 0) sh.q_up[c] = exp2_int(f);
   }
@@ -147,23 +177,53 @@ __device__ __forceinline__ void score_tiles(const SelectParams& p, int b, int g,
     }
     if (((!cur.ok0 && col0 + gi < ncols) || (!cur.ok1 && col0 + gi + 8 < ncols)) && qi == 0)
       record_error(p.err, kErrBlockId);
+    // products: [0..1] of block gi, rows 2qi, 2qi + 1; [2..3] of block gi + 8
     float best0 = -INFINITY, best1 = -INFINITY;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    auto rows_of = [&](int nt, float x0, float x1, float x2, float x3) {
+      if (8 * nt + 2 * qi < R) {
+        best0 = fmaxf(best0, x0 * up[nt][0]);
+        best1 = fmaxf(best1, x2 * up[nt][0]);
+      }
+      if (8 * nt + 2 * qi + 1 < R) {
+        best0 = fmaxf(best0, x1 * up[nt][1]);
+        best1 = fmaxf(best1, x3 * up[nt][1]);
+      }
+    };
+    if constexpr (S::kInt8) {
       int acc[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < 2 * kChunks; ++k) {
-        const uint4 q = sh.q_frag[nt][k][lane];
+        const uint4 q = sh.q_frag[0][k][0][lane];
         mma_s8(acc, cur.a0[k].x, cur.a1[k].x, cur.a0[k].y, cur.a1[k].y, q.x, q.y);
         mma_s8(acc, cur.a0[k].z, cur.a1[k].z, cur.a0[k].w, cur.a1[k].w, q.z, q.w);
       }
-      // acc[0..1]: block gi, rows 2qi, 2qi + 1; acc[2..3]: block gi + 8
+      rows_of(0, (float)acc[0], (float)acc[1], (float)acc[2], (float)acc[3]);
+    } else {
+      float acc[NT][4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (8 * nt + 2 * qi + e < R) {
-          best0 = fmaxf(best0, (float)acc[e] * up[nt][e]);
-          best1 = fmaxf(best1, (float)acc[e + 2] * up[nt][e]);
+      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2 * kChunks; ++k) {
+        const uint32_t w0[4] = {cur.a0[k].x, cur.a0[k].y, cur.a0[k].z, cur.a0[k].w};
+        const uint32_t w1[4] = {cur.a1[k].x, cur.a1[k].y, cur.a1[k].z, cur.a1[k].w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s8x4_to_f16(w0[2 * h + e], a[e][0], a[e][2]);
+            s8x4_to_f16(w1[2 * h + e], a[e][1], a[e][3]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint4 q = sh.q_frag[nt][k][S::kInt8 ? 0 : h][lane];
+            mma_16816<false>(acc[nt], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
+            mma_16816<false>(acc[nt], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
+          }
         }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) rows_of(nt, acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
@@ -281,12 +341,13 @@ cudaError_t score(const SelectParams& p, int num_sms, cudaStream_t st) {
   const int64_t tiles = (p.max_cols + 15) / 16, units = (int64_t)p.num_seqs * p.num_kv_heads;
   int64_t per = tiles * units / ((int64_t)num_sms * 32);
   per = per < 1 ? 1 : per > 16 ? 16 : per;
-  const bool heads = p.num_kv_heads >= kScoreWarps;
+  constexpr bool kHeads = NT <= 2;  // (the rows of four heads fit in shared memory)
+  const bool heads = kHeads && p.num_kv_heads >= kScoreWarps;
   const int64_t cover = per * (heads ? 1 : kScoreWarps);
   const dim3 grid((unsigned)((tiles + cover - 1) / cover),
                   heads ? (p.num_kv_heads + kScoreWarps - 1) / kScoreWarps : p.num_kv_heads, p.num_seqs);
   if (heads)
-    block_score_kernel<D, NT, true><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)per);
+    block_score_kernel<D, NT, kHeads><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)per);
   else
     block_score_kernel<D, NT, false><<<grid, kScoreWarps * 32, 0, st>>>(p, (int)per);
   return cudaGetLastError();
