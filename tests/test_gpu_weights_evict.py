@@ -28,7 +28,8 @@ def _hold_weights(c, before, after, decay, dots, probs):
     additions, and the exponentials' own (2^-19); where partial rows meet in memory also the log2-sum-exps that they are
     kept as, of a part and of the row: the logarithm of a sum below 2^16 is below 16, so that two units in its last place
     (2^-20) are 2^-19, and the sum with the maximum, below 32, rounds by 2^-20, twice each and times ln 2 < 0.7; then
-    decay * sum + weight in fp32 (2^-23 of it)."""
+    decay * sum + weight in fp32, decay the fp32 number that the call takes (a product's and a sum's rounding, 2^-23 of it)."""
+    decay = float(np.float32(decay))
     want = before.double().numpy().copy()
     slack = np.zeros(want.shape)
     hkv, d = want.shape[1], c["d"]
