@@ -359,7 +359,8 @@ int paged_attn_weighted_decode(const void* q, const void* k_cache, const void* v
  * below everything -- and they move in their order, with their sums, to the blocks of new_table.
  *   k_cache, v_cache, k_scale, v_scale, kv_dtype, block_table, context_lens, max_context_len as in paged_attn_decode
  *                (4-bit caches: the scales are not used and may be NULL).
- *   weights      [num_blocks, num_kv_heads, 16] fp32, device, as paged_attn_weighted_decode keeps them.
+ *   weights      [num_blocks, num_kv_heads, 16] fp32, device, 16-byte aligned, as paged_attn_weighted_decode keeps
+ *                them.
  *   new_table    [num_seqs, new_blocks_per_seq] int32, device, new_blocks_per_seq * 16 >= keep: blocks that hold no
  *                token of any of the call's sequences, each once.  Blocks past the kept tokens are not touched.
  *   new_lens     [num_seqs] int32, device, written: the new context lengths.

@@ -937,7 +937,7 @@ int paged_attn_evict(void* k_cache, void* v_cache, float* weights, const int32_t
   if (keep < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep) return PA_ERR_INVALID_ARG;
   if ((int64_t)keep > (int64_t)new_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
   if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return PA_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(weights, 16)) return PA_ERR_INVALID_ARG;
   if (block_size != 16 || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
   if (num_seqs > 65535 || num_kv_heads > 65535 || max_context_len > (1 << 30)) return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;

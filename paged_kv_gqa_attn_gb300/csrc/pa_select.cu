@@ -338,7 +338,7 @@ cudaError_t score(const SelectParams& p, int num_sms, cudaStream_t st) {
   }
   // a tile a warp until there are several waves of warps; then up to sixteen, so that a warp's loads run ahead (64 contexts
   // of 8000 to 32768 tokens, 8 heads, with selection and attention: 2 tiles 147 us, 4 143, 8 141, 16 139, 32 155)
-  const int64_t tiles = (p.max_cols + 15) / 16, units = (int64_t)p.num_seqs * p.num_kv_heads;
+  const int64_t tiles = p.max_cols > 0 ? (p.max_cols + 15) / 16 : 1, units = (int64_t)p.num_seqs * p.num_kv_heads;
   int64_t per = tiles * units / ((int64_t)num_sms * 32);
   per = per < 1 ? 1 : per > 16 ? 16 : per;
   constexpr bool kHeads = NT <= 2;  // (the rows of four heads fit in shared memory)

@@ -119,3 +119,58 @@ def test_the_largest_batches():
     with pytest.raises(pa.PagedAttnError):
         pa.decode(q[:1].repeat(65536, 1, 1, 1), k, v, table[:1].repeat(65536, 1), lens[:1].repeat(65536), 0.1,
                   blocks=blocks[:1].repeat(65536, 1, 1))
+
+
+@pytest.mark.parametrize("n", [1, 200])
+def test_a_bound_of_no_tokens_at_all(n):
+    # max_context_len 0: every context is cut to nothing and flagged, on either route of each call
+    c = A.make("bf16", [40] * n, [1] * n, 4, 2, 64, seed=1, junk=False)
+    (q, k, v, table, lens), _ = S.on_gpu(c)
+    nb = len(k)
+    codes, scale = torch.zeros(nb, 2, 2, 64, dtype=torch.int8, device="cuda"), torch.ones(nb, 2, device="cuda")
+    w = torch.ones(nb, 2, 16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    kw = {"max_context_len": 0}
+    blocks = pa.select_blocks(q, codes, scale, table, lens, 4, **kw)
+    assert (blocks == -1).all() and pa.check_device_errors() == pa.PA_ERR_DEVICE_BOUNDS
+    starts, pre = torch.tensor([0, n], **i32), torch.tensor([16], **i32)
+    for more in ({"blocks": blocks}, {"weights": w}, {"group_starts": starts, "prefix_lens": pre}):
+        assert (pa.decode(q, k, v, table, lens, 0.1, **kw, **more) == 0).all()
+        assert pa.check_device_errors() == pa.PA_ERR_DEVICE_BOUNDS
+    assert (w == 1).all()
+    assert (pa.evict(k, v, w, table, lens, table.clone(), 5, **kw) == 0).all()
+    assert pa.check_device_errors() == pa.PA_ERR_DEVICE_BOUNDS
+
+
+def test_4_bit_caches_without_head_scales():
+    lens = [40, 333, 17]
+    c = A.make("fp4", lens, [1] * 3, 8, 2, 128, seed=2, head_scales=False)
+    S._check_bounds(c, 400)
+    B._run(c, B._lists(c, 2, 9, 3))
+    c = A.make("fp4", lens, [1] * 3, 8, 2, 128, seed=2, head_scales=False)
+    W._decode(c, W._sums(c), 1.0)
+    W._evict(c, W._sums(c), 30, 2, 5)
+
+
+@pytest.mark.parametrize("sign", [-1.0, 0.0, 2.0 ** -20])
+def test_odd_e4m3_scales(sign):
+    def odd(c):
+        from oracle import plain
+
+        c["k_scale"][::2] *= sign
+        c["v_scale"][1::2] *= sign
+        c["kf"], c["vf"] = (plain.e4m3_values(c[n].numpy(), c[n + "_scale"].numpy()) for n in ("k", "v"))
+        return c
+    lens = [40, 333, 170]
+    for r in (1, 3):
+        c = odd(A.make("e4m3", lens, [r] * 3, 8, 2, 64, seed=4, junk=False))
+        B._run(c, B._lists(c, 2, 9, 3), as_verify=r > 1)
+    W._decode(odd(A.make("e4m3", lens, [1] * 3, 8, 2, 64, seed=4, junk=False)), W._sums(c), 1.0)
+    (q, k, v, table, n), s = S.on_gpu(odd(A.make("e4m3", lens, [1] * 3, 8, 2, 64, seed=4, junk=False)))
+    table[1:, :2] = table[0, :2]
+    got = pa.decode(q, k, v, table, n, 0.125, group_starts=torch.tensor([0, 3], dtype=torch.int32, device="cuda"),
+                    prefix_lens=torch.tensor([32], dtype=torch.int32, device="cuda"), **s)
+    ref = pa.decode(q, k, v, table, n, 0.125, **s)
+    # two kernels' roundings of the same rows: 2^-8 of the outputs each, f16 weights 2^-11 of the values' sizes each
+    assert (got.float() - ref.float()).abs().max() <= 2.0 ** -6 * ref.float().abs().max()
+    assert pa.check_device_errors() == pa.PA_OK

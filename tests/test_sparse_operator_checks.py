@@ -170,6 +170,7 @@ def _evict(**over):
     (dict(), pa.PA_OK),
     (dict(w=None), pa.PA_ERR_INVALID_ARG),
     (dict(nt=None), pa.PA_ERR_INVALID_ARG),
+    (dict(w=FAKE + 8), pa.PA_ERR_INVALID_ARG),
     (dict(out=None), pa.PA_ERR_INVALID_ARG),
     (dict(keep=0), pa.PA_ERR_INVALID_ARG),
     (dict(keep=32), pa.PA_OK),
