@@ -150,11 +150,13 @@ __global__ void __launch_bounds__(PfTraits<D>::threads(KV), 2) prefill_tc_kernel
     b = -1;
     tile = QL = 0;
     int before = 0;
-    for (int i0 = 0; i0 < p.num_groups && b < 0; i0 += 32) {
+    const bool checks = z == 0 && g == 0 && part == 0;  // this CTA looks at every group
+    for (int i0 = 0; i0 < p.num_groups && (b < 0 || checks); i0 += 32) {
       PrefixGroup r = {0, 0, 0};
       unsigned wrong = 0;
       if (i0 + lane < p.num_groups) r = prefix_group(p, i0 + lane, wrong);
-      if (wrong && z == 0 && g == 0 && part == 0 && threadIdx.x < 32) record_error(p.err, wrong);
+      if (wrong && checks && threadIdx.x < 32) record_error(p.err, wrong);
+      if (b >= 0) continue;  // (its tile is found)
       const int tiles_here = r.tokens > 0 ? ((r.last - r.first) * p.q_len + Tt - 1) / Tt : 0;
       int upto = tiles_here;
 #pragma unroll

@@ -174,3 +174,25 @@ def test_odd_e4m3_scales(sign):
     # two kernels' roundings of the same rows: 2^-8 of the outputs each, f16 weights 2^-11 of the values' sizes each
     assert (got.float() - ref.float()).abs().max() <= 2.0 ** -6 * ref.float().abs().max()
     assert pa.check_device_errors() == pa.PA_OK
+
+
+@pytest.mark.parametrize("at", [1, 33, 69])
+def test_wrong_groups_are_flagged_wherever_they_stand(at):
+    n = 70
+    c = A.make("bf16", [40] * n, [1] * n, 4, 2, 64, seed=3, junk=False)
+    (q, k, v, table, lens), _ = S.on_gpu(c)
+    table[1:] = table[:1]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    starts, prefixes = torch.arange(n + 1, **i32), torch.full((n,), 16, **i32)
+    kw = {"group_starts": starts, "prefix_lens": prefixes, "max_prefix_len": 16}
+    ref = pa.decode(q, k, v, table, lens, 0.1, **kw)
+    assert pa.check_device_errors() == pa.PA_OK
+    prefixes[at] = 32  # past its bound: cut to it
+    assert torch.equal(pa.decode(q, k, v, table, lens, 0.1, **kw), ref)
+    assert pa.check_device_errors() == pa.PA_ERR_DEVICE_BOUNDS
+    prefixes[at] = 16
+    starts[at + 1] = n + 5  # the group, and the next one, share nothing
+    got = pa.decode(q, k, v, table, lens, 0.1, **kw)
+    assert pa.check_device_errors() == pa.PA_ERR_DEVICE_BOUNDS
+    assert torch.equal(got[:at], ref[:at])
+    assert (got.float() - ref.float()).abs().max() <= 2.0 ** -6 * ref.float().abs().max()
