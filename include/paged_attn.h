@@ -234,7 +234,8 @@ int paged_attn_window_prefill(const void* q, const void* k_cache, const void* v_
  * Both are written for every block that holds one of a sequence's last n tokens (context_lens counts them;
  * n past the context: all of its blocks), from all of the block's stored tokens; the others stay as they are.
  * A step calls it after paged_attn_append_kv with the same n, a prompt once with its length.  k_cache, kv_dtype and
- * k_scale as in paged_attn_decode; the key of a scaled cache is its fp32 value (code, times the 16-dim scale of
+ * k_scale as in paged_attn_decode (a block that several sequences share is written for each of them: they must hold the
+ * same tokens of it); the key of a scaled cache is its fp32 value (code, times the 16-dim scale of
  * a 4-bit one, times k_scale: one rounding).  Keys must be finite: a NaN gives way to the block's other tokens, an
  * infinity to the largest code.  Out-of-range block ids and contexts past the table are skipped and flagged.
  * Asynchronous on `stream`; never allocates.  Returns PA_OK (also for num_seqs == 0 or n == 0),
@@ -251,7 +252,8 @@ int paged_attn_block_bounds(const void* k_cache, const int32_t* block_table,
  * row is rounded (to nearest even) to int8 codes c times 2^f by the rule of the bounds, f from the row's largest
  * |q|; block j's score for it is 2^f 2^e sum_i (c_i > 0 ? c_i hi_i : c_i lo_i), and its score for a kv head the
  * largest over the head's rows (every new token, every query head of the group).  The sum is a whole number
- * below 2^22: the selection does not depend on the order of the arithmetic.
+ * below 2^22: the selection does not depend on the order of the arithmetic (while the products of the powers of
+ * two and those sums stay between 2^-126 and 2^127).
  *   q            [num_seqs, q_len, num_q_heads, head_dim] bf16, device, 16-byte aligned, finite.
  *   bounds, bound_scale  as paged_attn_block_bounds writes them, for every block of the contexts.
  *   count        blocks to select: the first sink_blocks and the last recent_blocks (together at most count)
@@ -260,8 +262,8 @@ int paged_attn_block_bounds(const void* k_cache, const int32_t* block_table,
  *   blocks       [num_seqs, num_kv_heads, count] int32, device, written: columns of the block table, ascending, then -1
  *                where the context has fewer.
  * Limits: q_len * (num_q_heads / num_kv_heads) at most 32, head_dim 64 or 128, block_size 16.  A block id out of range is
- * flagged and comes behind every other.  Scratch: 4 bytes per (block, kv head) of max_context_len.  Asynchronous on
- * `stream`.  Returns PA_OK (also for num_seqs == 0), PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_NO_MEMORY
+ * flagged and comes behind every other.  Scratch: 4 bytes per (block, kv head) of max_context_len where num_seqs *
+ * num_kv_heads exceeds the SMs or max_context_len 65536, else none.  Asynchronous on `stream`.  Returns PA_OK (also for num_seqs == 0), PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_NO_MEMORY
  * or PA_ERR_CUDA.
  */
 int paged_attn_select_blocks(const void* q, const int8_t* bounds, const float* bound_scale,
@@ -311,8 +313,9 @@ int paged_attn_sparse_verify(const void* q, const void* k_cache, const void* v_c
  *                  and scratch only.
  * The new tokens lie behind the prefix: a sequence with context_lens[b] < prefix + q_len, or with more of its own
  * than max_own_len, comes out as zeros and is flagged (PA_ERR_DEVICE_BOUNDS).  A prefix longer than its bound is cut to
- * it and flagged; group offsets that do not fit are flagged, their group shares nothing, and outputs of
- * sequences that two groups claim are undefined.  Same arguments and errors otherwise; limits: max_context_len at
+ * it and flagged (a bound below 16 shares nothing, and the groups are not read); group offsets that do not fit are
+ * flagged and their group shares nothing, but where offsets decrease so that two groups claim a sequence, the
+ * outputs of both groups and of those behind them are undefined.  Same arguments and errors otherwise; limits: max_context_len at
  * most 2^30, and the 128-row tiles of all groups (num_seqs * q_len rows of 128 / group tokens, one more a group) at most 65535.
  * Kernels: the tile kernel of paged_attn_prefill over the rows of all of a group's sequences (the prefix, split into
  * partitions), the window forms' kernels over the own tokens, one merge.
@@ -339,12 +342,13 @@ int paged_attn_prefix_verify(const void* q, const void* k_cache, const void* v_c
  *   weights[block, g, slot] = decay * weights[block, g, slot] + sum_h softmax(s_h)_j
  * for every token j of every sequence, h over the query heads of kv head g; the step's own token, j =
  * context_lens[b] - 1, has no sum yet and its slot is set to its weight.
- *   weights      [num_blocks, num_kv_heads, 16] fp32, device, 16-byte aligned: caller-owned, laid out as the cache (the sums of a prompt's tokens
- *                start at what the caller stores, zeros for instance).  Slots past a context are not touched.
+ *   weights      [num_blocks, num_kv_heads, 16] fp32, device, 16-byte aligned: caller-owned, laid out as the cache
+ *                (the sums of a prompt's tokens start at what the caller stores, zeros for instance).  Slots past a context are not touched.
  *   decay        finite; 0 overwrites without reading, 1 adds, less than 1 forgets.
  * Blocks that two sequences of the call share would get both sums in an undefined order: their sums are undefined.
  * Same arguments and errors otherwise; limits: num_q_heads / num_kv_heads at most 32, max_context_len at most 2^30.
- * Scratch: 4 bytes per (query head, token) of num_seqs * max_context_len beside the split's.
+ * Scratch: where the scores of max_context_len tokens do not fit in the shared memory of a cluster, 4 bytes per (query
+ * head, token) of num_seqs * max_context_len beside the split's.
  */
 int paged_attn_weighted_decode(const void* q, const void* k_cache, const void* v_cache,
                                const int32_t* block_table, const int32_t* context_lens,
@@ -363,7 +367,7 @@ int paged_attn_weighted_decode(const void* q, const void* k_cache, const void* v
  *                them.
  *   new_table    [num_seqs, new_blocks_per_seq] int32, device, new_blocks_per_seq * 16 >= keep: blocks that hold no
  *                token of any of the call's sequences, each once.  Blocks past the kept tokens are not touched.
- *   new_lens     [num_seqs] int32, device, written: the new context lengths.
+ *   new_lens     [num_seqs] int32, device, written: the new context lengths; not the memory of context_lens.
  * The old blocks are only read, so they may be shared, and the caller gives them back afterwards.  bf16 and 4-bit rows move as they
  * are; E4M3 pages get the scale amax / 448 of their tokens and are re-encoded as paged_attn_append_kv does.  Different
  * heads keep different tokens: a slot no longer stands for one position, so attention over what is left uses keys

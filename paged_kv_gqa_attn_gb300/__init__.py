@@ -666,8 +666,8 @@ def evict(k_cache, v_cache, weights, block_table, context_lens, new_table, keep,
           v_scale=None, max_context_len=None, head_dim=None, new_lens=None, stream=None):
     """Keep of every sequence and kv head the first `sinks` tokens, the last `recent` and, up to `keep` in all, those of
     the largest sums in weights [NB, Hkv, 16] fp32 (decode(weights=)); they move in order, with their sums, to the
-    blocks of new_table [B, M2] int32, which must hold no token of the batch.  Returns the new lengths [B] int32; the old blocks
-    stay as they are for the caller to give back.  head_dim as in read_kv.  See paged_attn_evict."""
+    blocks of new_table [B, M2] int32, which must hold no token of the batch.  Returns the new lengths [B] int32
+    (new_lens, which may not be context_lens); the old blocks stay as they are for the caller to give back.  head_dim as in read_kv.  See paged_attn_evict."""
     lib = load_library()
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or k_cache.shape != v_cache.shape \
             or block_table.dim() != 2 or new_table.dim() != 2:

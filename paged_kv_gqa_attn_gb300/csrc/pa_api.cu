@@ -279,6 +279,12 @@ int check_extra(const Extra& x, Form form, int num_seqs, int max_blocks_per_seq,
   return max_context_len > (1 << 30) ? PA_ERR_UNSUPPORTED : PA_OK;
 }
 
+// Whether int32 arrays of m and n elements share memory.
+bool overlap(const int32_t* a, int64_t m, const int32_t* b, int64_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * (uintptr_t)n && y < x + 4 * (uintptr_t)m;
+}
+
 size_t round_up(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
 // The split of shared prefixes of `pages` pages at most, in `units` (tile, kv head) pairs.  One CTA an SM or fewer: a
@@ -421,9 +427,11 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
         st = paged_attn_plan(dev->num_sms, num_seqs, num_kv_heads, covered, block_size, q_len, kv_dtype, &ppp, &nparts);
         if (st != PA_OK) return st;
       } else {
-        plan_split(mma_decode ? (l.form == pa::kFormOwn ? Split::kOwnDecode : Split::kDecode) : few_rows ? Split::kRows : Split::kTiles, kv_dtype, l.group * q_len,
-                   l.form == pa::kFormWindow || l.form == pa::kFormBlocks, dev->num_sms, (int64_t)num_seqs * num_kv_heads,
-                   ((int64_t)covered + block_size - 1) / block_size, align, &ppp, &nparts);
+        const Split kernel = mma_decode ? (l.form == pa::kFormOwn ? Split::kOwnDecode : Split::kDecode)
+                             : few_rows ? Split::kRows
+                                        : Split::kTiles;
+        plan_split(kernel, kv_dtype, l.group * q_len, l.form == pa::kFormWindow || l.form == pa::kFormBlocks, dev->num_sms,
+                   (int64_t)num_seqs * num_kv_heads, ((int64_t)covered + block_size - 1) / block_size, align, &ppp, &nparts);
       }
     } else {
       st = paged_attn_plan(dev->num_sms, num_seqs, num_kv_heads, covered, block_size, q_len, kv_dtype, &ppp, &nparts);
@@ -940,6 +948,7 @@ int paged_attn_evict(void* k_cache, void* v_cache, float* weights, const int32_t
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(weights, 16)) return PA_ERR_INVALID_ARG;
   if (block_size != 16 || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
   if (num_seqs > 65535 || num_kv_heads > 65535 || max_context_len > (1 << 30)) return PA_ERR_UNSUPPORTED;
+  if (overlap(new_lens, num_seqs, context_lens, num_seqs)) return PA_ERR_INVALID_ARG;  // (read by other CTAs)
   if (num_seqs == 0) return PA_OK;
   if (keep > max_context_len) keep = max_context_len > 0 ? max_context_len : 1;  // (every token of every sequence)
   DeviceState* dev = nullptr;

@@ -190,7 +190,7 @@ cudaError_t launch_accept(const float* p, const float* q, const int32_t* draft, 
 cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, int smem, cudaStream_t st, void** args);
 
 // launch_pdl for kernels whose every CTA waits (griddepcontrol.wait) before its first read of what the kernel before
-// it wrote, and before it returns.
+// it wrote, and before it returns; and for those over own tokens, which read nothing of it and whose first CTA waits.
 cudaError_t launch_dependent(const void* fn, dim3 grid, dim3 block, int smem, cudaStream_t st, void** args);
 
 // Launch in clusters of `ctas` along x (at most 8).

@@ -172,6 +172,9 @@ def _evict(**over):
     (dict(nt=None), pa.PA_ERR_INVALID_ARG),
     (dict(w=FAKE + 8), pa.PA_ERR_INVALID_ARG),
     (dict(out=None), pa.PA_ERR_INVALID_ARG),
+    (dict(B=3), pa.PA_ERR_INVALID_ARG),  # new_lens is context_lens
+    (dict(B=3, out=FAKE + 8), pa.PA_ERR_INVALID_ARG),
+    (dict(B=3, out=FAKE - 8), pa.PA_ERR_INVALID_ARG),
     (dict(keep=0), pa.PA_ERR_INVALID_ARG),
     (dict(keep=32), pa.PA_OK),
     (dict(keep=33), pa.PA_ERR_INVALID_ARG),
