@@ -6,11 +6,13 @@
 // not depend on how they are computed.  2 d + 4 bytes stand for the 32 d of a bf16 block's keys.
 //
 // A pass over the keys bound by their bytes: one warp takes the page of one (block, head), all of its loads in flight
-// at once (bf16, d = 128: eight 16-byte pieces a lane), and folds rows in packed 16-bit maxima and minima: E4M3 codes and
-// 4-bit codes times their scales are exact in f16, and the page's (head's) fp32 scale is applied once, at the end, as
-// rounding a product is monotone in its factor.  The lanes that hold the same dims of different rows then halve the dims
-// between them at every exchange, so that each ends with d / 32 dims of its own to round (all of them ending with all dims
-// cost 700 instructions a page where this takes 300, and more than half the time).
+// at once, a row of 128 or 256 bytes in one load of all lanes, so that a lane holds the same dims of every row (narrower rows:
+// of every second or fourth; the lanes that share dims then halve them between them, an exchange each).  Rows are folded in
+// packed 16-bit maxima and minima: E4M3 codes and 4-bit codes times their scales are exact in f16, and the page's (head's)
+// fp32 scale is applied once, at the end, as rounding a product is monotone in its factor.  Measured with 8 E4M3 contexts of
+// 9000 to 32768 tokens (floor 29.6 us): 16-byte loads, the lanes of a piece exchanging their dims, 54 us with all dims in every
+// lane and 43 with halves (the logic unit at three quarters of its rate), rounding without conversions 41; a lane's dims its own
+// 37, with ten CTAs an SM and no page ahead (a page ahead takes registers: eight CTAs and 39 us; two ahead 48).
 #include "pa_fp4.cuh"
 #include "pa_kernels.h"
 #include "pa_tc.cuh"
@@ -19,7 +21,7 @@ namespace pa {
 namespace {
 
 constexpr int kBoundsWarps = 4;
-constexpr int kBoundsCols = 4;  // columns of a CTA at most
+constexpr int kBoundsCols = 4;  // columns of a CTA at most (one a lane)
 
 // Folds of 16-bit pairs; a NaN gives way to the other operand.
 template <bool BF16>
@@ -45,20 +47,22 @@ template <int D, int KV>
 struct BoundsTraits {
   static constexpr bool kBf16 = KV == kKvBf16;
   static constexpr int kRowBytes = kBf16 ? 2 * D : KV == kKvE4m3 ? D : D / 2;  // of codes
-  static constexpr int kPieces = kRowBytes / 16;   // 16-byte pieces of a row: a lane each
+  static constexpr int kPieceBytes = kRowBytes == 256 ? 8 : 4;  // of a row: a lane each
+  static constexpr int kWords = kPieceBytes / 4;
+  static constexpr int kPieces = kRowBytes / kPieceBytes;
   static constexpr int kRowsAtOnce = 32 / kPieces;
   static constexpr int kLoads = 16 / kRowsAtOnce;
-  static constexpr int kDims = D / kPieces;        // dims of a lane: 8, 16 or 32
+  static constexpr int kDims = D / kPieces;        // dims of a lane: 2, 4 or 8
   static constexpr int kPairs = kDims / 2;
   static constexpr int kPageBytes = KV == kKvFp4 ? Fp4Page<D>::kBytes : 16 * kRowBytes;
+  static constexpr int kMinCtas = kRowBytes == 256 ? 8 : 10;  // of an SM (a page in registers: 32 or 16 a thread)
   static constexpr int kOwnPairs = D / 64;         // of a lane in the end
   static_assert(kPairs / kRowsAtOnce == kOwnPairs, "the lanes of a piece share its dims");
 };
 
 template <int D, int KV>
-__global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const BoundsParams p, int cols) {
+__global__ void __launch_bounds__(kBoundsWarps * 32, (BoundsTraits<D, KV>::kMinCtas)) block_bounds_kernel(const BoundsParams p, int cols) {
   using T = BoundsTraits<D, KV>;
-  constexpr uint32_t kLowest = T::kBf16 ? 0xff80ff80u : 0xfc00fc00u, kHighest = T::kBf16 ? 0x7f807f80u : 0x7c007c00u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y;
   const int L = p.context_lens[b];
@@ -69,79 +73,58 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const B
   const int col0 = max(0, L - p.n) / 16 + blockIdx.x * cols;  // the CTA's columns [col0, col0 + count)
   const int count = min(cols, (L + 15) / 16 - col0);
   if (count <= 0) return;
-  int ids[kBoundsCols];
-#pragma unroll
-  for (int c = 0; c < kBoundsCols; ++c) {
-    ids[c] = c < count ? p.block_table[(size_t)b * p.max_blocks_per_seq + col0 + c] : 0;
-    if (ids[c] < 0 || ids[c] >= p.num_blocks) {
-      ids[c] = -1;
-      if (blockIdx.z == 0 && threadIdx.x == 0) record_error(p.err, kErrBlockId);
-    }
+  int ids = lane < count ? p.block_table[(size_t)b * p.max_blocks_per_seq + col0 + lane] : 0;  // lane c: column c's block
+  if (ids < 0 || ids >= p.num_blocks) {
+    ids = -1;
+    if (blockIdx.z == 0 && warp == 0) record_error(p.err, kErrBlockId);
   }
   const int piece = lane % T::kPieces, row0 = lane / T::kPieces;
-  // a page's loads: its codes (4-bit: and their scales)
-  struct Page {
-    uint4 x[T::kLoads];
-    uint32_t sc[KV == kKvFp4 ? T::kLoads : 1];
-    float s;
-  };
-  auto load = [&](Page& q, int c, int g) {
-    const size_t page = (size_t)max(ids[c], 0) * p.num_kv_heads + g;
+  auto bounds_of = [&](int id, int col, int g) {
+    const size_t page = (size_t)id * p.num_kv_heads + g;
     const uint8_t* src = p.k_cache + page * T::kPageBytes;
-    const int valid = ids[c] < 0 ? 0 : min(16, L - (col0 + c) * 16);
-#pragma unroll
-    for (int i = 0; i < T::kLoads; ++i) {
-      const int r = row0 + i * T::kRowsAtOnce;
-      if (r < valid) {
-        q.x[i] = *reinterpret_cast<const uint4*>(src + r * T::kRowBytes + piece * 16);
-        if constexpr (KV == kKvFp4)
-          q.sc[i] = *reinterpret_cast<const uint16_t*>(src + Fp4Page<D>::kCodeBytes + r * Fp4Page<D>::kScaleRow + piece * 2);
+    const int last = min(16, L - col * 16) - 1;
+    uint32_t x[T::kLoads][T::kWords], sc[KV == kKvFp4 ? T::kLoads : 1];  // codes (4-bit: and their scales)
+    auto row = [&](int i, int r) {
+      const uint8_t* at = src + r * T::kRowBytes + piece * T::kPieceBytes;
+      if constexpr (T::kWords == 2) {
+        const uint2 w = *reinterpret_cast<const uint2*>(at);
+        x[i][0] = w.x;
+        x[i][1] = w.y;
+      } else {
+        x[i][0] = *reinterpret_cast<const uint32_t*>(at);
       }
+      if constexpr (KV == kKvFp4) sc[i] = src[Fp4Page<D>::kCodeBytes + r * Fp4Page<D>::kScaleRow + piece / 2];
+    };
+    if (last == 15) {
+#pragma unroll
+      for (int i = 0; i < T::kLoads; ++i) row(i, row0 + i * T::kRowsAtOnce);
+    } else {  // rows past the last: it once more
+#pragma unroll
+      for (int i = 0; i < T::kLoads; ++i) row(i, min(row0 + i * T::kRowsAtOnce, last));
     }
-    q.s = 1.f;
-    if constexpr (KV == kKvE4m3) q.s = p.k_scale[page];
-    if constexpr (KV == kKvFp4) q.s = p.k_scale ? p.k_scale[g] : 1.f;
-  };
-  auto bounds_of = [&](const Page& q, int c, int g) {
-    if (ids[c] < 0) return;
-    const size_t page = (size_t)ids[c] * p.num_kv_heads + g;
-    const int valid = min(16, L - (col0 + c) * 16);
-    const float s = q.s;
+    float s = 1.f;
+    if constexpr (KV == kKvE4m3) s = p.k_scale[page];
+    if constexpr (KV == kKvFp4) s = p.k_scale ? p.k_scale[g] : 1.f;
     uint32_t hi[T::kPairs], lo[T::kPairs];
 #pragma unroll
-    for (int j = 0; j < T::kPairs; ++j) {
-      hi[j] = kLowest;
-      lo[j] = kHighest;
-    }
-#pragma unroll
     for (int i = 0; i < T::kLoads; ++i) {
-      if (row0 + i * T::kRowsAtOnce >= valid) continue;
-      const uint32_t w[4] = {q.x[i].x, q.x[i].y, q.x[i].z, q.x[i].w};
       uint32_t v[T::kPairs];
       if constexpr (KV == kKvBf16) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = w[j];
+        for (int j = 0; j < T::kWords; ++j) v[j] = x[i][j];
       } else if constexpr (KV == kKvE4m3) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[2 * j] = e4m3x2_to_f16x2(w[j]);
-          v[2 * j + 1] = e4m3x2_to_f16x2(w[j] >> 16);
-        }
+        v[0] = e4m3x2_to_f16x2(x[i][0]);
+        v[1] = e4m3x2_to_f16x2(x[i][0] >> 16);
       } else {
-        const uint32_t s2 = e4m3x2_to_f16x2(q.sc[i]);
+        const uint32_t s2 = e4m3x2_to_f16x2(sc[i]), sp = __byte_perm(s2, s2, 0x1010);
+        e2m1x8_to_f16x2(x[i][0], v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t h[4];
-          e2m1x8_to_f16x2(w[j], h);
-          const uint32_t sp = __byte_perm(s2, s2, j < 2 ? 0x1010 : 0x3232);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * j + e] = mul_f16x2(h[e], sp);
-        }
+        for (int j = 0; j < 4; ++j) v[j] = mul_f16x2(v[j], sp);
       }
 #pragma unroll
       for (int j = 0; j < T::kPairs; ++j) {
-        hi[j] = max_pair<T::kBf16>(hi[j], v[j]);
-        lo[j] = min_pair<T::kBf16>(lo[j], v[j]);
+        hi[j] = i == 0 ? v[j] : max_pair<T::kBf16>(hi[j], v[j]);
+        lo[j] = i == 0 ? v[j] : min_pair<T::kBf16>(lo[j], v[j]);
       }
     }
     // lanes of the same piece, o apart: each keeps one half of the pairs it still has and gets the other's of it
@@ -158,57 +141,63 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) block_bounds_kernel(const B
       if (top) kept += left;
     }
     // the lane's dims, times the fp32 scale; a negative scale turns the ends round
+    const bool turned = !T::kBf16 && s < 0.f;
     float top[2 * T::kOwnPairs], bottom[2 * T::kOwnPairs];
     float amax = 0.f;
 #pragma unroll
     for (int j = 0; j < T::kOwnPairs; ++j) {
+      const uint32_t above = turned ? lo[j] : hi[j], below = turned ? hi[j] : lo[j];
       float2 a, c;
       if constexpr (T::kBf16) {
-        a = bf16x2_to_f2(hi[j]);
-        c = bf16x2_to_f2(lo[j]);
+        a = bf16x2_to_f2(above);
+        c = bf16x2_to_f2(below);
       } else {
-        a = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
-        c = __half22float2(*reinterpret_cast<const __half2*>(&lo[j]));
+        a = __half22float2(*reinterpret_cast<const __half2*>(&above));
+        c = __half22float2(*reinterpret_cast<const __half2*>(&below));
         a = make_float2(a.x * s, a.y * s);
         c = make_float2(c.x * s, c.y * s);
       }
-      top[2 * j] = fmaxf(a.x, c.x);
-      top[2 * j + 1] = fmaxf(a.y, c.y);
-      bottom[2 * j] = fminf(a.x, c.x);
-      bottom[2 * j + 1] = fminf(a.y, c.y);
-#pragma unroll
-      for (int i = 2 * j; i < 2 * j + 2; ++i) amax = fmaxf(amax, fmaxf(fabsf(top[i]), fabsf(bottom[i])));
+      top[2 * j] = a.x;
+      top[2 * j + 1] = a.y;
+      bottom[2 * j] = c.x;
+      bottom[2 * j + 1] = c.y;
+      amax = fmaxf(fmaxf(amax, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(c.x), fabsf(c.y)));
     }
-    // (magnitudes in the order of their bits; an infinity: the widest bounds)
-    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(fminf(amax, 3.4028235e38f)));
+    // (magnitudes in the order of their bits)
+    constexpr float kMax = 3.4028235e38f;
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(fminf(amax, kMax)));
+    if (bits == __float_as_uint(kMax)) {  // an infinity: the widest bounds
+#pragma unroll
+      for (int i = 0; i < 2 * T::kOwnPairs; ++i) {
+        top[i] = fmaxf(fminf(top[i], kMax), -kMax);
+        bottom[i] = fmaxf(fminf(bottom[i], kMax), -kMax);
+      }
+    }
     int e = (int)(bits >> 23) - 127 - 6 + ((bits & 0x7fffffu) > 0x7e0000u ? 1 : 0);  // above 127 / 64: one more
     e = bits == 0 ? 0 : max(e, -126);
     const float down = exp2_int(-e);
-    uint32_t upper = 0u, lower = 0u;
+    // rounded up and down to whole numbers by the addition of 1.5 2^23, whose low byte then is the code
+    uint32_t up[2 * T::kOwnPairs], dn[2 * T::kOwnPairs];
 #pragma unroll
     for (int i = 0; i < 2 * T::kOwnPairs; ++i) {
-      upper |= (uint32_t)(max(-127, min(127, __float2int_ru(top[i] * down))) & 0xff) << (8 * i);
-      lower |= (uint32_t)(max(-127, min(127, __float2int_rd(bottom[i] * down))) & 0xff) << (8 * i);
+      up[i] = __float_as_uint(__fmaf_ru(top[i], down, 12582912.f));
+      dn[i] = __float_as_uint(__fmaf_rd(bottom[i], down, 12582912.f));
     }
     int8_t* dst = p.bounds + page * (2 * D) + piece * T::kDims + 2 * kept;
     if constexpr (T::kOwnPairs == 2) {
-      *reinterpret_cast<uint32_t*>(dst) = upper;
-      *reinterpret_cast<uint32_t*>(dst + D) = lower;
+      *reinterpret_cast<uint32_t*>(dst) = __byte_perm(__byte_perm(up[0], up[1], 0x0040), __byte_perm(up[2], up[3], 0x0040), 0x5410);
+      *reinterpret_cast<uint32_t*>(dst + D) =
+          __byte_perm(__byte_perm(dn[0], dn[1], 0x0040), __byte_perm(dn[2], dn[3], 0x0040), 0x5410);
     } else {
-      *reinterpret_cast<uint16_t*>(dst) = (uint16_t)upper;
-      *reinterpret_cast<uint16_t*>(dst + D) = (uint16_t)lower;
+      *reinterpret_cast<uint16_t*>(dst) = (uint16_t)__byte_perm(up[0], up[1], 0x0040);
+      *reinterpret_cast<uint16_t*>(dst + D) = (uint16_t)__byte_perm(dn[0], dn[1], 0x0040);
     }
     if (lane == 0) p.bound_scale[page] = exp2_int(e);
   };
   for (int g = blockIdx.z * kBoundsWarps + warp; g < p.num_kv_heads; g += gridDim.z * kBoundsWarps) {
-    Page cur, next;
-    load(cur, 0, g);
-#pragma unroll
-    for (int c = 0; c < kBoundsCols; ++c) {  // the next page's loads before this one's arithmetic
-      if (c >= count) break;
-      if (c + 1 < kBoundsCols && c + 1 < count) load(next, c + 1 < kBoundsCols ? c + 1 : 0, g);
-      bounds_of(cur, c, g);
-      cur = next;
+    for (int c = 0; c < count; ++c) {
+      const int id = __shfl_sync(0xffffffffu, ids, c);
+      if (id >= 0) bounds_of(id, col0 + c, g);
     }
   }
 }
@@ -217,7 +206,7 @@ template <int D>
 cudaError_t launch_d(const BoundsParams& p, int kv, cudaStream_t st) {
   const int touched = min((p.n + 14) / 16 + 1, p.max_blocks_per_seq);  // columns that n tokens touch at most
   const int z = min((p.num_kv_heads + kBoundsWarps - 1) / kBoundsWarps, 64);
-  // several columns a CTA where there are enough of them to fill the device all the same (152 SMs of six to eight CTAs)
+  // several columns a CTA where there are enough of them to fill the device all the same (152 SMs of eight to ten CTAs)
   const int cols = (int64_t)touched * p.num_seqs * z >= 152 * 8 * kBoundsCols ? kBoundsCols : 1;
   const dim3 grid((touched + cols - 1) / cols, p.num_seqs, z);
   if (kv == kKvBf16)
