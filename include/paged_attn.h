@@ -262,8 +262,8 @@ int paged_attn_block_bounds(const void* k_cache, const int32_t* block_table,
  *   blocks       [num_seqs, num_kv_heads, count] int32, device, written: columns of the block table, ascending, then -1
  *                where the context has fewer.
  * Limits: q_len * (num_q_heads / num_kv_heads) at most 32, head_dim 64 or 128, block_size 16.  A block id out of range is
- * flagged and comes behind every other.  Scratch: 4 bytes per (block, kv head) of max_context_len where num_seqs *
- * num_kv_heads exceeds the SMs or max_context_len 65536, else none.  Asynchronous on `stream`.  Returns PA_OK (also for num_seqs == 0), PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_NO_MEMORY
+ * flagged and comes behind every other.  Scratch: 4 bytes per (block, kv head) of max_context_len where that exceeds
+ * 65536, or 16384 with more (sequence, kv head) pairs than SMs, else none.  Asynchronous on `stream`.  Returns PA_OK (also for num_seqs == 0), PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_NO_MEMORY
  * or PA_ERR_CUDA.
  */
 int paged_attn_select_blocks(const void* q, const int8_t* bounds, const float* bound_scale,

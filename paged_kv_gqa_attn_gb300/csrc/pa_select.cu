@@ -14,10 +14,12 @@
 // warps, in shared memory).  Bound by the bounds' bytes: a warp's next tile is loaded before this one's products.  (A
 // ring of cp.async copies in shared memory, two tiles ahead, measured no faster: its room leaves fewer warps.)
 //
-// Selection (pa_topk.cuh): up to one wave of clusters, contexts of up to 4096 blocks take one kernel, a cluster of eight CTAs
-// for each (sequence, kv head), whose scores meet as keys in the first CTA's shared memory: one launch, no scratch.  Else
-// two: scores in scratch, then one CTA per (sequence, kv head).  With bounds and attention, 4 contexts of up to 16384
-// tokens take 24.6 us in one kernel and 26.6 in two, 64 of up to 32768 152 and 141: a cluster's CTAs leave together.
+// Selection (pa_topk.cuh): contexts of up to 1024 blocks, or up to 4096 of no more (sequence, kv head) pairs than there are
+// SMs, take one kernel, a cluster of one to eight CTAs for each pair, whose scores meet as keys in the first CTA's shared memory:
+// one launch, no scratch.  Else two: scores in scratch, then one CTA per pair.  In one kernel and in two, us: 4 contexts of
+// 8 heads, up to 4096 / 16384 / 65536 tokens 10.3 and 11.8 / 12.3 and 14.7 / 20.6 and 22.0; 64 contexts 14.4 and 17.3 /
+// 30.1 and 29.5 / 82 and 66; 256 contexts 28.7 and 35.3 / 73.5 and 80.8; 64 of 2 heads, 65536 33.4 and 35.1.  (Many long ones lose:
+// a cluster's CTAs leave together, and its selection waits for the last of their scores.)
 #include "pa_kernels.h"
 #include "pa_mma.cuh"
 #include "pa_tc.cuh"
@@ -247,10 +249,12 @@ __device__ __forceinline__ int select_cols(const SelectParams& p, int b, bool fl
 
 constexpr int kClusterCtas = 8;     // at most
 constexpr int kClusterCols = 4096;  // keys in the first CTA's shared memory
+constexpr int kClusterColsMany = 1024;  // where there are more pairs than SMs
 
 // Whether a call takes the one kernel.
 bool in_clusters(int num_seqs, int num_kv_heads, int max_context_len, int num_sms) {
-  return max_context_len <= kClusterCols * 16 && (int64_t)num_seqs * num_kv_heads <= num_sms;
+  const bool few = (int64_t)num_seqs * num_kv_heads <= num_sms;
+  return max_context_len <= (few ? kClusterCols : kClusterColsMany) * 16;
 }
 
 template <int D, int NT>

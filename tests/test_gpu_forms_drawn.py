@@ -196,3 +196,15 @@ def test_wrong_groups_are_flagged_wherever_they_stand(at):
     assert pa.check_device_errors() == pa.PA_ERR_DEVICE_BOUNDS
     assert torch.equal(got[:at], ref[:at])
     assert (got.float() - ref.float()).abs().max() <= 2.0 ** -6 * ref.float().abs().max()
+
+
+@pytest.mark.parametrize("r,hq,hkv,d", [(1, 8, 4, 128), (1, 32, 8, 64), (3, 8, 2, 128), (1, 40, 2, 64), (1, 30, 1, 128), (2, 5, 5, 64)])
+def test_many_sequences_behind_a_wide_table(r, hq, hkv, d):
+    # more pairs than SMs and a bound past 16384 tokens: scores in scratch, whatever the lengths are
+    rng = random.Random(hq)
+    lens = _lens(rng, 160 // hkv + 40, 3000, 0)
+    q, codes, scale, table, n = S._problem(lens, r, hq, hkv, d, seed=hq, nb=3000)
+    wide = torch.full((len(lens), 2100), A.BAD_ID, dtype=torch.int32)
+    wide[:, : table.shape[1]] = table
+    S._check_select((q, codes, scale, wide, n), 24)
+    S._check_select((q, codes, scale, table, n), 24)
