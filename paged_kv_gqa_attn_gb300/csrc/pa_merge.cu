@@ -11,17 +11,19 @@ namespace pa {
 namespace {
 
 // One pass over a row's partitions, kBatch per turn with their loads issued together; the running
-// maximum M rescales what was summed before it grew (log-sum-exp rule).
-template <int D, int kBatch>
+// maximum M rescales what was summed before it grew (log-sum-exp rule).  GAP: partitions from `own` on lie `gap` slots
+// further on.
+template <int D, int kBatch, bool GAP = false>
 __device__ __forceinline__ void merge_partitions(const float* lse, const float* po, int nparts, int lane, float& M,
-                                                 float& wsum, float (&acc)[D / 32]) {
+                                                 float& wsum, float (&acc)[D / 32], int own = 0, int gap = 0) {
   constexpr int kDPL = D / 32;
   for (int q0 = 0; q0 < nparts; q0 += kBatch) {
     float lq[kBatch];
     float vv[kBatch][kDPL];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int q = min(q0 + k, nparts - 1);
+      int q = min(q0 + k, nparts - 1);
+      if (GAP && q >= own) q += gap;
       lq[k] = q0 + k < nparts ? lse[q] : -INFINITY;
       const float* src = po + (size_t)q * D + lane * kDPL;
       if constexpr (kDPL == 4) {
@@ -91,17 +93,19 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttnParams p) {
 #pragma unroll
   for (int e = 0; e < kDPL; ++e) acc[e] = 0.f;
   // a few partitions: eight per turn; many (long contexts): thirty-two per turn, fewer round trips
-  if (nparts <= 8)
-    merge_partitions<D, 8>(lse, po, nparts, lane, M, wsum, acc);
-  else
-    merge_partitions<D, 32>(lse, po, nparts, lane, M, wsum, acc);
-  if constexpr (FORM == kFormOwn) {
-    lse += p.own_partitions;
-    po += (size_t)p.own_partitions * D;
-    if (prefix_parts > 8)
-      merge_partitions<D, 32>(lse, po, prefix_parts, lane, M, wsum, acc);
-    else if (prefix_parts > 0)
-      merge_partitions<D, 8>(lse, po, prefix_parts, lane, M, wsum, acc);
+  if constexpr (FORM == kFormOwn) {  // a sequence's own and its prefix's, all in flight together
+    const int all = nparts + prefix_parts, gap = p.own_partitions - nparts;
+    if (all <= 8)
+      merge_partitions<D, 8, true>(lse, po, all, lane, M, wsum, acc, nparts, gap);
+    else if (all <= 16)
+      merge_partitions<D, 16, true>(lse, po, all, lane, M, wsum, acc, nparts, gap);
+    else
+      merge_partitions<D, 32, true>(lse, po, all, lane, M, wsum, acc, nparts, gap);
+  } else {
+    if (nparts <= 8)
+      merge_partitions<D, 8>(lse, po, nparts, lane, M, wsum, acc);
+    else
+      merge_partitions<D, 32>(lse, po, nparts, lane, M, wsum, acc);
   }
   if (FORM == kFormScores && lane == 0) p.lse[row] = M + __log2f(wsum);
   __nv_bfloat16* dst = p.out + row * D + lane * kDPL;
