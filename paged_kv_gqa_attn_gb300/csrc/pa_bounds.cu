@@ -1,18 +1,19 @@
 // Bounds of the keys of cache blocks: what the selection of blocks reads in place of their keys.
 //
-// For each (block, kv head) the largest and the smallest value of every dim over the block's tokens, as int8 codes times
-// one power of two 2^e: the smallest e with amax 2^-e <= 127, upper codes rounded up and lower ones down, so that
-// q . k <= sum_i max(q_i hi_i, q_i lo_i) holds for every token.  Scaling by a power of two is exact, so the codes do
-// not depend on how they are computed.  2 d + 4 bytes stand for the 32 d of a bf16 block's keys.
+// For each (block, kv head) the largest and the smallest value of every dim over the block's tokens, as int8 codes
+// times one power of two 2^e: the smallest e with amax 2^-e <= 127, upper codes rounded up and lower ones down, so
+// that q . k <= sum_i max(q_i hi_i, q_i lo_i) holds for every token.  Scaling by a power of two is exact, so the
+// codes do not depend on how they are computed.  2 d + 4 bytes stand for the 32 d of a bf16 block's keys.
 //
-// A pass over the keys bound by their bytes: one warp takes the page of one (block, head), all of its loads in flight
-// at once, a row of 128 or 256 bytes in one load of all lanes, so that a lane holds the same dims of every row (narrower rows:
-// of every second or fourth; the lanes that share dims then halve them between them, an exchange each).  Rows are folded in
-// packed 16-bit maxima and minima: E4M3 codes and 4-bit codes times their scales are exact in f16, and the page's (head's)
-// fp32 scale is applied once, at the end, as rounding a product is monotone in its factor.  Measured with 8 E4M3 contexts of
-// 9000 to 32768 tokens (floor 29.6 us): 16-byte loads, the lanes of a piece exchanging their dims, 54 us with all dims in every
-// lane and 43 with halves (the logic unit at three quarters of its rate), rounding without conversions 41; a lane's dims its own
-// 37, with ten CTAs an SM and no page ahead (a page ahead takes registers: eight CTAs and 39 us; two ahead 48).
+// A pass over the keys bound by their bytes: one warp takes the page of one (block, head), all of its loads in
+// flight at once, a row of 128 or 256 bytes in one load of all lanes, so that a lane holds the same dims of every
+// row (narrower rows: of every second or fourth; the lanes that share dims then halve them between them, an
+// exchange each).  Rows are folded in packed 16-bit maxima and minima: E4M3 codes and 4-bit codes times their
+// scales are exact in f16, and the page's (head's) fp32 scale is applied once, at the end, as rounding a product
+// is monotone in its factor.  Measured with 8 E4M3 contexts of 9000 to 32768 tokens (floor 29.6 us): 16-byte
+// loads, the lanes of a piece exchanging their dims, 54 us with all dims in every lane and 43 with halves (the
+// logic unit at three quarters of its rate), rounding without conversions 41; a lane's dims its own 37, with ten
+// CTAs an SM and no page ahead (a page ahead takes registers: eight CTAs and 39 us; two ahead 48).
 #include "pa_fp4.cuh"
 #include "pa_kernels.h"
 #include "pa_tc.cuh"

@@ -1,21 +1,22 @@
 // Eviction from the cache by accumulated attention weight.
 //
-// Each (sequence, kv head) keeps the first `sinks` tokens, the last `recent` ones and, up to `keep` in all, those whose
-// sums (pa_weights.cu) are the largest, ties to the earliest.  The kept tokens move in order to the blocks of another
-// table; the old blocks are only read, so blocks that other sequences share stay whole, every row moves
+// Each (sequence, kv head) keeps the first `sinks` tokens, the last `recent` ones and, up to `keep` in all, those
+// whose sums (pa_weights.cu) are the largest, ties to the earliest.  The kept tokens move in order to the blocks
+// of another table; the old blocks are only read, so blocks that other sequences share stay whole, every row moves
 // independently of the others, and the caller gives the old ones back afterwards.
 //
-// Contexts of up to 98304 tokens are selected by a cluster of eight CTAs for each (sequence, kv head), a share of the sums in
-// each one's shared memory as keys.  The k-th largest is found digit by digit (as in pa_topk.cuh), each CTA adding its counters to
-// everybody's, and the kept positions go to scratch.  Few (sequence, kv head) pairs are moved by the same cluster
-// after a barrier; many by a second kernel, whose warps spread over the device (16 contexts of up to 32768 tokens, 8 heads, 4096
-// kept: 116 us; moved by the clusters 147, as they all select, then all move; selected by one CTA each 120; with the
-// second kernel's CTAs started early, to wait on the SMs for the first's, 131).  Longer contexts are selected by one CTA each, with the keys in scratch.  A page is moved by a warp with all of its K and V
-// loads in flight.
+// Contexts of up to 98304 tokens are selected by a cluster of eight CTAs for each (sequence, kv head), a share of
+// the sums in each one's shared memory as keys.  The k-th largest is found digit by digit (as in pa_topk.cuh),
+// each CTA adding its counters to everybody's, and the kept positions go to scratch.  Few (sequence, kv head)
+// pairs are moved by the same cluster after a barrier; many by a second kernel, whose warps spread over the device
+// (16 contexts of up to 32768 tokens, 8 heads, 4096 kept: 116 us; moved by the clusters 147, as they all select,
+// then all move; selected by one CTA each 120; with the second kernel's CTAs started early, to wait on the SMs for
+// the first's, 131).  Longer contexts are selected by one CTA each, with the keys in scratch.  A page is moved by
+// a warp with all of its K and V loads in flight.
 //
-// bf16 rows and 4-bit rows (codes and their scales belong to the token) move as they are; E4M3 pages get the scale amax /
-// 448 of their new tokens, values times the old scales re-encoded in fp32 to nearest even as the append does.  Bound by
-// the kept rows' bytes, read and written once.
+// bf16 rows and 4-bit rows (codes and their scales belong to the token) move as they are; E4M3 pages get the scale
+// amax / 448 of their new tokens, values times the old scales re-encoded in fp32 to nearest even as the append
+// does.  Bound by the kept rows' bytes, read and written once.
 #include "pa_fp4.cuh"
 #include "pa_kernels.h"
 #include "pa_tc.cuh"

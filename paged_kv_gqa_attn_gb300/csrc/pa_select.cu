@@ -1,25 +1,28 @@
 // Selection of the cache blocks that a step's queries should read: a cheap score for each block, the highest kept.
 //
 // A query row is rounded to int8 codes times a power of two 2^f, a block's bounds are int8 codes times 2^e
-// (pa_bounds.cu), and its score for the row is 2^f 2^e sum_i max(c_i hi_i, c_i lo_i): with c+ = max(c, 0) and c- = min(c, 0)
-// a product of [c+ | c-] with [hi | lo], 2 d long: a matrix product of 16 blocks by 8 rows on the tensor cores, whose
-// partial sums are whole numbers below 2^22.  No rounding anywhere, so the selection does not depend on how it is computed: up to
-// eight rows take the int8 form of the instruction, more the f16 form (codes are exact in f16, sums in fp32), as int8 runs
-// at a small part of f16's rate here and its pipe was the bound (20 rows a head: 2 us a tile; a step with them 50 us in
-// int8, 45 in f16), while turning bytes into f16 costs the few-row form more than it saves (151 us against 140, 64
-// contexts of up to 32768).  A block counts for a kv head with its best row.
+// (pa_bounds.cu), and its score for the row is 2^f 2^e sum_i max(c_i hi_i, c_i lo_i): with c+ = max(c, 0) and c- =
+// min(c, 0) a product of [c+ | c-] with [hi | lo], 2 d long: a matrix product of 16 blocks by 8 rows on the tensor
+// cores, whose partial sums are whole numbers below 2^22.  No rounding anywhere, so the selection does not depend
+// on how it is computed: up to eight rows take the int8 form of the instruction, more the f16 form (codes are
+// exact in f16, sums in fp32), as int8 runs at a small part of f16's rate here and its pipe was the bound (20 rows
+// a head: 2 us a tile; a step with them 50 us in int8, 45 in f16), while turning bytes into f16 costs the few-row
+// form more than it saves (151 us against 140, 64 contexts of up to 32768).  A block counts for a kv head with its
+// best row.
 //
-// Scores: a warp takes 16 blocks of one (sequence, kv head) at a time, straight from global memory into A fragments (the
-// contraction's order is free: a lane reads whole 16-byte pieces, and the rows' codes are laid out alike, once for the CTA's
-// warps, in shared memory).  Bound by the bounds' bytes: a warp's next tile is loaded before this one's products.  (A
-// ring of cp.async copies in shared memory, two tiles ahead, measured no faster: its room leaves fewer warps.)
+// Scores: a warp takes 16 blocks of one (sequence, kv head) at a time, straight from global memory into A
+// fragments (the contraction's order is free: a lane reads whole 16-byte pieces, and the rows' codes are laid out
+// alike, once for the CTA's warps, in shared memory).  Bound by the bounds' bytes: a warp's next tile is loaded
+// before this one's products.  (A ring of cp.async copies in shared memory, two tiles ahead, measured no faster:
+// its room leaves fewer warps.)
 //
-// Selection (pa_topk.cuh): contexts of up to 1024 blocks, or up to 4096 of no more (sequence, kv head) pairs than there are
-// SMs, take one kernel, a cluster of one to eight CTAs for each pair, whose scores meet as keys in the first CTA's shared memory:
-// one launch, no scratch.  Else two: scores in scratch, then one CTA per pair.  In one kernel and in two, us: 4 contexts of
-// 8 heads, up to 4096 / 16384 / 65536 tokens 10.3 and 11.8 / 12.3 and 14.7 / 20.6 and 22.0; 64 contexts 14.4 and 17.3 /
-// 30.1 and 29.5 / 82 and 66; 256 contexts 28.7 and 35.3 / 73.5 and 80.8; 64 of 2 heads, 65536 33.4 and 35.1.  (Many long ones lose:
-// a cluster's CTAs leave together, and its selection waits for the last of their scores.)
+// Selection (pa_topk.cuh): contexts of up to 1024 blocks, or up to 4096 of no more (sequence, kv head) pairs than
+// there are SMs, take one kernel, a cluster of one to eight CTAs for each pair, whose scores meet as keys in the
+// first CTA's shared memory: one launch, no scratch.  Else two: scores in scratch, then one CTA per pair.  In one
+// kernel and in two, us: 4 contexts of 8 heads, up to 4096 / 16384 / 65536 tokens 10.3 and 11.8 / 12.3 and 14.7 /
+// 20.6 and 22.0; 64 contexts 14.4 and 17.3 / 30.1 and 29.5 / 82 and 66; 256 contexts 28.7 and 35.3 / 73.5 and
+// 80.8; 64 of 2 heads, 65536 33.4 and 35.1.  (Many long ones lose: a cluster's CTAs leave together, and its
+// selection waits for the last of their scores.)
 #include "pa_kernels.h"
 #include "pa_mma.cuh"
 #include "pa_tc.cuh"

@@ -1,11 +1,12 @@
 // The k largest of n numbers by one CTA, in the order of their indices (sm_103a).
 //
-// Numbers become unsigned keys of the same order.  The k-th largest key is found eight bits at a time, from the highest bit
-// in which the keys differ (scores of one query have the same sign and nearly the same exponent: from bit 31 all of
-// them would meet in one counter): a histogram of the next digit over the keys that agree with what is known so far, in
-// shared memory with four counters a digit (a lane takes one by its number), and one warp's scan from the highest digit down.  A
-// digit whose keys are all taken ends it early; equal keys at the border run to the last bit and are then taken from
-// the lowest index on.  Counts are whole numbers: nothing depends on an order of atomics.
+// Numbers become unsigned keys of the same order.  The k-th largest key is found eight bits at a time, from the
+// highest bit in which the keys differ (scores of one query have the same sign and nearly the same exponent: from
+// bit 31 all of them would meet in one counter): a histogram of the next digit over the keys that agree with what
+// is known so far, in shared memory with four counters a digit (a lane takes one by its number), and one warp's
+// scan from the highest digit down.  A digit whose keys are all taken ends it early; equal keys at the border run
+// to the last bit and are then taken from the lowest index on.  Counts are whole numbers: nothing depends on an
+// order of atomics.
 #pragma once
 
 #include <stdint.h>

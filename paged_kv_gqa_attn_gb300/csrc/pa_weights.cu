@@ -1,9 +1,9 @@
 // The step's softmax weights, folded into the sums that are kept for every cached token.
 //
-// Attention with kept scores leaves the base-2 scores x of a token's G query heads and each row's log2-sum-exp; the
-// token's weight is sum_h 2^(x_h - lse_h), and its sum becomes decay * sum + weight; the step's own token has no sum yet,
-// so that its slot is set.  A pass bound by bytes (4 G read, 4 read and written a token): a second one over K in place
-// of the kept scores would read 2 d bytes a token instead.
+// Attention with kept scores leaves the base-2 scores x of a token's G query heads and each row's log2-sum-exp;
+// the token's weight is sum_h 2^(x_h - lse_h), and its sum becomes decay * sum + weight; the step's own token has
+// no sum yet, so that its slot is set.  A pass bound by bytes (4 G read, 4 read and written a token): a second one
+// over K in place of the kept scores would read 2 d bytes a token instead.
 #include "pa_kernels.h"
 
 namespace pa {
