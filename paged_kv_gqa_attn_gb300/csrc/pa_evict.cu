@@ -8,11 +8,12 @@
 // Contexts of up to 98304 tokens are selected by a cluster of eight CTAs for each (sequence, kv head), a share of
 // the sums in each one's shared memory as keys.  The k-th largest is found digit by digit (as in pa_topk.cuh),
 // each CTA adding its counters to everybody's, and the kept positions go to scratch.  Few (sequence, kv head)
-// pairs are moved by the same cluster after a barrier; many by a second kernel, whose warps spread over the device
-// (16 contexts of up to 32768 tokens, 8 heads, 4096 kept: 116 us; moved by the clusters 147, as they all select,
-// then all move; selected by one CTA each 120; with the second kernel's CTAs started early, to wait on the SMs for
-// the first's, 131).  Longer contexts are selected by one CTA each, with the keys in scratch.  A page is moved by
-// a warp with all of its K and V loads in flight.
+// pairs are moved by the same cluster after a barrier; many by a second kernel, whose warps spread over the
+// device.  Measured with 16 contexts of up to 32768 tokens, 8 heads, 4096 kept: 111 us (116 while the selection
+// moved the sums; then moved by the clusters 147, as they all select, then all move; selected by one CTA each 120;
+// with the second kernel's CTAs started early, to wait on the SMs for the first's, 131).  Longer contexts are
+// selected by one CTA each, with the keys in scratch.  A page and its sums are moved by a warp with all of its
+// loads in flight.
 //
 // bf16 rows and 4-bit rows (codes and their scales belong to the token) move as they are; E4M3 pages get the scale
 // amax / 448 of their new tokens, values times the old scales re-encoded in fp32 to nearest even as the append
@@ -37,7 +38,6 @@ __global__ void __launch_bounds__(1024) evict_pick_kernel(const EvictParams p, u
   __shared__ TopkShared sh;
   const int g = blockIdx.x, b = blockIdx.y;
   const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
-  const int32_t* to = p.new_table + (size_t)b * p.new_blocks;
   const int L = evict_len(p, b), k = min(L, p.keep);
   const size_t unit = (size_t)b * p.num_kv_heads + g;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -46,36 +46,9 @@ __global__ void __launch_bounds__(1024) evict_pick_kernel(const EvictParams p, u
     if (p.context_lens[b] > p.max_context_len) record_error(p.err, kErrShortContext);
   }
   int32_t* kept = p.kept + unit * p.keep;
-  // the sums of k kept positions (pos(at) ascending) go to the new blocks, kMoves of a thread in flight at once
-  constexpr int kMoves = 4;
   const int threads = blockDim.x;
-  auto move_sums = [&](auto pos) {
-    for (int a0 = threadIdx.x; a0 < k; a0 += kMoves * threads) {
-      int from[kMoves], i[kMoves];
-      float w[kMoves];
-#pragma unroll
-      for (int j = 0; j < kMoves; ++j) i[j] = a0 + j * threads < k ? pos(a0 + j * threads) : 0;
-#pragma unroll
-      for (int j = 0; j < kMoves; ++j) from[j] = bt[i[j] / 16];
-#pragma unroll
-      for (int j = 0; j < kMoves; ++j) {
-        const bool there = from[j] >= 0 && from[j] < p.num_blocks;
-        if (!there) record_error(p.err, kErrBlockId);
-        w[j] = there ? p.weights[((size_t)from[j] * p.num_kv_heads + g) * 16 + i[j] % 16] : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < kMoves; ++j) {
-        const int at = a0 + j * threads;
-        if (at >= k) continue;
-        const int pb = to[at / 16];
-        if (pb >= 0 && pb < p.num_blocks)  // (out of range: flagged by the kernel that moves the rows)
-          p.weights[((size_t)pb * p.num_kv_heads + g) * 16 + at % 16] = w[j];
-      }
-    }
-  };
   if (L <= p.keep) {
     for (int i = threadIdx.x; i < L; i += threads) kept[i] = i;
-    move_sums([](int at) { return at; });
     return;
   }
   uint32_t* keys = all_keys + unit * p.max_context_len;
@@ -101,11 +74,9 @@ __global__ void __launch_bounds__(1024) evict_pick_kernel(const EvictParams p, u
   }
   __syncthreads();
   topk_in_order(keys, L, k, sh, [&](int at, int i) { kept[at] = i; });
-  __syncthreads();  // (the CTA's own writes)
-  move_sums([&](int at) { return kept[at]; });
 }
 
-// A warp moves the page (new block, head): lane t < 16 knows where token t comes from.
+// A warp moves the page (new block, head), rows and sums: lane t < 16 knows where token t comes from.
 template <int D, int KV>
 __device__ __forceinline__ void move_page(const EvictParams& p, int b, int g, int page, int k) {
   constexpr int kRowBytes = KV == kKvBf16 ? 2 * D : KV == kKvE4m3 ? D : D / 2;  // of codes
@@ -126,8 +97,13 @@ __device__ __forceinline__ void move_page(const EvictParams& p, int b, int g, in
     const int at = __ldcg(&p.kept[((size_t)b * p.num_kv_heads + g) * p.keep + page * 16 + lane]);
     src_block = p.block_table[(size_t)b * p.max_blocks_per_seq + at / 16];
     src_slot = at % 16;
-    if (src_block < 0 || src_block >= p.num_blocks) src_block = -1;  // its row becomes zeros (flagged with its sum)
+    if (src_block < 0 || src_block >= p.num_blocks) {  // its row and its sum become zeros
+      src_block = -1;
+      record_error(p.err, kErrBlockId);
+    }
   }
+  float sum = 0.f;
+  if (src_block >= 0) sum = p.weights[((size_t)src_block * p.num_kv_heads + g) * 16 + src_slot];
   const int piece = lane % kPieces, row0 = lane / kPieces;
   uint4 x[2][kLoads];
   float s[2][kLoads];
@@ -147,6 +123,7 @@ __device__ __forceinline__ void move_page(const EvictParams& p, int b, int g, in
       }
     }
   }
+  if (lane < valid) p.weights[dst_page * 16 + lane] = sum;
   if constexpr (KV == kKvFp4) {  // lanes 0-15: a token's K scales, lanes 16-31: its V scales
     using P = Fp4Page<D>;
     const int t = lane & 15, kv = lane >> 4;
@@ -238,12 +215,11 @@ __device__ __forceinline__ void cluster_sync() {
 // the rows as well (D, KV: of the caches).
 template <int D, int KV, bool MOVE>
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams p) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ EvictShared sh;
   const int ctas = gridDim.x, rank = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t* bt = p.block_table + (size_t)b * p.max_blocks_per_seq;
-  const int32_t* to = p.new_table + (size_t)b * p.new_blocks;
   const int L = evict_len(p, b), k = min(L, p.keep);
   const size_t unit = (size_t)b * p.num_kv_heads + g;
   int32_t* kept = p.kept + unit * p.keep;
@@ -251,38 +227,10 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
     p.new_lens[b] = k;
     if (p.context_lens[b] > p.max_context_len) record_error(p.err, kErrShortContext);
   }
-  auto sums = [&](auto pos, int n, auto use) {  // use(i, pos(i), its sum) for i of [0, n), kBatch of a thread in flight
-    constexpr int kBatch = 8;
-    for (int i0 = tid; i0 < n; i0 += kBatch * kEvictThreads) {
-      int pb[kBatch], at[kBatch];
-      float w[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) at[j] = i0 + j * kEvictThreads < n ? pos(i0 + j * kEvictThreads) : -1;
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) pb[j] = at[j] >= 0 ? bt[at[j] / 16] : 0;
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const bool there = pb[j] >= 0 && pb[j] < p.num_blocks;
-        if (!there) record_error(p.err, kErrBlockId);
-        w[j] = there && at[j] >= 0 ? p.weights[((size_t)pb[j] * p.num_kv_heads + g) * 16 + at[j] % 16] : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (at[j] >= 0) use(i0 + j * kEvictThreads, at[j], w[j]);
-    }
-  };
-  auto place = [&](int at, float w) {  // of kept token `at`
-    const int pb = to[at / 16];
-    if (pb >= 0 && pb < p.num_blocks)  // (out of range: flagged with the rows)
-      p.weights[((size_t)pb * p.num_kv_heads + g) * 16 + at % 16] = w;
-  };
   const int share = (L + ctas * 16 - 1) / (ctas * 16) * 16;
   const int begin = min(rank * share, L), n = min(share, L - begin);
   if (L <= p.keep) {  // (the whole cluster) every token
-    sums([&](int i) { return begin + i; }, n, [&](int i, int at, float w) {
-      kept[at] = at;
-      place(at, w);
-    });
+    for (int i = tid; i < n; i += kEvictThreads) kept[begin + i] = begin + i;
   } else {
     static_assert(kEvictThreads == 256, "a thread a digit");
     sh.total[0][tid] = sh.total[1][tid] = 0;
@@ -318,17 +266,20 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
 #pragma unroll
       for (int j = 0; j < kQuads; ++j) {
         const float w4[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        const int i = i0 + j * 4 * kEvictThreads, from = begin + i;
+        if (i >= n) break;
+        uint32_t x4[4];
+        const bool inner = from >= p.sinks && from + 4 <= L - p.recent && i + 4 <= n;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int i = i0 + j * 4 * kEvictThreads + e;
-          if (i >= n) break;
-          const bool forced = begin + i < p.sinks || begin + i >= L - p.recent;
-          const uint32_t x = forced ? kKeyAlways : order_key(w4[e]);
-          keys[i] = x;
-          always += forced;
-          top = max(top, forced ? 0u : x);
-          bottom = min(bottom, x);
+          // (past the share's end a key that no digit counts; the room is there, shares are multiples of 16)
+          const bool forced = !inner && (from + e < p.sinks || from + e >= L - p.recent || i + e >= n);
+          x4[e] = forced ? kKeyAlways : order_key(w4[e]);
+          always += forced && i + e < n;
+          top = max(top, forced ? 0u : x4[e]);
+          bottom = min(bottom, x4[e]);
         }
+        *reinterpret_cast<uint4*>(keys + i) = make_uint4(x4[0], x4[1], x4[2], x4[3]);
       }
     }
     top = __reduce_max_sync(0xffffffffu, top);
@@ -351,9 +302,13 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       shift = max(shift - 8, 0);
       for (int i = tid; i < 256; i += kEvictThreads) *reinterpret_cast<int4*>(&sh.hist[4 * i]) = make_int4(0, 0, 0, 0);
       __syncthreads();
-      for (int i = tid; i < n; i += kEvictThreads) {
-        const uint32_t x = keys[i];
-        if ((x & known) == low && x != kKeyAlways) atomicAdd(&sh.hist[((x & ~known) >> shift) * 4 + (lane & 3)], 1);
+      for (int i = 4 * tid; i < n; i += 4 * kEvictThreads) {
+        const uint4 x4 = *reinterpret_cast<const uint4*>(keys + i);
+        const uint32_t xs[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((xs[e] & known) == low && xs[e] != kKeyAlways)
+            atomicAdd(&sh.hist[((xs[e] & ~known) >> shift) * 4 + (lane & 3)], 1);
       }
       __syncthreads();
       const int4 c = *reinterpret_cast<const int4*>(&sh.hist[4 * tid]);
@@ -451,15 +406,11 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       eq_before += __popc(ea);
     }
   }
-  cluster_sync();  // the kept positions, written by all of the cluster
   if constexpr (MOVE) {
+    cluster_sync();  // the kept positions, written by all of the cluster
     const int pages = (k + 15) / 16;
     for (int page = rank * (kEvictThreads / 32) + warp; page < pages; page += ctas * (kEvictThreads / 32))
       move_page<D, KV>(p, b, g, page, k);
-  }
-  if (L > p.keep) {  // the sums of this CTA's share of the kept tokens
-    const int part = (k + ctas - 1) / ctas, a0 = rank * part;
-    sums([&](int i) { return __ldcg(&kept[a0 + i]); }, min(part, k - a0), [&](int i, int at, float w) { place(a0 + i, w); });
   }
 }
 
