@@ -167,16 +167,17 @@ __global__ void __launch_bounds__(kBoundsWarps * 32, (BoundsTraits<D, KV>::kMinC
     // (magnitudes in the order of their bits)
     constexpr float kMax = 3.4028235e38f;
     const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(fminf(amax, kMax)));
-    if (bits == __float_as_uint(kMax)) {  // an infinity: the widest bounds
-#pragma unroll
-      for (int i = 0; i < 2 * T::kOwnPairs; ++i) {
-        top[i] = fmaxf(fminf(top[i], kMax), -kMax);
-        bottom[i] = fmaxf(fminf(bottom[i], kMax), -kMax);
-      }
-    }
     int e = (int)(bits >> 23) - 127 - 6 + ((bits & 0x7fffffu) > 0x7e0000u ? 1 : 0);  // above 127 / 64: one more
     e = bits == 0 ? 0 : max(e, -126);
-    const float down = exp2_int(-e);
+    float down = exp2_int(-e);
+    if (bits == __float_as_uint(kMax)) {  // perhaps an infinity: the largest code
+#pragma unroll
+      for (int i = 0; i < 2 * T::kOwnPairs; ++i) {
+        top[i] = fmaxf(fminf(__fmul_ru(top[i], down), 127.f), -127.f);
+        bottom[i] = fmaxf(fminf(__fmul_rd(bottom[i], down), 127.f), -127.f);
+      }
+      down = 1.f;
+    }
     // rounded up and down to whole numbers by the addition of 1.5 2^23, whose low byte then is the code
     uint32_t up[2 * T::kOwnPairs], dn[2 * T::kOwnPairs];
 #pragma unroll

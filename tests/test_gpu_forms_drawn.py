@@ -208,3 +208,29 @@ def test_many_sequences_behind_a_wide_table(r, hq, hkv, d):
     wide[:, : table.shape[1]] = table
     S._check_select((q, codes, scale, wide, n), 24)
     S._check_select((q, codes, scale, table, n), 24)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_bounds_of_infinities_and_nans(d):
+    # an infinity takes the largest code of the widest scale, 2^122; a NaN gives way to the block's other tokens
+    k = torch.randn(3, 2, 16, d, generator=torch.Generator().manual_seed(d)).to(torch.bfloat16)
+    plain_k = k.clone()
+    k[0, 0, 5, 7], k[0, 0, 6, 8], k[0, 1, 0, 9] = float("inf"), float("-inf"), 3.3e38
+    k[1, 0, 0, 3] = k[1, 1, 15, 4] = k[2, 0, 7, 5] = float("nan")
+    plain_k[1, 0, 0, 3] = plain_k[1, 0, 1, 3]  # a token of the same block in the NaN's place
+    plain_k[1, 1, 15, 4] = plain_k[1, 1, 2, 4]
+    plain_k[2, 0, 7, 5] = plain_k[2, 0, 8, 5]
+    table, lens = torch.tensor([[0, 1, 2]], dtype=torch.int32, device="cuda"), torch.tensor([48], dtype=torch.int32, device="cuda")
+
+    def bounds(keys):
+        codes, scale = torch.zeros(3, 2, 2, d, dtype=torch.int8, device="cuda"), torch.zeros(3, 2, device="cuda")
+        pa.block_bounds(keys.cuda(), table, lens, 48, codes, scale)
+        assert pa.check_device_errors() == pa.PA_OK
+        return codes.cpu(), scale.cpu()
+    codes, scale = bounds(k)
+    want, want_scale = bounds(plain_k)
+    assert torch.equal(codes[1:], want[1:]) and torch.equal(scale[1:], want_scale[1:])
+    assert scale[0].tolist() == [2.0 ** 122, 2.0 ** 121 if float(k[0, 1, 0, 9]) <= 127 * 2.0 ** 121 else 2.0 ** 122]
+    assert codes[0, 0, 0, 7] == 127 and codes[0, 0, 1, 8] == -127
+    assert codes[0, 0, 0, 0] == 1 and codes[0, 0, 1, 0] == -1  # ordinary keys beside them: rounded outwards
+    assert codes[0, 1, 0, 9] == int(np.ceil(float(k[0, 1, 0, 9]) / float(scale[0, 1])))
