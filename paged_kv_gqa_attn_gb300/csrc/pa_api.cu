@@ -287,19 +287,22 @@ bool overlap(const int32_t* a, int64_t m, const int32_t* b, int64_t n) {
 
 size_t round_up(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
-// The split of shared prefixes of `pages` pages at most, in `units` (tile, kv head) pairs.  One CTA an SM or fewer: a
-// tile's shared memory leaves room for three CTAs over own tokens beside one, for none beside two.  As the ragged split
-// above, with the SMs as slots and CTAs whose start and end cost 90 pages where all are equally long, 38 where they are
-// not.  Measured (with the own tokens at their best split; partitions: us): 64 sequences behind 8192 tokens, bf16: 3 51.5, 6 43.6,
-// 9 47.1, 12 48.6, 19 53.1; 128 in 5 groups behind up to 16384, E4M3: 4 143, 8 119, 11 124, 16 133; 8 x 5 rows
-// behind 2048, 4-bit: 2 32.8, 4 26.9, 8 28.7, 16 34.4.
-void plan_prefix(bool one_group, int num_sms, int64_t units, int64_t pages, int* ppp, int* nparts) {
+// The split of shared prefixes of `pages` pages at most, in `units` (tile, kv head) pairs, beside `own` pages of own
+// tokens.  One CTA an SM or fewer: a tile's shared memory leaves room for three CTAs over own tokens beside one, for none
+// beside two.  As the ragged split above, with the SMs as slots and a cost of a CTA's start and end in pages.  Equally long
+// prefixes (one group): 90, and 180 where the own tokens are more than twice the prefixes' work, as every CTA takes room
+// from them; several groups, most of them shorter than the bound: 30.  Measured (costs 45, 60, 90, 130, 180, 250; us): 64
+// sequences behind 8192 tokens, bf16: 47.5, 46.1, 45.0, 43.4, 41.2, 43.1; 8 x 5 rows behind 2048, 4-bit: 28.1, 28.4, 26.9,
+// 30.2, 30.3, 32.8; 128 sequences in 5 groups behind up to 16384, E4M3 (costs 20, 24, 28, 32, 38, 50, 70): 122, 117, 115,
+// 115, 117, 120, 121.
+void plan_prefix(bool one_group, int num_sms, int64_t units, int64_t pages, int64_t own, int* ppp, int* nparts) {
   int64_t P = 1;
   const int forced = g_forced_partitions.load();
   if (forced > 0) {
     P = forced;
   } else {
-    const double x = (double)pages * num_sms / ((double)units * (one_group ? 90. : 38.));
+    const double cost = !one_group ? 30. : own > 2 * units * pages ? 180. : 90.;
+    const double x = (double)pages * num_sms / ((double)units * cost);
     while ((P + 0.5) * (P + 0.5) <= x && P < kAutoMaxPartitions) ++P;
   }
   if (P > pages) P = pages;
@@ -417,7 +420,9 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
       if (p.num_groups > 0)
         plan_prefix(p.num_groups == 1, dev->num_sms,
                     (int64_t)pa::prefix_tiles(num_seqs, q_len, l.group, p.num_groups) * num_kv_heads,
-                    p.max_prefix_len / block_size, &p.prefix_ppp, &prefix_parts);
+                    p.max_prefix_len / block_size,
+                    (int64_t)num_seqs * num_kv_heads * ((p.max_own_len + block_size - 1) / block_size), &p.prefix_ppp,
+                    &prefix_parts);
       const int64_t own = (int64_t)p.max_own_len + (align - 1) * block_size;  // (its first pages rounded down)
       covered = (int)(own < max_context_len ? own : max_context_len);
     }
