@@ -41,7 +41,8 @@
 namespace pa {
 namespace {
 
-template <int D, int NT, int KV>
+// JOIN: the partials that the CTAs of a cluster read from each other lie behind the warps' own.
+template <int D, int NT, int KV, bool JOIN>
 struct RowsTraits {
   static constexpr bool kBf16 = KV == kKvBf16, kFp8 = KV == kKvE4m3, kFp4 = KV == kKvFp4;
   static constexpr int kWarps = 4;
@@ -59,7 +60,8 @@ struct RowsTraits {
   static constexpr int kMTiles = D / 16;
   static constexpr int kMerge = kWarps * kCols * (D + 2) * 4;  // per-warp outputs, maxima, sums
   static constexpr int kStageRegion = kWarps * kStages * kStageBytes;
-  static constexpr int kDataRegion = kStageRegion > kMerge + kCols * (D + 4) * 4 ? kStageRegion : kMerge + kCols * (D + 4) * 4;
+  static constexpr int kJoin = JOIN ? kCols * (D + 4) * 4 : 0;  // joined rows, their masses and what they come to
+  static constexpr int kDataRegion = kStageRegion > kMerge + kJoin ? kStageRegion : kMerge + kJoin;
   static constexpr int kBarRegion = kWarps * kStages * 8;  // (a multiple of 16: kWarps is even)
   static constexpr int kQRegion = NT * (kKSteps / 2) * 32 * 16;
   static constexpr int kSmem = 1024 + kDataRegion + kBarRegion + kQRegion;  // 1 KiB: alignment of the swizzle
@@ -202,10 +204,10 @@ struct RowsMask {
 };
 
 template <int D, int NT, int KV, int FORM, bool JOIN>
-__global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits<D, NT, KV>::kMinBlocks))
+__global__ void __launch_bounds__((RowsTraits<D, NT, KV, JOIN>::kThreads), (RowsTraits<D, NT, KV, JOIN>::kMinBlocks))
     rows_mma_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv) {
-  using T = RowsTraits<D, NT, KV>;
+  using T = RowsTraits<D, NT, KV, JOIN>;
   constexpr bool LIST = FORM == kFormBlocks, OWN = FORM == kFormOwn, SCORES = FORM == kFormScores;
   constexpr bool WIN = FORM == kFormWindow || OWN;  // pages numbered with a gap
   constexpr bool kIdsAhead = !WIN && !LIST && !JOIN;  // the first block ids depend on the partition only
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__((RowsTraits<D, NT, KV>::kThreads), (RowsTraits
 
 template <int D, int NT, int KV, int FORM, bool JOIN>
 cudaError_t rows_launch(const AttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
-  using T = RowsTraits<D, NT, KV>;
+  using T = RowsTraits<D, NT, KV, JOIN>;
   constexpr int kKept = JOIN && FORM == kFormScores ? kJoinScores : 0;
   const void* fn = reinterpret_cast<const void*>(rows_mma_kernel<D, NT, KV, FORM, JOIN>);
   cudaError_t e = set_smem_once(fn, T::kSmem + kKept);
