@@ -877,8 +877,8 @@ int paged_attn_block_bounds(const void* k_cache, const int32_t* block_table, con
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.num_kv_heads = num_kv_heads;
-  return pa::launch_block_bounds(p, head_dim, kv_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
-                                                                                                          : PA_ERR_CUDA;
+  const cudaError_t e = pa::launch_block_bounds(p, head_dim, kv_dtype, dev->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 int paged_attn_select_blocks(const void* q, const int8_t* bounds, const float* bound_scale, const int32_t* block_table,

@@ -205,11 +205,11 @@ __global__ void __launch_bounds__(kBoundsWarps * 32, (BoundsTraits<D, KV>::kMinC
 }
 
 template <int D>
-cudaError_t launch_d(const BoundsParams& p, int kv, cudaStream_t st) {
+cudaError_t launch_d(const BoundsParams& p, int kv, int num_sms, cudaStream_t st) {
   const int touched = min((p.n + 14) / 16 + 1, p.max_blocks_per_seq);  // columns that n tokens touch at most
   const int z = min((p.num_kv_heads + kBoundsWarps - 1) / kBoundsWarps, 64);
-  // several columns a CTA where there are enough of them to fill the device all the same (152 SMs of eight to ten CTAs)
-  const int cols = (int64_t)touched * p.num_seqs * z >= 152 * 8 * kBoundsCols ? kBoundsCols : 1;
+  // several columns a CTA where there are enough of them to fill the device all the same (SMs of eight to ten CTAs)
+  const int cols = (int64_t)touched * p.num_seqs * z >= (int64_t)num_sms * 8 * kBoundsCols ? kBoundsCols : 1;
   const dim3 grid((touched + cols - 1) / cols, p.num_seqs, z);
   if (kv == kKvBf16)
     block_bounds_kernel<D, kKvBf16><<<grid, kBoundsWarps * 32, 0, st>>>(p, cols);
@@ -222,9 +222,9 @@ cudaError_t launch_d(const BoundsParams& p, int kv, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_block_bounds(const BoundsParams& p, int head_dim, int kv_dtype, cudaStream_t st) {
-  if (head_dim == 128) return launch_d<128>(p, kv_dtype, st);
-  if (head_dim == 64) return launch_d<64>(p, kv_dtype, st);
+cudaError_t launch_block_bounds(const BoundsParams& p, int head_dim, int kv_dtype, int num_sms, cudaStream_t st) {
+  if (head_dim == 128) return launch_d<128>(p, kv_dtype, num_sms, st);
+  if (head_dim == 64) return launch_d<64>(p, kv_dtype, num_sms, st);
   return cudaErrorInvalidConfiguration;
 }
 

@@ -113,7 +113,7 @@ struct BoundsParams {
   unsigned* err;
   int num_seqs, n, max_blocks_per_seq, num_blocks, num_kv_heads;
 };
-cudaError_t launch_block_bounds(const BoundsParams& p, int head_dim, int kv_dtype, cudaStream_t st);
+cudaError_t launch_block_bounds(const BoundsParams& p, int head_dim, int kv_dtype, int num_sms, cudaStream_t st);
 
 // The highest-scoring blocks of each (sequence, kv head).  scratch holds select_scratch_bytes(...) bytes.
 struct SelectParams {
