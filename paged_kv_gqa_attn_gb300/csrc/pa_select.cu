@@ -270,7 +270,13 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_select_kernel(const Se
   int32_t* out = p.blocks + ((size_t)b * p.num_kv_heads + g) * p.count;
   if (ncols <= p.count) {  // (the whole cluster) every block
     if (rank == 0)
-      for (int i = threadIdx.x; i < p.count; i += blockDim.x) out[i] = i < ncols ? i : -1;
+      for (int i = threadIdx.x; i < p.count; i += blockDim.x) {
+        out[i] = i < ncols ? i : -1;
+        if (g == 0 && i < ncols) {  // (nothing is scored here: the ids are looked at for the flag alone)
+          const int id = p.block_table[(size_t)b * p.max_blocks_per_seq + i];
+          if (id < 0 || id >= p.num_blocks) record_error(p.err, kErrBlockId);
+        }
+      }
     return;
   }
   cluster_arrive();
