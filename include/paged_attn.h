@@ -248,10 +248,12 @@ int paged_attn_block_bounds(const void* k_cache, const int32_t* block_table,
                             float* bound_scale, void* stream);
 
 /*
- * The blocks of each sequence that a step's queries should read, by an upper bound of their scores.  A query
+ * The blocks of each sequence that a step's queries should read, by what their keys can come to.  A query
  * row is rounded (to nearest even) to int8 codes c times 2^f by the rule of the bounds, f from the row's largest
  * |q|; block j's score for it is 2^f 2^e sum_i (c_i > 0 ? c_i hi_i : c_i lo_i), and its score for a kv head the
- * largest over the head's rows (every new token, every query head of the group).  The sum is a whole number
+ * largest over the head's rows (every new token, every query head of the group).  It is an upper bound of the rounded
+ * row's product with every key of the block; the row's own q . k may pass it by half a code of the row, 2^f / 2, times
+ * sum_i |k_i|.  The sum is a whole number
  * below 2^22: the selection does not depend on the order of the arithmetic (while the products of the powers of
  * two and those sums stay between 2^-126 and 2^127).
  *   q            [num_seqs, q_len, num_q_heads, head_dim] bf16, device, 16-byte aligned, finite.
