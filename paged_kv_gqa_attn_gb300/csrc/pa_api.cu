@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "paged_attn.h"
@@ -273,7 +274,7 @@ int check_extra(const Extra& x, Form form, int num_seqs, int max_blocks_per_seq,
         pa::prefix_tiles(num_seqs, q_len, num_q_heads / num_kv_heads, x.num_groups) > 65535)
       return PA_ERR_UNSUPPORTED;  // a grid dimension
   } else {
-    if (!x.weights || !aligned(x.weights, 16) || !(x.decay >= -3.4e38f && x.decay <= 3.4e38f)) return PA_ERR_INVALID_ARG;
+    if (!x.weights || !aligned(x.weights, 16) || !std::isfinite(x.decay)) return PA_ERR_INVALID_ARG;
     if (rows > pa::kRowsMax) return PA_ERR_UNSUPPORTED;
   }
   return max_context_len > (1 << 30) ? PA_ERR_UNSUPPORTED : PA_OK;
