@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(128) append_fp8_kernel(const AppendParams p) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
     __syncthreads();
     amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float new_scale = amax > 0.f ? amax / 448.f : 1.f;
+    const float new_scale = e4m3_page_scale(amax);
     // older tokens are re-encoded only when the scale moved
     if (mine && (sl >= s0 || new_scale != old_scale)) {
       uint32_t w[4];

@@ -268,6 +268,12 @@ __device__ __forceinline__ float2 e4m3x2_to_f2(uint16_t w) {
   return __half22float2(h);
 }
 
+// The scale of an E4M3 page whose largest magnitude is amax (not below the smallest fp32 number: a quotient that underflows to
+// zero would make NaNs of the codes).
+__device__ __forceinline__ float e4m3_page_scale(float amax) {
+  return amax > 0.f ? fmaxf(amax / 448.f, 0x1p-149f) : 1.f;
+}
+
 __device__ __forceinline__ void record_error(unsigned* err, unsigned bit) {
   if (err) atomicOr(err, bit);
 }

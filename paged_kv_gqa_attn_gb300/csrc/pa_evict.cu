@@ -162,7 +162,7 @@ __device__ __forceinline__ void move_page(const EvictParams& p, int b, int g, in
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const float scale = amax > 0.f ? amax / 448.f : 1.f;
+      const float scale = e4m3_page_scale(amax);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int r = row0 + i * kRowsAtOnce;
