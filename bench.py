@@ -91,7 +91,7 @@ def measured_peaks():
 
 # Source files each profiled kernel is built and launched from: a traffic figure stays valid
 # while none of them changes.
-COMMON_SOURCES = ("pa_api.cu", "pa_kernels.h", "pa_device.cuh", "pa_work_item.h")
+COMMON_SOURCES = ("pa_api.cu", "pa_kernels.h", "pa_device.cuh", "pa_prefix_plan.h", "pa_work_item.h")
 KERNEL_SOURCES = {
     "decode": ("pa_decode.cu", "pa_decode_mma.cu", "pa_decode_mma.cuh", "pa_mma.cuh", "pa_merge.cu", "pa_tc.cuh") + COMMON_SOURCES,
     "verify": ("pa_verify.cu", "pa_tc.cuh") + COMMON_SOURCES,

@@ -9,6 +9,7 @@
 
 #include "paged_attn.h"
 #include "pa_kernels.h"
+#include "pa_prefix_plan.h"
 #include "pa_work_item.h"
 
 // Per-device error word written by the kernels (see pa::kErr*).
@@ -242,7 +243,11 @@ void plan_split(Split kernel, int kv_dtype, int rows, bool windowed, int num_sms
   SplitCost cost = {38., 14., 1.5};
   if (bf16) cost = {decode ? 20. : 38., 8., 1.2};  // a page of twice the bytes or more
   if (few_rows && windowed && rows > 8) cost.fixed = 60.;
-  if (kernel == Split::kOwnDecode) cost.fixed *= 0.5;  // beside the prefixes' CTAs, which take room of some SMs only
+  // Beside the prefixes' CTAs, which take room of some SMs only.  How far above the best split of the own tokens this factor
+  // ends, on average over 63 shapes of each type with 500 own tokens or more: a quarter 4.3 (bf16) and 2.9 % (E4M3), a half 3.0
+  // and 2.6, three quarters 3.9 and 4.2, one 4.7 and 3.3; with fewer own tokens all within 1 %.  The rows and the tile kernel
+  // keep one: 4.1 and 3.5 %, 4-bit pages 3.2 (a half: 2.2, 3.0 and 4.2).
+  if (kernel == Split::kOwnDecode) cost.fixed *= 0.5;
   plan_rows(windowed, units, (int64_t)num_sms * per_sm, pages, cost, align, ppp, nparts);
 }
 
@@ -287,30 +292,6 @@ bool overlap(const int32_t* a, int64_t m, const int32_t* b, int64_t n) {
 }
 
 size_t round_up(size_t bytes) { return (bytes + 255) / 256 * 256; }
-
-// The split of shared prefixes of `pages` pages at most, in `units` (tile, kv head) pairs, beside `own` pages of own
-// tokens.  One CTA an SM or fewer: a tile's shared memory leaves room for three CTAs over own tokens beside one, for none
-// beside two.  As the ragged split above, with the SMs as slots and a cost of a CTA's start and end in pages.  Equally long
-// prefixes (one group): 90, and 180 where the own tokens are more than twice the prefixes' work, as every CTA takes room
-// from them; several groups, most of them shorter than the bound: 30.  Measured (costs 45, 60, 90, 130, 180, 250; us): 64
-// sequences behind 8192 tokens, bf16: 47.5, 46.1, 45.0, 43.4, 41.2, 43.1; 8 x 5 rows behind 2048, 4-bit: 28.1, 28.4, 26.9,
-// 30.2, 30.3, 32.8; 128 sequences in 5 groups behind up to 16384, E4M3 (costs 20, 24, 28, 32, 38, 50, 70): 122, 117, 115,
-// 115, 117, 120, 121.
-void plan_prefix(bool one_group, int num_sms, int64_t units, int64_t pages, int64_t own, int* ppp, int* nparts) {
-  int64_t P = 1;
-  const int forced = g_forced_partitions.load();
-  if (forced > 0) {
-    P = forced;
-  } else {
-    const double cost = !one_group ? 30. : own > 2 * units * pages ? 180. : 90.;
-    const double x = (double)pages * num_sms / ((double)units * cost);
-    while ((P + 0.5) * (P + 0.5) <= x && P < kAutoMaxPartitions) ++P;
-  }
-  if (P > pages) P = pages;
-  const int64_t per = ((pages + P - 1) / P + 3) / 4 * 4;  // whole 64-token steps
-  *ppp = (int)per;
-  *nparts = (int)((pages + per - 1) / per);
-}
 
 int run(Form form, const Window& win, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
         const int32_t* context_lens, const uint32_t* tree_mask, int num_seqs, int max_blocks_per_seq,
@@ -418,12 +399,14 @@ int run(Form form, const Window& win, const void* q, const void* k_cache, const 
       p.window = 1 << 30;  // no row's window ends in front of its sequence
       p.page_align = align;
       p.prefix_ppp = 1;
-      if (p.num_groups > 0)
-        plan_prefix(p.num_groups == 1, dev->num_sms,
-                    (int64_t)pa::prefix_tiles(num_seqs, q_len, l.group, p.num_groups) * num_kv_heads,
-                    p.max_prefix_len / block_size,
-                    (int64_t)num_seqs * num_kv_heads * ((p.max_own_len + block_size - 1) / block_size), &p.prefix_ppp,
-                    &prefix_parts);
+      if (p.num_groups > 0) {
+        const double units = pa::prefix_units(num_seqs, q_len, pa::prefix_tile_tokens(l.group), p.num_groups, num_kv_heads);
+        const int64_t own_pages = (int64_t)num_seqs * num_kv_heads * (((int64_t)p.max_own_len + block_size - 1) / block_size);
+        const pa::PrefixSplit split = pa::plan_prefix(units, p.max_prefix_len / block_size, own_pages, 2 * dev->num_sms,
+                                                      kAutoMaxPartitions, g_forced_partitions.load());
+        p.prefix_ppp = split.pages;
+        prefix_parts = split.parts;
+      }
       const int64_t own = (int64_t)p.max_own_len + (align - 1) * block_size;  // (its first pages rounded down)
       covered = (int)(own < max_context_len ? own : max_context_len);
     }

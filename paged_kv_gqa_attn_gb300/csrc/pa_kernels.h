@@ -76,8 +76,9 @@ cudaError_t rows_blocks_form(const AttnParams& p, const Launch& l, const CUtenso
 cudaError_t rows_own_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
 cudaError_t rows_scores_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
 cudaError_t tiles_own_form(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
-// The shared prefixes of p.num_groups groups, in at most prefix_tiles(...) tiles of 128 rows per kv head (a bound
-// without the groups' sizes: each but one may leave a tile part full).
+// The shared prefixes of p.num_groups groups, in at most prefix_tiles(...) tiles of 128 rows (prefix_tile_tokens new tokens) per
+// kv head: a bound without the groups' sizes, as each but one may leave a tile part full.
+int prefix_tile_tokens(int group);
 int prefix_tiles(int num_seqs, int q_len, int group, int num_groups);
 cudaError_t launch_prefix(const AttnParams& p, const Launch& l, const CUtensorMap& tk, const CUtensorMap& tv);
 // KV append (bf16 scatter, fp8 with per-(block, head) rescaling, or E2M1 codes with a scale for each

@@ -3,8 +3,10 @@
 
 namespace pa {
 
+int prefix_tile_tokens(int group) { return PfTraits<128>::kRows / group; }
+
 int prefix_tiles(int num_seqs, int q_len, int group, int num_groups) {
-  const int tt = PfTraits<128>::kRows / group;
+  const int tt = prefix_tile_tokens(group);
   return (num_seqs * q_len + tt - 1) / tt + num_groups - 1;
 }
 
