@@ -5,15 +5,17 @@
 // of another table; the old blocks are only read, so blocks that other sequences share stay whole, every row moves
 // independently of the others, and the caller gives the old ones back afterwards.
 //
-// Contexts of up to 98304 tokens are selected by a cluster of eight CTAs for each (sequence, kv head), a share of
+// Contexts of up to 98304 tokens are selected by a cluster of up to eight CTAs for each (sequence, kv head), a share of
 // the sums in each one's shared memory as keys.  The k-th largest is found digit by digit (as in pa_topk.cuh),
-// each CTA adding its counters to everybody's, and the kept positions go to scratch.  Few (sequence, kv head)
-// pairs are moved by the same cluster after a barrier; many by a second kernel, whose warps spread over the
-// device.  Measured with 16 contexts of up to 32768 tokens, 8 heads, 4096 kept: 111 us (116 while the selection
-// moved the sums; then moved by the clusters 147, as they all select, then all move; selected by one CTA each 120;
-// with the second kernel's CTAs started early, to wait on the SMs for the first's, 131).  Longer contexts are
-// selected by one CTA each, with the keys in scratch.  A page and its sums are moved by a warp with all of its
-// loads in flight.
+// each CTA adding its counters to everybody's, and the kept positions go to scratch.  A second kernel moves the rows, its
+// warps spread over the device.  Measured with 16 contexts of up to 32768 tokens, 8 heads, 4096 kept: 111 us (116 while
+// the selection moved the sums; selected by one CTA each 120; with the second kernel's CTAs started early, to wait on
+// the SMs for the first's, 131).  Moved by the selecting clusters instead, after a barrier, over contexts of 2048 to 32768
+// tokens and 512 to 4096 kept: 8 (sequence, head) pairs 1.06 to 1.46 times as long (bf16; E4M3 1.0 to 1.83, 4-bit 0.99 to
+// 1.33), 16 pairs 1.13 to 1.25 (1.03 to 1.44, 0.99 to 1.18), 32 0.99 to 1.06 (0.95 to 1.03, 0.96 to 1.01), 38 to 128 1.09 to
+// 1.47 (1.09 to 1.64, 0.92 to 1.27): few clusters leave most of the device idle, many select, then move, all at once.  Longer
+// contexts are selected by one CTA each, with the keys in scratch.  A page and its sums are moved by a warp with all of
+// its loads in flight.
 //
 // bf16 rows and 4-bit rows (codes and their scales belong to the token) move as they are; E4M3 pages get the scale
 // amax / 448 of their new tokens, values times the old scales re-encoded in fp32 to nearest even as the append
@@ -93,8 +95,7 @@ __device__ __forceinline__ void move_page(const EvictParams& p, int b, int g, in
   const size_t dst_page = (size_t)nb * p.num_kv_heads + g;
   int src_block = -1, src_slot = 0;
   if (lane < valid) {
-    // (from the L2: other CTAs of the cluster wrote it)
-    const int at = __ldcg(&p.kept[((size_t)b * p.num_kv_heads + g) * p.keep + page * 16 + lane]);
+    const int at = p.kept[((size_t)b * p.num_kv_heads + g) * p.keep + page * 16 + lane];
     src_block = p.block_table[(size_t)b * p.max_blocks_per_seq + at / 16];
     src_slot = at % 16;
     if (src_block < 0 || src_block >= p.num_blocks) {  // its row and its sum become zeros
@@ -211,9 +212,7 @@ __device__ __forceinline__ void cluster_sync() {
   cluster_wait();
 }
 
-// One cluster per (sequence, kv head).  CTA r has the keys of tokens [r * share, r * share + share).  MOVE: the cluster moves
-// the rows as well (D, KV: of the caches).
-template <int D, int KV, bool MOVE>
+// One cluster per (sequence, kv head).  CTA r has the keys of tokens [r * share, r * share + share).
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams p) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ EvictShared sh;
@@ -406,12 +405,6 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       eq_before += __popc(ea);
     }
   }
-  if constexpr (MOVE) {
-    cluster_sync();  // the kept positions, written by all of the cluster
-    const int pages = (k + 15) / 16;
-    for (int page = rank * (kEvictThreads / 32) + warp; page < pages; page += ctas * (kEvictThreads / 32))
-      move_page<D, KV>(p, b, g, page, k);
-  }
 }
 
 template <int D>
@@ -419,13 +412,6 @@ const void* move_kernel(int kv) {
   return kv == kKvBf16   ? reinterpret_cast<const void*>(evict_move_kernel<D, kKvBf16>)
          : kv == kKvE4m3 ? reinterpret_cast<const void*>(evict_move_kernel<D, kKvE4m3>)
                          : reinterpret_cast<const void*>(evict_move_kernel<D, kKvFp4>);
-}
-
-template <int D>
-const void* cluster_kernel(int kv) {
-  return kv == kKvBf16   ? reinterpret_cast<const void*>(evict_kernel<D, kKvBf16, true>)
-         : kv == kKvE4m3 ? reinterpret_cast<const void*>(evict_kernel<D, kKvE4m3, true>)
-                         : reinterpret_cast<const void*>(evict_kernel<D, kKvFp4, true>);
 }
 
 }  // namespace
@@ -442,19 +428,15 @@ cudaError_t launch_evict(const EvictParams& p, int head_dim, int kv_dtype, int n
   EvictParams pp = p;
   void* args[] = {&pp};
   if (p.max_context_len <= kEvictCtas * kEvictKeys) {
-    // moved by the clusters as well while all of their CTAs are resident at once, two an SM
     const int64_t units = (int64_t)p.num_seqs * p.num_kv_heads;
-    const bool move = units * kEvictCtas <= 2 * (int64_t)num_sms;
     int ctas = kEvictCtas;  // one wave of four CTAs an SM where the keys fit
     while (ctas > 1 && units * ctas > 4 * (int64_t)num_sms && (ctas / 2) * kEvictKeys >= p.max_context_len) ctas /= 2;
-    const void* fn = !move               ? reinterpret_cast<const void*>(evict_kernel<64, kKvBf16, false>)
-                     : head_dim == 128 ? cluster_kernel<128>(kv_dtype)
-                                       : cluster_kernel<64>(kv_dtype);
+    const void* fn = reinterpret_cast<const void*>(evict_kernel);
     cudaError_t e = set_smem_once(fn, kEvictKeys * 4);
     if (e != cudaSuccess) return e;
     const int share = (p.max_context_len + ctas * 16 - 1) / (ctas * 16) * 16;
     e = launch_clusters(fn, dim3(ctas, p.num_kv_heads, p.num_seqs), dim3(kEvictThreads), share * 4, ctas, st, args);
-    if (move || e != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
   } else {
     uint32_t* keys = reinterpret_cast<uint32_t*>(p.kept + (size_t)p.num_seqs * p.num_kv_heads * p.keep);
     evict_pick_kernel<<<dim3(p.num_kv_heads, p.num_seqs), 1024, 0, st>>>(p, keys);

@@ -1,6 +1,6 @@
 """Eviction around block ids that are not there, on the GPU: the whole pools and sums against an expected state, bit for bit.
 Tokens of a lost block count as sum 0 and move as zeros with a sum of 0; a page of the new table that is not there is
-left out, and nothing else changes.  Both ways that rows move (the selecting clusters, a second kernel)."""
+left out, and nothing else changes.  Few and many (sequence, head) pairs."""
 
 import pytest
 import torch
@@ -60,7 +60,7 @@ def _move(c, caches, sums, scales, table, fresh, sinks, recent):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3", "fp4"])
-@pytest.mark.parametrize("hkv", [2, 20])  # 6 and 60 (sequence, head) pairs: moved by their clusters, by a second kernel
+@pytest.mark.parametrize("hkv", [2, 20])  # 6 and 60 (sequence, head) pairs
 def test_lost_tokens_are_zeros_and_lost_pages_left_out(kv, hkv):
     c = A.make(kv, LENS, [1] * 3, hkv, hkv, 64, seed=hkv, junk=False)
     nb = c["k"].shape[0]

@@ -24,7 +24,7 @@ def _values(codes, scale):
     return codes.cpu().view(torch.float8_e4m3fn).double() * (scale.cpu().double() / TINY)[..., None, None]
 
 
-@pytest.mark.parametrize("hkv", [1, 40])  # moved by the selecting clusters, by a second kernel
+@pytest.mark.parametrize("hkv", [1, 40])
 @pytest.mark.parametrize("d", [64, 128])
 def test_evicted_pages(hkv, d):
     k, ks = _pages(6, hkv, d, 1)
