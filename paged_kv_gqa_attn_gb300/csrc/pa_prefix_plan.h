@@ -21,7 +21,7 @@ inline double prefix_units(int num_seqs, int q_len, int tokens_of_a_tile, int nu
 
 // The split of `units` such pairs over a longest prefix of `pages` pages, beside `own` pages of own tokens.  In pages of a tile's
 // work, n partitions of P pages cost about
-//   hypot(waves (P + 16), (units (pages + 16 n) + 2 own) / slots) + n:
+//   sqrt((waves (P + 16))^2 + ((units (pages + 16 n) + 2 own) / slots)^2) + n:
 // the longest chain of a slot (two CTAs an SM; 16 a CTA's start and end; a quarter of the way from whole waves to CTAs that fill
 // up each other's, as the groups' lengths are not known here), all of the work over all slots, and the merge.  The least of up to
 // `most` partitions is taken.  Measured over the splits of 704 shapes (1 to 12 groups of equal and unequal lengths, 4 to 256
@@ -38,8 +38,10 @@ inline PrefixSplit plan_prefix(double units, int64_t pages, int64_t own, int slo
     const int64_t P = n < pages ? n : pages;
     const int64_t per = ((pages + P - 1) / P + 3) / 4 * 4;
     const int parts = (int)((pages + per - 1) / per);
-    const double x = units * parts / slots, fill = 0.75 * ceil(x) + 0.25 * (x + 0.5), waves = fill > 1. ? fill : 1.;
-    const double t = hypot(waves * (per + kFixed), (units * (pages + kFixed * parts) + 2. * own) / slots) + parts;
+    const double x = units * parts / slots, all = (units * (pages + kFixed * parts) + 2. * own) / slots;
+    if (best.parts > 0 && all + parts >= least) break;  // (this much only grows with n)
+    const double fill = 0.75 * ceil(x) + 0.25 * (x + 0.5), chain = (fill > 1. ? fill : 1.) * (per + kFixed);
+    const double t = sqrt(chain * chain + all * all) + parts;
     if (best.parts == 0 || t < least) {
       least = t;
       best = {(int)per, parts};

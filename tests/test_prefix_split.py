@@ -85,7 +85,7 @@ def test_a_group_of_nothing_changes_little(plan):
 
 
 def test_more_own_tokens_never_take_more_partitions(plan):
-    """d cost / d own = 2 / slots * B / hypot(A, B), B the work over all slots and A the longest chain.  Of two splits neither of
+    """d cost / d own = 2 / slots * B / sqrt(A^2 + B^2), B the work over all slots and A the longest chain.  Of two splits neither of
     which has both smaller, the one of more partitions has the larger B and the smaller A, so that its cost grows faster."""
     for seqs in (8, 64, 256):
         for prefix in (2048, 8192, 16384):
