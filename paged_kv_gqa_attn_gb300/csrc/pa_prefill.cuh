@@ -45,10 +45,10 @@
 // both leave partials.
 // bf16 weights of a prefix are a high part and the rounded remainder, 16 significant bits as in the decode kernel, whose
 // results a call that names its prefixes should have: the remainder takes the other half of the step's S columns and
-// a second P.V, 43.6 -> 45.6 us a call for 64 sequences behind 8192 tokens in 5 partitions (cut instead of rounded high parts: the
-// same; root mean square error of 16 behind 1024: 8.43e-5
-// as decode's; with the high part alone 1.16e-4).  E4M3 scores at head_dim 128 stay on two E4M3 terms of Q, off by 2^-8 of
-// it at most: a third would take shared memory from the own tokens' CTAs beside the tile's.
+// a second P.V.  64 sequences behind 8192 tokens in 5 partitions: 43.6 -> 45.6 us a call, with cut instead of rounded high
+// parts the same; root mean square error of 16 sequences behind 1024: 8.43e-5 as decode's, with the high part alone
+// 1.16e-4.  E4M3 scores at head_dim 128 stay on two E4M3 terms of Q, off by 2^-8 of it at most: a third would take
+// shared memory from the own tokens' CTAs beside the tile's.
 #pragma once
 
 #include "pa_fp4.cuh"
