@@ -320,10 +320,9 @@ int paged_attn_sparse_verify(const void* q, const void* k_cache, const void* v_c
  * outputs of both groups and of those behind them are undefined.  Same arguments and errors otherwise; limits: max_context_len at
  * most 2^30, and the 128-row tiles of all groups (num_seqs * q_len rows of 128 / group tokens, one more a group) at most 65535.
  * Kernels: the tile kernel of paged_attn_prefill over the rows of all of a group's sequences (the prefix, split into
- * partitions), the window forms' kernels over the own tokens, one merge.  Precision: that of paged_attn_decode up to 16 rows
- * per kv head (more rows of bf16 caches: the own tokens' softmax weights are single bf16 numbers, as in paged_attn_verify),
- * but E4M3 caches of head_dim 128 take the prefix's scores from the query as two E4M3 terms, off by at most 2^-8 of it, as
- * paged_attn_verify and paged_attn_prefill do.
+ * partitions), the window forms' kernels over the own tokens, one merge.  Precision: that of paged_attn_decode, but for
+ * E4M3 caches of head_dim 128: the scores of the prefix, and of the own tokens of more than 32 rows per kv head, take
+ * the query as two E4M3 terms, off by at most 2^-8 of it, as in paged_attn_verify and paged_attn_prefill.
  */
 int paged_attn_prefix_decode(const void* q, const void* k_cache, const void* v_cache,
                              const int32_t* block_table, const int32_t* context_lens,

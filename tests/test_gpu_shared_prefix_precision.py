@@ -1,4 +1,4 @@
-"""Decode behind shared prefixes keeps the precision of ordinary decode, on the GPU against fp64: prefixes whose softmax has few
+"""Attention behind shared prefixes has the precision of ordinary decode, on the GPU against fp64: prefixes whose softmax has few
 heavy tokens, so that a weight's rounding shows, and rows outside every prefix, which only the own tokens' kernels compute.
 
 The bound is form_cases.check's for the decode and rows kernels (tiles=False): the output's rounding to bf16 (2^-8 |out|), bf16
@@ -36,6 +36,16 @@ LAYOUTS = [(8, 2, 128), (8, 8, 64), (16, 2, 64), (4, 2, 128), (6, 2, 128), (16, 
 def test_decode_behind_a_prefix(kv, groups, hq, hkv, d):
     c = _peaked(make(kv, groups, OWN, 1, hq, hkv, d, seed=hq + d), 3)
     check(c, run(c), causal(c["lens"], 1), tiles=False)
+
+
+@pytest.mark.parametrize("kv,r,hq,hkv,d", [
+    (kv, *shape) for kv in ("bf16", "fp4", "e4m3") for shape in [(2, 8, 2, 128), (5, 8, 2, 64), (9, 16, 2, 128), (7, 8, 1, 64),
+                                                                 (16, 8, 1, 64), (1, 32, 1, 128), (1, 64, 2, 64)]
+    if kv != "e4m3" or shape[3] != 128])
+def test_rows_behind_a_prefix(kv, r, hq, hkv, d):
+    # verify, and decode of large groups: 8 to 128 rows a kv head, own tokens on the rows and on the tile kernel
+    c = _peaked(make(kv, [(3, 64), (1, 333), (4, 0), (2, 400)], [1, 3, 70, 16, 200], r, hq, hkv, d, seed=r + hq), 3)
+    check(c, run(c), causal(c["lens"], r), tiles=False)
 
 
 @pytest.mark.parametrize("parts", [1, 3, 100])
