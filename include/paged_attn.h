@@ -314,8 +314,9 @@ int paged_attn_sparse_verify(const void* q, const void* k_cache, const void* v_c
  *   max_own_len    host-side bound of what a sequence has behind its prefix (context_lens[b] - prefix).  Both size grids
  *                  and scratch only.
  * The new tokens lie behind the prefix: a sequence with context_lens[b] < prefix + q_len, or with more of its own
- * than max_own_len, comes out as zeros and is flagged (PA_ERR_DEVICE_BOUNDS).  A prefix longer than its bound is cut to
- * it and flagged (a bound below 16 shares nothing, and the groups are not read); group offsets that do not fit are
+ * than max_own_len, comes out as zeros and is flagged (PA_ERR_DEVICE_BOUNDS).  Where a group that has sequences shares
+ * whole blocks past the bound (or past max_context_len), its prefix is cut to the bound and flagged (a bound below 16
+ * shares nothing, and the groups are not read); group offsets that do not fit are
  * flagged and their group shares nothing, but where offsets decrease so that two groups claim a sequence, the
  * outputs of both groups and of those behind them are undefined.  Same arguments and errors otherwise; limits: max_context_len at
  * most 2^30, and the 128-row tiles of all groups (num_seqs * q_len rows of 128 / group tokens, one more a group) at most 65535.

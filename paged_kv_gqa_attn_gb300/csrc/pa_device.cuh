@@ -90,11 +90,11 @@ __device__ __forceinline__ PrefixGroup prefix_group(const AttnParams& p, int i, 
     wrong |= kErrBadInput;
     r.first = r.last = 0;
   }
-  if (r.tokens > p.max_prefix_len) {
-    wrong |= kErrShortContext;
-    r.tokens = p.max_prefix_len;
-  }
   r.tokens = max(r.tokens, 0) / 16 * 16;
+  if (r.tokens > p.max_prefix_len) {
+    if (r.last > r.first) wrong |= kErrShortContext;  // (a group of no sequences shares nothing)
+    r.tokens = p.max_prefix_len / 16 * 16;
+  }
   return r;
 }
 // The grid over the own tokens is a programmatic dependent of the one over the prefixes, which it does not read from: they
